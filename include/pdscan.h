@@ -330,6 +330,99 @@ int pdssm_soft_select(const pdssm_dims* dims, const void* u, const void* W_sel, 
  *   M [H,K,N,N] fp32 (in); dict_idx [H,K,N] int32 (out). */
 int pdssm_dict_hardmax(int32_t H, int32_t K, int32_t N, const float* M, int32_t* dict_idx, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the state-space recurrence of
+ * the calls above with the transition a_t I in place of P D and an outer
+ * product as the drive, the layer that hybrids mix with PD-SSM layers.  Per
+ * sequence b and value head h (its query / key head is h / (H / Hk)):
+ *   S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T       S [dk, dv], S_{-1} = h0
+ *   o_t = scale * S_t^T q_t                          h_L = the last S
+ *
+ * Conventions of the linattn calls where they differ from those above:
+ *   - q, k, v, o, log_decay and their gradients are pdssm_views: a device
+ *     pointer and element strides of the batch, head and step axes; the last
+ *     axis is contiguous.  [B,H,L,d], [B,L,H,d] and slices of a wider row all
+ *     pass as they are.  The pointer and every stride are multiples of 16
+ *     bytes (log_decay: 4); strides are >= 0, and an input's may be 0
+ *     (broadcast).  The stride of an axis of one element is not looked at.
+ *   - q, k, v, o and their gradients have one type, in_dtype.  log_decay, the
+ *     states and their gradients are fp32, states contiguous [B,H,dk,dv].
+ *   - log_decay <= 0, finite or minus infinity (the state starts anew: its
+ *     exponential is zero).  Not checked on the device.
+ *   - q, k, v, g_o and the states are finite (as everywhere in this library:
+ *     not checked).  A token that is not finite can spoil every output of
+ *     its chunk of 64 tokens, and of the rest of its sequence.
+ *   - packed = 1: one step axis of L rows holds B sequences end to end;
+ *     sequence b has the rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (device,
+ *     int32 [B+1], not decreasing, within [0, L]; lengths of 0 pass h0 on).
+ *     Rows outside every sequence are neither read nor written.  Offsets out
+ *     of [0, L] or out of order are cut to it: nothing outside the tensors is
+ *     touched, the results of the sequences concerned are unspecified.
+ *   - Outputs must not overlap inputs, one another or themselves.
+ *   - Results are the same from run to run, bit for bit.
+ *   - The workspace header's error word stays zero: no call here waits for
+ *     another workgroup.
+ *   - Shape limits (else PDSSM_EUNSUPPORTED): dk and dv multiples of 8, at
+ *     most 256.
+ * Precision: products of bf16 inputs are exact and summed in fp32; decay
+ * sums, states and weights are fp32 or better, and enter matrix products as
+ * two bf16 pieces or more (relative error 2^-16 of a term in o, none to speak
+ * of in states and gradients).  fp32 inputs use fp32 products. */
+typedef struct {
+  int32_t B;               /* sequences */
+  int32_t H, Hk;           /* value heads; query / key heads (Hk divides H) */
+  int32_t L;               /* steps per sequence; packed: rows of the step axis */
+  int32_t dk, dv;
+  int32_t in_dtype;        /* pdssm_dtype of q, k, v, o and their gradients */
+  int32_t packed;          /* 1: cu_seqlens holds the sequences' bounds */
+  int32_t decay_per_head;  /* 0: log_decay [B,H,L]; 1: [H], contiguous, one constant a head */
+  float scale;
+} pdssm_linattn_dims;
+
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_h, stride_t;   /* elements */
+} pdssm_view;
+
+/* Bytes of workspace pdssm_linattn_fwd / pdssm_linattn_bwd need.  With few
+ * sequences and heads a long step axis is cut into segments that run side by
+ * side, and their states live there. */
+int pdssm_linattn_workspace_bytes(const pdssm_linattn_dims* dims, size_t* bytes);
+int pdssm_linattn_bwd_workspace_bytes(const pdssm_linattn_dims* dims, size_t* bytes);
+
+/* Prompts.
+ *   q, k [B,Hk,L,dk]; v, o [B,H,L,dv]; log_decay [B,H,L] or [H] (views)
+ *   cu_seqlens: packed = 1 only (NULL otherwise); h0 [B,H,dk,dv] or NULL (zero)
+ *   h_L [B,H,dk,dv] (out, required) */
+int pdssm_linattn_fwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const pdssm_view* k,
+                      const pdssm_view* v, const pdssm_view* log_decay, const int32_t* cu_seqlens,
+                      const float* h0, const pdssm_view* o, float* h_L, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Gradient of a scalar loss, given g_o [B,H,L,dv] and g_hL [B,H,dk,dv] (NULL:
+ * zero).  Nothing of the forward pass is kept: the states are formed again.
+ *   g_q, g_k [B,Hk,L,dk] (summed over the value heads that share them),
+ *   g_v [B,H,L,dv], g_log_decay [B,H,L] or [H] (summed over b and t)
+ *   (out, required); g_h0 [B,H,dk,dv] (out, optional) */
+int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const pdssm_view* k,
+                      const pdssm_view* v, const pdssm_view* log_decay, const int32_t* cu_seqlens,
+                      const float* h0, const pdssm_view* g_o, const float* g_hL,
+                      const pdssm_view* g_q, const pdssm_view* g_k, const pdssm_view* g_v,
+                      const pdssm_view* g_log_decay, float* g_h0, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* One token of every row, on a pool of states that is updated in place.
+ *   dims: L = 1, packed = 0, B rows.  q, k [B,Hk,dk]; v, o [B,H,dv];
+ *   log_decay [B,H] or [H] (views; the step stride is not looked at)
+ *   state [n_slots,H,dk,dv] fp32 (in and out)
+ *   state_idx [B] int32 on the device: row b's slot; NULL: slot b (B <= n_slots)
+ * A negative slot marks an empty row: its o is zero and no state is touched.
+ * A slot >= n_slots, or one that an earlier row of the call has, gives NaN in
+ * that row's o and touches no state. */
+int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, const pdssm_view* k,
+                       const pdssm_view* v, const pdssm_view* log_decay, const int32_t* state_idx,
+                       int32_t n_slots, float* state, const pdssm_view* o, void* stream);
+
 /* Static text for a status code. */
 const char* pdssm_status_str(int status);
 

@@ -14,6 +14,8 @@ Entry points (same names as the C ABI):
 * ``pdssm_fwd(u, W_sel, dict_idx, W_d, b_d, Bu, C, h0=None, chunk=...,
               want_k=False, want_D=False)``
     -> dict(y, h_L[, k_star][, D])
+* ``pdssm_linattn_fwd``, ``pdssm_linattn_bwd``, ``pdssm_linattn_step``:
+  linear attention with a decay for each head (see ``_linattn.py``)
 
 Shapes: u [B,H,L,d] (per head) or [B,L,d] (shared by all heads, detected by
 its rank); W_sel [H,K,d]; W_d [H,N,d]; b_d [H,N]; dict_idx [H,K,N] int32;
@@ -517,3 +519,16 @@ def workspace_error_flag(workspace):
 
 
 __all__ += ["pdssm_workspace_status", "workspace_error_flag", "pdssm_fwd_noalloc"]
+
+
+from ._linattn import (  # noqa: E402,F401
+    linattn_bwd_workspace_bytes,
+    linattn_dims,
+    linattn_workspace_bytes,
+    pdssm_linattn_bwd,
+    pdssm_linattn_fwd,
+    pdssm_linattn_step,
+)
+
+__all__ += ["linattn_dims", "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "pdssm_linattn_fwd",
+            "pdssm_linattn_bwd", "pdssm_linattn_step"]

@@ -21,6 +21,16 @@ class PdssmDims(ctypes.Structure):
                 ("B", "H", "L", "N", "K", "d_in", "u_shared", "in_dtype")]
 
 
+class PdssmLinattnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "H", "Hk", "L", "dk", "dv", "in_dtype", "packed", "decay_per_head")] + [("scale", ctypes.c_float)]
+
+
+class PdssmView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64)]
+
+
 class PdssmError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -39,6 +49,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     dp = ctypes.POINTER(PdssmDims)
+    ldp, wp = ctypes.POINTER(PdssmLinattnDims), ctypes.POINTER(PdssmView)
     sig = {
         "pdssm_select": [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         "pdssm_scan_workspace_bytes": [dp, i32, ctypes.POINTER(sz)],
@@ -56,6 +67,11 @@ def _load():
         "pdssm_scan_states": [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "pdssm_scan_bwd_workspace_bytes": [dp, i32, ctypes.POINTER(sz)],
         "pdssm_scan_bwd": [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "pdssm_linattn_workspace_bytes": [ldp, ctypes.POINTER(sz)],
+        "pdssm_linattn_bwd_workspace_bytes": [ldp, ctypes.POINTER(sz)],
+        "pdssm_linattn_fwd": [ldp, wp, wp, wp, wp, vp, vp, wp, vp, vp, sz, vp],
+        "pdssm_linattn_bwd": [ldp, wp, wp, wp, wp, vp, vp, wp, vp, wp, wp, wp, wp, vp, vp, sz, vp],
+        "pdssm_linattn_step": [ldp, wp, wp, wp, wp, vp, i32, vp, wp, vp],
         "pdssm_status_str": [ctypes.c_int],
         "pdssm_last_error": [],
         "pdssm_abi_version": [],

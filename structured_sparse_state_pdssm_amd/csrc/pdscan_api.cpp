@@ -12,6 +12,7 @@
 
 #include "pdscan.h"
 #include "pdscan_bwd_plan.h"
+#include "pdscan_error.h"
 #include "pdscan_plan.h"
 #include "pdscan_gemm_sel_plan.h"
 #include "pdscan_sens_plan.h"
@@ -46,6 +47,21 @@ int fail(int code, const char* fmt, ...) {
   va_end(ap);
   return code;
 }
+
+}  // namespace
+
+namespace pdscan {
+int set_error(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return code;
+}
+void clear_error() { g_err[0] = 0; }
+}  // namespace pdscan
+
+namespace {
 
 struct Range {
   const char* name;

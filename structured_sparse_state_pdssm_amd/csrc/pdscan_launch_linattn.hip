@@ -1,0 +1,351 @@
+// Launchers of the linear-attention passes, and their small kernels: the
+// segment table of packed sequences, the carry between segments, the
+// log-decay gradient, the sum over heads that share a query or key head, and
+// the single-token step.
+#include <cfloat>
+
+#include "pdscan_linattn.h"
+#include "pdscan_linattn_launch.h"
+
+namespace pdscan {
+
+// Segments of packed sequences, in order: {sequence, first row, rows,
+// first | last << 1}, then the first segment of every sequence.  Every
+// sequence has at least one segment (an empty one passes its state through);
+// entries behind the last hold -1 rows.
+__global__ __launch_bounds__(256) void pdssm_linattn_table_kernel(const int32_t* cu, int32_t* table,
+                                                                  int32_t* starts, int B, int L, int seg, int segs) {
+  __shared__ int wsum[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  for (int b0 = 0; b0 < B; b0 += 256) {
+    const int b = b0 + tid;
+    int t0 = 0, len = 0, n = 0;
+    if (b < B) {
+      t0 = cu[b];
+      int t1 = cu[b + 1];
+      t0 = t0 < 0 ? 0 : t0 > L ? L : t0;
+      t1 = t1 < t0 ? t0 : t1 > L ? L : t1;
+      len = t1 - t0;
+      n = len <= seg ? 1 : (len - 1) / seg + 1;
+    }
+    int x = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(x, d, 64);
+      if (lane >= d) x += up;
+    }
+    if (lane == 63) wsum[wave] = x;
+    __syncthreads();
+    int before = base;
+    for (int w = 0; w < wave; ++w) before += wsum[w];
+    const int total = wsum[0] + wsum[1] + wsum[2] + wsum[3];
+    const int at = before + x - n;
+    if (b < B) {
+      starts[b] = at < segs ? at : segs;
+      for (int i = 0; i < n; ++i) {
+        // offsets that overlap could ask for more segments than their rows hold: those behind the bound are dropped
+        if (at + i >= segs) break;
+        int4 e;
+        e.x = b;
+        e.y = t0 + i * seg;
+        e.z = len - i * seg < seg ? len - i * seg : seg;
+        e.w = (i == 0 ? 1 : 0) | (i == n - 1 ? 2 : 0);
+        *(int4*)(table + 4 * (long long)(at + i)) = e;
+      }
+    }
+    base += total;
+    __syncthreads();
+  }
+  if (tid == 0) starts[B] = base < segs ? base : segs;
+  for (int i = base + tid; i < segs; i += 256) *(int4*)(table + 4 * (long long)i) = make_int4(0, 0, -1, 0);
+}
+
+// Entering states of all segments of a sequence and head from the segments'
+// contributions, in place, four state elements a thread.
+__global__ __launch_bounds__(256) void pdssm_linattn_carry_kernel(LaCarryArgs a) {
+  const LaCarry& c = a.c[blockIdx.z];
+  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const long long e = ((long long)blockIdx.y * 256 + threadIdx.x) * 4;
+  if (e >= a.state) return;
+  const int s0 = a.starts ? a.starts[b] : b * a.nseg;
+  const int s1 = a.starts ? a.starts[b + 1] : s0 + a.nseg;
+  const int n = s1 - s0 - 1;
+  float4 S = make_float4(0, 0, 0, 0);
+  if (c.user) S = *(const float4*)(c.user + ((long long)b * a.H + h) * a.state + e);
+  constexpr int U = 8;
+  for (int i0 = 0; i0 < n; i0 += U) {
+    float4 v[U];
+    float d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u < n ? i0 + u : n - 1;
+      const long long at = (long long)(c.rev ? s1 - 2 - i : s0 + 1 + i) * a.H + h;
+      v[u] = *(const float4*)(c.seg + at * a.state + e);
+      d[u] = c.decay[at];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= n) break;
+      const long long at = (long long)(c.rev ? s1 - 2 - (i0 + u) : s0 + 1 + i0 + u) * a.H + h;
+      S.x = d[u] * S.x + v[u].x;
+      S.y = d[u] * S.y + v[u].y;
+      S.z = d[u] * S.z + v[u].z;
+      S.w = d[u] * S.w + v[u].w;
+      *(float4*)(c.seg + at * a.state + e) = S;
+    }
+  }
+}
+
+__device__ __forceinline__ double block_sum(double x, double* red, int tid) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m, 64);
+  __syncthreads();
+  if ((tid & 63) == 0) red[tid >> 6] = x;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// d loss / d log a_t of one segment and head.  Pairs (key at or before t-1,
+// query at or behind t) meet at t, so with r_i = q_i . dq_i (every key before
+// query i) and c_j = k_j . dk_j (every query behind key j)
+//   g_t = sum_{i >= t} r_i - sum_{j >= t} c_j + <S_end, dS_end>
+// over the rest of the segment: pairs inside it cancel but for those that
+// meet at t, and the last term holds those that meet behind its end.  The
+// sums run in 64 bits over one segment only.
+__global__ __launch_bounds__(256) void pdssm_linattn_decay_kernel(const LaDecayArgs a) {
+  __shared__ double red[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int sid = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
+  LaSeg s;
+  const bool live = la_segment(a.c, sid, s);
+  double total = 0.0;
+  if (live) {
+    double x = 0.0;
+    if (!s.last) {
+      const float4* A = (const float4*)(a.sS + ((long long)(sid + 1) * a.c.H + h) * a.c.state);
+      const float4* R = (const float4*)(a.sR + ((long long)sid * a.c.H + h) * a.c.state);
+      for (int e = tid; e < a.c.state / 4; e += 256) {
+        const float4 p = A[e], q = R[e];
+        x += (double)((p.x * q.x + p.y * q.y) + (p.z * q.z + p.w * q.w));
+      }
+      x = block_sum(x, red, tid);
+    } else if (a.xd) {
+      for (int w = 0; w < a.xd_slabs; ++w) x += a.xd[((long long)w * a.c.segs + sid) * a.c.H + h];
+    }
+    double carry = x;
+    for (int t1 = s.len; t1 > 0; t1 -= 256) {
+      const int t = t1 - 1 - tid;
+      double d = 0.0;
+      if (t >= 0) {
+        const long long at = (long long)h * a.c.rows + s.row0 + t;
+        const long long slab = (long long)a.c.H * a.c.rows;
+        for (int w = 0; w < a.r_slabs; ++w) d += (double)a.r[w * slab + at];
+        for (int w = 0; w < a.k_slabs; ++w) d -= (double)a.k[w * slab + at];
+      }
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {
+        const double up = __shfl_up(d, m, 64);
+        if (lane >= m) d += up;
+      }
+      __syncthreads();
+      if (lane == 63) red[wave] = d;
+      __syncthreads();
+      double before = carry;
+      for (int w = 0; w < wave; ++w) before += red[w];
+      carry += (red[0] + red[1]) + (red[2] + red[3]);
+      if (t >= 0) {
+        const double g = before + d;
+        if (a.per_head)
+          total += g;
+        else
+          ((float*)a.out.p)[(int64_t)s.vb * a.out.sb + (int64_t)h * a.out.sh + (int64_t)(s.t0 + t) * a.out.st] =
+              (float)g;
+      }
+    }
+  }
+  if (a.per_head) {
+    total = block_sum(total, red, tid);
+    if (tid == 0) a.part[(long long)sid * a.c.H + h] = total;
+  }
+}
+
+__global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int segs) {
+  __shared__ double red[4];
+  const int h = blockIdx.x;
+  double x = 0.0;
+  for (int s = threadIdx.x; s < segs; s += 256) x += part[(long long)s * H + h];
+  x = block_sum(x, red, threadIdx.x);
+  if (threadIdx.x == 0) out[h] = (float)x;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void pdssm_linattn_fold_kernel(const LaFoldArgs a) {
+  const int Hk = a.H / a.ratio, c4 = a.d / 4;
+  long long r0 = 0, r1 = a.rows;
+  if (a.cu) {   // rows outside the sequences stay as they are
+    r0 = a.cu[0];
+    r1 = a.cu[a.B];
+    r0 = r0 < 0 ? 0 : r0 > a.rows ? a.rows : r0;
+    r1 = r1 < r0 ? r0 : r1 > a.rows ? a.rows : r1;
+  }
+  const long long n = (r1 - r0) * Hk * c4;
+  for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < n; q += (long long)gridDim.x * 256) {
+    const int c = (int)(q % c4) * 4;
+    const int hk = (int)(q / c4 % Hk);
+    const long long row = r0 + q / c4 / Hk;
+    const float* p = a.part + (row * a.H + (long long)hk * a.ratio) * a.d + c;
+    float v[4] = {0, 0, 0, 0};
+    for (int r = 0; r < a.ratio; ++r) {
+      const float4 w = *(const float4*)(p + (long long)r * a.d);
+      v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+    }
+    const int64_t b = a.cu ? 0 : row / a.L, t = a.cu ? row : row % a.L;
+    T::store4((typename T::store*)a.out.p + b * a.out.sb + hk * a.out.sh + t * a.out.st + c, v);
+  }
+}
+
+// One token: S = a S + k v^T in place, o = s S^T q.  One workgroup owns `cols`
+// value columns of one row and head; a thread owns four columns of every
+// nr-th state row.  The state is read and written once, which is all the time.
+template <typename T>
+__global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArgs a) {
+  __shared__ float qs[kLaMaxD], ks[kLaMaxD];
+  __shared__ __align__(16) float red[256 * 4];
+  __shared__ int dup;
+  const int tid = threadIdx.x;
+  const int tiles = (a.dv + a.cols - 1) / a.cols;
+  unsigned id = blockIdx.x;
+  const int tile = id % tiles;
+  id /= tiles;
+  const int h = id % a.H, b = id / a.H;
+  const int c0 = tile * a.cols;
+  const int cols = a.dv - c0 < a.cols ? a.dv - c0 : a.cols;
+  using E = typename T::store;
+  const int slot = a.idx ? a.idx[b] : b;
+  E* op = (E*)a.o.p + (int64_t)b * a.o.sb + (int64_t)h * a.o.sh + c0;
+  if (slot < 0 || slot >= a.slots) {
+    // an empty row gives zeros; a slot past the pool gives NaN
+    const float f = slot < 0 ? 0.0f : __builtin_nanf("");
+    const float v[4] = {f, f, f, f};
+    for (int c = tid * 4; c < cols; c += 1024) T::store4(op + c, v);
+    return;
+  }
+  if (tid == 0) dup = 0;
+  const E* qp = (const E*)a.q.p + (int64_t)b * a.q.sb + (int64_t)(h / a.qd) * a.q.sh;
+  const E* kp = (const E*)a.k.p + (int64_t)b * a.k.sb + (int64_t)(h / a.qd) * a.k.sh;
+  for (int c = tid * 4; c < a.dk; c += 1024) {
+    T::load4(qp + c, qs + c);
+    T::load4(kp + c, ks + c);
+  }
+  __syncthreads();
+  if (a.idx) {
+    // a slot named twice: the first row has it
+    int found = 0;
+    for (int r = tid; r < b; r += 256) found |= a.idx[r] == slot;
+    if (found) dup = 1;
+    __syncthreads();
+    if (dup) {
+      const float f = __builtin_nanf("");
+      const float v[4] = {f, f, f, f};
+      for (int c = tid * 4; c < cols; c += 1024) T::store4(op + c, v);
+      return;
+    }
+  }
+  const int W = cols / 4, nr = 256 / W;
+  const int rg = tid / W, c = tid % W * 4;
+  const float decay = expf(((const float*)a.g.p)[(int64_t)b * a.g.sb + (int64_t)h * a.g.sh]);
+  float o[4] = {0, 0, 0, 0};
+  if (rg < nr) {
+    float v[4];
+    T::load4((const E*)a.v.p + (int64_t)b * a.v.sb + (int64_t)h * a.v.sh + c0 + c, v);
+    float* st = a.state + ((int64_t)slot * a.H + h) * a.dk * a.dv + c0 + c;
+#pragma unroll 8
+    for (int r = rg; r < a.dk; r += nr) {
+      float4 x = *(float4*)(st + (int64_t)r * a.dv);
+      const float kk = ks[r], qq = qs[r];
+      x.x = decay * x.x + kk * v[0];
+      x.y = decay * x.y + kk * v[1];
+      x.z = decay * x.z + kk * v[2];
+      x.w = decay * x.w + kk * v[3];
+      *(float4*)(st + (int64_t)r * a.dv) = x;
+      o[0] += qq * x.x; o[1] += qq * x.y; o[2] += qq * x.z; o[3] += qq * x.w;
+    }
+    *(float4*)(red + 4 * tid) = make_float4(o[0], o[1], o[2], o[3]);
+  }
+  __syncthreads();
+  if (tid < W) {
+    float x[4] = {0, 0, 0, 0};
+    for (int g = 0; g < nr; ++g) {
+      const float4 p = *(const float4*)(red + 4 * (g * W + tid));
+      x[0] += p.x; x[1] += p.y; x[2] += p.z; x[3] += p.w;
+    }
+    for (int e = 0; e < 4; ++e) x[e] *= a.scale;
+    T::store4(op + c, x);
+  }
+}
+
+hipError_t launch_linattn_step(const LaStepArgs& a, hipStream_t st) {
+  const int tiles = (a.dv + a.cols - 1) / a.cols;
+  const long long grid = (long long)a.B * a.H * tiles;
+  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  if (a.bf16)
+    hipLaunchKernelGGL(pdssm_linattn_step_kernel<LaBf16>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(pdssm_linattn_step_kernel<LaF32>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_linattn_table(const int32_t* cu, int32_t* table, int32_t* starts, int B, int L, int seg, int segs,
+                                hipStream_t st) {
+  hipLaunchKernelGGL(pdssm_linattn_table_kernel, dim3(1), dim3(256), 0, st, cu, table, starts, B, L, seg, segs);
+  return hipGetLastError();
+}
+
+hipError_t launch_linattn_carry(const LaCarryArgs& a, int passes, hipStream_t st) {
+  const long long grid = (long long)a.B * a.H;
+  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(pdssm_linattn_carry_kernel, dim3((unsigned)grid, (unsigned)((a.state / 4 + 255) / 256), passes),
+                     dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_linattn_decay(const LaDecayArgs& a, hipStream_t st) {
+  const long long grid = (long long)a.c.segs * a.c.H;
+  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(pdssm_linattn_decay_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
+  if (a.per_head)
+    hipLaunchKernelGGL(pdssm_linattn_decay_sum_kernel, dim3((unsigned)a.c.H), dim3(256), 0, st, a.part,
+                       (float*)a.out.p, a.c.H, a.c.segs);
+  return hipGetLastError();
+}
+
+hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
+  const long long n = a.rows * (a.H / a.ratio) * (a.d / 4);
+  long long grid = (n + 255) / 256;
+  if (grid > 8192) grid = 8192;
+  if (grid < 1) grid = 1;
+  if (a.bf16)
+    hipLaunchKernelGGL(pdssm_linattn_fold_kernel<LaBf16>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(pdssm_linattn_fold_kernel<LaF32>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+// The product kernels, by type, x-row width and waves; pieces: 2 or 3 (bf16).
+hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pieces, hipStream_t st) {
+  const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DV);
+  const long long grid = (long long)a.segs * a.H * a.slabs * a.njobs;
+  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  if (bf16)
+    return dk == 32    ? la_bf16_32(a, nw, pieces, (unsigned)grid, st)
+           : dk == 64  ? la_bf16_64(a, nw, pieces, (unsigned)grid, st)
+           : dk == 128 ? la_bf16_128(a, nw, pieces, (unsigned)grid, st)
+                       : la_bf16_256(a, nw, pieces, (unsigned)grid, st);
+  return dk == 32    ? la_f32_32(a, nw, pieces, (unsigned)grid, st)
+         : dk == 64  ? la_f32_64(a, nw, pieces, (unsigned)grid, st)
+         : dk == 128 ? la_f32_128(a, nw, pieces, (unsigned)grid, st)
+                     : la_f32_256(a, nw, pieces, (unsigned)grid, st);
+}
+
+}  // namespace pdscan

@@ -1,0 +1,8 @@
+// Linear-attention products, bf16 inputs, x rows of up to 128 elements.
+#include "pdscan_linattn_inst.h"
+
+namespace pdscan {
+hipError_t la_bf16_128(const LaArgs& a, int nw, int pieces, unsigned grid, hipStream_t st) {
+  return la_launch<LaBf16, 128>(a, nw, pieces, grid, st);
+}
+}  // namespace pdscan

@@ -1,0 +1,8 @@
+// Linear-attention products, fp32 inputs, x rows of up to 64 elements.
+#include "pdscan_linattn_inst.h"
+
+namespace pdscan {
+hipError_t la_f32_64(const LaArgs& a, int nw, int pieces, unsigned grid, hipStream_t st) {
+  return la_launch<LaF32, 64>(a, nw, pieces, grid, st);
+}
+}  // namespace pdscan
