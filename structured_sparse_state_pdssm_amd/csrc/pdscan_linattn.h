@@ -211,48 +211,87 @@ __device__ __forceinline__ const typename T::store* la_ptr(const LaView& v, int 
   return (const typename T::store*)v.p + (int64_t)b * v.sb + (int64_t)h * v.sh + (int64_t)t * v.st;
 }
 
-// C rows of D elements (zeros behind row n and column D) into LDS rows of W elements.
+// A tile of C rows and W elements on its way from memory to LDS: thread
+// `tid` owns 16 bytes of every RP-th row.  fetch() only issues the loads (the
+// next chunk's while this one is worked on); rows behind n and columns behind
+// D are loaded from a place that exists and become zero in commit().
 template <typename T, int C, int W, int NT>
-__device__ __forceinline__ void la_stage(typename T::store* lds, const typename T::store* g, int64_t st, int n,
-                                         int D, int tid) {
-  constexpr int kCols = W / T::kVec;
-#pragma unroll 4
-  for (int q = tid; q < C * kCols; q += NT) {
-    const int r = q / kCols, c = (q % kCols) * T::kVec;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (r < n && c < D) w = *(const uint4*)(g + (int64_t)r * st + c);
-    *(uint4*)(lds + r * (W + T::kPad) + c) = w;
+struct LaTileIO {
+  using E = typename T::store;
+  static constexpr int kCols = W / T::kVec, RP = NT / kCols, N = C / RP, kStride = W + T::kPad;
+  uint4 r[N];
+  int row0, col;
+  bool ok;
+  __device__ __forceinline__ void init(int tid, int D) {
+    row0 = tid / kCols;
+    col = tid % kCols * T::kVec;
+    ok = col < D;
+    if (!ok) col = 0;
   }
+  __device__ __forceinline__ void fetch(const E* chunk, int64_t st, int n) {
+    if (n >= C) {
+      const E* p = chunk + (int64_t)row0 * st + col;
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = *(const uint4*)(p + (int64_t)(i * RP) * st);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int row = row0 + i * RP;
+        r[i] = *(const uint4*)(chunk + (int64_t)(row < n ? row : n - 1) * st + col);
+      }
+    }
+  }
+  __device__ __forceinline__ void commit(E* lds, int tid, int n) const {
+    E* q = lds + row0 * kStride + tid % kCols * T::kVec;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint4 w = r[i];
+      if (!ok || row0 + i * RP >= n) w = make_uint4(0, 0, 0, 0);
+      *(uint4*)(q + i * RP * kStride) = w;
+    }
+  }
+};
+
+__device__ __forceinline__ double la_dpp_add(double x, uint64_t up) { return x + __longlong_as_double((long long)up); }
+
+// x plus the value of the lane that DPP control CTRL names (zero where there
+// is none or the row is masked)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double la_scan_step(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+  return la_dpp_add(x, ((uint64_t)hi << 32) | lo);
 }
 
-// Exponents of one chunk, by one wave (lane = token): G as two floats in units
-// of log 2, the output scale and the update weight of every token, and the
-// chunk's whole decay.  A log decay under -1e4 (minus infinity: the state
-// starts anew) counts as -1e4, whose exponential is zero all the same.
+// Exponents of one chunk, by one wave (lane = token, g = its log decay, 0
+// behind the last): G as two floats in units of log 2, the output scale and
+// the update weight of every token, and the chunk's whole decay behind them.
+// A log decay under -1e4 (minus infinity: the state starts anew) counts as
+// -1e4, whose exponential is zero all the same.  Returns the sum of log2.
 template <int C>
-__device__ __forceinline__ double la_exponents(const LaArgs& a, const LaSeg& s, int h, int t, int n, int rev,
-                                               float s_inter, float s_upd, float* ghi, float* glo, float* ea,
-                                               float* ew, int lane) {
-  double G = 0.0;
-  if (lane < n) {
-    float g = ((const float*)a.g.p)[(int64_t)s.vb * a.g.sb + (int64_t)h * a.g.sh + (int64_t)(t + lane) * a.g.st];
-    if (g < -1e4f) g = -1e4f;
-    G = (double)g * 1.4426950408889634074;
-  }
-#pragma unroll
-  for (int d = 1; d < C; d <<= 1) {
-    const double up = __shfl_up(G, d, 64);
-    if (lane >= d) G += up;
-  }
-  const double tot = __shfl(G, C - 1, 64);
+__device__ __forceinline__ double la_exponents(float g, int rev, float s_inter, float s_upd, float* e, int lane) {
+  if (g < -1e4f) g = -1e4f;
+  double G = (double)g * 1.4426950408889634074;
+  G = la_scan_step<0x111, 0xf>(G);   // row_shr:1
+  G = la_scan_step<0x112, 0xf>(G);   // row_shr:2
+  G = la_scan_step<0x114, 0xf>(G);   // row_shr:4
+  G = la_scan_step<0x118, 0xf>(G);   // row_shr:8
+  G = la_scan_step<0x142, 0xa>(G);   // row_bcast:15 into rows 1 and 3
+  G = la_scan_step<0x143, 0xc>(G);   // row_bcast:31 into rows 2 and 3
+  const uint64_t b = (uint64_t)__double_as_longlong(G);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  const double tot = __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
   if (lane < C) {
-    const float hi = (float)G;
-    ghi[lane] = hi;
-    glo[lane] = (float)(G - (double)hi);
+    const float gh = (float)G;
+    e[lane] = gh;
+    e[C + lane] = (float)(G - (double)gh);
     const float from = __builtin_amdgcn_exp2f((float)G), to = __builtin_amdgcn_exp2f((float)(tot - G));
-    ea[lane] = (rev ? to : from) * s_inter;
-    ew[lane] = (rev ? from : to) * s_upd;
+    e[2 * C + lane] = (rev ? to : from) * s_inter;
+    e[3 * C + lane] = (rev ? from : to) * s_upd;
   }
+  if (lane == 0) e[4 * C] = __builtin_amdgcn_exp2f((float)tot);
   return tot;
 }
 
@@ -264,13 +303,23 @@ struct LaTile {
   static constexpr int IT = C / 32;              // 32-token tiles of a chunk
   static constexpr int KT = DKP / 32;            // 32-row tiles of the state
   static constexpr int NPS = kF32 ? 1 : 3;       // pieces of the state's update
-  static constexpr int XS = DKP + T::kPad, ZS = NW * 32 + T::kPad, PS = C + T::kPad;
+  // One or two waves form all scores of the chunk each, in registers; four
+  // share them through LDS (each wave forms one tile of 32 x 32).
+  static constexpr bool kShareP = NW == 4;
+  static constexpr int XS = DKP + T::kPad, ZS = NW * 32 + T::kPad, PS = C + 4;
+  static constexpr int kExp = 4 * C + 4;         // floats of one chunk's exponents
   static constexpr size_t kX = (size_t)C * XS * sizeof(typename T::store);
   static constexpr size_t kZ = (size_t)C * ZS * sizeof(typename T::store);
-  static constexpr size_t kP = (size_t)C * PS * sizeof(typename T::store);
-  static constexpr size_t kSmall = (size_t)(4 + NW) * C * 4 + 64;
+  static constexpr size_t kP = kShareP ? (size_t)C * PS * sizeof(typename T::store) : 0;
+  static constexpr size_t kSmall = (size_t)(2 * kExp + NW * C) * 4;
   static constexpr size_t main_bytes(int np) { return 2 * kX + kZ + np * kP + kSmall; }
-  static constexpr size_t state_bytes() { return kX + kZ + kSmall; }
+  static constexpr size_t state_bytes() { return kX + kZ + (size_t)2 * kExp * 4; }
+  using X = LaTileIO<T, C, DKP, NT>;
+  using Z = LaTileIO<T, C, NW * 32, NT>;
+  // registers: state, outputs and the tiles under way; under about 200 of
+  // them two waves share a SIMD
+  static constexpr int kRegs = 16 * (KT + IT) + 4 * (2 * X::N + Z::N);
+  static constexpr int kWaves = kRegs <= 180 ? 2 : 1;
 };
 
 // acc (C layout of a 32 x 32 product: column lane % 32, rows 8 (r / 4) + 4 h +
@@ -303,33 +352,89 @@ __device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const typename 
   }
 }
 
+// A state's rows m and column `col` of this lane, zero where p is NULL or the
+// state ends.  sm = 1: the rows lie side by side (the state is stored
+// transposed) and four come in one load.
 template <int KT>
 __device__ __forceinline__ void la_load_state(la_f16 (&S)[KT], const float* p, int sm, int sn, int DK, int DV,
                                               int col, int h) {
 #pragma unroll
+  for (int t = 0; t < KT; ++t) S[t] = la_f16{};
+  if (!p) return;
+  const float* q = p + (long long)(col < DV ? col : 0) * sn;
+#pragma unroll
   for (int t = 0; t < KT; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int m = 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
-      S[t][r] = (p && m < DK && col < DV) ? p[(long long)m * sm + (long long)col * sn] : 0.0f;
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const int m = 32 * t + 8 * r4 + 4 * h;
+      const bool in = m < DK && col < DV;
+      const int mm = m < DK ? m : 0;
+      float v[4];
+      if (sm == 1) {
+        const float4 w = *(const float4*)(q + mm);
+        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = q[(long long)(mm + e) * sm];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][4 * r4 + e] = in ? v[e] : 0.0f;
     }
 }
 
 template <int KT>
 __device__ __forceinline__ void la_store_state(const la_f16 (&S)[KT], float* p, int sm, int sn, int DK, int DV,
                                                int col, int h) {
+  if (col >= DV) return;
+  float* q = p + (long long)col * sn;
 #pragma unroll
   for (int t = 0; t < KT; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int m = 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
-      if (m < DK && col < DV) p[(long long)m * sm + (long long)col * sn] = S[t][r];
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const int m = 32 * t + 8 * r4 + 4 * h;
+      if (m >= DK) continue;
+      if (sm == 1)
+        *(float4*)(q + m) = make_float4(S[t][4 * r4], S[t][4 * r4 + 1], S[t][4 * r4 + 2], S[t][4 * r4 + 3]);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[(long long)(m + e) * sm] = S[t][4 * r4 + e];
     }
+}
+
+// Scores of one 32 x 32 tile (rows j of y, columns i of x), weighted by the
+// decay between the two tokens and zero on the wrong side of the diagonal.
+template <typename T, int DKP, int NW>
+__device__ __forceinline__ la_f16 la_scores(const typename T::store* X, const typename T::store* Y, const float* e,
+                                            int jt, int it, int rev, float s_intra, int lane) {
+  using K = LaTile<T, DKP, NW>;
+  const int h = lane >> 5, n32 = lane & 31;
+  la_f16 c = {};
+#pragma unroll
+  for (int ks = 0; ks < DKP / 16; ++ks)
+    T::mma(c, T::row(Y + (32 * jt + n32) * K::XS + 16 * ks, h), T::row(X + (32 * it + n32) * K::XS + 16 * ks, h));
+  const int i = 32 * it + n32;
+  const float gi = e[i], gl = e[K::C + i];
+  const float sign = rev ? -1.0f : 1.0f;
+#pragma unroll
+  for (int r4 = 0; r4 < 4; ++r4) {
+    const int j0 = 32 * jt + 8 * r4 + 4 * h;
+    const float4 jh = *(const float4*)(e + j0), jl = *(const float4*)(e + K::C + j0);
+    const float hh[4] = {jh.x, jh.y, jh.z, jh.w}, ll[4] = {jl.x, jl.y, jl.z, jl.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float d = ((gi - hh[q]) + (gl - ll[q])) * sign;
+      const float w = __builtin_amdgcn_exp2f(d) * s_intra;
+      const float v = c[4 * r4 + q] * w;
+      c[4 * r4 + q] = jt != it || (rev ? j0 + q >= i : j0 + q <= i) ? v : 0.0f;
+    }
+  }
+  return c;
 }
 
 // o = form(x, y, z) over one segment, head and slab of 32 NW columns.
 template <typename T, int DKP, int NW, int NP>
-__global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
+pdssm_linattn_kernel(const LaArgs a) {
   using K = LaTile<T, DKP, NW>;
   using E = typename T::store;
   using F = typename T::frag;
@@ -339,14 +444,11 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) 
   E* Y = (E*)(smem + K::kX);
   E* Z = (E*)(smem + 2 * K::kX);
   E* P = (E*)(smem + 2 * K::kX + K::kZ);
-  float* ghi = (float*)(smem + 2 * K::kX + K::kZ + NP * K::kP);
-  float* glo = ghi + C;
-  float* ea = glo + C;
-  float* ew = ea + C;
-  float* dots = ew + C;            // [NW][C]
-  float* tot = dots + NW * C;
+  float* exps = (float*)(smem + 2 * K::kX + K::kZ + NP * K::kP);   // of this chunk and the next
+  float* dots = exps + 2 * K::kExp;                                // [NW][C]
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, n32 = lane & 31;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
+            n32 = lane & 31;
   unsigned id = blockIdx.x;
   if (id == 0 && tid < 2) a.header[tid] = 0;
   const int jn = id % a.njobs;
@@ -359,58 +461,61 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) 
   LaSeg s;
   if (!la_segment(a, sid, s)) return;
 
-  const int c0 = slab * NW * 32 + wave * 32;      // first column of this wave
+  const int rev = J.rev;
+  const int slab0 = slab * NW * 32;
+  const int c0 = slab0 + wave * 32;      // first column of this wave
   const int col = c0 + n32;
   const long long unit = (long long)s.b * a.H + hd;
-  const bool starts = J.rev ? s.last : s.first, ends = J.rev ? s.first : s.last;
+  const bool starts = rev ? s.last : s.first, ends = rev ? s.first : s.last;
+  const int chunks = (s.len + C - 1) / C;
+  const E* xp = la_ptr<T>(J.x, s.vb, hd / J.xd, s.t0);
+  const E* yp = la_ptr<T>(J.y, s.vb, hd / J.yd, s.t0);
+  const E* zp = la_ptr<T>(J.z, s.vb, hd / J.zd, s.t0) + slab0;
+  const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh + (int64_t)s.t0 * a.g.st;
+  typename K::X tx, ty;
+  typename K::Z tz;
+  tx.init(tid, J.DK);
+  ty.init(tid, J.DK);
+  tz.init(tid, J.DV - slab0);
+  float gv = 0.0f;
+  constexpr int kExpWave = NW - 1;
+
+  auto fetch = [&](int ci) {
+    const int n = s.len - ci * C;
+    tx.fetch(xp + (int64_t)(ci * C) * J.x.st, J.x.st, n);
+    ty.fetch(yp + (int64_t)(ci * C) * J.y.st, J.y.st, n);
+    tz.fetch(zp + (int64_t)(ci * C) * J.z.st, J.z.st, n);
+    if (wave == kExpWave) gv = lane < n && lane < C ? gp[(int64_t)(ci * C + lane) * a.g.st] : 0.0f;
+  };
+  if (chunks) fetch(rev ? chunks - 1 : 0);
+
   const float* init = starts ? (J.s_user ? J.s_user + unit * a.state : nullptr)
                              : J.s_seg + ((long long)sid * a.H + hd) * a.state;
   la_f16 S[K::KT];
   la_load_state<K::KT>(S, init, J.sm, J.sn, J.DK, J.DV, col, h);
-  // the state of a reversed job starts as the gradient itself; s_upd carries the scale
+  if (wave == kExpWave) la_exponents<C>(gv, rev, J.s_inter, J.s_upd, exps, lane);
 
-  const int chunks = (s.len + C - 1) / C;
   for (int q = 0; q < chunks; ++q) {
-    const int ci = J.rev ? chunks - 1 - q : q;
+    const int ci = rev ? chunks - 1 - q : q;
     const int t = s.t0 + ci * C;
     const int n = s.len - ci * C < C ? s.len - ci * C : C;
-    const int slab0 = slab * NW * 32;
-    const int zc = J.DV - slab0 < NW * 32 ? J.DV - slab0 : NW * 32;
-    la_stage<T, C, DKP, K::NT>(X, la_ptr<T>(J.x, s.vb, hd / J.xd, t), J.x.st, n, J.DK, tid);
-    la_stage<T, C, DKP, K::NT>(Y, la_ptr<T>(J.y, s.vb, hd / J.yd, t), J.y.st, n, J.DK, tid);
-    la_stage<T, C, NW * 32, K::NT>(Z, la_ptr<T>(J.z, s.vb, hd / J.zd, t) + slab0, J.z.st, n, zc, tid);
-    if (wave == 0) {
-      const double d = la_exponents<C>(a, s, hd, t, n, J.rev, J.s_inter, J.s_upd, ghi, glo, ea, ew, lane);
-      if (lane == 0) tot[0] = __builtin_amdgcn_exp2f((float)d);
-    }
+    const float* e = exps + (q & 1) * K::kExp;
+    tx.commit(X, tid, n);
+    ty.commit(Y, tid, n);
+    tz.commit(Z, tid, n);
     __syncthreads();
+    if (q + 1 < chunks) fetch(rev ? ci - 1 : ci + 1);
 
-    // weighted scores, transposed: rows j of y, columns i of x; a tile per wave
-    for (int u = wave; u < IT * IT; u += NW) {
-      const int jt = u / IT, it = u % IT;
-      if (J.rev ? jt < it : jt > it) continue;
-      la_f16 c = {};
+    if constexpr (K::kShareP) {
+      static_assert(IT * IT <= NW, "a score tile per wave");
+      const int jt = wave / IT, it = wave % IT;
+      if (wave < IT * IT && (rev ? jt >= it : jt <= it)) {
+        const la_f16 c = la_scores<T, DKP, NW>(X, Y, e, jt, it, rev, J.s_intra, lane);
 #pragma unroll
-      for (int ks = 0; ks < DKP / 16; ++ks) {
-        const F ya = T::row(Y + (32 * jt + n32) * K::XS + 16 * ks, h);
-        const F xb = T::row(X + (32 * it + n32) * K::XS + 16 * ks, h);
-        T::mma(c, ya, xb);
-      }
-      const int i = 32 * it + n32;
-      const float gi = ghi[i], gl = glo[i];
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const int j0 = 32 * jt + 8 * r4 + 4 * h;
-        const float4 jh = *(const float4*)(ghi + j0), jl = *(const float4*)(glo + j0);
-        const float hh[4] = {jh.x, jh.y, jh.z, jh.w}, ll[4] = {jl.x, jl.y, jl.z, jl.w};
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float d = (gi - hh[e]) + (gl - ll[e]);
-          const float w = __builtin_amdgcn_exp2f(J.rev ? -d : d) * J.s_intra;
-          v[e] = (J.rev ? j0 + e >= i : j0 + e <= i) ? c[4 * r4 + e] * w : 0.0f;
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const float v[4] = {c[4 * r4], c[4 * r4 + 1], c[4 * r4 + 2], c[4 * r4 + 3]};
+          T::template put4<NP>(P + (32 * it + n32) * K::PS + 32 * jt + 8 * r4 + 4 * h, C * K::PS, v);
         }
-        T::template put4<NP>(P + i * K::PS + j0, C * K::PS, v);
       }
     }
 
@@ -424,7 +529,7 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) 
       for (int k2 = 0; k2 < 2; ++k2) {
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = S[t4][8 * k2 + e];
+        for (int r = 0; r < 8; ++r) v[r] = S[t4][8 * k2 + r];
         F sp[NP];
         T::template pieces<NP>(v, sp);
 #pragma unroll
@@ -436,27 +541,45 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) 
       }
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      const float w = ea[32 * it + n32];
+      const float w = e[2 * C + 32 * it + n32];
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[it][r] *= w;
     }
-    __syncthreads();
 
     // what the chunk's own tokens give
     F zf[C / 16];
 #pragma unroll
     for (int js = 0; js < C / 16; ++js) zf[js] = T::col(Z, K::ZS, 16 * js, wave * 32, lane);
+    if constexpr (K::kShareP) {
+      __syncthreads();
 #pragma unroll
-    for (int it = 0; it < IT; ++it)
+      for (int it = 0; it < IT; ++it)
 #pragma unroll
-      for (int js = 0; js < C / 16; ++js) {
-        if (J.rev ? js < 2 * it : js >= 2 * it + 2) continue;
+        for (int js = 0; js < C / 16; ++js) {
+          if (rev ? js < 2 * it : js >= 2 * it + 2) continue;
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const F pb = T::row(P + p * C * K::PS + (32 * it + n32) * K::PS + 16 * js, h);
-          T::mma(o[it], zf[js], pb);
+          for (int p = 0; p < NP; ++p)
+            T::mma(o[it], zf[js], T::row(P + p * C * K::PS + (32 * it + n32) * K::PS + 16 * js, h));
         }
-      }
+    } else {
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int jt = 0; jt < IT; ++jt) {
+          if (rev ? jt < it : jt > it) continue;
+          const la_f16 c = la_scores<T, DKP, NW>(X, Y, e, jt, it, rev, J.s_intra, lane);
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            float v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = c[8 * k2 + r];
+            F pp[NP];
+            T::template pieces<NP>(v, pp);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) T::mma(o[it], zf[2 * jt + k2], pp[p]);
+          }
+        }
+    }
 
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
@@ -469,7 +592,7 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) 
         for (int r4 = 0; r4 < 4; ++r4) {
           const int cc = c0 + 8 * r4 + 4 * h;
           if (cc >= J.DV) continue;
-          float v[4] = {o[it][4 * r4], o[it][4 * r4 + 1], o[it][4 * r4 + 2], o[it][4 * r4 + 3]};
+          const float v[4] = {o[it][4 * r4], o[it][4 * r4 + 1], o[it][4 * r4 + 2], o[it][4 * r4 + 3]};
           if (J.o_f32)
             *(float4*)((float*)J.o.p + oo + cc) = make_float4(v[0], v[1], v[2], v[3]);
           else
@@ -487,7 +610,9 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) 
       }
     }
 
-    la_update<T, DKP, NW>(S, Y, zf, ew, tot[0], lane);
+    la_update<T, DKP, NW>(S, Y, zf, e + 3 * C, e[4 * C], lane);
+    if (wave == kExpWave && q + 1 < chunks)
+      la_exponents<C>(gv, rev, J.s_inter, J.s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
     __syncthreads();
     if (J.dot && tid < n) {
       float d = 0.0f;
@@ -528,7 +653,8 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_kernel(const LaArgs a) 
 // reversed job), written at that segment's place.  The last segment in the
 // job's direction has none behind it and does nothing.
 template <typename T, int DKP, int NW>
-__global__ __launch_bounds__(NW * 64) void pdssm_linattn_state_kernel(const LaArgs a) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
+pdssm_linattn_state_kernel(const LaArgs a) {
   using K = LaTile<T, DKP, NW>;
   using E = typename T::store;
   using F = typename T::frag;
@@ -536,12 +662,9 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_state_kernel(const LaAr
   extern __shared__ __align__(16) unsigned char smem[];
   E* Y = (E*)smem;
   E* Z = (E*)(smem + K::kX);
-  float* ghi = (float*)(smem + K::kX + K::kZ);
-  float* glo = ghi + C;
-  float* ea = glo + C;
-  float* ew = ea + C;
-  float* tot = ew + C;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, n32 = lane & 31;
+  float* exps = (float*)(smem + K::kX + K::kZ);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
+            n32 = lane & 31;
   unsigned id = blockIdx.x;
   const int jn = id % a.njobs;
   id /= a.njobs;
@@ -552,36 +675,50 @@ __global__ __launch_bounds__(NW * 64) void pdssm_linattn_state_kernel(const LaAr
   const LaJob& J = a.job[jn];
   LaSeg s;
   if (!la_segment(a, sid, s)) return;
-  if (J.rev ? s.first : s.last) return;
-  const int c0 = slab * NW * 32 + wave * 32, col = c0 + n32;
+  const int rev = J.rev;
+  if (rev ? s.first : s.last) return;
+  const int slab0 = slab * NW * 32, c0 = slab0 + wave * 32, col = c0 + n32;
+  const int chunks = (s.len + C - 1) / C;
+  const E* yp = la_ptr<T>(J.y, s.vb, hd / J.yd, s.t0);
+  const E* zp = la_ptr<T>(J.z, s.vb, hd / J.zd, s.t0) + slab0;
+  const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh + (int64_t)s.t0 * a.g.st;
+  typename K::X ty;
+  typename K::Z tz;
+  ty.init(tid, J.DK);
+  tz.init(tid, J.DV - slab0);
+  float gv = 0.0f;
+  constexpr int kExpWave = NW - 1;
+  auto fetch = [&](int ci) {
+    const int n = s.len - ci * C;
+    ty.fetch(yp + (int64_t)(ci * C) * J.y.st, J.y.st, n);
+    tz.fetch(zp + (int64_t)(ci * C) * J.z.st, J.z.st, n);
+    if (wave == kExpWave) gv = lane < n && lane < C ? gp[(int64_t)(ci * C + lane) * a.g.st] : 0.0f;
+  };
+  if (chunks) fetch(rev ? chunks - 1 : 0);
   la_f16 S[K::KT];
 #pragma unroll
   for (int t = 0; t < K::KT; ++t) S[t] = la_f16{};
   double sum = 0.0;
-  const int chunks = (s.len + C - 1) / C;
+  if (wave == kExpWave) sum += la_exponents<C>(gv, rev, 1.0f, J.s_upd, exps, lane);
   for (int q = 0; q < chunks; ++q) {
-    const int ci = J.rev ? chunks - 1 - q : q;
-    const int t = s.t0 + ci * C;
+    const int ci = rev ? chunks - 1 - q : q;
     const int n = s.len - ci * C < C ? s.len - ci * C : C;
-    const int slab0 = slab * NW * 32;
-    const int zc = J.DV - slab0 < NW * 32 ? J.DV - slab0 : NW * 32;
-    la_stage<T, C, DKP, K::NT>(Y, la_ptr<T>(J.y, s.vb, hd / J.yd, t), J.y.st, n, J.DK, tid);
-    la_stage<T, C, NW * 32, K::NT>(Z, la_ptr<T>(J.z, s.vb, hd / J.zd, t) + slab0, J.z.st, n, zc, tid);
-    if (wave == 0) {
-      const double d = la_exponents<C>(a, s, hd, t, n, J.rev, 1.0f, J.s_upd, ghi, glo, ea, ew, lane);
-      sum += d;
-      if (lane == 0) tot[0] = __builtin_amdgcn_exp2f((float)d);
-    }
+    const float* e = exps + (q & 1) * K::kExp;
+    ty.commit(Y, tid, n);
+    tz.commit(Z, tid, n);
     __syncthreads();
+    if (q + 1 < chunks) fetch(rev ? ci - 1 : ci + 1);
     F zf[C / 16];
 #pragma unroll
     for (int js = 0; js < C / 16; ++js) zf[js] = T::col(Z, K::ZS, 16 * js, wave * 32, lane);
-    la_update<T, DKP, NW>(S, Y, zf, ew, tot[0], lane);
+    la_update<T, DKP, NW>(S, Y, zf, e + 3 * C, e[4 * C], lane);
+    if (wave == kExpWave && q + 1 < chunks)
+      sum += la_exponents<C>(gv, rev, 1.0f, J.s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
     __syncthreads();
   }
-  const long long at = ((long long)(sid + (J.rev ? -1 : 1)) * a.H + hd);
+  const long long at = ((long long)(sid + (rev ? -1 : 1)) * a.H + hd);
   la_store_state<K::KT>(S, J.seg_out + at * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
-  if (slab == 0 && tid == 0) J.seg_decay[at] = __builtin_amdgcn_exp2f((float)sum);
+  if (slab == 0 && wave == kExpWave && lane == 0) J.seg_decay[at] = __builtin_amdgcn_exp2f((float)sum);
 }
 
 }  // namespace pdscan
