@@ -106,38 +106,49 @@ __device__ __forceinline__ double block_sum(double x, double* red, int tid) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// d loss / d log a_t of one segment and head.  Pairs (key at or before t-1,
-// query at or behind t) meet at t, so with r_i = q_i . dq_i (every key before
-// query i) and c_j = k_j . dk_j (every query behind key j)
+// d loss / d log a_t of one piece of a segment (kLaKeep steps) and head.
+// Pairs (key at or before t-1, query at or behind t) meet at t, so with
+// r_i = q_i . dq_i (every key before query i) and c_j = k_j . dk_j (every query
+// behind key j)
 //   g_t = sum_{i >= t} r_i - sum_{j >= t} c_j + <S_end, dS_end>
-// over the rest of the segment: pairs inside it cancel but for those that
-// meet at t, and the last term holds those that meet behind its end.  The
-// sums run in 64 bits over one segment only.
+// over the rest of the piece: pairs inside it cancel but for those that meet
+// at t, and the last term holds those that meet behind its end.  The sums run
+// in 64 bits, but r and c carry fp32 errors that do not cancel and grow with
+// the square root of their number: 2048 steps in one sum left 1.6e-6 of the
+// gradient, pieces of 512 half of that, for 2 states stored and read a piece.
 __global__ __launch_bounds__(256) void pdssm_linattn_decay_kernel(const LaDecayArgs a) {
   __shared__ double red[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int sid = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
+  const int h = blockIdx.x % a.c.H, piece = blockIdx.x / a.c.H;
+  const int sub = piece % a.subs, sid = piece / a.subs;
   LaSeg s;
-  const bool live = la_segment(a.c, sid, s);
   double total = 0.0;
-  if (live) {
+  if (la_segment(a.c, sid, s) && sub * kLaKeep < s.len) {
+    const int lo = sub * kLaKeep, hi = lo + kLaKeep < s.len ? lo + kLaKeep : s.len;
+    const float4 *A = nullptr, *R = nullptr;
     double x = 0.0;
-    if (!s.last) {
-      const float4* A = (const float4*)(a.sS + ((long long)(sid + 1) * a.c.H + h) * a.c.state);
-      const float4* R = (const float4*)(a.sR + ((long long)sid * a.c.H + h) * a.c.state);
+    if (hi < s.len) {
+      const long long at = (la_keep_slot(a.c, s, s.t0 + hi) * a.c.H + h) * a.c.state;
+      A = (const float4*)(a.kS + at);
+      R = (const float4*)(a.kR + at);
+    } else if (!s.last) {
+      A = (const float4*)(a.sS + ((long long)(sid + 1) * a.c.H + h) * a.c.state);
+      R = (const float4*)(a.sR + ((long long)sid * a.c.H + h) * a.c.state);
+    } else if (a.xd) {
+      for (int w = 0; w < a.xd_slabs; ++w) x += a.xd[((long long)w * a.c.segs + sid) * a.c.H + h];
+    }
+    if (A) {
       for (int e = tid; e < a.c.state / 4; e += 256) {
         const float4 p = A[e], q = R[e];
         x += (double)((p.x * q.x + p.y * q.y) + (p.z * q.z + p.w * q.w));
       }
       x = block_sum(x, red, tid);
-    } else if (a.xd) {
-      for (int w = 0; w < a.xd_slabs; ++w) x += a.xd[((long long)w * a.c.segs + sid) * a.c.H + h];
     }
     double carry = x;
-    for (int t1 = s.len; t1 > 0; t1 -= 256) {
+    for (int t1 = hi; t1 > lo; t1 -= 256) {
       const int t = t1 - 1 - tid;
       double d = 0.0;
-      if (t >= 0) {
+      if (t >= lo) {
         const long long at = (long long)h * a.c.rows + s.row0 + t;
         const long long slab = (long long)a.c.H * a.c.rows;
         for (int w = 0; w < a.r_slabs; ++w) d += (double)a.r[w * slab + at];
@@ -154,7 +165,7 @@ __global__ __launch_bounds__(256) void pdssm_linattn_decay_kernel(const LaDecayA
       double before = carry;
       for (int w = 0; w < wave; ++w) before += red[w];
       carry += (red[0] + red[1]) + (red[2] + red[3]);
-      if (t >= 0) {
+      if (t >= lo) {
         const double g = before + d;
         if (a.per_head)
           total += g;
@@ -166,15 +177,15 @@ __global__ __launch_bounds__(256) void pdssm_linattn_decay_kernel(const LaDecayA
   }
   if (a.per_head) {
     total = block_sum(total, red, tid);
-    if (tid == 0) a.part[(long long)sid * a.c.H + h] = total;
+    if (tid == 0) a.part[(long long)piece * a.c.H + h] = total;
   }
 }
 
-__global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int segs) {
+__global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int pieces) {
   __shared__ double red[4];
   const int h = blockIdx.x;
   double x = 0.0;
-  for (int s = threadIdx.x; s < segs; s += 256) x += part[(long long)s * H + h];
+  for (int s = threadIdx.x; s < pieces; s += 256) x += part[(long long)s * H + h];
   x = block_sum(x, red, threadIdx.x);
   if (threadIdx.x == 0) out[h] = (float)x;
 }
@@ -311,12 +322,12 @@ hipError_t launch_linattn_carry(const LaCarryArgs& a, int passes, hipStream_t st
 }
 
 hipError_t launch_linattn_decay(const LaDecayArgs& a, hipStream_t st) {
-  const long long grid = (long long)a.c.segs * a.c.H;
+  const long long grid = (long long)a.c.segs * a.subs * a.c.H;
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;
   hipLaunchKernelGGL(pdssm_linattn_decay_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
   if (a.per_head)
     hipLaunchKernelGGL(pdssm_linattn_decay_sum_kernel, dim3((unsigned)a.c.H), dim3(256), 0, st, a.part,
-                       (float*)a.out.p, a.c.H, a.c.segs);
+                       (float*)a.out.p, a.c.H, a.c.segs * a.subs);
   return hipGetLastError();
 }
 
@@ -332,7 +343,7 @@ hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The product kernels, by type, x-row width and waves; pieces: 2 or 3 (bf16).
+// The product kernels, by type, x-row width and waves.
 hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pieces, hipStream_t st) {
   const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DV);
   const long long grid = (long long)a.segs * a.H * a.slabs * a.njobs;

@@ -33,16 +33,44 @@
 namespace pdscan {
 
 typedef __bf16 la_bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 la_bf2 __attribute__((ext_vector_type(2)));
+typedef float la_f2 __attribute__((ext_vector_type(2)));
 typedef float la_f16 __attribute__((ext_vector_type(16)));
 typedef short la_s4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) la_s4 la_lds_s4;
 
+// ---- operand layout
+//
+// A 32 x 32 x 16 product takes from lane (n = lane % 32, h = lane / 32) the
+// eight contraction slots of its half and leaves in accumulator register r
+// the row 8 (r / 4) + 4 h + r % 4 of column n.  Rows are fed in the order
+// pi(m) = m with bits 2 and 3 exchanged, so registers 8 s .. 8 s + 7 of a lane
+// hold the rows 16 s + 8 h .. + 7: eight neighbours.  They are stored and read
+// 16 bytes at a time, and they are exactly the slots that the next product's
+// operand wants of that lane, so an accumulator becomes an operand without any
+// exchange between lanes.
+__device__ __forceinline__ int la_pi(int m) { return (m & ~12) | ((m & 4) << 1) | ((m & 8) >> 1); }
+
+// ---- LDS layout
+//
+// Tiles lie row by row without padding; 16-byte unit u of row r is kept at
+// unit u ^ f(r).  f is linear in the bits of r and such that 16 rows read at
+// one unit (row operands), and four rows read at four neighbouring units
+// (column operands through the transposing read), fall on different banks.
+template <int ROW_BYTES>
+__device__ __forceinline__ constexpr int la_f(int r) {
+  return ROW_BYTES >= 256   ? ((((r & 3) << 2) | ((r >> 2) & 3)) ^ (r & 8))
+         : ROW_BYTES == 128 ? (((r >> 1 & 1) << 2) | (r >> 2 & 3))
+                            : (r >> 2 & 3);
+}
+
 struct LaBf16 {
   using store = uint16_t;
   static constexpr int kVec = 8;    // elements of 16 bytes
-  static constexpr int kPad = 8;    // row padding in LDS: rows land 4 banks apart
+  static constexpr int kHalf = 1;   // 16-byte units of eight elements
   union frag {
     uint32_t u[4];
+    uint4 w;
     la_s4 s[2];
     la_bf8 v;
   };
@@ -53,23 +81,29 @@ struct LaBf16 {
     const uint32_t w = f.u[e >> 1];
     return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
   }
-  // elements k0 + 4h + {0..3} and k0 + 8 + 4h + {0..3} of a row
-  static __device__ __forceinline__ frag row(const store* p, int h) {
+  // eight elements of a row at byte address a
+  static __device__ __forceinline__ frag row(const unsigned char* a) {
     frag f;
-    *(uint2*)&f.u[0] = *(const uint2*)(p + 4 * h);
-    *(uint2*)&f.u[2] = *(const uint2*)(p + 8 + 4 * h);
+    f.w = *(const uint4*)a;
     return f;
   }
-  // the same elements of a column: rows r0 + 4h + {0..3} and r0 + 8 + 4h + {0..3}
-  // of column c0 + lane % 32.  The transposing read hands the 16 lanes of a
-  // group four rows of 16 columns: lane p points at row p / 4, columns
-  // 4 (p % 4).. and receives column p.
-  static __device__ __forceinline__ frag col(const store* base, int stride, int r0, int c0, int lane) {
-    const int p = lane & 15;
-    const store* a = base + (r0 + 4 * (lane >> 5) + (p >> 2)) * stride + c0 + (lane & 16) + 4 * (p & 3);
+  // Byte offset, for this lane, of column operands: rows 8 h .. 8 h + 7 of the
+  // columns pi(0 .. 31).  The transposing read hands the 16 lanes of a group
+  // four rows of four times four columns: lane p points at row p / 4, its
+  // (p % 4)-th four columns, and receives column p; pi swaps the second and
+  // third four.
+  template <int RB>
+  static __device__ __forceinline__ uint32_t col_base(int lane, int c0) {
+    const int p = lane & 15, r = 8 * (lane >> 5) + (p >> 2), q = p & 3, c4 = ((q & 1) << 1) | (q >> 1);
+    const int unit = c0 / 8 + ((lane & 16) >> 3) + (c4 >> 1);
+    return r * RB + ((unit ^ la_f<RB>(r)) << 4) + (c4 & 1) * 8;
+  }
+  template <int RB>
+  static __device__ __forceinline__ frag col(const unsigned char* lds, uint32_t base, int r0, int tile) {
+    const uint32_t b = base ^ (uint32_t)(tile * 64);
     frag f;
-    f.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s4*)(a));
-    f.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s4*)(a + 8 * stride));
+    f.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s4*)(lds + b + r0 * RB));
+    f.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s4*)(lds + (b ^ (la_f<RB>(4) << 4)) + (r0 + 4) * RB));
     return f;
   }
   // eight floats as bf16 pieces, cut (not rounded) so that each rest is exact
@@ -91,35 +125,16 @@ struct LaBf16 {
       }
     }
   }
-  template <int NP>
-  static __device__ __forceinline__ void put4(store* p, int piece_stride, const float* v) {
-    float x[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-    for (int q = 0; q < NP; ++q) {
-      uint2 w;
-      const uint32_t b0 = __float_as_uint(x[0]), b1 = __float_as_uint(x[1]), b2 = __float_as_uint(x[2]),
-                     b3 = __float_as_uint(x[3]);
-      w.x = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
-      w.y = __builtin_amdgcn_perm(b3, b2, 0x07060302u);
-      *(uint2*)(p + q * piece_stride) = w;
-      if (q + 1 < NP) {
-        x[0] -= __uint_as_float(b0 & 0xffff0000u);
-        x[1] -= __uint_as_float(b1 & 0xffff0000u);
-        x[2] -= __uint_as_float(b2 & 0xffff0000u);
-        x[3] -= __uint_as_float(b3 & 0xffff0000u);
-      }
-    }
-  }
-  static __device__ __forceinline__ uint32_t round(float x) {   // nearest, ties to even
-    const uint32_t b = __float_as_uint(x);
-    if ((b & 0x7fffffffu) > 0x7f800000u) return (b >> 16) | 0x40u;
-    return (b + 0x7fffu + ((b >> 16) & 1u)) >> 16;
+  static __device__ __forceinline__ void put(unsigned char* a, const frag& f) { *(uint4*)a = f.w; }
+  static __device__ __forceinline__ uint32_t round2(float x, float y) {   // nearest, ties to even
+    const la_f2 v = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, la_bf2));
   }
   static __device__ __forceinline__ void store4(store* p, const float* v) {
-    uint2 w;
-    w.x = round(v[0]) | (round(v[1]) << 16);
-    w.y = round(v[2]) | (round(v[3]) << 16);
-    *(uint2*)p = w;
+    *(uint2*)p = make_uint2(round2(v[0], v[1]), round2(v[2], v[3]));
+  }
+  static __device__ __forceinline__ void store8(store* p, const float* v) {
+    *(uint4*)p = make_uint4(round2(v[0], v[1]), round2(v[2], v[3]), round2(v[4], v[5]), round2(v[6], v[7]));
   }
   static __device__ __forceinline__ void load4(const store* p, float* v) {
     const uint2 w = *(const uint2*)p;
@@ -133,7 +148,7 @@ struct LaBf16 {
 struct LaF32 {
   using store = float;
   static constexpr int kVec = 4;
-  static constexpr int kPad = 4;
+  static constexpr int kHalf = 2;
   struct frag {
     float f[8];
   };
@@ -142,20 +157,23 @@ struct LaF32 {
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.f[e], b.f[e], c, 0, 0, 0);
   }
   static __device__ __forceinline__ float get(const frag& f, int e) { return f.f[e]; }
-  static __device__ __forceinline__ frag row(const store* p, int h) {
+  static __device__ __forceinline__ frag row(const unsigned char* a) {
     frag f;
-    *(float4*)&f.f[0] = *(const float4*)(p + 4 * h);
-    *(float4*)&f.f[4] = *(const float4*)(p + 8 + 4 * h);
+    *(float4*)&f.f[0] = *(const float4*)a;
+    *(float4*)&f.f[4] = *(const float4*)((uintptr_t)a ^ 16);
     return f;
   }
-  static __device__ __forceinline__ frag col(const store* base, int stride, int r0, int c0, int lane) {
-    const store* a = base + (r0 + 4 * (lane >> 5)) * stride + c0 + (lane & 31);
+  template <int RB>
+  static __device__ __forceinline__ uint32_t col_base(int lane, int c0) {
+    const int r = 8 * (lane >> 5), c = c0 + la_pi(lane & 31);
+    return r * RB + (((c >> 2) ^ la_f<RB>(r)) << 4) + (c & 3) * 4;
+  }
+  template <int RB>
+  static __device__ __forceinline__ frag col(const unsigned char* lds, uint32_t base, int r0, int tile) {
+    const uint32_t b = base ^ (uint32_t)(tile * 128);
     frag f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f.f[e] = a[e * stride];
-      f.f[4 + e] = a[(8 + e) * stride];
-    }
+    for (int e = 0; e < 8; ++e) f.f[e] = *(const float*)(lds + (b ^ (uint32_t)(la_f<RB>(e) << 4)) + (r0 + e) * RB);
     return f;
   }
   template <int NP>
@@ -163,12 +181,16 @@ struct LaF32 {
 #pragma unroll
     for (int e = 0; e < 8; ++e) out[0].f[e] = v[e];
   }
-  template <int NP>
-  static __device__ __forceinline__ void put4(store* p, int, const float* v) {
-    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+  static __device__ __forceinline__ void put(unsigned char* a, const frag& f) {
+    *(float4*)a = *(const float4*)&f.f[0];
+    *(float4*)((uintptr_t)a ^ 16) = *(const float4*)&f.f[4];
   }
   static __device__ __forceinline__ void store4(store* p, const float* v) {
     *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  static __device__ __forceinline__ void store8(store* p, const float* v) {
+    store4(p, v);
+    store4(p + 4, v + 4);
   }
   static __device__ __forceinline__ void load4(const store* p, float* v) {
     const float4 w = *(const float4*)p;
@@ -206,6 +228,11 @@ __device__ __forceinline__ bool la_segment(const LaArgs& a, int sid, LaSeg& s) {
   return true;
 }
 
+// Place of the state kept at step t of a view's axis (every kLaKeep steps of a segment).
+__device__ __forceinline__ long long la_keep_slot(const LaArgs& a, const LaSeg& s, int t) {
+  return (long long)s.vb * ((a.L + kLaKeep - 1) / kLaKeep) + t / kLaKeep;
+}
+
 template <typename T>
 __device__ __forceinline__ const typename T::store* la_ptr(const LaView& v, int b, int h, int t) {
   return (const typename T::store*)v.p + (int64_t)b * v.sb + (int64_t)h * v.sh + (int64_t)t * v.st;
@@ -214,45 +241,50 @@ __device__ __forceinline__ const typename T::store* la_ptr(const LaView& v, int 
 // A tile of C rows and W elements on its way from memory to LDS: thread
 // `tid` owns 16 bytes of every RP-th row.  fetch() only issues the loads (the
 // next chunk's while this one is worked on); rows behind n and columns behind
-// D are loaded from a place that exists and become zero in commit().
+// D are loaded from a place that exists and become zero in commit().  The
+// chunk's place is uniform, a lane adds 32 bits (the host bounds the stride).
 template <typename T, int C, int W, int NT>
 struct LaTileIO {
   using E = typename T::store;
-  static constexpr int kCols = W / T::kVec, RP = NT / kCols, N = C / RP, kStride = W + T::kPad;
+  static constexpr int kCols = W / T::kVec, RP = NT / kCols, N = C / RP, RB = W * (int)sizeof(E);
+  static_assert(RP * kCols == NT && N * RP == C, "whole passes");
   uint4 r[N];
-  int row0, col;
+  const char* base;      // the chunk under way
+  uint32_t st, off;      // bytes of a row's stride; this thread's offset
+  int row0;
   bool ok;
-  __device__ __forceinline__ void init(int tid, int D) {
+  __device__ __forceinline__ void init(const E* chunk, int64_t stride, int tid, int D) {
+    base = (const char*)chunk;
+    st = (uint32_t)stride * (uint32_t)sizeof(E);
     row0 = tid / kCols;
-    col = tid % kCols * T::kVec;
+    const int col = tid % kCols * T::kVec;
     ok = col < D;
-    if (!ok) col = 0;
+    off = row0 * st + (ok ? col : 0) * (uint32_t)sizeof(E);
   }
-  __device__ __forceinline__ void fetch(const E* chunk, int64_t st, int n) {
+  __device__ __forceinline__ void fetch(int n) {
     if (n >= C) {
-      const E* p = chunk + (int64_t)row0 * st + col;
+      uint32_t o = off;
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = *(const uint4*)(p + (int64_t)(i * RP) * st);
+      for (int i = 0; i < N; ++i, o += RP * st) r[i] = *(const uint4*)(base + o);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int row = row0 + i * RP;
-        r[i] = *(const uint4*)(chunk + (int64_t)(row < n ? row : n - 1) * st + col);
+        r[i] = *(const uint4*)(base + (uint32_t)(off + (uint32_t)((row < n ? row : n - 1) - row0) * st));
       }
     }
   }
-  __device__ __forceinline__ void commit(E* lds, int tid, int n) const {
-    E* q = lds + row0 * kStride + tid % kCols * T::kVec;
+  __device__ __forceinline__ void commit(unsigned char* lds, int tid, int n, bool whole) {
+    const uint32_t a = row0 * RB + (((tid % kCols) ^ la_f<RB>(row0)) << 4);
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      uint4 w = r[i];
-      if (!ok || row0 + i * RP >= n) w = make_uint4(0, 0, 0, 0);
-      *(uint4*)(q + i * RP * kStride) = w;
+      for (int i = 0; i < N; ++i)
+        if (!ok || row0 + i * RP >= n) r[i] = make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) *(uint4*)(lds + (a ^ (uint32_t)(la_f<RB>(i * RP) << 4)) + i * RP * RB) = r[i];
   }
 };
-
-__device__ __forceinline__ double la_dpp_add(double x, uint64_t up) { return x + __longlong_as_double((long long)up); }
 
 // x plus the value of the lane that DPP control CTRL names (zero where there
 // is none or the row is masked)
@@ -261,7 +293,7 @@ __device__ __forceinline__ double la_scan_step(double x) {
   const uint64_t b = (uint64_t)__double_as_longlong(x);
   const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
-  return la_dpp_add(x, ((uint64_t)hi << 32) | lo);
+  return x + __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
 // Exponents of one chunk, by one wave (lane = token, g = its log decay, 0
@@ -306,27 +338,24 @@ struct LaTile {
   // One or two waves form all scores of the chunk each, in registers; four
   // share them through LDS (each wave forms one tile of 32 x 32).
   static constexpr bool kShareP = NW == 4;
-  static constexpr int XS = DKP + T::kPad, ZS = NW * 32 + T::kPad, PS = C + 4;
+  static constexpr int ES = (int)sizeof(typename T::store);
+  static constexpr int XB = DKP * ES, ZB = NW * 32 * ES, PB = C * ES;   // bytes of a row
   static constexpr int kExp = 4 * C + 4;         // floats of one chunk's exponents
-  static constexpr size_t kX = (size_t)C * XS * sizeof(typename T::store);
-  static constexpr size_t kZ = (size_t)C * ZS * sizeof(typename T::store);
-  static constexpr size_t kP = kShareP ? (size_t)C * PS * sizeof(typename T::store) : 0;
+  static constexpr size_t kX = (size_t)C * XB, kZ = (size_t)C * ZB, kP = kShareP ? (size_t)C * PB : 0;
   static constexpr size_t kSmall = (size_t)(2 * kExp + NW * C) * 4;
   static constexpr size_t main_bytes(int np) { return 2 * kX + kZ + np * kP + kSmall; }
   static constexpr size_t state_bytes() { return kX + kZ + (size_t)2 * kExp * 4; }
   using X = LaTileIO<T, C, DKP, NT>;
   using Z = LaTileIO<T, C, NW * 32, NT>;
-  // registers: state, outputs and the tiles under way; under about 200 of
+  // registers: state, outputs and the tiles under way; with few enough of
   // them two waves share a SIMD
   static constexpr int kRegs = 16 * (KT + IT) + 4 * (2 * X::N + Z::N);
-  static constexpr int kWaves = kRegs <= 180 ? 2 : 1;
+  static constexpr int kWaves = kRegs <= 150 ? 2 : 1;
 };
 
-// acc (C layout of a 32 x 32 product: column lane % 32, rows 8 (r / 4) + 4 h +
-// r % 4) gives the eight contraction slots of step q of the next product: the
-// operand loads above use the same order, so no lane exchanges anything.
+// S = decay S + sum_j y_j (w_j z_j)^T
 template <typename T, int DKP, int NW>
-__device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const typename T::store* Y,
+__device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const unsigned char* Y, uint32_t ycol,
                                           const typename T::frag* zf, const float* ew, float decay, int lane) {
   using K = LaTile<T, DKP, NW>;
   const int h = lane >> 5;
@@ -337,7 +366,7 @@ __device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const typename 
 #pragma unroll
   for (int js = 0; js < K::C / 16; ++js) {
     float v[8];
-    const float4 w0 = *(const float4*)(ew + 16 * js + 4 * h), w1 = *(const float4*)(ew + 16 * js + 8 + 4 * h);
+    const float4 w0 = *(const float4*)(ew + 16 * js + 8 * h), w1 = *(const float4*)(ew + 16 * js + 8 * h + 4);
     const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = T::get(zf[js], e) * w[e];
@@ -345,7 +374,7 @@ __device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const typename 
     T::template pieces<K::NPS>(v, b);
 #pragma unroll
     for (int t = 0; t < K::KT; ++t) {
-      const typename T::frag y = T::col(Y, K::XS, 16 * js, 32 * t, lane);
+      const typename T::frag y = T::template col<K::XB>(Y, ycol, 16 * js, t);
 #pragma unroll
       for (int p = 0; p < K::NPS; ++p) T::mma(S[t], y, b[p]);
     }
@@ -354,7 +383,7 @@ __device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const typename 
 
 // A state's rows m and column `col` of this lane, zero where p is NULL or the
 // state ends.  sm = 1: the rows lie side by side (the state is stored
-// transposed) and four come in one load.
+// transposed) and come four to a load.
 template <int KT>
 __device__ __forceinline__ void la_load_state(la_f16 (&S)[KT], const float* p, int sm, int sn, int DK, int DV,
                                               int col, int h) {
@@ -365,20 +394,20 @@ __device__ __forceinline__ void la_load_state(la_f16 (&S)[KT], const float* p, i
 #pragma unroll
   for (int t = 0; t < KT; ++t)
 #pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const int m = 32 * t + 8 * r4 + 4 * h;
+    for (int s = 0; s < 2; ++s) {
+      const int m = 32 * t + 16 * s + 8 * h;
       const bool in = m < DK && col < DV;
       const int mm = m < DK ? m : 0;
-      float v[4];
+      float v[8];
       if (sm == 1) {
-        const float4 w = *(const float4*)(q + mm);
-        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        *(float4*)&v[0] = *(const float4*)(q + mm);
+        *(float4*)&v[4] = *(const float4*)(q + mm + 4);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = q[(long long)(mm + e) * sm];
+        for (int e = 0; e < 8; ++e) v[e] = q[(long long)(mm + e) * sm];
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[t][4 * r4 + e] = in ? v[e] : 0.0f;
+      for (int e = 0; e < 8; ++e) S[t][8 * s + e] = in ? v[e] : 0.0f;
     }
 }
 
@@ -390,131 +419,165 @@ __device__ __forceinline__ void la_store_state(const la_f16 (&S)[KT], float* p, 
 #pragma unroll
   for (int t = 0; t < KT; ++t)
 #pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const int m = 32 * t + 8 * r4 + 4 * h;
+    for (int s = 0; s < 2; ++s) {
+      const int m = 32 * t + 16 * s + 8 * h;
       if (m >= DK) continue;
-      if (sm == 1)
-        *(float4*)(q + m) = make_float4(S[t][4 * r4], S[t][4 * r4 + 1], S[t][4 * r4 + 2], S[t][4 * r4 + 3]);
-      else
+      if (sm == 1) {
+        *(float4*)(q + m) = make_float4(S[t][8 * s], S[t][8 * s + 1], S[t][8 * s + 2], S[t][8 * s + 3]);
+        *(float4*)(q + m + 4) = make_float4(S[t][8 * s + 4], S[t][8 * s + 5], S[t][8 * s + 6], S[t][8 * s + 7]);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q[(long long)(m + e) * sm] = S[t][4 * r4 + e];
+        for (int e = 0; e < 8; ++e) q[(long long)(m + e) * sm] = S[t][8 * s + e];
+      }
     }
 }
 
 // Scores of one 32 x 32 tile (rows j of y, columns i of x), weighted by the
 // decay between the two tokens and zero on the wrong side of the diagonal.
-template <typename T, int DKP, int NW>
-__device__ __forceinline__ la_f16 la_scores(const typename T::store* X, const typename T::store* Y, const float* e,
-                                            int jt, int it, int rev, float s_intra, int lane) {
+template <typename T, int DKP, int NW, bool REV>
+__device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsigned char* Y, uint32_t xrow,
+                                            uint32_t yrow, const float* e, int jt, int it, float s_intra,
+                                            int lane) {
   using K = LaTile<T, DKP, NW>;
   const int h = lane >> 5, n32 = lane & 31;
   la_f16 c = {};
 #pragma unroll
   for (int ks = 0; ks < DKP / 16; ++ks)
-    T::mma(c, T::row(Y + (32 * jt + n32) * K::XS + 16 * ks, h), T::row(X + (32 * it + n32) * K::XS + 16 * ks, h));
+    T::mma(c, T::row(Y + (yrow ^ (uint32_t)(ks * 32 * T::kHalf)) + jt * 32 * K::XB),
+           T::row(X + (xrow ^ (uint32_t)(ks * 32 * T::kHalf)) + it * 32 * K::XB));
   const int i = 32 * it + n32;
   const float gi = e[i], gl = e[K::C + i];
-  const float sign = rev ? -1.0f : 1.0f;
 #pragma unroll
-  for (int r4 = 0; r4 < 4; ++r4) {
-    const int j0 = 32 * jt + 8 * r4 + 4 * h;
-    const float4 jh = *(const float4*)(e + j0), jl = *(const float4*)(e + K::C + j0);
-    const float hh[4] = {jh.x, jh.y, jh.z, jh.w}, ll[4] = {jl.x, jl.y, jl.z, jl.w};
+  for (int s = 0; s < 2; ++s) {
+    const int j0 = 32 * jt + 16 * s + 8 * h;
+    float hh[8], ll[8];
+    *(float4*)&hh[0] = *(const float4*)(e + j0);
+    *(float4*)&hh[4] = *(const float4*)(e + j0 + 4);
+    *(float4*)&ll[0] = *(const float4*)(e + K::C + j0);
+    *(float4*)&ll[4] = *(const float4*)(e + K::C + j0 + 4);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float d = ((gi - hh[q]) + (gl - ll[q])) * sign;
+    for (int q = 0; q < 8; ++q) {
+      const float d = REV ? (hh[q] - gi) + (ll[q] - gl) : (gi - hh[q]) + (gl - ll[q]);
       const float w = __builtin_amdgcn_exp2f(d) * s_intra;
-      const float v = c[4 * r4 + q] * w;
-      c[4 * r4 + q] = jt != it || (rev ? j0 + q >= i : j0 + q <= i) ? v : 0.0f;
+      const float v = c[8 * s + q] * w;
+      c[8 * s + q] = jt != it || (REV ? j0 + q >= i : j0 + q <= i) ? v : 0.0f;
     }
   }
   return c;
 }
 
 // o = form(x, y, z) over one segment, head and slab of 32 NW columns.
-template <typename T, int DKP, int NW, int NP>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
-pdssm_linattn_kernel(const LaArgs a) {
+// BWD: what only the gradient asks for (w . o per token, states kept, the
+// final product, fp32 outputs).
+template <typename T, int DKP, int NW, int NP, bool REV, bool BWD>
+__device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const LaSeg& s, int sid, int hd, int slab,
+                                        unsigned char* smem) {
   using K = LaTile<T, DKP, NW>;
   using E = typename T::store;
   using F = typename T::frag;
   constexpr int C = K::C, IT = K::IT;
-  extern __shared__ __align__(16) unsigned char smem[];
-  E* X = (E*)smem;
-  E* Y = (E*)(smem + K::kX);
-  E* Z = (E*)(smem + 2 * K::kX);
-  E* P = (E*)(smem + 2 * K::kX + K::kZ);
+  unsigned char* X = smem;
+  unsigned char* Y = smem + K::kX;
+  unsigned char* Z = smem + 2 * K::kX;
+  unsigned char* P = smem + 2 * K::kX + K::kZ;
   float* exps = (float*)(smem + 2 * K::kX + K::kZ + NP * K::kP);   // of this chunk and the next
   float* dots = exps + 2 * K::kExp;                                // [NW][C]
-
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
-            n32 = lane & 31;
-  unsigned id = blockIdx.x;
-  if (id == 0 && tid < 2) a.header[tid] = 0;
-  const int jn = id % a.njobs;
-  id /= a.njobs;
-  const int slab = id % a.slabs;
-  id /= a.slabs;
-  const int hd = id % a.H;
-  const int sid = id / a.H;
-  const LaJob& J = a.job[jn];
-  LaSeg s;
-  if (!la_segment(a, sid, s)) return;
-
-  const int rev = J.rev;
+            n32 = lane & 31, pm = la_pi(n32);
   const int slab0 = slab * NW * 32;
   const int c0 = slab0 + wave * 32;      // first column of this wave
-  const int col = c0 + n32;
+  const int col = c0 + pm;               // the state's column of this lane
   const long long unit = (long long)s.b * a.H + hd;
-  const bool starts = rev ? s.last : s.first, ends = rev ? s.first : s.last;
   const int chunks = (s.len + C - 1) / C;
-  const E* xp = la_ptr<T>(J.x, s.vb, hd / J.xd, s.t0);
-  const E* yp = la_ptr<T>(J.y, s.vb, hd / J.yd, s.t0);
-  const E* zp = la_ptr<T>(J.z, s.vb, hd / J.zd, s.t0) + slab0;
-  const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh + (int64_t)s.t0 * a.g.st;
+  const int first = REV ? (chunks ? chunks - 1 : 0) * C : 0;   // first step worked on
+  constexpr int dir = REV ? -C : C;
   typename K::X tx, ty;
   typename K::Z tz;
-  tx.init(tid, J.DK);
-  ty.init(tid, J.DK);
-  tz.init(tid, J.DV - slab0);
+  tx.init(la_ptr<T>(J.x, s.vb, hd / J.xd, s.t0 + first), J.x.st, tid, J.DK);
+  ty.init(la_ptr<T>(J.y, s.vb, hd / J.yd, s.t0 + first), J.y.st, tid, J.DK);
+  tz.init(la_ptr<T>(J.z, s.vb, hd / J.zd, s.t0 + first) + slab0, J.z.st, tid, J.DV - slab0);
+  const int64_t dx = dir * J.x.st * K::ES, dy = dir * J.y.st * K::ES, dz = dir * J.z.st * K::ES, dg = dir * a.g.st;
+  const bool whole = J.DK == DKP && J.DV - slab0 >= NW * 32;
+  const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh +
+                    (int64_t)(s.t0 + first) * a.g.st;
+  const int64_t goff = (int64_t)lane * a.g.st;
   float gv = 0.0f;
   constexpr int kExpWave = NW - 1;
-
-  auto fetch = [&](int ci) {
-    const int n = s.len - ci * C;
-    tx.fetch(xp + (int64_t)(ci * C) * J.x.st, J.x.st, n);
-    ty.fetch(yp + (int64_t)(ci * C) * J.y.st, J.y.st, n);
-    tz.fetch(zp + (int64_t)(ci * C) * J.z.st, J.z.st, n);
-    if (wave == kExpWave) gv = lane < n && lane < C ? gp[(int64_t)(ci * C + lane) * a.g.st] : 0.0f;
+  auto fetch = [&](int n) {
+    tx.fetch(n);
+    ty.fetch(n);
+    tz.fetch(n);
+    if (wave == kExpWave) gv = lane < n && lane < C ? gp[goff] : 0.0f;
   };
-  if (chunks) fetch(rev ? chunks - 1 : 0);
+  if (chunks) fetch(s.len - first);
 
-  const float* init = starts ? (J.s_user ? J.s_user + unit * a.state : nullptr)
-                             : J.s_seg + ((long long)sid * a.H + hd) * a.state;
   la_f16 S[K::KT];
-  la_load_state<K::KT>(S, init, J.sm, J.sn, J.DK, J.DV, col, h);
-  if (wave == kExpWave) la_exponents<C>(gv, rev, J.s_inter, J.s_upd, exps, lane);
+  {
+    const bool starts = REV ? s.last : s.first;
+    const float* init = starts ? (J.s_user ? J.s_user + unit * a.state : nullptr)
+                               : J.s_seg + ((long long)sid * a.H + hd) * a.state;
+    la_load_state<K::KT>(S, init, J.sm, J.sn, J.DK, J.DV, col, h);
+  }
+  if (wave == kExpWave) la_exponents<C>(gv, REV, J.s_inter, J.s_upd, exps, lane);
+
+  // lane offsets of the operands in LDS
+  uint32_t xrow = n32 * K::XB + (((h * T::kHalf) ^ la_f<K::XB>(n32)) << 4);
+  uint32_t yrow = pm * K::XB + (((h * T::kHalf) ^ la_f<K::XB>(pm)) << 4);
+  uint32_t ycol = T::template col_base<K::XB>(lane, 0);
+  uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
+  uint32_t prow = n32 * K::PB + (((h * T::kHalf) ^ la_f<K::PB>(n32)) << 4);
+
+  const int oes = BWD && J.o_f32 ? 4 : K::ES;
+  char* ob = (char*)J.o.p +
+             ((int64_t)s.vb * J.o.sb + (int64_t)(hd / J.od) * J.o.sh + (int64_t)(s.t0 + first) * J.o.st + c0) * oes;
+  const uint32_t ost = (uint32_t)J.o.st * (uint32_t)oes, ooff = n32 * ost + 8 * h * oes;
+  const bool dot = BWD && J.dot != nullptr;
+  const char* wb = nullptr;
+  uint32_t wst = 0, woff = 0;
+  if (dot) {
+    wb = (const char*)(la_ptr<T>(J.w, s.vb, hd / J.wd, s.t0 + first) + c0);
+    wst = (uint32_t)J.w.st * K::ES;
+    woff = n32 * wst + 8 * h * K::ES;
+  }
+  const float s_intra = J.s_intra, s_inter = J.s_inter, s_upd = J.s_upd;
+  int n = s.len - first;                 // steps of this chunk
+  int at = first;                        // its first step in the segment
 
   for (int q = 0; q < chunks; ++q) {
-    const int ci = rev ? chunks - 1 - q : q;
-    const int t = s.t0 + ci * C;
-    const int n = s.len - ci * C < C ? s.len - ci * C : C;
+    if (n > C) n = C;
+    // the operands' places are one exclusive-or away from these: cheaper than the registers to keep them all
+    asm volatile("" : "+v"(xrow), "+v"(yrow), "+v"(ycol), "+v"(zcol), "+v"(prow));
     const float* e = exps + (q & 1) * K::kExp;
-    tx.commit(X, tid, n);
-    ty.commit(Y, tid, n);
-    tz.commit(Z, tid, n);
+    tx.commit(X, tid, n, whole && n == C);
+    ty.commit(Y, tid, n, whole && n == C);
+    tz.commit(Z, tid, n, whole && n == C);
     __syncthreads();
-    if (q + 1 < chunks) fetch(rev ? ci - 1 : ci + 1);
+    if (q + 1 < chunks) {
+      tx.base += dx;
+      ty.base += dy;
+      tz.base += dz;
+      gp += dg;
+      fetch(REV ? C : s.len - at - C);
+    }
+    if (BWD && !REV && J.keep && at && at % kLaKeep == 0)
+      la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + at) * a.H + hd) * a.state, J.sm, J.sn, J.DK, J.DV,
+                            col, h);
 
     if constexpr (K::kShareP) {
       static_assert(IT * IT <= NW, "a score tile per wave");
       const int jt = wave / IT, it = wave % IT;
-      if (wave < IT * IT && (rev ? jt >= it : jt <= it)) {
-        const la_f16 c = la_scores<T, DKP, NW>(X, Y, e, jt, it, rev, J.s_intra, lane);
+      if (wave < IT * IT && (REV ? jt >= it : jt <= it)) {
+        const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, jt, it, s_intra, lane);
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const float v[4] = {c[4 * r4], c[4 * r4 + 1], c[4 * r4 + 2], c[4 * r4 + 3]};
-          T::template put4<NP>(P + (32 * it + n32) * K::PS + 32 * jt + 8 * r4 + 4 * h, C * K::PS, v);
+        for (int k2 = 0; k2 < 2; ++k2) {
+          float v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] = c[8 * k2 + r];
+          F pp[NP];
+          T::template pieces<NP>(v, pp);
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            T::put(P + p * K::kP + (prow ^ (uint32_t)((2 * jt + k2) * 32 * T::kHalf)) + it * 32 * K::PB, pp[p]);
         }
       }
     }
@@ -534,7 +597,7 @@ pdssm_linattn_kernel(const LaArgs a) {
         T::template pieces<NP>(v, sp);
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
-          const F xb = T::row(X + (32 * it + n32) * K::XS + 32 * t4 + 16 * k2, h);
+          const F xb = T::row(X + (xrow ^ (uint32_t)((2 * t4 + k2) * 32 * T::kHalf)) + it * 32 * K::XB);
 #pragma unroll
           for (int p = 0; p < NP; ++p) T::mma(o[it], sp[p], xb);
         }
@@ -549,25 +612,26 @@ pdssm_linattn_kernel(const LaArgs a) {
     // what the chunk's own tokens give
     F zf[C / 16];
 #pragma unroll
-    for (int js = 0; js < C / 16; ++js) zf[js] = T::col(Z, K::ZS, 16 * js, wave * 32, lane);
+    for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB>(Z, zcol, 16 * js, 0);
     if constexpr (K::kShareP) {
       __syncthreads();
 #pragma unroll
       for (int it = 0; it < IT; ++it)
 #pragma unroll
         for (int js = 0; js < C / 16; ++js) {
-          if (rev ? js < 2 * it : js >= 2 * it + 2) continue;
+          if (REV ? js < 2 * it : js >= 2 * it + 2) continue;
 #pragma unroll
           for (int p = 0; p < NP; ++p)
-            T::mma(o[it], zf[js], T::row(P + p * C * K::PS + (32 * it + n32) * K::PS + 16 * js, h));
+            T::mma(o[it], zf[js], T::row(P + p * K::kP + (prow ^ (uint32_t)(js * 32 * T::kHalf)) + it * 32 * K::PB));
         }
     } else {
 #pragma unroll
       for (int it = 0; it < IT; ++it)
 #pragma unroll
         for (int jt = 0; jt < IT; ++jt) {
-          if (rev ? jt < it : jt > it) continue;
-          const la_f16 c = la_scores<T, DKP, NW>(X, Y, e, jt, it, rev, J.s_intra, lane);
+          if (REV ? jt < it : jt > it) continue;
+          __builtin_amdgcn_sched_barrier(0);   // one tile at a time: all at once would not fit the registers
+          const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, jt, it, s_intra, lane);
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
             float v[8];
@@ -586,44 +650,57 @@ pdssm_linattn_kernel(const LaArgs a) {
       const int i = 32 * it + n32;
       float dsum = 0.0f;
       if (i < n) {
-        const int64_t oo = (int64_t)s.vb * J.o.sb + (int64_t)(hd / J.od) * J.o.sh + (int64_t)(t + i) * J.o.st;
-        const E* wp = J.dot ? la_ptr<T>(J.w, s.vb, hd / J.wd, t + i) : nullptr;
+        char* oi = ob + (ooff + 32 * it * ost);
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const int cc = c0 + 8 * r4 + 4 * h;
-          if (cc >= J.DV) continue;
-          const float v[4] = {o[it][4 * r4], o[it][4 * r4 + 1], o[it][4 * r4 + 2], o[it][4 * r4 + 3]};
-          if (J.o_f32)
-            *(float4*)((float*)J.o.p + oo + cc) = make_float4(v[0], v[1], v[2], v[3]);
+        for (int k2 = 0; k2 < 2; ++k2) {
+          if (c0 + 16 * k2 + 8 * h >= J.DV) continue;
+          float v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] = o[it][8 * k2 + r];
+          if (BWD && J.o_f32)
+            LaF32::store8((float*)oi + 16 * k2, v);
           else
-            T::store4((E*)J.o.p + oo + cc, v);
-          if (wp) {
-            float w[4];
-            T::load4(wp + cc, w);
-            dsum += (w[0] * v[0] + w[1] * v[1]) + (w[2] * v[2] + w[3] * v[3]);
+            T::store8((E*)oi + 16 * k2, v);
+          if (dot) {
+            const E* wp = (const E*)(wb + (woff + 32 * it * wst)) + 16 * k2;
+            float w[8];
+            T::load4(wp, w);
+            T::load4(wp + 4, w + 4);
+            dsum += ((w[0] * v[0] + w[1] * v[1]) + (w[2] * v[2] + w[3] * v[3])) +
+                    ((w[4] * v[4] + w[5] * v[5]) + (w[6] * v[6] + w[7] * v[7]));
           }
         }
       }
-      if (J.dot) {
+      if (dot) {
         dsum += __shfl_xor(dsum, 32, 64);
         if (h == 0) dots[wave * C + i] = dsum;
       }
     }
 
-    la_update<T, DKP, NW>(S, Y, zf, e + 3 * C, e[4 * C], lane);
+    __builtin_amdgcn_sched_barrier(0);
+    la_update<T, DKP, NW>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
     if (wave == kExpWave && q + 1 < chunks)
-      la_exponents<C>(gv, rev, J.s_inter, J.s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
+      la_exponents<C>(gv, REV, s_inter, s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
     __syncthreads();
-    if (J.dot && tid < n) {
-      float d = 0.0f;
-      for (int w = 0; w < NW; ++w) d += dots[w * C + tid];
-      J.dot[((long long)slab * a.H + hd) * a.rows + s.row0 + (t - s.t0) + tid] = d;
+    if (dot) {
+      if (tid < n) {
+        float d = 0.0f;
+        for (int w = 0; w < NW; ++w) d += dots[w * C + tid];
+        J.dot[((long long)slab * a.H + hd) * a.rows + s.row0 + at + tid] = d;
+      }
+      wb += (int64_t)dir * wst;
     }
+    if (BWD && REV && J.keep && at && at % kLaKeep == 0)
+      la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + at) * a.H + hd) * a.state, J.sm, J.sn, J.DK, J.DV,
+                            col, h);
+    ob += (int64_t)dir * ost;
+    at += dir;
+    n = REV ? C : s.len - at;
   }
 
-  if (!ends) return;
+  if (!(REV ? s.first : s.last)) return;
   if (J.s_fin) la_store_state<K::KT>(S, J.s_fin + unit * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
-  if (J.xd_out) {
+  if (BWD && !REV && J.xd_out) {
     // final state . its gradient
     la_f16 R[K::KT];
     la_load_state<K::KT>(R, J.xd_with + unit * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
@@ -649,19 +726,39 @@ pdssm_linattn_kernel(const LaArgs a) {
   }
 }
 
+template <typename T, int DKP, int NW, int NP, bool BWD>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
+pdssm_linattn_kernel(const LaArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned id = blockIdx.x;
+  if (id == 0 && threadIdx.x < 2) a.header[threadIdx.x] = 0;
+  const int jn = BWD ? id % a.njobs : 0;
+  if (BWD) id /= a.njobs;
+  const int slab = id % a.slabs;
+  id /= a.slabs;
+  const int hd = id % a.H;
+  const int sid = id / a.H;
+  const LaJob& J = a.job[jn];
+  LaSeg s;
+  if (!la_segment(a, sid, s)) return;
+  if (BWD && J.rev)
+    la_body<T, DKP, NW, NP, BWD, BWD>(a, J, s, sid, hd, slab, smem);
+  else
+    la_body<T, DKP, NW, NP, false, BWD>(a, J, s, sid, hd, slab, smem);
+}
+
 // Contribution of one segment to the state behind it (before it, for a
 // reversed job), written at that segment's place.  The last segment in the
 // job's direction has none behind it and does nothing.
 template <typename T, int DKP, int NW>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void
 pdssm_linattn_state_kernel(const LaArgs a) {
   using K = LaTile<T, DKP, NW>;
-  using E = typename T::store;
   using F = typename T::frag;
   constexpr int C = K::C;
   extern __shared__ __align__(16) unsigned char smem[];
-  E* Y = (E*)smem;
-  E* Z = (E*)(smem + K::kX);
+  unsigned char* Y = smem;
+  unsigned char* Z = smem + K::kX;
   float* exps = (float*)(smem + K::kX + K::kZ);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n32 = lane & 31;
@@ -677,48 +774,60 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   if (!la_segment(a, sid, s)) return;
   const int rev = J.rev;
   if (rev ? s.first : s.last) return;
-  const int slab0 = slab * NW * 32, c0 = slab0 + wave * 32, col = c0 + n32;
+  const int slab0 = slab * NW * 32, col = slab0 + wave * 32 + la_pi(n32);
   const int chunks = (s.len + C - 1) / C;
-  const E* yp = la_ptr<T>(J.y, s.vb, hd / J.yd, s.t0);
-  const E* zp = la_ptr<T>(J.z, s.vb, hd / J.zd, s.t0) + slab0;
-  const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh + (int64_t)s.t0 * a.g.st;
+  const int first = rev ? (chunks ? chunks - 1 : 0) * C : 0;
   typename K::X ty;
   typename K::Z tz;
-  ty.init(tid, J.DK);
-  tz.init(tid, J.DV - slab0);
+  ty.init(la_ptr<T>(J.y, s.vb, hd / J.yd, s.t0 + first), J.y.st, tid, J.DK);
+  tz.init(la_ptr<T>(J.z, s.vb, hd / J.zd, s.t0 + first) + slab0, J.z.st, tid, J.DV - slab0);
+  const int64_t dir = rev ? -C : C;
+  const int64_t dy = dir * J.y.st * K::ES, dz = dir * J.z.st * K::ES, dg = dir * a.g.st;
+  const bool whole = J.DK == DKP && J.DV - slab0 >= NW * 32;
+  const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh +
+                    (int64_t)(s.t0 + first + lane) * a.g.st;
   float gv = 0.0f;
   constexpr int kExpWave = NW - 1;
-  auto fetch = [&](int ci) {
-    const int n = s.len - ci * C;
-    ty.fetch(yp + (int64_t)(ci * C) * J.y.st, J.y.st, n);
-    tz.fetch(zp + (int64_t)(ci * C) * J.z.st, J.z.st, n);
-    if (wave == kExpWave) gv = lane < n && lane < C ? gp[(int64_t)(ci * C + lane) * a.g.st] : 0.0f;
+  auto fetch = [&](int n) {
+    ty.fetch(n);
+    tz.fetch(n);
+    if (wave == kExpWave) gv = lane < n && lane < C ? *gp : 0.0f;
   };
-  if (chunks) fetch(rev ? chunks - 1 : 0);
+  if (chunks) fetch(s.len - first);
   la_f16 S[K::KT];
 #pragma unroll
   for (int t = 0; t < K::KT; ++t) S[t] = la_f16{};
+  uint32_t ycol = T::template col_base<K::XB>(lane, 0);
+  uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
   double sum = 0.0;
   if (wave == kExpWave) sum += la_exponents<C>(gv, rev, 1.0f, J.s_upd, exps, lane);
+  int n = s.len - first, at = first;
   for (int q = 0; q < chunks; ++q) {
-    const int ci = rev ? chunks - 1 - q : q;
-    const int n = s.len - ci * C < C ? s.len - ci * C : C;
+    if (n > C) n = C;
     const float* e = exps + (q & 1) * K::kExp;
-    ty.commit(Y, tid, n);
-    tz.commit(Z, tid, n);
+    asm volatile("" : "+v"(ycol), "+v"(zcol));
+    ty.commit(Y, tid, n, whole && n == C);
+    tz.commit(Z, tid, n, whole && n == C);
     __syncthreads();
-    if (q + 1 < chunks) fetch(rev ? ci - 1 : ci + 1);
+    if (q + 1 < chunks) {
+      ty.base += dy;
+      tz.base += dz;
+      gp += dg;
+      fetch(rev ? C : s.len - at - C);
+    }
     F zf[C / 16];
 #pragma unroll
-    for (int js = 0; js < C / 16; ++js) zf[js] = T::col(Z, K::ZS, 16 * js, wave * 32, lane);
-    la_update<T, DKP, NW>(S, Y, zf, e + 3 * C, e[4 * C], lane);
+    for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB>(Z, zcol, 16 * js, 0);
+    la_update<T, DKP, NW>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
     if (wave == kExpWave && q + 1 < chunks)
       sum += la_exponents<C>(gv, rev, 1.0f, J.s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
     __syncthreads();
+    at += (int)dir;
+    n = rev ? C : s.len - at;
   }
-  const long long at = ((long long)(sid + (rev ? -1 : 1)) * a.H + hd);
-  la_store_state<K::KT>(S, J.seg_out + at * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
-  if (slab == 0 && wave == kExpWave && lane == 0) J.seg_decay[at] = __builtin_amdgcn_exp2f((float)sum);
+  const long long to = ((long long)(sid + (rev ? -1 : 1)) * a.H + hd);
+  la_store_state<K::KT>(S, J.seg_out + to * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
+  if (slab == 0 && wave == kExpWave && lane == 0) J.seg_decay[to] = __builtin_amdgcn_exp2f((float)sum);
 }
 
 }  // namespace pdscan

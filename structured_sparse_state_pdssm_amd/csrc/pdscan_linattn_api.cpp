@@ -123,6 +123,9 @@ int view_span(Span& s, LaView& v, const char* name, const pdssm_view* a, const p
     if (width > 1 && (str[i] * es) % 16)
       return set_error(PDSSM_EINVAL, "%s has a stride of %lld elements, not a multiple of 16 bytes", name,
                        (long long)str[i]);
+    if (width > 1 && i == 2 && str[i] > pdscan::kLaMaxStep)
+      return set_error(PDSSM_EUNSUPPORTED, "%s has a step stride of %lld elements, above %d", name, (long long)str[i],
+                       pdscan::kLaMaxStep);
     s.str[i] = str[i] * es;
   }
   v.sb = s.str[0] / es;
@@ -192,7 +195,8 @@ FwdWs fwd_ws(const pdssm_linattn_dims* d) {
 
 struct BwdWs {
   LaSplit split;
-  size_t table, starts, segS, segR, decS, decR, r, k, xd, part, fq, fk, total;
+  size_t table, starts, segS, segR, decS, decR, keepS, keepR, r, k, xd, part, fq, fk, total;
+  int subs;                      // pieces of a segment in the log-decay gradient
   int qslabs, vslabs;            // slabs of the passes whose outputs are dk and dv wide
 };
 
@@ -220,10 +224,18 @@ BwdWs bwd_ws(const pdssm_linattn_dims* d) {
     w.decS = put(units * 4);
     w.decR = put(units * 4);
   }
+  // states inside the segments: none where they are short
+  w.subs = pdscan::la_subs(w.split, d->L);
+  w.keepS = w.keepR = at;
+  if (w.subs > 1) {
+    const size_t kept = (size_t)(d->packed ? 1 : d->B) * (((size_t)d->L + pdscan::kLaKeep - 1) / pdscan::kLaKeep);
+    w.keepS = put(kept * d->H * d->dk * d->dv * 4);
+    w.keepR = put(kept * d->H * d->dk * d->dv * 4);
+  }
   w.r = put((size_t)w.qslabs * d->H * rows * 4);
   w.k = put((size_t)w.qslabs * d->H * rows * 4);
   w.xd = put(units * w.qslabs * 8);
-  w.part = put(d->decay_per_head ? units * 8 : 0);
+  w.part = put(d->decay_per_head ? units * w.subs * 8 : 0);
   w.fq = w.fk = at;
   if (d->Hk != d->H) {
     w.fq = put(rows * d->H * d->dk * 4);
@@ -240,7 +252,9 @@ int launched(hipError_t e) {
 }
 
 int grid_ok(const LaSplit& s, const pdssm_linattn_dims* d) {
-  if ((uint64_t)s.segs * d->H * 24 > 0x7fffffffull)
+  // three jobs of two slabs each, or one workgroup per piece of a segment
+  const uint64_t subs = (uint64_t)pdscan::la_subs(s, d->L);
+  if ((uint64_t)s.segs * d->H * (subs > 6 ? subs : 6) > 0x7fffffffull)
     return set_error(PDSSM_EUNSUPPORTED, "too many segments and heads (%d, %d)", s.segs, d->H);
   return PDSSM_OK;
 }
@@ -444,6 +458,11 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   v_job.s_intra = v_job.s_upd = d.scale;
   v_job.rev = 1;
 
+  if (w.subs > 1) {
+    q_job.keep = (float*)(ws + w.keepS);
+    v_job.keep = (float*)(ws + w.keepR);
+  }
+
   hipError_t e = hipSuccess;
   if (w.split.split) {
     if (d.packed)
@@ -494,6 +513,9 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   g.k = (const float*)(ws + w.k);
   g.sS = (const float*)(ws + w.segS);
   g.sR = (const float*)(ws + w.segR);
+  g.kS = (const float*)(ws + w.keepS);
+  g.kR = (const float*)(ws + w.keepR);
+  g.subs = w.subs;
   g.xd = q_job.xd_out;
   g.part = (double*)(ws + w.part);
   g.out = gg;

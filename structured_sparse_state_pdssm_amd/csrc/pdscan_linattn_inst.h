@@ -12,15 +12,12 @@ hipError_t la_launch_nw(const LaArgs& a, int pieces, unsigned grid, hipStream_t 
   if (pieces == 0)
     hipLaunchKernelGGL((pdssm_linattn_state_kernel<T, DKP, NW>), dim3(grid), dim3(K::NT), (unsigned)K::state_bytes(),
                        st, a);
-  else if constexpr (K::kF32)
-    hipLaunchKernelGGL((pdssm_linattn_kernel<T, DKP, NW, 1>), dim3(grid), dim3(K::NT), (unsigned)K::main_bytes(1), st,
-                       a);
   else if (pieces == 2)
-    hipLaunchKernelGGL((pdssm_linattn_kernel<T, DKP, NW, 2>), dim3(grid), dim3(K::NT), (unsigned)K::main_bytes(2), st,
-                       a);
+    hipLaunchKernelGGL((pdssm_linattn_kernel<T, DKP, NW, K::kF32 ? 1 : 2, false>), dim3(grid), dim3(K::NT),
+                       (unsigned)K::main_bytes(K::kF32 ? 1 : 2), st, a);
   else
-    hipLaunchKernelGGL((pdssm_linattn_kernel<T, DKP, NW, 3>), dim3(grid), dim3(K::NT), (unsigned)K::main_bytes(3), st,
-                       a);
+    hipLaunchKernelGGL((pdssm_linattn_kernel<T, DKP, NW, K::kF32 ? 1 : 3, true>), dim3(grid), dim3(K::NT),
+                       (unsigned)K::main_bytes(K::kF32 ? 1 : 3), st, a);
   return hipGetLastError();
 }
 

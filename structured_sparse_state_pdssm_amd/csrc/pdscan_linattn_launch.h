@@ -20,7 +20,7 @@ struct LaCarryArgs {
   long long state;
 };
 
-// pieces 0: the state pass
+// pieces 0: the state pass, 2: forward, 3: gradient (fp32 inputs are not cut)
 hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pieces, hipStream_t st);
 hipError_t launch_linattn_table(const int32_t* cu, int32_t* table, int32_t* starts, int B, int L, int seg, int segs,
                                 hipStream_t st);

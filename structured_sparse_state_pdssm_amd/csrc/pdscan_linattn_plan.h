@@ -9,6 +9,8 @@ namespace pdscan {
 
 constexpr int kLaChunk = 64;     // tokens per step of a sequence's serial axis (32 for wide fp32 rows)
 constexpr int kLaMaxD = 256;     // widest key or value row
+constexpr int kLaMaxStep = 1 << 23;   // longest step stride, elements: 64 rows stay within 31 bits of bytes
+constexpr int kLaKeep = 512;     // steps of a segment between states kept for the log-decay gradient
 constexpr int kLaHeader = 256;   // workspace header: word 1 stays zero (nothing here waits on another workgroup)
 
 // A strided tensor: element strides of the batch, head and step axes; the
@@ -30,6 +32,7 @@ struct LaJob {
   double* xd_out;              // that product [slab][segment][H]
   float* seg_out;              // (state pass) contributions [segment][H], written at the next segment
   float* seg_decay;            // (state pass) log2 decay of the segment [segment][H]
+  float* keep;                 // states inside a segment, every kLaKeep steps [row / kLaKeep][H], NULL: none
   float* dot;                  // w . o per token [slab][H][rows], NULL: none
   int sm, sn;                  // strides of a state's x-row and z-row axes
   float s_inter, s_intra, s_upd;
@@ -64,10 +67,13 @@ struct LaDecayArgs {
   const float* k;              // k . dk per token [k_slabs][H][rows]
   const float* sS;             // entering states [segment][H]
   const float* sR;             // entering adjoints [segment][H]
+  const float* kS;             // the same every kLaKeep steps inside a segment [row / kLaKeep][H]
+  const float* kR;
   const double* xd;            // final state . its gradient [xd_slabs][segment][H], NULL: zero
-  double* part;                // per (segment, head) sums (one decay per head)
+  double* part;                // sums per piece of kLaKeep steps and head (one decay per head)
   LaView out;
   int r_slabs, k_slabs, xd_slabs, per_head;
+  int subs;                    // pieces of kLaKeep steps of the longest segment
 };
 
 // Sum over the value heads that share a query or key head.
@@ -111,6 +117,8 @@ inline LaSplit la_split(int B, int L, int packed, int width) {
   s.split = true;
   return s;
 }
+
+inline int la_subs(const LaSplit& s, int L) { return ((s.seg < L ? s.seg : L) + kLaKeep - 1) / kLaKeep; }
 
 inline size_t la_align(size_t n) { return (n + 255) / 256 * 256; }
 
