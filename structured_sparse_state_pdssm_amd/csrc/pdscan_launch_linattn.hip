@@ -345,7 +345,7 @@ hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
 
 // The product kernels, by type, x-row width and waves.
 hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pieces, hipStream_t st) {
-  const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DV);
+  const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DK, a.job[0].DV, bf16);
   const long long grid = (long long)a.segs * a.H * a.slabs * a.njobs;
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;
   if (bf16)

@@ -330,7 +330,10 @@ __device__ __forceinline__ double la_exponents(float g, int rev, float s_inter, 
 template <typename T, int DKP, int NW>
 struct LaTile {
   static constexpr bool kF32 = sizeof(typename T::store) == 4;
-  static constexpr int C = (kF32 && DKP == 256) ? 32 : 64;
+  // Tokens of a chunk.  64 where four waves share the scores; else 32, which
+  // halves the registers and the LDS of a workgroup (two to three waves a SIMD
+  // instead of one: 24 heads of 64/32 at 16 x 2048 tokens 122 -> 104 us).
+  static constexpr int C = NW < 4 || (kF32 && DKP == 256) ? 32 : 64;
   static constexpr int NT = NW * 64;
   static constexpr int IT = C / 32;              // 32-token tiles of a chunk
   static constexpr int KT = DKP / 32;            // 32-row tiles of the state
@@ -353,16 +356,18 @@ struct LaTile {
   static constexpr int kWaves = kRegs <= 150 ? 2 : 1;
 };
 
-// S = decay S + sum_j y_j (w_j z_j)^T
-template <typename T, int DKP, int NW>
+// S = decay S + sum_j y_j (w_j z_j)^T (KEEP: S as it is)
+template <typename T, int DKP, int NW, bool KEEP>
 __device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const unsigned char* Y, uint32_t ycol,
                                           const typename T::frag* zf, const float* ew, float decay, int lane) {
   using K = LaTile<T, DKP, NW>;
   const int h = lane >> 5;
+  if constexpr (!KEEP) {
 #pragma unroll
-  for (int t = 0; t < K::KT; ++t)
+    for (int t = 0; t < K::KT; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) S[t][r] *= decay;
+      for (int r = 0; r < 16; ++r) S[t][r] *= decay;
+  }
 #pragma unroll
   for (int js = 0; js < K::C / 16; ++js) {
     float v[8];
@@ -678,7 +683,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     }
 
     __builtin_amdgcn_sched_barrier(0);
-    la_update<T, DKP, NW>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
+    la_update<T, DKP, NW, false>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
     if (wave == kExpWave && q + 1 < chunks)
       la_exponents<C>(gv, REV, s_inter, s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
     __syncthreads();
@@ -750,6 +755,11 @@ pdssm_linattn_kernel(const LaArgs a) {
 // Contribution of one segment to the state behind it (before it, for a
 // reversed job), written at that segment's place.  The last segment in the
 // job's direction has none behind it and does nothing.
+//
+// It goes through its chunks from that end on, each weighted with the decay f
+// of all that lie between: the state needs no rescaling, chunks behind a decay
+// that leaves nothing (f = 0) are not read, and what it reads last is what the
+// product kernel starts with, still in the caches.
 template <typename T, int DKP, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void
 pdssm_linattn_state_kernel(const LaArgs a) {
@@ -776,22 +786,30 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   if (rev ? s.first : s.last) return;
   const int slab0 = slab * NW * 32, col = slab0 + wave * 32 + la_pi(n32);
   const int chunks = (s.len + C - 1) / C;
-  const int first = rev ? (chunks ? chunks - 1 : 0) * C : 0;
+  const int first = rev ? 0 : (chunks ? chunks - 1 : 0) * C;
   typename K::X ty;
   typename K::Z tz;
   ty.init(la_ptr<T>(J.y, s.vb, hd / J.yd, s.t0 + first), J.y.st, tid, J.DK);
   tz.init(la_ptr<T>(J.z, s.vb, hd / J.zd, s.t0 + first) + slab0, J.z.st, tid, J.DV - slab0);
-  const int64_t dir = rev ? -C : C;
+  const int64_t dir = rev ? C : -C;
   const int64_t dy = dir * J.y.st * K::ES, dz = dir * J.z.st * K::ES, dg = dir * a.g.st;
   const bool whole = J.DK == DKP && J.DV - slab0 >= NW * 32;
   const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh +
-                    (int64_t)(s.t0 + first + lane) * a.g.st;
+                    (int64_t)(s.t0 + first) * a.g.st;
+  const int64_t goff = (int64_t)lane * a.g.st;
+  const float s_upd = J.s_upd;
   float gv = 0.0f;
   constexpr int kExpWave = NW - 1;
   auto fetch = [&](int n) {
     ty.fetch(n);
     tz.fetch(n);
-    if (wave == kExpWave) gv = lane < n && lane < C ? *gp : 0.0f;
+    if (wave == kExpWave) gv = lane < n && lane < C ? gp[goff] : 0.0f;
+  };
+  double sum = 0.0;      // log2 of f
+  auto exponents = [&](float* e) {
+    const float f = __builtin_amdgcn_exp2f((float)sum);
+    sum += la_exponents<C>(gv, rev, 1.0f, s_upd * f, e, lane);
+    if (lane == 0) e[4 * C + 1] = f;
   };
   if (chunks) fetch(s.len - first);
   la_f16 S[K::KT];
@@ -799,8 +817,7 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   for (int t = 0; t < K::KT; ++t) S[t] = la_f16{};
   uint32_t ycol = T::template col_base<K::XB>(lane, 0);
   uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
-  double sum = 0.0;
-  if (wave == kExpWave) sum += la_exponents<C>(gv, rev, 1.0f, J.s_upd, exps, lane);
+  if (wave == kExpWave) exponents(exps);
   int n = s.len - first, at = first;
   for (int q = 0; q < chunks; ++q) {
     if (n > C) n = C;
@@ -809,21 +826,21 @@ pdssm_linattn_state_kernel(const LaArgs a) {
     ty.commit(Y, tid, n, whole && n == C);
     tz.commit(Z, tid, n, whole && n == C);
     __syncthreads();
+    if (e[4 * C + 1] == 0.0f) break;
     if (q + 1 < chunks) {
       ty.base += dy;
       tz.base += dz;
       gp += dg;
-      fetch(rev ? C : s.len - at - C);
+      fetch(rev ? s.len - at - C : C);
     }
     F zf[C / 16];
 #pragma unroll
     for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB>(Z, zcol, 16 * js, 0);
-    la_update<T, DKP, NW>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
-    if (wave == kExpWave && q + 1 < chunks)
-      sum += la_exponents<C>(gv, rev, 1.0f, J.s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
+    la_update<T, DKP, NW, true>(S, Y, ycol, zf, e + 3 * C, 1.0f, lane);
+    if (wave == kExpWave && q + 1 < chunks) exponents(exps + ((q + 1) & 1) * K::kExp);
     __syncthreads();
     at += (int)dir;
-    n = rev ? C : s.len - at;
+    n = rev ? s.len - at : C;
   }
   const long long to = ((long long)(sid + (rev ? -1 : 1)) * a.H + hd);
   la_store_state<K::KT>(S, J.seg_out + to * a.state, J.sm, J.sn, J.DK, J.DV, col, h);

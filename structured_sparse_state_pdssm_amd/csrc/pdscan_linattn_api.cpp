@@ -15,6 +15,8 @@
 
 namespace {
 
+constexpr int kCus = 256;        // compute units of the card
+
 using pdscan::LaArgs;
 using pdscan::LaJob;
 using pdscan::LaSplit;
@@ -172,7 +174,9 @@ struct FwdWs {
 
 FwdWs fwd_ws(const pdssm_linattn_dims* d) {
   FwdWs w;
-  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * pdscan::la_slabs(d->dv));
+  const int bf16 = d->in_dtype == PDSSM_BF16;
+  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * pdscan::la_slabs(d->dk, d->dv, bf16),
+                             kCus * pdscan::la_resident(d->dk, d->dv, bf16));
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -197,14 +201,20 @@ struct BwdWs {
   LaSplit split;
   size_t table, starts, segS, segR, decS, decR, keepS, keepR, r, k, xd, part, fq, fk, total;
   int subs;                      // pieces of a segment in the log-decay gradient
+  bool one;                      // all three jobs have one shape
   int qslabs, vslabs;            // slabs of the passes whose outputs are dk and dv wide
 };
 
 BwdWs bwd_ws(const pdssm_linattn_dims* d) {
   BwdWs w;
-  w.qslabs = pdscan::la_slabs(d->dk);
-  w.vslabs = pdscan::la_slabs(d->dv);
-  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * (2 * w.qslabs + w.vslabs));
+  const int bf16 = d->in_dtype == PDSSM_BF16;
+  w.qslabs = pdscan::la_slabs(d->dv, d->dk, bf16);
+  w.vslabs = pdscan::la_slabs(d->dk, d->dv, bf16);
+  w.one = pdscan::la_pad(d->dk) == pdscan::la_pad(d->dv) && w.qslabs == w.vslabs &&
+          pdscan::la_waves(d->dk, d->dv, bf16) == pdscan::la_waves(d->dv, d->dk, bf16);
+  // the launch that holds the fewest workgroups decides: three jobs in one, or two and one
+  const int vroom = kCus * pdscan::la_resident(d->dk, d->dv, bf16);
+  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * (w.one ? 3 : 1) * w.vslabs, vroom);
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -332,7 +342,7 @@ int pdssm_linattn_fwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   unsigned char* ws = (unsigned char*)workspace;
   const int bf16 = d.in_dtype == PDSSM_BF16, ratio = d.H / d.Hk;
   LaArgs a = common(dims, vg, cu_seqlens, w.split, ws, w.table);
-  a.slabs = pdscan::la_slabs(d.dv);
+  a.slabs = pdscan::la_slabs(d.dk, d.dv, bf16);
   a.njobs = 1;
   LaJob& J = a.job[0];
   J.x = vq; J.y = vk; J.z = vv; J.o = vo;
@@ -494,14 +504,12 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   m.job[0] = q_job;
   m.job[1] = k_job;
   m.njobs = 2;
-  const bool one = pdscan::la_pad(d.dk) == pdscan::la_pad(d.dv) && pdscan::la_waves(d.dk) == pdscan::la_waves(d.dv) &&
-                   w.qslabs == w.vslabs;
-  if (one) {   // one launch: the three jobs of a segment read the same rows
+  if (w.one) {   // one launch: the three jobs of a segment read the same rows
     m.job[2] = v_job;
     m.njobs = 3;
   }
   if (e == hipSuccess) e = pdscan::launch_linattn_form(m, bf16, 3, st);
-  if (!one) {
+  if (!w.one) {
     m.slabs = w.vslabs;
     m.job[0] = v_job;
     m.njobs = 1;

@@ -23,9 +23,11 @@ hipError_t la_launch_nw(const LaArgs& a, int pieces, unsigned grid, hipStream_t 
 
 template <typename T, int DKP>
 hipError_t la_launch(const LaArgs& a, int nw, int pieces, unsigned grid, hipStream_t st) {
-  return nw == 1   ? la_launch_nw<T, DKP, 1>(a, pieces, grid, st)
-         : nw == 2 ? la_launch_nw<T, DKP, 2>(a, pieces, grid, st)
-                   : la_launch_nw<T, DKP, 4>(a, pieces, grid, st);
+  if constexpr (DKP < 256)
+    if (nw == 1) return la_launch_nw<T, DKP, 1>(a, pieces, grid, st);
+  if constexpr (DKP < 256 || !LaTile<T, DKP, 4>::kF32)
+    if (nw == 2) return la_launch_nw<T, DKP, 2>(a, pieces, grid, st);
+  return la_launch_nw<T, DKP, 4>(a, pieces, grid, st);
 }
 
 }  // namespace pdscan

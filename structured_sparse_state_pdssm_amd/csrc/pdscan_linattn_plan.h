@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 
 namespace pdscan {
 
@@ -86,35 +87,53 @@ struct LaFoldArgs {
 };
 
 inline int la_pad(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-inline int la_waves(int d) { return d <= 32 ? 1 : d <= 64 ? 2 : 4; }          // 32 columns each
-inline int la_slabs(int d) { return (d + 32 * la_waves(d) - 1) / (32 * la_waves(d)); }
+// Waves of a workgroup, 32 columns each, for x rows of DK and z rows of DV
+// elements.  Rows of more than 128 elements take more waves than columns need
+// where fewer would not hold the tiles under way in their registers.
+inline int la_waves(int DK, int DV, int bf16) {
+  const int w = DV <= 32 ? 1 : DV <= 64 ? 2 : 4;
+  return DK <= 128 ? w : bf16 ? (w < 2 ? 2 : w) : 4;
+}
+inline int la_slabs(int DK, int DV, int bf16) {
+  const int w = 32 * la_waves(DK, DV, bf16);
+  return (DV + w - 1) / w;
+}
+// Workgroups of the product kernel that a compute unit holds, by LDS (160 KiB)
+// and by registers (two waves a SIMD; one with wide rows).
+inline int la_resident(int DK, int DV, int bf16) {
+  const int es = bf16 ? 2 : 4, nw = la_waves(DK, DV, bf16), d = la_pad(DK);
+  const int C = nw < 4 || (!bf16 && d == 256) ? 32 : 64;
+  const int lds = C * es * (2 * d + 32 * nw) + (nw == 4 ? (bf16 ? 2 : 1) * C * C * es : 0) + 4 * (8 * C + 8 + nw * C);
+  const int waves = d == 256 || (!bf16 && d == 128) ? 4 : 8;
+  const int n = 163840 / lds < waves / nw ? 163840 / lds : waves / nw;
+  return n < 1 ? 1 : n;
+}
 
 struct LaSplit {
   int seg, nseg, segs;         // steps per segment, segments per sequence (not packed), bound in all
   bool split;
 };
 
-// Steps per segment of a pass with `width` workgroups per segment.
-inline LaSplit la_split(int B, int L, int packed, int width) {
+// Cuts the step axis into segments so that a launch of `width` workgroups per
+// segment fills the card once (`room` workgroups).  Whole sequences where
+// they do that, and up to 256 steps: the three launches more cost what the
+// shorter chains save.  Sequences of different lengths take 7/4 of it, so that
+// no long one is left alone at the end.
+//   65536 steps, 16 heads, 128/128 bf16: 32 segments of 2048 434 us, of 1024 459, of 4096 506, uncut over 5000
+//   16 x 2048 steps, 24 heads, 64/32 bf16: 4 segments of 512 104 us, 8 of 256 114, uncut 131
+//   4 x 4096 steps, 8 heads, 16/64 fp32: 128 steps 53 us, 64 63, 256 71
+//   23 sequences in 12001 rows, 24 heads, 128/64 bf16: 320 steps 109 us, 640 117, 128 128
+inline LaSplit la_split(int B, int L, int packed, int width, int room) {
   LaSplit s;
-  const long long rows = packed ? (long long)L : (long long)B * L;
-  const long long want = 1024;
-  long long seg = (rows * width + want - 1) / want;
-  if (seg < 256) seg = 256;
-  seg = (seg + kLaChunk - 1) / kLaChunk * kLaChunk;
-  if (seg >= L || (!packed && (long long)B * width >= want / 2)) {
-    s.seg = (int)((L + (long long)kLaChunk - 1) / kLaChunk * kLaChunk > 0x7fffffc0ll ? 0x7fffffc0ll
-                  : (L + (long long)kLaChunk - 1) / kLaChunk * kLaChunk);
-    s.nseg = 1;
-    s.segs = B;
-    s.split = false;
-    return s;
-  }
-  s.seg = (int)seg;
-  s.nseg = (int)((L + seg - 1) / seg);
-  const long long n = packed ? (long long)(L / seg) + B : (long long)B * s.nseg;
-  s.segs = n > 0x7fffffffll ? 0x7fffffff : (int)n;
-  s.split = true;
+  long long n = (long long)room / (packed ? width : (long long)B * width);   // segments of a sequence
+  if (packed) n = n * 7 / 4;
+  if (n > L / kLaChunk) n = L / kLaChunk;
+  s.split = n > 1 && L > 256;
+  const long long each = s.split ? ((long long)L + n - 1) / n : L;
+  s.seg = (int)((each + kLaChunk - 1) / kLaChunk * kLaChunk);
+  s.nseg = s.split ? (L + s.seg - 1) / s.seg : 1;
+  const long long segs = !packed ? (long long)B * s.nseg : s.split ? (long long)(L / s.seg) + B : B;
+  s.segs = segs > 0x7fffffffll ? 0x7fffffff : (int)segs;
   return s;
 }
 
