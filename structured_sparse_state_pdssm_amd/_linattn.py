@@ -18,12 +18,37 @@ outputs are made here they hold whatever the memory held.
 """
 
 import ctypes
+import struct
 
 import torch
 
-from ._lib import PDSSM_BF16, PDSSM_F32, PDSSM_OK, PdssmError, PdssmLinattnDims, PdssmView, lib
+from ._lib import PDSSM_BF16, PDSSM_F32, PDSSM_OK, PdssmError, PdssmLinattnDims, lib
 
 _FLOATS = {torch.float32: PDSSM_F32, torch.bfloat16: PDSSM_BF16}
+_f32, _i32 = torch.float32, torch.int32
+_WHOLE, _ROWS, _ANY = range(3)   # layouts: contiguous, contiguous last axis, any strides
+
+# A call is a few microseconds of host work, which is all of a small step's
+# time: arguments go as packed bytes (pdssm_linattn_dims, pdssm_view) through
+# functions of their own, and the checks run as one expression whose failure
+# is explained by the slower ones.
+_pack_dims = struct.Struct("9if").pack
+_pack_view = struct.Struct("Pqqq").pack
+
+
+def _fn(name, types):
+    f = lib[name]
+    f.argtypes = [{"s": ctypes.c_char_p, "p": ctypes.c_void_p, "n": ctypes.c_size_t, "i": ctypes.c_int32}[c]
+                  for c in types]
+    f.restype = ctypes.c_int
+    return f
+
+
+_fwd = _fn("pdssm_linattn_fwd", "sssssppsppnp")
+_bwd = _fn("pdssm_linattn_bwd", "sssssppspsssspp" + "np")
+_fwd_bytes = _fn("pdssm_linattn_workspace_bytes", "sp")
+_bwd_bytes = _fn("pdssm_linattn_bwd_workspace_bytes", "sp")
+_step = _fn("pdssm_linattn_step", "ssssspipsp")
 
 
 def _check(rc):
@@ -31,11 +56,10 @@ def _check(rc):
         raise PdssmError(rc, lib.pdssm_last_error().decode())
 
 
-def _tensors(specs):
-    """Type, dtype and shape of every argument first, then where it lies: the
-    C ABI cannot see allocation sizes.  specs: (tensor or None, name, shape,
-    dtype, layout), layout "whole" (contiguous), "rows" (contiguous last axis)
-    or "any".  Returns the device."""
+def _explain(specs):
+    """Raise what is wrong with the arguments: type, dtype and shape of every
+    one first, then where it lies (the C ABI cannot see allocation sizes).
+    specs: (tensor or None, name, shape, dtype, layout)."""
     for t, name, shape, dtype, _ in specs:
         if t is None:
             continue
@@ -53,22 +77,37 @@ def _tensors(specs):
             raise ValueError(f"{name} must be a device tensor (got {t.device})")
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, {specs[0][1]} on {dev}")
-        if layout == "whole":
+        if layout is _WHOLE:
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        elif layout == "rows" and shape[-1] > 1 and t.stride(-1) != 1:
+        elif layout is _ROWS and t.stride(-1) != 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
-    return dev
 
 
-def _view(t, heads=1, step=2):
-    """A tensor [B,heads,L,..] (or [B,heads,..] with step=None) as strides."""
+def _verify(specs, dev):
+    if dev < 0:
+        return _explain(specs)
+    for t, _, shape, dtype, layout in specs:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                                  and t.get_device() == dev
+                                  and (layout is _ANY or (t.stride(-1) == 1 if layout is _ROWS else t.is_contiguous()))):
+            return _explain(specs)
+
+
+def _view(t):
+    """A tensor [B,heads,L,..] as pointer and strides."""
     s = t.stride()
-    return PdssmView(t.data_ptr(), s[0], s[heads], s[step] if step is not None else 0)
+    return _pack_view(t.data_ptr(), s[0], s[1], s[2])
 
 
-def _decay_view(t, per_head, step=2):
-    return PdssmView(t.data_ptr(), 0, 1, 0) if per_head else _view(t, 1, step)
+def _view1(t):
+    """A tensor [B,heads,..] of single tokens."""
+    s = t.stride()
+    return _pack_view(t.data_ptr(), s[0], s[1], 0)
+
+
+def _decay_view(t, per_head):
+    return _pack_view(t.data_ptr(), 0, 1, 0) if per_head else _view(t)
 
 
 def _ptr(t):
@@ -83,7 +122,7 @@ def _like(t, shape, dev):
     return torch.empty((B, H, L, d), dtype=t.dtype, device=dev)
 
 
-def _dims(q, k, v, log_decay, scale, cu_seqlens, names=("[B,Hk,L,dk]", "[B,H,L,dv]"), rank=4):
+def _shapes(q, k, v, log_decay, rank, names):
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (log_decay, "log_decay")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
@@ -93,38 +132,38 @@ def _dims(q, k, v, log_decay, scale, cu_seqlens, names=("[B,Hk,L,dk]", "[B,H,L,d
         raise ValueError(f"v must be {names[1]}")
     if v.dtype not in _FLOATS:
         raise TypeError(f"v must be float32 or bfloat16 (got {v.dtype})")
-    B, Hk = q.shape[:2]
-    H, dv = v.shape[1], v.shape[-1]
-    dk = q.shape[-1]
-    L = q.shape[2] if rank == 4 else 1
+
+
+def _dims(q, k, v, log_decay, scale, cu_seqlens):
+    """(fields of pdssm_linattn_dims, rows of the batch axis)."""
+    _shapes(q, k, v, log_decay, 4, ("[B,Hk,L,dk]", "[B,H,L,dv]"))
+    rows, Hk, L, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    B = rows
     packed = cu_seqlens is not None
     if packed:
         if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
             raise ValueError("cu_seqlens must be a tensor [S+1]")
-        if B != 1:
-            raise ValueError(f"with cu_seqlens the batch axis has one element (got {B})")
+        if rows != 1:
+            raise ValueError(f"with cu_seqlens the batch axis has one element (got {rows})")
         B = cu_seqlens.shape[0] - 1
-    per_head = log_decay.dim() == 1
     if scale is None:
         scale = dk ** -0.5
-    return PdssmLinattnDims(B, H, Hk, L, dk, dv, _FLOATS[v.dtype], packed, per_head, scale)
+    return (B, H, Hk, L, dk, dv, _FLOATS[v.dtype], packed, log_decay.dim() == 1, scale), rows
 
 
-class _on:
-    """The tensors' device as the current one for the length of a call."""
+def _call(index, fn):
+    """fn(stream) with the tensors' device as the current one."""
+    if torch._C._cuda_getDevice() == index:
+        return fn(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return fn(torch._C._cuda_getCurrentRawStream(index))
 
-    def __init__(self, dev):
-        self.to = dev.index if dev.index is not None else torch.cuda.current_device()
 
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.to:
-            torch.cuda.set_device(self.to)
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *_):
-        if self.back != self.to:
-            torch.cuda.set_device(self.back)
+def _bytes(fn, packed):
+    n = ctypes.c_size_t(0)
+    _check(fn(packed, ctypes.addressof(n)))
+    return n.value
 
 
 def linattn_workspace_bytes(dims):
@@ -148,10 +187,9 @@ def linattn_dims(B, H, L, dk, dv, Hk=None, bf16=False, packed=False, decay_per_h
 def _workspace(nbytes, dev, workspace):
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _tensors([(workspace, "workspace", workspace.shape if isinstance(workspace, torch.Tensor) else None, torch.uint8,
-               "whole")])
-    if workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, q on {dev}")
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
+        raise TypeError("workspace must be a torch.uint8 tensor")
+    _verify([(workspace, "workspace", workspace.shape, torch.uint8, _WHOLE)], dev.index)
     if workspace.numel() < nbytes:
         raise ValueError(f"workspace holds {workspace.numel()} bytes, {nbytes} needed")
     return workspace
@@ -160,26 +198,27 @@ def _workspace(nbytes, dev, workspace):
 def pdssm_linattn_fwd(q, k, v, log_decay, h0=None, scale=None, cu_seqlens=None, workspace=None, out=None):
     """Prompts.  Returns (o [B,H,L,dv], h_L [B,H,dk,dv]).  ``scale`` is
     dk ** -0.5 when not given; ``out`` may hold "o" and "h_L" to write to."""
-    d = _dims(q, k, v, log_decay, scale, cu_seqlens)
-    rows = v.shape[0]
-    H, L, dk, dv, dt = d.H, d.L, d.dk, d.dv, v.dtype
-    kshape, vshape, sshape = (rows, d.Hk, L, dk), (rows, H, L, dv), (d.B, H, dk, dv)
+    d, rows = _dims(q, k, v, log_decay, scale, cu_seqlens)
+    B, H, Hk, L, dk, dv, _, _, per_head, _ = d
+    dt, index = v.dtype, q.get_device()
+    kshape, vshape, sshape = (rows, Hk, L, dk), (rows, H, L, dv), (B, H, dk, dv)
+    o = hL = None
+    if out:
+        o, hL = out.get("o"), out.get("h_L")
+    _verify([(q, "q", kshape, dt, _ROWS), (k, "k", kshape, dt, _ROWS), (v, "v", vshape, dt, _ROWS),
+             (log_decay, "log_decay", (H,) if per_head else (rows, H, L), _f32, _WHOLE if per_head else _ANY),
+             (h0, "h0", sshape, _f32, _WHOLE), (cu_seqlens, "cu_seqlens", (B + 1,), _i32, _WHOLE),
+             (o, "o", vshape, dt, _ROWS), (hL, "h_L", sshape, _f32, _WHOLE)], index)
     dev = q.device
-    res = out or {}
-    o, hL = res.get("o"), res.get("h_L")
-    f32 = torch.float32
-    _tensors([(q, "q", kshape, dt, "rows"), (k, "k", kshape, dt, "rows"), (v, "v", vshape, dt, "rows"),
-              (log_decay, "log_decay", (H,) if d.decay_per_head else (rows, H, L), f32, "whole" if d.decay_per_head else "any"),
-              (h0, "h0", sshape, f32, "whole"), (cu_seqlens, "cu_seqlens", (d.B + 1,), torch.int32, "whole"),
-              (o, "o", vshape, dt, "rows"), (hL, "h_L", sshape, f32, "whole")])
-    with _on(dev) as stream:
-        if o is None:
-            o = _like(v, vshape, dev)
-        if hL is None:
-            hL = torch.empty(sshape, dtype=f32, device=dev)
-        ws = _workspace(linattn_workspace_bytes(d), dev, workspace)
-        _check(lib.pdssm_linattn_fwd(d, _view(q), _view(k), _view(v), _decay_view(log_decay, d.decay_per_head),
-                                     _ptr(cu_seqlens), _ptr(h0), _view(o), _ptr(hL), _ptr(ws), ws.numel(), stream))
+    dims = _pack_dims(*d)
+    if o is None:
+        o = _like(v, vshape, dev)
+    if hL is None:
+        hL = torch.empty(sshape, dtype=_f32, device=dev)
+    ws = _workspace(_bytes(_fwd_bytes, dims), dev, workspace)
+    _check(_call(index, lambda stream: _fwd(
+        dims, _view(q), _view(k), _view(v), _decay_view(log_decay, per_head), _ptr(cu_seqlens), _ptr(h0), _view(o),
+        hL.data_ptr(), ws.data_ptr(), ws.numel(), stream)))
     return o, hL
 
 
@@ -188,40 +227,39 @@ def pdssm_linattn_bwd(q, k, v, log_decay, g_o, h0=None, g_hL=None, scale=None, c
     """Gradient of pdssm_linattn_fwd, given the gradients of o and (optional)
     h_L.  Returns dict(g_q, g_k, g_v, g_log_decay[, g_h0]), shaped and typed
     as their inputs; g_h0 is dLoss/dh0 also where h0 is left out (zero)."""
-    d = _dims(q, k, v, log_decay, scale, cu_seqlens)
-    rows = v.shape[0]
-    H, L, dk, dv, dt = d.H, d.L, d.dk, d.dv, v.dtype
-    kshape, vshape, sshape = (rows, d.Hk, L, dk), (rows, H, L, dv), (d.B, H, dk, dv)
-    gshape = (H,) if d.decay_per_head else (rows, H, L)
-    per_head = bool(d.decay_per_head)
-    dev = q.device
-    f32 = torch.float32
+    d, rows = _dims(q, k, v, log_decay, scale, cu_seqlens)
+    B, H, Hk, L, dk, dv, _, _, per_head, _ = d
+    dt, index = v.dtype, q.get_device()
+    kshape, vshape, sshape = (rows, Hk, L, dk), (rows, H, L, dv), (B, H, dk, dv)
+    gshape = (H,) if per_head else (rows, H, L)
+    glayout = _WHOLE if per_head else _ANY
     given = out or {}
     res = {n: given.get(n) for n in ("g_q", "g_k", "g_v", "g_log_decay")}
     if want_h0:
         res["g_h0"] = given.get("g_h0")
-    _tensors([(q, "q", kshape, dt, "rows"), (k, "k", kshape, dt, "rows"), (v, "v", vshape, dt, "rows"),
-              (log_decay, "log_decay", gshape, f32, "whole" if per_head else "any"), (g_o, "g_o", vshape, dt, "rows"),
-              (h0, "h0", sshape, f32, "whole"), (g_hL, "g_hL", sshape, f32, "whole"),
-              (cu_seqlens, "cu_seqlens", (d.B + 1,), torch.int32, "whole"), (res["g_q"], "g_q", kshape, dt, "rows"),
-              (res["g_k"], "g_k", kshape, dt, "rows"), (res["g_v"], "g_v", vshape, dt, "rows"),
-              (res["g_log_decay"], "g_log_decay", gshape, f32, "whole" if per_head else "any"), (res.get("g_h0"), "g_h0", sshape, f32, "whole")])
-    with _on(dev) as stream:
-        for n, t, shape in (("g_q", q, kshape), ("g_k", k, kshape), ("g_v", v, vshape)):
-            if res[n] is None:
-                res[n] = _like(t, shape, dev)
-        if res["g_log_decay"] is None:
-            g = log_decay
-            res["g_log_decay"] = (torch.empty((rows, L, H), dtype=f32, device=dev).transpose(1, 2)
-                                  if not per_head and g.stride(2) > g.stride(1)
-                                  else torch.empty(gshape, dtype=f32, device=dev))
-        if want_h0 and res["g_h0"] is None:
-            res["g_h0"] = torch.empty(sshape, dtype=f32, device=dev)
-        ws = _workspace(linattn_bwd_workspace_bytes(d), dev, workspace)
-        _check(lib.pdssm_linattn_bwd(d, _view(q), _view(k), _view(v), _decay_view(log_decay, per_head),
-                                     _ptr(cu_seqlens), _ptr(h0), _view(g_o), _ptr(g_hL), _view(res["g_q"]),
-                                     _view(res["g_k"]), _view(res["g_v"]), _decay_view(res["g_log_decay"], per_head),
-                                     _ptr(res.get("g_h0")), _ptr(ws), ws.numel(), stream))
+    _verify([(q, "q", kshape, dt, _ROWS), (k, "k", kshape, dt, _ROWS), (v, "v", vshape, dt, _ROWS),
+             (log_decay, "log_decay", gshape, _f32, glayout), (g_o, "g_o", vshape, dt, _ROWS),
+             (h0, "h0", sshape, _f32, _WHOLE), (g_hL, "g_hL", sshape, _f32, _WHOLE),
+             (cu_seqlens, "cu_seqlens", (B + 1,), _i32, _WHOLE), (res["g_q"], "g_q", kshape, dt, _ROWS),
+             (res["g_k"], "g_k", kshape, dt, _ROWS), (res["g_v"], "g_v", vshape, dt, _ROWS),
+             (res["g_log_decay"], "g_log_decay", gshape, _f32, glayout),
+             (res.get("g_h0"), "g_h0", sshape, _f32, _WHOLE)], index)
+    dev = q.device
+    dims = _pack_dims(*d)
+    for n, t, shape in (("g_q", q, kshape), ("g_k", k, kshape), ("g_v", v, vshape)):
+        if res[n] is None:
+            res[n] = _like(t, shape, dev)
+    if res["g_log_decay"] is None:
+        res["g_log_decay"] = (torch.empty((rows, L, H), dtype=_f32, device=dev).transpose(1, 2)
+                              if not per_head and log_decay.stride(2) > log_decay.stride(1)
+                              else torch.empty(gshape, dtype=_f32, device=dev))
+    if want_h0 and res["g_h0"] is None:
+        res["g_h0"] = torch.empty(sshape, dtype=_f32, device=dev)
+    ws = _workspace(_bytes(_bwd_bytes, dims), dev, workspace)
+    _check(_call(index, lambda stream: _bwd(
+        dims, _view(q), _view(k), _view(v), _decay_view(log_decay, per_head), _ptr(cu_seqlens), _ptr(h0), _view(g_o),
+        _ptr(g_hL), _view(res["g_q"]), _view(res["g_k"]), _view(res["g_v"]),
+        _decay_view(res["g_log_decay"], per_head), _ptr(res.get("g_h0")), ws.data_ptr(), ws.numel(), stream)))
     return res
 
 
@@ -232,21 +270,24 @@ def pdssm_linattn_step(q, k, v, log_decay, state, state_idx=None, scale=None, ou
     row (o zero, no state touched); one past the pool, or named by an earlier
     row too, gives NaN in o and touches nothing.  Returns o [B,H,dv]
     (``out``: a tensor to write it to)."""
-    d = _dims(q, k, v, log_decay, scale, None, ("[B,Hk,dk]", "[B,H,dv]"), 3)
-    B, H, dk, dv, dt = d.B, d.H, d.dk, d.dv, v.dtype
+    _shapes(q, k, v, log_decay, 3, ("[B,Hk,dk]", "[B,H,dv]"))
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a tensor [n_slots,H,dk,dv]")
+    kshape, vshape = q.shape, v.shape
+    B, Hk, dk = kshape
+    H, dv = vshape[1], vshape[2]
     slots = state.shape[0]
-    per_head = bool(d.decay_per_head)
-    f32 = torch.float32
-    dev = _tensors([(q, "q", (B, d.Hk, dk), dt, "rows"), (k, "k", (B, d.Hk, dk), dt, "rows"), (v, "v", (B, H, dv), dt, "rows"),
-                    (log_decay, "log_decay", (H,) if per_head else (B, H), f32, "whole" if per_head else "any"),
-                    (state, "state", (slots, H, dk, dv), f32, "whole"),
-                    (state_idx, "state_idx", (B,), torch.int32, "whole"), (out, "out", (B, H, dv), dt, "rows")])
-    with _on(dev) as stream:
-        if out is None:
-            out = torch.empty((B, H, dv), dtype=dt, device=dev)
-        _check(lib.pdssm_linattn_step(d, _view(q, 1, None), _view(k, 1, None), _view(v, 1, None),
-                                      _decay_view(log_decay, per_head, None), _ptr(state_idx), slots, _ptr(state),
-                                      _view(out, 1, None), stream))
+    per_head = log_decay.dim() == 1
+    dt, index = v.dtype, q.get_device()
+    _verify([(q, "q", (B, Hk, dk), dt, _ROWS), (k, "k", kshape, dt, _ROWS), (v, "v", (B, H, dv), dt, _ROWS),
+             (log_decay, "log_decay", (H,) if per_head else (B, H), _f32, _WHOLE if per_head else _ANY),
+             (state, "state", (slots, H, dk, dv), _f32, _WHOLE), (state_idx, "state_idx", (B,), _i32, _WHOLE),
+             (out, "out", vshape, dt, _ROWS)], index)
+    if out is None:
+        out = torch.empty(vshape, dtype=dt, device=q.device)
+    dims = _pack_dims(B, H, Hk, 1, dk, dv, _FLOATS[dt], 0, per_head, dk ** -0.5 if scale is None else scale)
+    _check(_call(index, lambda stream: _step(
+        dims, _view1(q), _view1(k), _view1(v),
+        _pack_view(log_decay.data_ptr(), 0, 1, 0) if per_head else _view1(log_decay), _ptr(state_idx), slots,
+        state.data_ptr(), _view1(out), stream)))
     return out

@@ -81,6 +81,14 @@ struct LaBf16 {
     const uint32_t w = f.u[e >> 1];
     return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
   }
+  static __device__ __forceinline__ void unpack(const uint4* p, float* v) {   // eight elements
+    const uint32_t u[4] = {p->x, p->y, p->z, p->w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(u[e] << 16);
+      v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+  }
   // eight elements of a row at byte address a
   static __device__ __forceinline__ frag row(const unsigned char* a) {
     frag f;
@@ -157,6 +165,15 @@ struct LaF32 {
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.f[e], b.f[e], c, 0, 0, 0);
   }
   static __device__ __forceinline__ float get(const frag& f, int e) { return f.f[e]; }
+  static __device__ __forceinline__ void unpack(const uint4* p, float* v) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      v[4 * u] = __uint_as_float(p[u].x);
+      v[4 * u + 1] = __uint_as_float(p[u].y);
+      v[4 * u + 2] = __uint_as_float(p[u].z);
+      v[4 * u + 3] = __uint_as_float(p[u].w);
+    }
+  }
   static __device__ __forceinline__ frag row(const unsigned char* a) {
     frag f;
     *(float4*)&f.f[0] = *(const float4*)a;
@@ -228,6 +245,26 @@ __device__ __forceinline__ bool la_segment(const LaArgs& a, int sid, LaSeg& s) {
   return true;
 }
 
+struct LaUnit {
+  int job, slab, hd, sid;
+};
+
+// What workgroup `id` works on: `dies` sets of workgroups that share rows are
+// interleaved, the members of a set one after the other on its die.
+__device__ __forceinline__ bool la_unit(const LaArgs& a, unsigned id, LaUnit& u) {
+  const unsigned die = id % a.dies;
+  id /= a.dies;
+  u.job = id % a.njobs;
+  id /= a.njobs;
+  u.slab = id % a.slabs;
+  id /= a.slabs;
+  const unsigned member = id % a.ratio;
+  const unsigned set = id / a.ratio * a.dies + die, groups = a.H / a.ratio;
+  u.hd = set % groups * a.ratio + member;
+  u.sid = set / groups;
+  return u.sid < a.segs;
+}
+
 // Place of the state kept at step t of a view's axis (every kLaKeep steps of a segment).
 __device__ __forceinline__ long long la_keep_slot(const LaArgs& a, const LaSeg& s, int t) {
   return (long long)s.vb * ((a.L + kLaKeep - 1) / kLaKeep) + t / kLaKeep;
@@ -296,13 +333,28 @@ __device__ __forceinline__ double la_scan_step(double x) {
   return x + __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
-// Exponents of one chunk, by one wave (lane = token, g = its log decay, 0
-// behind the last): G as two floats in units of log 2, the output scale and
-// the update weight of every token, and the chunk's whole decay behind them.
+// 2^x, x in 64 bits: whole part and rest apart, so that large |x| costs no digits.
+__device__ __forceinline__ float la_exp2(double x) {
+  const double n = __builtin_rint(x);
+  const float f = __builtin_amdgcn_exp2f((float)(x - n));
+  return __builtin_amdgcn_ldexpf(f, x < -1000.0 ? -1000 : (int)n);
+}
+
+// What a chunk's tokens are weighted with, by one wave (lane = token, g = its
+// log decay, 0 behind the last).  With A the log2 of the decay between a token
+// and the entering state (G, or G_C - G backwards):
+//   e[2C + i] = 2^A s_out, the output's scale
+//   e[3C + j] the update's weight
+//   e[4C]     the chunk's whole decay
+//   e[4C + 2] 1 where no |A| is above kLaNear: then the weight of a pair is
+//             2^{A_i} 2^{-A_j}, its first factor common to the whole output,
+//             and e[j] = 2^{-A_j} s_ratio; else 0, and e[i], e[C + i] hold G as
+//             two floats for the difference of every pair.
 // A log decay under -1e4 (minus infinity: the state starts anew) counts as
 // -1e4, whose exponential is zero all the same.  Returns the sum of log2.
 template <int C>
-__device__ __forceinline__ double la_exponents(float g, int rev, float s_inter, float s_upd, float* e, int lane) {
+__device__ __forceinline__ double la_exponents(float g, int rev, float s_out, float s_ratio, float s_upd, float* e,
+                                               int lane) {
   if (g < -1e4f) g = -1e4f;
   double G = (double)g * 1.4426950408889634074;
   G = la_scan_step<0x111, 0xf>(G);   // row_shr:1
@@ -315,15 +367,23 @@ __device__ __forceinline__ double la_exponents(float g, int rev, float s_inter, 
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
   const double tot = __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+  const double A = rev ? tot - G : G, B = rev ? G : tot - G;
+  const bool near = __all(A <= kLaNear && A >= -kLaNear);
   if (lane < C) {
-    const float gh = (float)G;
-    e[lane] = gh;
-    e[C + lane] = (float)(G - (double)gh);
-    const float from = __builtin_amdgcn_exp2f((float)G), to = __builtin_amdgcn_exp2f((float)(tot - G));
-    e[2 * C + lane] = (rev ? to : from) * s_inter;
-    e[3 * C + lane] = (rev ? from : to) * s_upd;
+    if (near) {
+      e[lane] = la_exp2(-A) * s_ratio;
+    } else {
+      const float gh = (float)G;
+      e[lane] = gh;
+      e[C + lane] = (float)(G - (double)gh);
+    }
+    e[2 * C + lane] = la_exp2(A) * s_out;
+    e[3 * C + lane] = la_exp2(B) * s_upd;
   }
-  if (lane == 0) e[4 * C] = __builtin_amdgcn_exp2f((float)tot);
+  if (lane == 0) {
+    e[4 * C] = la_exp2(tot);
+    e[4 * C + 2] = near ? 1.0f : 0.0f;
+  }
   return tot;
 }
 
@@ -337,6 +397,7 @@ struct LaTile {
   static constexpr int NT = NW * 64;
   static constexpr int IT = C / 32;              // 32-token tiles of a chunk
   static constexpr int KT = DKP / 32;            // 32-row tiles of the state
+  static constexpr int WV = kF32 ? 2 : 1;        // 16-byte units of eight elements
   static constexpr int NPS = kF32 ? 1 : 3;       // pieces of the state's update
   // One or two waves form all scores of the chunk each, in registers; four
   // share them through LDS (each wave forms one tile of 32 x 32).
@@ -350,10 +411,9 @@ struct LaTile {
   static constexpr size_t state_bytes() { return kX + kZ + (size_t)2 * kExp * 4; }
   using X = LaTileIO<T, C, DKP, NT>;
   using Z = LaTileIO<T, C, NW * 32, NT>;
-  // registers: state, outputs and the tiles under way; with few enough of
-  // them two waves share a SIMD
+  // registers: state, outputs and the tiles under way
   static constexpr int kRegs = 16 * (KT + IT) + 4 * (2 * X::N + Z::N);
-  static constexpr int kWaves = kRegs <= 150 ? 2 : 1;
+  static constexpr int waves(bool bwd) { return la_simd_waves(kRegs, kF32, bwd); }
 };
 
 // S = decay S + sum_j y_j (w_j z_j)^T (KEEP: S as it is)
@@ -438,10 +498,11 @@ __device__ __forceinline__ void la_store_state(const la_f16 (&S)[KT], float* p, 
 }
 
 // Scores of one 32 x 32 tile (rows j of y, columns i of x), weighted by the
-// decay between the two tokens and zero on the wrong side of the diagonal.
+// decay between the two tokens (near: by the part of it that is the key's) and
+// zero on the wrong side of the diagonal.
 template <typename T, int DKP, int NW, bool REV>
 __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsigned char* Y, uint32_t xrow,
-                                            uint32_t yrow, const float* e, int jt, int it, float s_intra,
+                                            uint32_t yrow, const float* e, bool near, int jt, int it, float s_intra,
                                             int lane) {
   using K = LaTile<T, DKP, NW>;
   const int h = lane >> 5, n32 = lane & 31;
@@ -450,23 +511,41 @@ __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsign
   for (int ks = 0; ks < DKP / 16; ++ks)
     T::mma(c, T::row(Y + (yrow ^ (uint32_t)(ks * 32 * T::kHalf)) + jt * 32 * K::XB),
            T::row(X + (xrow ^ (uint32_t)(ks * 32 * T::kHalf)) + it * 32 * K::XB));
-  const int i = 32 * it + n32;
-  const float gi = e[i], gl = e[K::C + i];
+  const int j0 = 32 * jt + 8 * h;
+  if (near) {
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int j0 = 32 * jt + 16 * s + 8 * h;
-    float hh[8], ll[8];
-    *(float4*)&hh[0] = *(const float4*)(e + j0);
-    *(float4*)&hh[4] = *(const float4*)(e + j0 + 4);
-    *(float4*)&ll[0] = *(const float4*)(e + K::C + j0);
-    *(float4*)&ll[4] = *(const float4*)(e + K::C + j0 + 4);
+    for (int s = 0; s < 2; ++s) {
+      float w[8];
+      *(float4*)&w[0] = *(const float4*)(e + j0 + 16 * s);
+      *(float4*)&w[4] = *(const float4*)(e + j0 + 16 * s + 4);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float d = REV ? (hh[q] - gi) + (ll[q] - gl) : (gi - hh[q]) + (gl - ll[q]);
-      const float w = __builtin_amdgcn_exp2f(d) * s_intra;
-      const float v = c[8 * s + q] * w;
-      c[8 * s + q] = jt != it || (REV ? j0 + q >= i : j0 + q <= i) ? v : 0.0f;
+      for (int q = 0; q < 8; ++q) c[8 * s + q] *= w[q];
     }
+  } else {
+    const int i = 32 * it + n32;
+    const float gi = e[i], gl = e[K::C + i];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float hh[8], ll[8];
+      *(float4*)&hh[0] = *(const float4*)(e + j0 + 16 * s);
+      *(float4*)&hh[4] = *(const float4*)(e + j0 + 16 * s + 4);
+      *(float4*)&ll[0] = *(const float4*)(e + K::C + j0 + 16 * s);
+      *(float4*)&ll[4] = *(const float4*)(e + K::C + j0 + 16 * s + 4);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float d = REV ? (hh[q] - gi) + (ll[q] - gl) : (gi - hh[q]) + (gl - ll[q]);
+        c[8 * s + q] *= __builtin_amdgcn_exp2f(d) * s_intra;
+      }
+    }
+  }
+  if (jt == it) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int j = 16 * s + 8 * h + q;
+        if (REV ? j < n32 : j > n32) c[8 * s + q] = 0.0f;
+      }
   }
   return c;
 }
@@ -523,7 +602,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
                                : J.s_seg + ((long long)sid * a.H + hd) * a.state;
     la_load_state<K::KT>(S, init, J.sm, J.sn, J.DK, J.DV, col, h);
   }
-  if (wave == kExpWave) la_exponents<C>(gv, REV, J.s_inter, J.s_upd, exps, lane);
+  if (wave == kExpWave) la_exponents<C>(gv, REV, J.s_out, J.s_ratio, J.s_upd, exps, lane);
 
   // lane offsets of the operands in LDS
   uint32_t xrow = n32 * K::XB + (((h * T::kHalf) ^ la_f<K::XB>(n32)) << 4);
@@ -544,7 +623,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     wst = (uint32_t)J.w.st * K::ES;
     woff = n32 * wst + 8 * h * K::ES;
   }
-  const float s_intra = J.s_intra, s_inter = J.s_inter, s_upd = J.s_upd;
+  const float s_out = J.s_out, s_ratio = J.s_ratio, s_upd = J.s_upd, s_intra = s_out * s_ratio;
   int n = s.len - first;                 // steps of this chunk
   int at = first;                        // its first step in the segment
 
@@ -557,6 +636,21 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     ty.commit(Y, tid, n, whole && n == C);
     tz.commit(Z, tid, n, whole && n == C);
     __syncthreads();
+    // loads are waited for in order: w, which this chunk needs, before the next chunk's tiles
+    uint4 wv[IT][2 * K::WV];
+    if (dot) {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int i = 32 * it + n32;
+        const char* wp = wb + (uint32_t)(woff + (uint32_t)((i < n ? i : n - 1) - n32) * wst);
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+          for (int u = 0; u < K::WV; ++u)
+            wv[it][k2 * K::WV + u] =
+                *(const uint4*)(wp + (c0 + 16 * k2 + 8 * h < J.DV ? 16 * k2 * K::ES + 16 * u : -(c0 + 8 * h) * K::ES));
+      }
+    }
     if (q + 1 < chunks) {
       tx.base += dx;
       ty.base += dy;
@@ -568,11 +662,12 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
       la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + at) * a.H + hd) * a.state, J.sm, J.sn, J.DK, J.DV,
                             col, h);
 
+    const bool near = __builtin_amdgcn_readfirstlane(__float_as_int(e[4 * C + 2])) != 0;
     if constexpr (K::kShareP) {
       static_assert(IT * IT <= NW, "a score tile per wave");
       const int jt = wave / IT, it = wave % IT;
       if (wave < IT * IT && (REV ? jt >= it : jt <= it)) {
-        const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, jt, it, s_intra, lane);
+        const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, near, jt, it, s_intra, lane);
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
           float v[8];
@@ -607,12 +702,15 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
           for (int p = 0; p < NP; ++p) T::mma(o[it], sp[p], xb);
         }
       }
+    auto scale_out = [&]() {
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const float w = e[2 * C + 32 * it + n32];
+      for (int it = 0; it < IT; ++it) {
+        const float w = e[2 * C + 32 * it + n32];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[it][r] *= w;
-    }
+        for (int r = 0; r < 16; ++r) o[it][r] *= w;
+      }
+    };
+    if (!near) scale_out();   // near: the chunk's own part has the same factor
 
     // what the chunk's own tokens give
     F zf[C / 16];
@@ -636,7 +734,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
         for (int jt = 0; jt < IT; ++jt) {
           if (REV ? jt < it : jt > it) continue;
           __builtin_amdgcn_sched_barrier(0);   // one tile at a time: all at once would not fit the registers
-          const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, jt, it, s_intra, lane);
+          const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, near, jt, it, s_intra, lane);
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
             float v[8];
@@ -649,6 +747,8 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
           }
         }
     }
+
+    if (near) scale_out();
 
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
@@ -667,10 +767,8 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
           else
             T::store8((E*)oi + 16 * k2, v);
           if (dot) {
-            const E* wp = (const E*)(wb + (woff + 32 * it * wst)) + 16 * k2;
             float w[8];
-            T::load4(wp, w);
-            T::load4(wp + 4, w + 4);
+            T::unpack(&wv[it][k2 * K::WV], w);
             dsum += ((w[0] * v[0] + w[1] * v[1]) + (w[2] * v[2] + w[3] * v[3])) +
                     ((w[4] * v[4] + w[5] * v[5]) + (w[6] * v[6] + w[7] * v[7]));
           }
@@ -685,7 +783,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     __builtin_amdgcn_sched_barrier(0);
     la_update<T, DKP, NW, false>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
     if (wave == kExpWave && q + 1 < chunks)
-      la_exponents<C>(gv, REV, s_inter, s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
+      la_exponents<C>(gv, REV, s_out, s_ratio, s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
     __syncthreads();
     if (dot) {
       if (tid < n) {
@@ -732,18 +830,15 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
 }
 
 template <typename T, int DKP, int NW, int NP, bool BWD>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::waves(BWD)))) void
 pdssm_linattn_kernel(const LaArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned id = blockIdx.x;
+  const unsigned id = blockIdx.x;
   if (id == 0 && threadIdx.x < 2) a.header[threadIdx.x] = 0;
-  const int jn = BWD ? id % a.njobs : 0;
-  if (BWD) id /= a.njobs;
-  const int slab = id % a.slabs;
-  id /= a.slabs;
-  const int hd = id % a.H;
-  const int sid = id / a.H;
-  const LaJob& J = a.job[jn];
+  LaUnit u;
+  if (!la_unit(a, id, u)) return;
+  const int slab = u.slab, hd = u.hd, sid = u.sid;
+  const LaJob& J = a.job[BWD ? u.job : 0];
   LaSeg s;
   if (!la_segment(a, sid, s)) return;
   if (BWD && J.rev)
@@ -772,14 +867,10 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   float* exps = (float*)(smem + K::kX + K::kZ);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n32 = lane & 31;
-  unsigned id = blockIdx.x;
-  const int jn = id % a.njobs;
-  id /= a.njobs;
-  const int slab = id % a.slabs;
-  id /= a.slabs;
-  const int hd = id % a.H;
-  const int sid = id / a.H;
-  const LaJob& J = a.job[jn];
+  LaUnit u;
+  if (!la_unit(a, blockIdx.x, u)) return;
+  const int slab = u.slab, hd = u.hd, sid = u.sid;
+  const LaJob& J = a.job[u.job];
   LaSeg s;
   if (!la_segment(a, sid, s)) return;
   const int rev = J.rev;
@@ -807,8 +898,8 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   };
   double sum = 0.0;      // log2 of f
   auto exponents = [&](float* e) {
-    const float f = __builtin_amdgcn_exp2f((float)sum);
-    sum += la_exponents<C>(gv, rev, 1.0f, s_upd * f, e, lane);
+    const float f = la_exp2(sum);
+    sum += la_exponents<C>(gv, rev, 1.0f, 1.0f, s_upd * f, e, lane);
     if (lane == 0) e[4 * C + 1] = f;
   };
   if (chunks) fetch(s.len - first);
@@ -844,7 +935,7 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   }
   const long long to = ((long long)(sid + (rev ? -1 : 1)) * a.H + hd);
   la_store_state<K::KT>(S, J.seg_out + to * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
-  if (slab == 0 && wave == kExpWave && lane == 0) J.seg_decay[to] = __builtin_amdgcn_exp2f((float)sum);
+  if (slab == 0 && wave == kExpWave && lane == 0) J.seg_decay[to] = la_exp2(sum);
 }
 
 }  // namespace pdscan

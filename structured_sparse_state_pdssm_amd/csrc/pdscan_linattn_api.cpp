@@ -176,7 +176,7 @@ FwdWs fwd_ws(const pdssm_linattn_dims* d) {
   FwdWs w;
   const int bf16 = d->in_dtype == PDSSM_BF16;
   w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * pdscan::la_slabs(d->dk, d->dv, bf16),
-                             kCus * pdscan::la_resident(d->dk, d->dv, bf16));
+                             kCus * pdscan::la_resident(d->dk, d->dv, bf16, 0));
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -212,9 +212,9 @@ BwdWs bwd_ws(const pdssm_linattn_dims* d) {
   w.vslabs = pdscan::la_slabs(d->dk, d->dv, bf16);
   w.one = pdscan::la_pad(d->dk) == pdscan::la_pad(d->dv) && w.qslabs == w.vslabs &&
           pdscan::la_waves(d->dk, d->dv, bf16) == pdscan::la_waves(d->dv, d->dk, bf16);
-  // the launch that holds the fewest workgroups decides: three jobs in one, or two and one
-  const int vroom = kCus * pdscan::la_resident(d->dk, d->dv, bf16);
-  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * (w.one ? 3 : 1) * w.vslabs, vroom);
+  // the launch with the most work decides: all three jobs in one, or those of q and k
+  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * (w.one ? 3 : 2) * w.qslabs,
+                             kCus * pdscan::la_resident(d->dv, d->dk, bf16, 1));
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -264,7 +264,7 @@ int launched(hipError_t e) {
 int grid_ok(const LaSplit& s, const pdssm_linattn_dims* d) {
   // three jobs of two slabs each, or one workgroup per piece of a segment
   const uint64_t subs = (uint64_t)pdscan::la_subs(s, d->L);
-  if ((uint64_t)s.segs * d->H * (subs > 6 ? subs : 6) > 0x7fffffffull)
+  if (((uint64_t)s.segs + 8) * d->H * (subs > 6 ? subs : 6) > 0x7fffffffull)
     return set_error(PDSSM_EUNSUPPORTED, "too many segments and heads (%d, %d)", s.segs, d->H);
   return PDSSM_OK;
 }
@@ -277,6 +277,8 @@ LaArgs common(const pdssm_linattn_dims* d, const LaView& g, const int32_t* cu, c
   a.table = (cu && s.split) ? (const int32_t*)(ws + table) : nullptr;
   a.header = (uint32_t*)ws;
   a.B = d->B; a.H = d->H; a.L = d->L;
+  a.ratio = d->H / d->Hk;
+  a.dies = 1;
   a.nseg = s.nseg; a.seg = s.seg; a.segs = s.segs;
   a.rows = (long long)(d->packed ? 1 : d->B) * d->L;
   a.state = (long long)d->dk * d->dv;
@@ -352,8 +354,8 @@ int pdssm_linattn_fwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   J.s_user = h0;
   J.s_fin = h_L;
   J.sm = d.dv; J.sn = 1;
-  J.s_inter = J.s_intra = d.scale;
-  J.s_upd = 1.0f;
+  J.s_out = d.scale;
+  J.s_ratio = J.s_upd = 1.0f;
   hipError_t e = hipSuccess;
   if (w.split.split) {
     // contributions of the segments, then the states that enter them
@@ -438,8 +440,8 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   q_job.xd_out = g_hL ? (double*)(ws + w.xd) : nullptr;
   q_job.dot = (float*)(ws + w.r);
   q_job.sm = 1; q_job.sn = d.dv;
-  q_job.s_inter = q_job.s_intra = d.scale;
-  q_job.s_upd = 1.0f;
+  q_job.s_out = d.scale;
+  q_job.s_ratio = q_job.s_upd = 1.0f;
   // dk: the reversed form of (v, do, q) on the adjoint states, transposed
   k_job.x = vv; k_job.y = vdo; k_job.z = vq; k_job.w = vk;
   k_job.xd = k_job.yd = 1;
@@ -450,8 +452,8 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   k_job.s_seg = (const float*)(ws + w.segR);
   k_job.dot = (float*)(ws + w.k);
   k_job.sm = 1; k_job.sn = d.dv;
-  k_job.s_inter = 1.0f;
-  k_job.s_intra = k_job.s_upd = d.scale;
+  k_job.s_out = 1.0f;
+  k_job.s_ratio = k_job.s_upd = d.scale;
   k_job.rev = 1;
   q_job.od = k_job.od = 1;
   q_job.o_f32 = k_job.o_f32 = fold;
@@ -464,8 +466,8 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   v_job.s_seg = (const float*)(ws + w.segR);
   v_job.s_fin = g_h0;
   v_job.sm = d.dv; v_job.sn = 1;
-  v_job.s_inter = 1.0f;
-  v_job.s_intra = v_job.s_upd = d.scale;
+  v_job.s_out = 1.0f;
+  v_job.s_ratio = v_job.s_upd = d.scale;
   v_job.rev = 1;
 
   if (w.subs > 1) {

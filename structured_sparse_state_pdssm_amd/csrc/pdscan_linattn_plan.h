@@ -12,6 +12,7 @@ constexpr int kLaChunk = 64;     // tokens per step of a sequence's serial axis 
 constexpr int kLaMaxD = 256;     // widest key or value row
 constexpr int kLaMaxStep = 1 << 23;   // longest step stride, elements: 64 rows stay within 31 bits of bytes
 constexpr int kLaKeep = 512;     // steps of a segment between states kept for the log-decay gradient
+constexpr double kLaNear = 24.0; // log2 of the decay over a chunk up to which it is split into factors of its tokens
 constexpr int kLaHeader = 256;   // workspace header: word 1 stays zero (nothing here waits on another workgroup)
 
 // A strided tensor: element strides of the batch, head and step axes; the
@@ -36,7 +37,7 @@ struct LaJob {
   float* keep;                 // states inside a segment, every kLaKeep steps [row / kLaKeep][H], NULL: none
   float* dot;                  // w . o per token [slab][H][rows], NULL: none
   int sm, sn;                  // strides of a state's x-row and z-row axes
-  float s_inter, s_intra, s_upd;
+  float s_out, s_ratio, s_upd; // scale of the output, of its own tokens' part beside the state's, of the update
   int rev;                     // 1: backwards in time
   int o_f32;                   // 1: o is fp32 whatever the inputs' type
 };
@@ -48,6 +49,8 @@ struct LaArgs {
   uint32_t* header;            // workspace header
   int B, H, L, nseg, seg, segs;   // nseg per sequence (not packed), steps per segment, segments in all (bound)
   int slabs, njobs;
+  int ratio;                   // value heads that share a query and key head
+  int dies;                    // workgroups that share rows sit on one of this many dies (1: as they come)
   long long rows, state;       // token rows in all; elements of one state
   LaJob job[3];
 };
@@ -98,13 +101,20 @@ inline int la_slabs(int DK, int DV, int bf16) {
   const int w = 32 * la_waves(DK, DV, bf16);
   return (DV + w - 1) / w;
 }
+// Waves of the product kernel on a SIMD, by the registers of a lane that its
+// state, outputs and tiles under way take (the compiler's spills confirm it).
+inline constexpr int la_simd_waves(int regs, bool f32, bool bwd) {
+  return regs <= (bwd ? f32 ? 0 : 56 : 72) ? 3 : regs <= 150 ? 2 : 1;
+}
 // Workgroups of the product kernel that a compute unit holds, by LDS (160 KiB)
-// and by registers (two waves a SIMD; one with wide rows).
-inline int la_resident(int DK, int DV, int bf16) {
+// and by those waves.
+inline int la_resident(int DK, int DV, int bf16, int bwd) {
   const int es = bf16 ? 2 : 4, nw = la_waves(DK, DV, bf16), d = la_pad(DK);
   const int C = nw < 4 || (!bf16 && d == 256) ? 32 : 64;
-  const int lds = C * es * (2 * d + 32 * nw) + (nw == 4 ? (bf16 ? 2 : 1) * C * C * es : 0) + 4 * (8 * C + 8 + nw * C);
-  const int waves = d == 256 || (!bf16 && d == 128) ? 4 : 8;
+  const int np = bf16 ? bwd ? 3 : 2 : 1;
+  const int lds = C * es * (2 * d + 32 * nw) + (nw == 4 ? np * C * C * es : 0) + 4 * (8 * C + 8 + nw * C);
+  const int regs = (d + C) / 2 + C * es * (2 * d + 32 * nw) / (256 * nw);
+  const int waves = 4 * la_simd_waves(regs, !bf16, bwd);
   const int n = 163840 / lds < waves / nw ? 163840 / lds : waves / nw;
   return n < 1 ? 1 : n;
 }
@@ -131,13 +141,22 @@ inline LaSplit la_split(int B, int L, int packed, int width, int room) {
   s.split = n > 1 && L > 256;
   const long long each = s.split ? ((long long)L + n - 1) / n : L;
   s.seg = (int)((each + kLaChunk - 1) / kLaChunk * kLaChunk);
-  s.nseg = s.split ? (L + s.seg - 1) / s.seg : 1;
+  s.nseg = s.split ? (int)(((long long)L + s.seg - 1) / s.seg) : 1;
   const long long segs = !packed ? (long long)B * s.nseg : s.split ? (long long)(L / s.seg) + B : B;
   s.segs = segs > 0x7fffffffll ? 0x7fffffff : (int)segs;
   return s;
 }
 
-inline int la_subs(const LaSplit& s, int L) { return ((s.seg < L ? s.seg : L) + kLaKeep - 1) / kLaKeep; }
+// Workgroups that read the same rows (the jobs, slabs and heads of one segment
+// and query / key head) go to one die and so to one L2, unless there are too
+// few such sets to fill the dies.  Workgroup i starts on die i mod 8.
+inline int la_dies(long long sets) { return sets >= 64 ? 8 : 1; }
+inline long long la_grid(const LaArgs& a) {
+  const long long sets = (long long)a.segs * (a.H / a.ratio);
+  return (sets + a.dies - 1) / a.dies * a.dies * a.ratio * a.slabs * a.njobs;
+}
+
+inline int la_subs(const LaSplit& s, int L) { return ((s.seg < L ? s.seg : L) - 1) / kLaKeep + 1; }
 
 inline size_t la_align(size_t n) { return (n + 255) / 256 * 256; }
 
