@@ -340,21 +340,24 @@ __device__ __forceinline__ float la_exp2(double x) {
   return __builtin_amdgcn_ldexpf(f, x < -1000.0 ? -1000 : (int)n);
 }
 
-// What a chunk's tokens are weighted with, by one wave (lane = token, g = its
-// log decay, 0 behind the last).  With A the log2 of the decay between a token
-// and the entering state (G, or G_C - G backwards):
+// What the tokens of 64 / C chunks are weighted with, by one wave (lane = token,
+// chunk by chunk in the job's direction; g = its log decay, 0 behind the last).
+// With A the log2 of the decay between a token and its chunk's entering state
+// (G, or G_C - G backwards), e, kExp floats per chunk, gets
 //   e[2C + i] = 2^A s_out, the output's scale
-//   e[3C + j] the update's weight
+//   e[3C + j] the update's weight (CHAIN: with the decay 2^`before` of all
+//             chunks before, which e[4C + 1] holds)
 //   e[4C]     the chunk's whole decay
 //   e[4C + 2] 1 where no |A| is above kLaNear: then the weight of a pair is
 //             2^{A_i} 2^{-A_j}, its first factor common to the whole output,
 //             and e[j] = 2^{-A_j} s_ratio; else 0, and e[i], e[C + i] hold G as
 //             two floats for the difference of every pair.
 // A log decay under -1e4 (minus infinity: the state starts anew) counts as
-// -1e4, whose exponential is zero all the same.  Returns the sum of log2.
-template <int C>
-__device__ __forceinline__ double la_exponents(float g, int rev, float s_out, float s_ratio, float s_upd, float* e,
-                                               int lane) {
+// -1e4, whose exponential is zero all the same.  Returns log2 of the decay
+// over all of it.
+template <int C, int EXP, bool CHAIN>
+__device__ __forceinline__ double la_exponents(float g, int rev, float s_out, float s_ratio, float s_upd,
+                                               double before, float* e, int lane) {
   if (g < -1e4f) g = -1e4f;
   double G = (double)g * 1.4426950408889634074;
   G = la_scan_step<0x111, 0xf>(G);   // row_shr:1
@@ -362,29 +365,42 @@ __device__ __forceinline__ double la_exponents(float g, int rev, float s_out, fl
   G = la_scan_step<0x114, 0xf>(G);   // row_shr:4
   G = la_scan_step<0x118, 0xf>(G);   // row_shr:8
   G = la_scan_step<0x142, 0xa>(G);   // row_bcast:15 into rows 1 and 3
-  G = la_scan_step<0x143, 0xc>(G);   // row_bcast:31 into rows 2 and 3
-  const uint64_t b = (uint64_t)__double_as_longlong(G);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
-  const double tot = __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-  const double A = rev ? tot - G : G, B = rev ? G : tot - G;
-  const bool near = __all(A <= kLaNear && A >= -kLaNear);
-  if (lane < C) {
-    if (near) {
-      e[lane] = la_exp2(-A) * s_ratio;
-    } else {
-      const float gh = (float)G;
-      e[lane] = gh;
-      e[C + lane] = (float)(G - (double)gh);
-    }
-    e[2 * C + lane] = la_exp2(A) * s_out;
-    e[3 * C + lane] = la_exp2(B) * s_upd;
+  if constexpr (C == 64) G = la_scan_step<0x143, 0xc>(G);   // row_bcast:31 into rows 2 and 3
+  auto at = [&](int l) {
+    const uint64_t b = (uint64_t)__double_as_longlong(G);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+  };
+  double tot = at(63), all = tot;
+  if constexpr (C == 32) {
+    const double t0 = at(31);
+    all += t0;
+    if (lane < 32)
+      tot = t0;
+    else
+      before += t0;
   }
-  if (lane == 0) {
+  const double A = rev ? tot - G : G, B = rev ? G : tot - G;
+  const uint64_t far_lanes = __ballot(!(A <= kLaNear && A >= -kLaNear));
+  const bool near = C == 64 ? far_lanes == 0 : (lane < 32 ? (uint32_t)far_lanes : (uint32_t)(far_lanes >> 32)) == 0;
+  const int i = lane & (C - 1);
+  e += C == 64 ? 0 : (lane >> 5) * EXP;
+  if (near) {
+    e[i] = la_exp2(-A) * s_ratio;
+  } else {
+    const float gh = (float)G;
+    e[i] = gh;
+    e[C + i] = (float)(G - (double)gh);
+  }
+  e[2 * C + i] = la_exp2(A) * s_out;
+  e[3 * C + i] = la_exp2(CHAIN ? B + before : B) * s_upd;
+  if (i == 0) {
     e[4 * C] = la_exp2(tot);
+    if (CHAIN) e[4 * C + 1] = la_exp2(before);
     e[4 * C + 2] = near ? 1.0f : 0.0f;
   }
-  return tot;
+  return all;
 }
 
 template <typename T, int DKP, int NW>
@@ -406,9 +422,10 @@ struct LaTile {
   static constexpr int XB = DKP * ES, ZB = NW * 32 * ES, PB = C * ES;   // bytes of a row
   static constexpr int kExp = 4 * C + 4;         // floats of one chunk's exponents
   static constexpr size_t kX = (size_t)C * XB, kZ = (size_t)C * ZB, kP = kShareP ? (size_t)C * PB : 0;
-  static constexpr size_t kSmall = (size_t)(2 * kExp + NW * C) * 4;
+  static constexpr int PAIR = 64 / C;            // chunks whose exponents are formed at once
+  static constexpr size_t kSmall = (size_t)(2 * PAIR * kExp + NW * C) * 4;
   static constexpr size_t main_bytes(int np) { return 2 * kX + kZ + np * kP + kSmall; }
-  static constexpr size_t state_bytes() { return kX + kZ + (size_t)2 * kExp * 4; }
+  static constexpr size_t state_bytes() { return kX + kZ + (size_t)2 * PAIR * kExp * 4; }
   using X = LaTileIO<T, C, DKP, NT>;
   using Z = LaTileIO<T, C, NW * 32, NT>;
   // registers: state, outputs and the tiles under way
@@ -564,8 +581,8 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   unsigned char* Y = smem + K::kX;
   unsigned char* Z = smem + 2 * K::kX;
   unsigned char* P = smem + 2 * K::kX + K::kZ;
-  float* exps = (float*)(smem + 2 * K::kX + K::kZ + NP * K::kP);   // of this chunk and the next
-  float* dots = exps + 2 * K::kExp;                                // [NW][C]
+  float* exps = (float*)(smem + 2 * K::kX + K::kZ + NP * K::kP);   // of the chunks under way and the next
+  float* dots = exps + 2 * K::PAIR * K::kExp;                      // [NW][C]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n32 = lane & 31, pm = la_pi(n32);
   const int slab0 = slab * NW * 32;
@@ -584,16 +601,22 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   const bool whole = J.DK == DKP && J.DV - slab0 >= NW * 32;
   const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh +
                     (int64_t)(s.t0 + first) * a.g.st;
-  const int64_t goff = (int64_t)lane * a.g.st;
+  const int64_t goff = (lane & (C - 1)) * a.g.st + (lane / C) * dg;
   float gv = 0.0f;
-  constexpr int kExpWave = NW - 1;
+  constexpr int kExpWave = NW - 1, PAIR = K::PAIR;
   auto fetch = [&](int n) {
     tx.fetch(n);
     ty.fetch(n);
     tz.fetch(n);
-    if (wave == kExpWave) gv = lane < n && lane < C ? gp[goff] : 0.0f;
   };
-  if (chunks) fetch(s.len - first);
+  // log decays of a chunk of n steps and the one after it (they run `rest` steps on)
+  auto fetch_g = [&](int n, int rest) {
+    if (wave == kExpWave) gv = (lane & (C - 1)) < (lane < C ? n : rest) ? gp[goff] : 0.0f;
+  };
+  if (chunks) {
+    fetch(s.len - first);
+    fetch_g(s.len - first, REV ? first : s.len - C);
+  }
 
   la_f16 S[K::KT];
   {
@@ -602,7 +625,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
                                : J.s_seg + ((long long)sid * a.H + hd) * a.state;
     la_load_state<K::KT>(S, init, J.sm, J.sn, J.DK, J.DV, col, h);
   }
-  if (wave == kExpWave) la_exponents<C>(gv, REV, J.s_out, J.s_ratio, J.s_upd, exps, lane);
+  if (wave == kExpWave) la_exponents<C, K::kExp, false>(gv, REV, J.s_out, J.s_ratio, J.s_upd, 0.0, exps, lane);
 
   // lane offsets of the operands in LDS
   uint32_t xrow = n32 * K::XB + (((h * T::kHalf) ^ la_f<K::XB>(n32)) << 4);
@@ -631,7 +654,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     if (n > C) n = C;
     // the operands' places are one exclusive-or away from these: cheaper than the registers to keep them all
     asm volatile("" : "+v"(xrow), "+v"(yrow), "+v"(ycol), "+v"(zcol), "+v"(prow));
-    const float* e = exps + (q & 1) * K::kExp;
+    const float* e = exps + (q % (2 * PAIR)) * K::kExp;
     tx.commit(X, tid, n, whole && n == C);
     ty.commit(Y, tid, n, whole && n == C);
     tz.commit(Z, tid, n, whole && n == C);
@@ -657,6 +680,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
       tz.base += dz;
       gp += dg;
       fetch(REV ? C : s.len - at - C);
+      if (q % PAIR == PAIR - 1) fetch_g(REV ? C : s.len - at - C, REV ? at - C : s.len - at - 2 * C);
     }
     if (BWD && !REV && J.keep && at && at % kLaKeep == 0)
       la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + at) * a.H + hd) * a.state, J.sm, J.sn, J.DK, J.DV,
@@ -782,8 +806,8 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
 
     __builtin_amdgcn_sched_barrier(0);
     la_update<T, DKP, NW, false>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
-    if (wave == kExpWave && q + 1 < chunks)
-      la_exponents<C>(gv, REV, s_out, s_ratio, s_upd, exps + ((q + 1) & 1) * K::kExp, lane);
+    if (wave == kExpWave && q + 1 < chunks && q % PAIR == PAIR - 1)
+      la_exponents<C, K::kExp, false>(gv, REV, s_out, s_ratio, s_upd, 0.0, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
     __syncthreads();
     if (dot) {
       if (tid < n) {
@@ -887,32 +911,32 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   const bool whole = J.DK == DKP && J.DV - slab0 >= NW * 32;
   const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh +
                     (int64_t)(s.t0 + first) * a.g.st;
-  const int64_t goff = (int64_t)lane * a.g.st;
+  const int64_t goff = (lane & (C - 1)) * a.g.st + (lane / C) * dg;
   const float s_upd = J.s_upd;
   float gv = 0.0f;
-  constexpr int kExpWave = NW - 1;
+  constexpr int kExpWave = NW - 1, PAIR = K::PAIR;
   auto fetch = [&](int n) {
     ty.fetch(n);
     tz.fetch(n);
-    if (wave == kExpWave) gv = lane < n && lane < C ? gp[goff] : 0.0f;
+  };
+  auto fetch_g = [&](int n, int rest) {
+    if (wave == kExpWave) gv = (lane & (C - 1)) < (lane < C ? n : rest) ? gp[goff] : 0.0f;
   };
   double sum = 0.0;      // log2 of f
-  auto exponents = [&](float* e) {
-    const float f = la_exp2(sum);
-    sum += la_exponents<C>(gv, rev, 1.0f, 1.0f, s_upd * f, e, lane);
-    if (lane == 0) e[4 * C + 1] = f;
-  };
-  if (chunks) fetch(s.len - first);
+  if (chunks) {
+    fetch(s.len - first);
+    fetch_g(s.len - first, rev ? s.len - C : first);
+  }
   la_f16 S[K::KT];
 #pragma unroll
   for (int t = 0; t < K::KT; ++t) S[t] = la_f16{};
   uint32_t ycol = T::template col_base<K::XB>(lane, 0);
   uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
-  if (wave == kExpWave) exponents(exps);
+  if (wave == kExpWave) sum = la_exponents<C, K::kExp, true>(gv, rev, 1.0f, 1.0f, s_upd, 0.0, exps, lane);
   int n = s.len - first, at = first;
   for (int q = 0; q < chunks; ++q) {
     if (n > C) n = C;
-    const float* e = exps + (q & 1) * K::kExp;
+    const float* e = exps + (q % (2 * PAIR)) * K::kExp;
     asm volatile("" : "+v"(ycol), "+v"(zcol));
     ty.commit(Y, tid, n, whole && n == C);
     tz.commit(Z, tid, n, whole && n == C);
@@ -923,12 +947,14 @@ pdssm_linattn_state_kernel(const LaArgs a) {
       tz.base += dz;
       gp += dg;
       fetch(rev ? s.len - at - C : C);
+      if (q % PAIR == PAIR - 1) fetch_g(rev ? s.len - at - C : C, rev ? s.len - at - 2 * C : at - C);
     }
     F zf[C / 16];
 #pragma unroll
     for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB>(Z, zcol, 16 * js, 0);
     la_update<T, DKP, NW, true>(S, Y, ycol, zf, e + 3 * C, 1.0f, lane);
-    if (wave == kExpWave && q + 1 < chunks) exponents(exps + ((q + 1) & 1) * K::kExp);
+    if (wave == kExpWave && q + 1 < chunks && q % PAIR == PAIR - 1)
+      sum += la_exponents<C, K::kExp, true>(gv, rev, 1.0f, 1.0f, s_upd, sum, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
     __syncthreads();
     at += (int)dir;
     n = rev ? s.len - at : C;

@@ -112,7 +112,7 @@ inline int la_resident(int DK, int DV, int bf16, int bwd) {
   const int es = bf16 ? 2 : 4, nw = la_waves(DK, DV, bf16), d = la_pad(DK);
   const int C = nw < 4 || (!bf16 && d == 256) ? 32 : 64;
   const int np = bf16 ? bwd ? 3 : 2 : 1;
-  const int lds = C * es * (2 * d + 32 * nw) + (nw == 4 ? np * C * C * es : 0) + 4 * (8 * C + 8 + nw * C);
+  const int lds = C * es * (2 * d + 32 * nw) + (nw == 4 ? np * C * C * es : 0) + 4 * (64 / C * (8 * C + 8) + nw * C);
   const int regs = (d + C) / 2 + C * es * (2 * d + 32 * nw) / (256 * nw);
   const int waves = 4 * la_simd_waves(regs, !bf16, bwd);
   const int n = 163840 / lds < waves / nw ? 163840 / lds : waves / nw;
