@@ -340,24 +340,12 @@ __device__ __forceinline__ float la_exp2(double x) {
   return __builtin_amdgcn_ldexpf(f, x < -1000.0 ? -1000 : (int)n);
 }
 
-// What the tokens of 64 / C chunks are weighted with, by one wave (lane = token,
-// chunk by chunk in the job's direction; g = its log decay, 0 behind the last).
-// With A the log2 of the decay between a token and its chunk's entering state
-// (G, or G_C - G backwards), e, kExp floats per chunk, gets
-//   e[2C + i] = 2^A s_out, the output's scale
-//   e[3C + j] the update's weight (CHAIN: with the decay 2^`before` of all
-//             chunks before, which e[4C + 1] holds)
-//   e[4C]     the chunk's whole decay
-//   e[4C + 2] 1 where no |A| is above kLaNear: then the weight of a pair is
-//             2^{A_i} 2^{-A_j}, its first factor common to the whole output,
-//             and e[j] = 2^{-A_j} s_ratio; else 0, and e[i], e[C + i] hold G as
-//             two floats for the difference of every pair.
-// A log decay under -1e4 (minus infinity: the state starts anew) counts as
-// -1e4, whose exponential is zero all the same.  Returns log2 of the decay
-// over all of it.
-template <int C, int EXP, bool CHAIN>
-__device__ __forceinline__ double la_exponents(float g, int rev, float s_out, float s_ratio, float s_upd,
-                                               double before, float* e, int lane) {
+// Inclusive sums of log2 decay over each of 64 / C chunks (lane = token, chunk
+// by chunk in the job's direction; g = its log decay, 0 behind the last), and
+// at `l` lane l's.  A log decay under -1e4 (minus infinity: the state starts
+// anew) counts as -1e4, whose exponential is zero all the same.
+template <int C>
+__device__ __forceinline__ double la_scan(float g) {
   if (g < -1e4f) g = -1e4f;
   double G = (double)g * 1.4426950408889634074;
   G = la_scan_step<0x111, 0xf>(G);   // row_shr:1
@@ -366,21 +354,31 @@ __device__ __forceinline__ double la_exponents(float g, int rev, float s_out, fl
   G = la_scan_step<0x118, 0xf>(G);   // row_shr:8
   G = la_scan_step<0x142, 0xa>(G);   // row_bcast:15 into rows 1 and 3
   if constexpr (C == 64) G = la_scan_step<0x143, 0xc>(G);   // row_bcast:31 into rows 2 and 3
-  auto at = [&](int l) {
-    const uint64_t b = (uint64_t)__double_as_longlong(G);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
-    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-  };
-  double tot = at(63), all = tot;
-  if constexpr (C == 32) {
-    const double t0 = at(31);
-    all += t0;
-    if (lane < 32)
-      tot = t0;
-    else
-      before += t0;
-  }
+  return G;
+}
+__device__ __forceinline__ double la_lane(double x, int l) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
+// What the tokens of 64 / C chunks are weighted with in the product kernel, by
+// one wave (lanes as in la_scan).  With A the log2 of the decay between a token and its chunk's entering state
+// (G, or G_C - G backwards), e, kExp floats per chunk, gets
+//   e[2C + i] = 2^A s_out, the output's scale
+//   e[3C + j] the update's weight
+//   e[4C]     the chunk's whole decay
+//   e[4C + 1] 1 where no |A| is above kLaNear: then the weight of a pair is
+//             2^{A_i} 2^{-A_j}, its first factor common to the whole output,
+//             and e[j] = 2^{-A_j} s_ratio; else 0, and e[i], e[C + i] hold G as
+//             two floats for the difference of every pair.
+template <int C, int EXP>
+__device__ __forceinline__ void la_exponents(float g, int rev, float s_out, float s_ratio, float s_upd, float* e,
+                                             int lane) {
+  const double G = la_scan<C>(g);
+  double tot = la_lane(G, 63);
+  if (C == 32 && lane < 32) tot = la_lane(G, 31);
   const double A = rev ? tot - G : G, B = rev ? G : tot - G;
   const uint64_t far_lanes = __ballot(!(A <= kLaNear && A >= -kLaNear));
   const bool near = C == 64 ? far_lanes == 0 : (lane < 32 ? (uint32_t)far_lanes : (uint32_t)(far_lanes >> 32)) == 0;
@@ -394,13 +392,11 @@ __device__ __forceinline__ double la_exponents(float g, int rev, float s_out, fl
     e[C + i] = (float)(G - (double)gh);
   }
   e[2 * C + i] = la_exp2(A) * s_out;
-  e[3 * C + i] = la_exp2(CHAIN ? B + before : B) * s_upd;
+  e[3 * C + i] = la_exp2(B) * s_upd;
   if (i == 0) {
     e[4 * C] = la_exp2(tot);
-    if (CHAIN) e[4 * C + 1] = la_exp2(before);
-    e[4 * C + 2] = near ? 1.0f : 0.0f;
+    e[4 * C + 1] = near ? 1.0f : 0.0f;
   }
-  return all;
 }
 
 template <typename T, int DKP, int NW>
@@ -425,11 +421,12 @@ struct LaTile {
   static constexpr int PAIR = 64 / C;            // chunks whose exponents are formed at once
   static constexpr size_t kSmall = (size_t)(2 * PAIR * kExp + NW * C) * 4;
   static constexpr size_t main_bytes(int np) { return 2 * kX + kZ + np * kP + kSmall; }
-  static constexpr size_t state_bytes() { return kX + kZ + (size_t)2 * PAIR * kExp * 4; }
+  static constexpr size_t state_bytes() { return 2 * (kX + kZ) + (size_t)NW * 64 * 4; }
   using X = LaTileIO<T, C, DKP, NT>;
   using Z = LaTileIO<T, C, NW * 32, NT>;
   // registers: state, outputs and the tiles under way
   static constexpr int kRegs = 16 * (KT + IT) + 4 * (2 * X::N + Z::N);
+  static constexpr int kStateWaves = 16 * KT + 4 * (X::N + Z::N) <= 96 ? 3 : 2;
   static constexpr int waves(bool bwd) { return la_simd_waves(kRegs, kF32, bwd); }
 };
 
@@ -602,20 +599,28 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   const float* gp = (const float*)a.g.p + (int64_t)s.vb * a.g.sb + (int64_t)hd * a.g.sh +
                     (int64_t)(s.t0 + first) * a.g.st;
   const int64_t goff = (lane & (C - 1)) * a.g.st + (lane / C) * dg;
-  float gv = 0.0f;
-  constexpr int kExpWave = NW - 1, PAIR = K::PAIR;
+  constexpr int PAIR = K::PAIR;
+  // The wave that forms the weights: with shared scores the one whose tile
+  // lies on the wrong side of the diagonal, while the others work on theirs.
+  constexpr int kExpWave = K::kShareP && IT == 2 ? (REV ? 1 : 2) : NW - 1;
   auto fetch = [&](int n) {
     tx.fetch(n);
     ty.fetch(n);
     tz.fetch(n);
   };
-  // log decays of a chunk of n steps and the one after it (they run `rest` steps on)
-  auto fetch_g = [&](int n, int rest) {
-    if (wave == kExpWave) gv = (lane & (C - 1)) < (lane < C ? n : rest) ? gp[goff] : 0.0f;
+  // log decays of PAIR chunks, the first of them `skip` chunks on from step `at`
+  auto fetch_g = [&](int at, int skip) {
+    const int mine = skip + lane / C;
+    const int n = REV ? (at >= mine * C ? s.len - (at - mine * C) : 0) : s.len - at - mine * C;
+    float g = 0.0f;
+    if (wave == kExpWave && (lane & (C - 1)) < n) g = gp[goff + skip * dg];
+    return g;
   };
+  float gv = 0.0f, g0 = 0.0f;
   if (chunks) {
+    g0 = fetch_g(first, 0);
+    if (PAIR == 1) gv = fetch_g(first, 1);
     fetch(s.len - first);
-    fetch_g(s.len - first, REV ? first : s.len - C);
   }
 
   la_f16 S[K::KT];
@@ -625,7 +630,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
                                : J.s_seg + ((long long)sid * a.H + hd) * a.state;
     la_load_state<K::KT>(S, init, J.sm, J.sn, J.DK, J.DV, col, h);
   }
-  if (wave == kExpWave) la_exponents<C, K::kExp, false>(gv, REV, J.s_out, J.s_ratio, J.s_upd, 0.0, exps, lane);
+  if (wave == kExpWave) la_exponents<C, K::kExp>(g0, REV, J.s_out, J.s_ratio, J.s_upd, exps, lane);
 
   // lane offsets of the operands in LDS
   uint32_t xrow = n32 * K::XB + (((h * T::kHalf) ^ la_f<K::XB>(n32)) << 4);
@@ -674,21 +679,24 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
                 *(const uint4*)(wp + (c0 + 16 * k2 + 8 * h < J.DV ? 16 * k2 * K::ES + 16 * u : -(c0 + 8 * h) * K::ES));
       }
     }
+    // the log decays two chunks on: their weights are formed in the next chunk's time
+    const float gnext = q % PAIR == 0 ? fetch_g(at, 2) : gv;
     if (q + 1 < chunks) {
       tx.base += dx;
       ty.base += dy;
       tz.base += dz;
       gp += dg;
       fetch(REV ? C : s.len - at - C);
-      if (q % PAIR == PAIR - 1) fetch_g(REV ? C : s.len - at - C, REV ? at - C : s.len - at - 2 * C);
     }
     if (BWD && !REV && J.keep && at && at % kLaKeep == 0)
       la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + at) * a.H + hd) * a.state, J.sm, J.sn, J.DK, J.DV,
                             col, h);
 
-    const bool near = __builtin_amdgcn_readfirstlane(__float_as_int(e[4 * C + 2])) != 0;
+    const bool near = __builtin_amdgcn_readfirstlane(__float_as_int(e[4 * C + 1])) != 0;
     if constexpr (K::kShareP) {
       static_assert(IT * IT <= NW, "a score tile per wave");
+      if (wave == kExpWave && q + 1 < chunks && q % PAIR == PAIR - 1)
+        la_exponents<C, K::kExp>(gv, REV, s_out, s_ratio, s_upd, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
       const int jt = wave / IT, it = wave % IT;
       if (wave < IT * IT && (REV ? jt >= it : jt <= it)) {
         const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, near, jt, it, s_intra, lane);
@@ -806,8 +814,9 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
 
     __builtin_amdgcn_sched_barrier(0);
     la_update<T, DKP, NW, false>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
-    if (wave == kExpWave && q + 1 < chunks && q % PAIR == PAIR - 1)
-      la_exponents<C, K::kExp, false>(gv, REV, s_out, s_ratio, s_upd, 0.0, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
+    if (!K::kShareP && wave == kExpWave && q + 1 < chunks && q % PAIR == PAIR - 1)
+      la_exponents<C, K::kExp>(gv, REV, s_out, s_ratio, s_upd, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
+    gv = gnext;
     __syncthreads();
     if (dot) {
       if (tid < n) {
@@ -880,17 +889,15 @@ pdssm_linattn_kernel(const LaArgs a) {
 // that leaves nothing (f = 0) are not read, and what it reads last is what the
 // product kernel starts with, still in the caches.
 template <typename T, int DKP, int NW>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kStateWaves))) void
 pdssm_linattn_state_kernel(const LaArgs a) {
   using K = LaTile<T, DKP, NW>;
   using F = typename T::frag;
   constexpr int C = K::C;
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char* Y = smem;
-  unsigned char* Z = smem + K::kX;
-  float* exps = (float*)(smem + K::kX + K::kZ);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n32 = lane & 31;
+  float* ew = (float*)(smem + 2 * (K::kX + K::kZ)) + wave * 64;   // this wave's own copy of the weights
   LaUnit u;
   if (!la_unit(a, blockIdx.x, u)) return;
   const int slab = u.slab, hd = u.hd, sid = u.sid;
@@ -914,54 +921,75 @@ pdssm_linattn_state_kernel(const LaArgs a) {
   const int64_t goff = (lane & (C - 1)) * a.g.st + (lane / C) * dg;
   const float s_upd = J.s_upd;
   float gv = 0.0f;
-  constexpr int kExpWave = NW - 1, PAIR = K::PAIR;
+  constexpr int PAIR = K::PAIR;
   auto fetch = [&](int n) {
     ty.fetch(n);
     tz.fetch(n);
   };
-  auto fetch_g = [&](int n, int rest) {
-    if (wave == kExpWave) gv = (lane & (C - 1)) < (lane < C ? n : rest) ? gp[goff] : 0.0f;
-  };
+  auto fetch_g = [&](int n, int rest) { gv = (lane & (C - 1)) < (lane < C ? n : rest) ? gp[goff] : 0.0f; };
   double sum = 0.0;      // log2 of f
+  // Weights of the next 64 / C chunks.  Every wave forms them for itself: one
+  // wave would do it in the others' way, and they find room between the
+  // matrix instructions.
+  auto weights = [&]() {
+    const double G = la_scan<C>(gv);
+    double tot = la_lane(G, 63), before = sum;
+    sum += tot;
+    if (C == 32) {
+      const double t0 = la_lane(G, 31);
+      sum += t0;
+      if (lane < 32)
+        tot = t0;
+      else
+        before += t0;
+    }
+    ew[lane] = la_exp2((rev ? G : tot - G) + before) * s_upd;
+  };
   if (chunks) {
-    fetch(s.len - first);
     fetch_g(s.len - first, rev ? s.len - C : first);
+    fetch(s.len - first);
   }
   la_f16 S[K::KT];
 #pragma unroll
   for (int t = 0; t < K::KT; ++t) S[t] = la_f16{};
   uint32_t ycol = T::template col_base<K::XB>(lane, 0);
   uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
-  if (wave == kExpWave) sum = la_exponents<C, K::kExp, true>(gv, rev, 1.0f, 1.0f, s_upd, 0.0, exps, lane);
+  weights();
   int n = s.len - first, at = first;
-  for (int q = 0; q < chunks; ++q) {
+  bool more = chunks > 0;
+  for (int q = 0; more; ++q) {
     if (n > C) n = C;
-    const float* e = exps + (q % (2 * PAIR)) * K::kExp;
     asm volatile("" : "+v"(ycol), "+v"(zcol));
+    // two places for the tiles: one barrier a chunk
+    unsigned char* Y = smem + (q & 1) * (K::kX + K::kZ);
+    unsigned char* Z = Y + K::kX;
     ty.commit(Y, tid, n, whole && n == C);
     tz.commit(Z, tid, n, whole && n == C);
     __syncthreads();
-    if (e[4 * C + 1] == 0.0f) break;
     if (q + 1 < chunks) {
       ty.base += dy;
       tz.base += dz;
       gp += dg;
+      if (q % PAIR == PAIR - 1) fetch_g(rev ? s.len - at - C : C, rev ? s.len - at - 2 * C : at - C);   // waited for first
       fetch(rev ? s.len - at - C : C);
-      if (q % PAIR == PAIR - 1) fetch_g(rev ? s.len - at - C : C, rev ? s.len - at - 2 * C : at - C);
+    } else {
+      gv = 0.0f;
     }
     F zf[C / 16];
 #pragma unroll
     for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB>(Z, zcol, 16 * js, 0);
-    la_update<T, DKP, NW, true>(S, Y, ycol, zf, e + 3 * C, 1.0f, lane);
-    if (wave == kExpWave && q + 1 < chunks && q % PAIR == PAIR - 1)
-      sum += la_exponents<C, K::kExp, true>(gv, rev, 1.0f, 1.0f, s_upd, sum, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
-    __syncthreads();
+    la_update<T, DKP, NW, true>(S, Y, ycol, zf, ew + q % PAIR * C, 1.0f, lane);
     at += (int)dir;
     n = rev ? s.len - at : C;
+    more = q + 1 < chunks;
+    if (q % PAIR == PAIR - 1) {
+      more = more && !(__builtin_amdgcn_readfirstlane((int)(sum < -200.0)));   // f = 0
+      weights();
+    }
   }
   const long long to = ((long long)(sid + (rev ? -1 : 1)) * a.H + hd);
   la_store_state<K::KT>(S, J.seg_out + to * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
-  if (slab == 0 && wave == kExpWave && lane == 0) J.seg_decay[to] = la_exp2(sum);
+  if (slab == 0 && tid == 0) J.seg_decay[to] = la_exp2(sum);
 }
 
 }  // namespace pdscan
