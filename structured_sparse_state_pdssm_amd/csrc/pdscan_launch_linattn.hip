@@ -344,21 +344,21 @@ hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
 }
 
 // The product kernels, by type, x-row width and waves.
-hipError_t launch_linattn_form(const LaArgs& args, int bf16, int pieces, hipStream_t st) {
+hipError_t launch_linattn_form(const LaArgs& args, int bf16, int pass, hipStream_t st) {
   LaArgs a = args;
   a.dies = la_dies((long long)a.segs * (a.H / a.ratio));
   const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DK, a.job[0].DV, bf16);
   const long long grid = la_grid(a);
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;
   if (bf16)
-    return dk == 32    ? la_bf16_32(a, nw, pieces, (unsigned)grid, st)
-           : dk == 64  ? la_bf16_64(a, nw, pieces, (unsigned)grid, st)
-           : dk == 128 ? la_bf16_128(a, nw, pieces, (unsigned)grid, st)
-                       : la_bf16_256(a, nw, pieces, (unsigned)grid, st);
-  return dk == 32    ? la_f32_32(a, nw, pieces, (unsigned)grid, st)
-         : dk == 64  ? la_f32_64(a, nw, pieces, (unsigned)grid, st)
-         : dk == 128 ? la_f32_128(a, nw, pieces, (unsigned)grid, st)
-                     : la_f32_256(a, nw, pieces, (unsigned)grid, st);
+    return dk == 32    ? la_bf16_32(a, nw, pass, (unsigned)grid, st)
+           : dk == 64  ? la_bf16_64(a, nw, pass, (unsigned)grid, st)
+           : dk == 128 ? la_bf16_128(a, nw, pass, (unsigned)grid, st)
+                       : la_bf16_256(a, nw, pass, (unsigned)grid, st);
+  return dk == 32    ? la_f32_32(a, nw, pass, (unsigned)grid, st)
+         : dk == 64  ? la_f32_64(a, nw, pass, (unsigned)grid, st)
+         : dk == 128 ? la_f32_128(a, nw, pass, (unsigned)grid, st)
+                     : la_f32_256(a, nw, pass, (unsigned)grid, st);
 }
 
 }  // namespace pdscan

@@ -420,6 +420,7 @@ struct LaTile {
   static constexpr size_t kX = (size_t)C * XB, kZ = (size_t)C * ZB, kP = kShareP ? (size_t)C * PB : 0;
   static constexpr int PAIR = 64 / C;            // chunks whose exponents are formed at once
   static constexpr size_t kSmall = (size_t)(2 * PAIR * kExp + NW * C) * 4;
+  static constexpr int pieces(int mode) { return kF32 ? 1 : mode == kLaQ || mode == kLaK ? 3 : 2; }
   static constexpr size_t main_bytes(int np) { return 2 * kX + kZ + np * kP + kSmall; }
   static constexpr size_t state_bytes() { return 2 * (kX + kZ) + (size_t)NW * 64 * 4; }
   using X = LaTileIO<T, C, DKP, NT>;
@@ -565,15 +566,19 @@ __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsign
 }
 
 // o = form(x, y, z) over one segment, head and slab of 32 NW columns.
-// BWD: what only the gradient asks for (w . o per token, states kept, the
-// final product, fp32 outputs).
-template <typename T, int DKP, int NW, int NP, bool REV, bool BWD>
+// MODE: the forward pass, or one of the gradient's jobs.  Those of q and k
+// also give w . o per token (for the log-decay gradient, so with three pieces
+// throughout), those of q and v keep states inside the segment, that of q
+// multiplies the final state with its gradient.
+template <typename T, int DKP, int NW, int MODE>
 __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const LaSeg& s, int sid, int hd, int slab,
                                         unsigned char* smem) {
   using K = LaTile<T, DKP, NW>;
   using E = typename T::store;
   using F = typename T::frag;
-  constexpr int C = K::C, IT = K::IT;
+  constexpr int C = K::C, IT = K::IT, NP = K::pieces(MODE);
+  constexpr bool REV = MODE == kLaK || MODE == kLaV, dot = MODE == kLaQ || MODE == kLaK;
+  constexpr bool keep = MODE == kLaQ || MODE == kLaV;
   unsigned char* X = smem;
   unsigned char* Y = smem + K::kX;
   unsigned char* Z = smem + 2 * K::kX;
@@ -639,11 +644,10 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
   uint32_t prow = n32 * K::PB + (((h * T::kHalf) ^ la_f<K::PB>(n32)) << 4);
 
-  const int oes = BWD && J.o_f32 ? 4 : K::ES;
+  const int oes = dot && J.o_f32 ? 4 : K::ES;
   char* ob = (char*)J.o.p +
              ((int64_t)s.vb * J.o.sb + (int64_t)(hd / J.od) * J.o.sh + (int64_t)(s.t0 + first) * J.o.st + c0) * oes;
   const uint32_t ost = (uint32_t)J.o.st * (uint32_t)oes, ooff = n32 * ost + 8 * h * oes;
-  const bool dot = BWD && J.dot != nullptr;
   const char* wb = nullptr;
   uint32_t wst = 0, woff = 0;
   if (dot) {
@@ -655,7 +659,13 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   int n = s.len - first;                 // steps of this chunk
   int at = first;                        // its first step in the segment
 
-  for (int q = 0; q < chunks; ++q) {
+  int q = 0, stop = chunks;
+  do {
+  if (keep && J.keep) {   // up to the next step whose state is kept
+    const int run = REV ? at % kLaKeep / C + 1 : kLaKeep / C - at % kLaKeep / C;
+    stop = q + run < chunks ? q + run : chunks;
+  }
+  for (; q < stop; ++q) {
     if (n > C) n = C;
     // the operands' places are one exclusive-or away from these: cheaper than the registers to keep them all
     asm volatile("" : "+v"(xrow), "+v"(yrow), "+v"(ycol), "+v"(zcol), "+v"(prow));
@@ -688,10 +698,6 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
       gp += dg;
       fetch(REV ? C : s.len - at - C);
     }
-    if (BWD && !REV && J.keep && at && at % kLaKeep == 0)
-      la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + at) * a.H + hd) * a.state, J.sm, J.sn, J.DK, J.DV,
-                            col, h);
-
     const bool near = __builtin_amdgcn_readfirstlane(__float_as_int(e[4 * C + 1])) != 0;
     if constexpr (K::kShareP) {
       static_assert(IT * IT <= NW, "a score tile per wave");
@@ -794,7 +800,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
           float v[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r) v[r] = o[it][8 * k2 + r];
-          if (BWD && J.o_f32)
+          if (dot && J.o_f32)
             LaF32::store8((float*)oi + 16 * k2, v);
           else
             T::store8((E*)oi + 16 * k2, v);
@@ -826,17 +832,18 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
       }
       wb += (int64_t)dir * wst;
     }
-    if (BWD && REV && J.keep && at && at % kLaKeep == 0)
-      la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + at) * a.H + hd) * a.state, J.sm, J.sn, J.DK, J.DV,
-                            col, h);
     ob += (int64_t)dir * ost;
     at += dir;
     n = REV ? C : s.len - at;
   }
+  if (keep && q < chunks)
+    la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + (REV ? at + C : at)) * a.H + hd) * a.state, J.sm, J.sn,
+                          J.DK, J.DV, col, h);
+  } while (q < chunks);
 
   if (!(REV ? s.first : s.last)) return;
-  if (J.s_fin) la_store_state<K::KT>(S, J.s_fin + unit * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
-  if (BWD && !REV && J.xd_out) {
+  if ((MODE == kLaFwd || MODE == kLaV) && J.s_fin) la_store_state<K::KT>(S, J.s_fin + unit * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
+  if (MODE == kLaQ && J.xd_out) {
     // final state . its gradient
     la_f16 R[K::KT];
     la_load_state<K::KT>(R, J.xd_with + unit * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
@@ -862,22 +869,26 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   }
 }
 
-template <typename T, int DKP, int NW, int NP, bool BWD>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::waves(BWD)))) void
-pdssm_linattn_kernel(const LaArgs a) {
+// JOBS: the modes of its jobs, a bit each.
+template <typename T, int DKP, int NW, int JOBS>
+__global__ __launch_bounds__(NW * 64)
+    __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::waves(JOBS != 1 << kLaFwd)))) void
+    pdssm_linattn_kernel(const LaArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const unsigned id = blockIdx.x;
   if (id == 0 && threadIdx.x < 2) a.header[threadIdx.x] = 0;
   LaUnit u;
   if (!la_unit(a, id, u)) return;
-  const int slab = u.slab, hd = u.hd, sid = u.sid;
-  const LaJob& J = a.job[BWD ? u.job : 0];
+  const LaJob& J = a.job[u.job];
   LaSeg s;
-  if (!la_segment(a, sid, s)) return;
-  if (BWD && J.rev)
-    la_body<T, DKP, NW, NP, BWD, BWD>(a, J, s, sid, hd, slab, smem);
-  else
-    la_body<T, DKP, NW, NP, false, BWD>(a, J, s, sid, hd, slab, smem);
+  if (!la_segment(a, u.sid, s)) return;
+  if constexpr (JOBS & 1 << kLaFwd) la_body<T, DKP, NW, kLaFwd>(a, J, s, u.sid, u.hd, u.slab, smem);
+  if constexpr (JOBS & 1 << kLaQ)
+    if (J.mode == kLaQ) la_body<T, DKP, NW, kLaQ>(a, J, s, u.sid, u.hd, u.slab, smem);
+  if constexpr (JOBS & 1 << kLaK)
+    if (J.mode == kLaK) la_body<T, DKP, NW, kLaK>(a, J, s, u.sid, u.hd, u.slab, smem);
+  if constexpr (JOBS & 1 << kLaV)
+    if (J.mode == kLaV) la_body<T, DKP, NW, kLaV>(a, J, s, u.sid, u.hd, u.slab, smem);
 }
 
 // Contribution of one segment to the state behind it (before it, for a

@@ -364,14 +364,14 @@ int pdssm_linattn_fwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
     if (d.packed)
       e = pdscan::launch_linattn_table(cu_seqlens, (int32_t*)(ws + w.table), (int32_t*)(ws + w.starts), d.B, d.L,
                                        w.split.seg, w.split.segs, st);
-    if (e == hipSuccess) e = pdscan::launch_linattn_form(a, bf16, 0, st);
+    if (e == hipSuccess) e = pdscan::launch_linattn_form(a, bf16, pdscan::kLaPassState, st);
     pdscan::LaCarryArgs c = {};
     c.c[0].seg = J.seg_out; c.c[0].decay = J.seg_decay; c.c[0].user = h0; c.c[0].rev = 0;
     c.starts = d.packed ? (const int32_t*)(ws + w.starts) : nullptr;
     c.B = d.B; c.H = d.H; c.nseg = w.split.nseg; c.state = a.state;
     if (e == hipSuccess) e = pdscan::launch_linattn_carry(c, 1, st);
   }
-  if (e == hipSuccess) e = pdscan::launch_linattn_form(a, bf16, 2, st);
+  if (e == hipSuccess) e = pdscan::launch_linattn_form(a, bf16, pdscan::kLaPassFwd, st);
   return launched(e);
 }
 
@@ -455,6 +455,8 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   k_job.s_out = 1.0f;
   k_job.s_ratio = k_job.s_upd = d.scale;
   k_job.rev = 1;
+  q_job.mode = pdscan::kLaQ;
+  k_job.mode = pdscan::kLaK;
   q_job.od = k_job.od = 1;
   q_job.o_f32 = k_job.o_f32 = fold;
   // dv: the reversed form of (k, q, do)
@@ -469,6 +471,7 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   v_job.s_out = 1.0f;
   v_job.s_ratio = v_job.s_upd = d.scale;
   v_job.rev = 1;
+  v_job.mode = pdscan::kLaV;
 
   if (w.subs > 1) {
     q_job.keep = (float*)(ws + w.keepS);
@@ -493,7 +496,7 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
     s.job[1] = v_job;
     s.job[1].seg_out = (float*)(ws + w.segR);
     s.job[1].seg_decay = (float*)(ws + w.decR);
-    if (e == hipSuccess) e = pdscan::launch_linattn_form(s, bf16, 0, st);
+    if (e == hipSuccess) e = pdscan::launch_linattn_form(s, bf16, pdscan::kLaPassState, st);
     pdscan::LaCarryArgs c = {};
     c.c[0].seg = s.job[0].seg_out; c.c[0].decay = s.job[0].seg_decay; c.c[0].user = h0; c.c[0].rev = 0;
     c.c[1].seg = s.job[1].seg_out; c.c[1].decay = s.job[1].seg_decay; c.c[1].user = g_hL; c.c[1].rev = 1;
@@ -510,12 +513,12 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
     m.job[2] = v_job;
     m.njobs = 3;
   }
-  if (e == hipSuccess) e = pdscan::launch_linattn_form(m, bf16, 3, st);
+  if (e == hipSuccess) e = pdscan::launch_linattn_form(m, bf16, w.one ? pdscan::kLaPassQKV : pdscan::kLaPassQK, st);
   if (!w.one) {
     m.slabs = w.vslabs;
     m.job[0] = v_job;
     m.njobs = 1;
-    if (e == hipSuccess) e = pdscan::launch_linattn_form(m, bf16, 3, st);
+    if (e == hipSuccess) e = pdscan::launch_linattn_form(m, bf16, pdscan::kLaPassV, st);
   }
   pdscan::LaDecayArgs g = {};
   g.c = a;

@@ -20,8 +20,8 @@ struct LaCarryArgs {
   long long state;
 };
 
-// pieces 0: the state pass, 2: forward, 3: gradient (fp32 inputs are not cut)
-hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pieces, hipStream_t st);
+enum { kLaPassState, kLaPassFwd, kLaPassQK, kLaPassV, kLaPassQKV };
+hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pass, hipStream_t st);
 hipError_t launch_linattn_table(const int32_t* cu, int32_t* table, int32_t* starts, int B, int L, int seg, int segs,
                                 hipStream_t st);
 hipError_t launch_linattn_carry(const LaCarryArgs& a, int passes, hipStream_t st);
@@ -29,7 +29,7 @@ hipError_t launch_linattn_decay(const LaDecayArgs& a, hipStream_t st);
 hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st);
 hipError_t launch_linattn_step(const LaStepArgs& a, hipStream_t st);
 
-#define PDSCAN_LA_LAUNCHER(name) hipError_t name(const LaArgs& a, int nw, int pieces, unsigned grid, hipStream_t st)
+#define PDSCAN_LA_LAUNCHER(name) hipError_t name(const LaArgs& a, int nw, int pass, unsigned grid, hipStream_t st)
 PDSCAN_LA_LAUNCHER(la_bf16_32);
 PDSCAN_LA_LAUNCHER(la_bf16_64);
 PDSCAN_LA_LAUNCHER(la_bf16_128);

@@ -15,6 +15,8 @@ constexpr int kLaKeep = 512;     // steps of a segment between states kept for t
 constexpr double kLaNear = 24.0; // log2 of the decay over a chunk up to which it is split into factors of its tokens
 constexpr int kLaHeader = 256;   // workspace header: word 1 stays zero (nothing here waits on another workgroup)
 
+enum { kLaFwd, kLaQ, kLaK, kLaV };   // jobs of the product kernel
+
 // A strided tensor: element strides of the batch, head and step axes; the
 // last axis is contiguous.
 struct LaView {
@@ -38,7 +40,8 @@ struct LaJob {
   float* dot;                  // w . o per token [slab][H][rows], NULL: none
   int sm, sn;                  // strides of a state's x-row and z-row axes
   float s_out, s_ratio, s_upd; // scale of the output, of its own tokens' part beside the state's, of the update
-  int rev;                     // 1: backwards in time
+  int mode;                    // kLaFwd ..
+  int rev;                     // 1: backwards in time (kLaK and kLaV)
   int o_f32;                   // 1: o is fp32 whatever the inputs' type
 };
 
