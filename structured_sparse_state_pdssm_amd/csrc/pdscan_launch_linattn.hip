@@ -190,8 +190,11 @@ __global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const doub
   if (threadIdx.x == 0) out[h] = (float)x;
 }
 
+// Sum over the value heads of a query or key head, of g_q (y = 0) and g_k.
 template <typename T>
 __global__ __launch_bounds__(256) void pdssm_linattn_fold_kernel(const LaFoldArgs a) {
+  const float* part = blockIdx.y ? a.part_k : a.part_q;
+  const LaView& out = blockIdx.y ? a.out_k : a.out_q;
   const int Hk = a.H / a.ratio, c4 = a.d / 4;
   long long r0 = 0, r1 = a.rows;
   if (a.cu) {   // rows outside the sequences stay as they are
@@ -205,14 +208,14 @@ __global__ __launch_bounds__(256) void pdssm_linattn_fold_kernel(const LaFoldArg
     const int c = (int)(q % c4) * 4;
     const int hk = (int)(q / c4 % Hk);
     const long long row = r0 + q / c4 / Hk;
-    const float* p = a.part + (row * a.H + (long long)hk * a.ratio) * a.d + c;
+    const float* p = part + (row * a.H + (long long)hk * a.ratio) * a.d + c;
     float v[4] = {0, 0, 0, 0};
     for (int r = 0; r < a.ratio; ++r) {
       const float4 w = *(const float4*)(p + (long long)r * a.d);
       v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
     }
     const int64_t b = a.cu ? 0 : row / a.L, t = a.cu ? row : row % a.L;
-    T::store4((typename T::store*)a.out.p + b * a.out.sb + hk * a.out.sh + t * a.out.st + c, v);
+    T::store4((typename T::store*)out.p + b * out.sb + hk * out.sh + t * out.st + c, v);
   }
 }
 
@@ -337,9 +340,9 @@ hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
   if (grid > 8192) grid = 8192;
   if (grid < 1) grid = 1;
   if (a.bf16)
-    hipLaunchKernelGGL(pdssm_linattn_fold_kernel<LaBf16>, dim3((unsigned)grid), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(pdssm_linattn_fold_kernel<LaBf16>, dim3((unsigned)grid, 2), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL(pdssm_linattn_fold_kernel<LaF32>, dim3((unsigned)grid), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(pdssm_linattn_fold_kernel<LaF32>, dim3((unsigned)grid, 2), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

@@ -67,7 +67,7 @@ __device__ __forceinline__ constexpr int la_f(int r) {
 struct LaBf16 {
   using store = uint16_t;
   static constexpr int kVec = 8;    // elements of 16 bytes
-  static constexpr int kHalf = 1;   // 16-byte units of eight elements
+  static constexpr int kPlanes = 1; // bf16 values that an element is in LDS
   union frag {
     uint32_t u[4];
     uint4 w;
@@ -89,7 +89,8 @@ struct LaBf16 {
       v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
     }
   }
-  // eight elements of a row at byte address a
+  // eight elements of a row at byte address a (PS: bytes of a plane)
+  template <int PS>
   static __device__ __forceinline__ frag row(const unsigned char* a) {
     frag f;
     f.w = *(const uint4*)a;
@@ -106,7 +107,7 @@ struct LaBf16 {
     const int unit = c0 / 8 + ((lane & 16) >> 3) + (c4 >> 1);
     return r * RB + ((unit ^ la_f<RB>(r)) << 4) + (c4 & 1) * 8;
   }
-  template <int RB>
+  template <int RB, int PS>
   static __device__ __forceinline__ frag col(const unsigned char* lds, uint32_t base, int r0, int tile) {
     const uint32_t b = base ^ (uint32_t)(tile * 64);
     frag f;
@@ -134,6 +135,11 @@ struct LaBf16 {
     }
   }
   static __device__ __forceinline__ void put(unsigned char* a, const frag& f) { *(uint4*)a = f.w; }
+  // 16 bytes of a row from memory to their place, column c in it, of a row of RB bytes (XOR x from its swizzle)
+  template <int RB, int PS>
+  static __device__ __forceinline__ void put_row(unsigned char* lds, int row, int c, uint32_t x, const uint4& w) {
+    *(uint4*)(lds + ((row * RB + (((c >> 3) ^ la_f<RB>(row)) << 4)) ^ x)) = w;
+  }
   static __device__ __forceinline__ uint32_t round2(float x, float y) {   // nearest, ties to even
     const la_f2 v = {x, y};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, la_bf2));
@@ -153,18 +159,28 @@ struct LaBf16 {
   }
 };
 
+// fp32 elements are three bf16 pieces in LDS, a plane each, cut so that their
+// sum is the element; of the nine products of two elements the six of weight
+// 2^-16 and up are formed, which leaves 2^-23 of a term.  Six bf16 products
+// take 3/8 of the time of the fp32 ones.
 struct LaF32 {
   using store = float;
   static constexpr int kVec = 4;
-  static constexpr int kHalf = 2;
+  static constexpr int kPlanes = 3;
   struct frag {
-    float f[8];
+    LaBf16::frag p[3];
   };
   static __device__ __forceinline__ void mma(la_f16& c, const frag& a, const frag& b) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.f[e], b.f[e], c, 0, 0, 0);
+    LaBf16::mma(c, a.p[0], b.p[2]);
+    LaBf16::mma(c, a.p[2], b.p[0]);
+    LaBf16::mma(c, a.p[1], b.p[1]);
+    LaBf16::mma(c, a.p[0], b.p[1]);
+    LaBf16::mma(c, a.p[1], b.p[0]);
+    LaBf16::mma(c, a.p[0], b.p[0]);
   }
-  static __device__ __forceinline__ float get(const frag& f, int e) { return f.f[e]; }
+  static __device__ __forceinline__ float get(const frag& f, int e) {
+    return (LaBf16::get(f.p[0], e) + LaBf16::get(f.p[1], e)) + LaBf16::get(f.p[2], e);
+  }
   static __device__ __forceinline__ void unpack(const uint4* p, float* v) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -174,33 +190,42 @@ struct LaF32 {
       v[4 * u + 3] = __uint_as_float(p[u].w);
     }
   }
+  template <int PS>
   static __device__ __forceinline__ frag row(const unsigned char* a) {
     frag f;
-    *(float4*)&f.f[0] = *(const float4*)a;
-    *(float4*)&f.f[4] = *(const float4*)((uintptr_t)a ^ 16);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) f.p[p] = LaBf16::row<0>(a + p * PS);
     return f;
   }
   template <int RB>
   static __device__ __forceinline__ uint32_t col_base(int lane, int c0) {
-    const int r = 8 * (lane >> 5), c = c0 + la_pi(lane & 31);
-    return r * RB + (((c >> 2) ^ la_f<RB>(r)) << 4) + (c & 3) * 4;
+    return LaBf16::col_base<RB>(lane, c0);
   }
-  template <int RB>
+  template <int RB, int PS>
   static __device__ __forceinline__ frag col(const unsigned char* lds, uint32_t base, int r0, int tile) {
-    const uint32_t b = base ^ (uint32_t)(tile * 128);
     frag f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f.f[e] = *(const float*)(lds + (b ^ (uint32_t)(la_f<RB>(e) << 4)) + (r0 + e) * RB);
+    for (int p = 0; p < 3; ++p) f.p[p] = LaBf16::col<RB, 0>(lds + p * PS, base, r0, tile);
     return f;
   }
   template <int NP>
   static __device__ __forceinline__ void pieces(const float* v, frag* out) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[0].f[e] = v[e];
+    LaBf16::pieces<3>(v, out[0].p);
   }
-  static __device__ __forceinline__ void put(unsigned char* a, const frag& f) {
-    *(float4*)a = *(const float4*)&f.f[0];
-    *(float4*)((uintptr_t)a ^ 16) = *(const float4*)&f.f[4];
+  static __device__ __forceinline__ void put(unsigned char*, const frag&) {}
+  template <int RB, int PS>
+  static __device__ __forceinline__ void put_row(unsigned char* lds, int row, int c, uint32_t x, const uint4& w) {
+    unsigned char* a = lds + ((row * RB + (((c >> 3) ^ la_f<RB>(row)) << 4) + (c & 4) * 2) ^ x);
+    uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      *(uint2*)(a + p * PS) = make_uint2(__builtin_amdgcn_perm(v[1], v[0], 0x07060302u),
+                                         __builtin_amdgcn_perm(v[3], v[2], 0x07060302u));
+      if (p < 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = __float_as_uint(__uint_as_float(v[e]) - __uint_as_float(v[e] & 0xffff0000u));
+    }
   }
   static __device__ __forceinline__ void store4(store* p, const float* v) {
     *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
@@ -283,7 +308,7 @@ __device__ __forceinline__ const typename T::store* la_ptr(const LaView& v, int 
 template <typename T, int C, int W, int NT>
 struct LaTileIO {
   using E = typename T::store;
-  static constexpr int kCols = W / T::kVec, RP = NT / kCols, N = C / RP, RB = W * (int)sizeof(E);
+  static constexpr int kCols = W / T::kVec, RP = NT / kCols, N = C / RP, RB = W * 2, PS = C * RB;
   static_assert(RP * kCols == NT && N * RP == C, "whole passes");
   uint4 r[N];
   const char* base;      // the chunk under way
@@ -312,14 +337,15 @@ struct LaTileIO {
     }
   }
   __device__ __forceinline__ void commit(unsigned char* lds, int tid, int n, bool whole) {
-    const uint32_t a = row0 * RB + (((tid % kCols) ^ la_f<RB>(row0)) << 4);
     if (!whole) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (!ok || row0 + i * RP >= n) r[i] = make_uint4(0, 0, 0, 0);
     }
+    const int c = tid % kCols * T::kVec;
 #pragma unroll
-    for (int i = 0; i < N; ++i) *(uint4*)(lds + (a ^ (uint32_t)(la_f<RB>(i * RP) << 4)) + i * RP * RB) = r[i];
+    for (int i = 0; i < N; ++i)
+      T::template put_row<RB, PS>(lds + i * RP * RB, row0, c, (uint32_t)(la_f<RB>(i * RP) << 4), r[i]);
   }
 };
 
@@ -402,22 +428,23 @@ __device__ __forceinline__ void la_exponents(float g, int rev, float s_out, floa
 template <typename T, int DKP, int NW>
 struct LaTile {
   static constexpr bool kF32 = sizeof(typename T::store) == 4;
-  // Tokens of a chunk.  64 where four waves share the scores; else 32, which
+  // Tokens of a chunk.  64 where four waves share the scores (bf16); else 32, which
   // halves the registers and the LDS of a workgroup (two to three waves a SIMD
   // instead of one: 24 heads of 64/32 at 16 x 2048 tokens 122 -> 104 us).
-  static constexpr int C = NW < 4 || (kF32 && DKP == 256) ? 32 : 64;
+  static constexpr int C = NW < 4 || kF32 ? 32 : 64;
   static constexpr int NT = NW * 64;
   static constexpr int IT = C / 32;              // 32-token tiles of a chunk
   static constexpr int KT = DKP / 32;            // 32-row tiles of the state
   static constexpr int WV = kF32 ? 2 : 1;        // 16-byte units of eight elements
   static constexpr int NPS = kF32 ? 1 : 3;       // pieces of the state's update
-  // One or two waves form all scores of the chunk each, in registers; four
-  // share them through LDS (each wave forms one tile of 32 x 32).
-  static constexpr bool kShareP = NW == 4;
+  // One or two waves form all scores of the chunk each, in registers, and so do
+  // four in fp32; four in bf16 share them through LDS (a tile of 32 x 32 each).
+  static constexpr bool kShareP = NW == 4 && !kF32;
   static constexpr int ES = (int)sizeof(typename T::store);
-  static constexpr int XB = DKP * ES, ZB = NW * 32 * ES, PB = C * ES;   // bytes of a row
+  static constexpr int XB = DKP * 2, ZB = NW * 64, PB = C * 2;   // bytes of a row in LDS
+  static constexpr int XP = C * XB, ZP = C * ZB;                 // and of a plane
   static constexpr int kExp = 4 * C + 4;         // floats of one chunk's exponents
-  static constexpr size_t kX = (size_t)C * XB, kZ = (size_t)C * ZB, kP = kShareP ? (size_t)C * PB : 0;
+  static constexpr size_t kX = (size_t)T::kPlanes * XP, kZ = (size_t)T::kPlanes * ZP, kP = kShareP ? (size_t)C * PB : 0;
   static constexpr int PAIR = 64 / C;            // chunks whose exponents are formed at once
   static constexpr size_t kSmall = (size_t)(2 * PAIR * kExp + NW * C) * 4;
   static constexpr int pieces(int mode) { return kF32 ? 1 : mode == kLaQ || mode == kLaK ? 3 : 2; }
@@ -454,7 +481,7 @@ __device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const unsigned 
     T::template pieces<K::NPS>(v, b);
 #pragma unroll
     for (int t = 0; t < K::KT; ++t) {
-      const typename T::frag y = T::template col<K::XB>(Y, ycol, 16 * js, t);
+      const typename T::frag y = T::template col<K::XB, K::XP>(Y, ycol, 16 * js, t);
 #pragma unroll
       for (int p = 0; p < K::NPS; ++p) T::mma(S[t], y, b[p]);
     }
@@ -524,8 +551,8 @@ __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsign
   la_f16 c = {};
 #pragma unroll
   for (int ks = 0; ks < DKP / 16; ++ks)
-    T::mma(c, T::row(Y + (yrow ^ (uint32_t)(ks * 32 * T::kHalf)) + jt * 32 * K::XB),
-           T::row(X + (xrow ^ (uint32_t)(ks * 32 * T::kHalf)) + it * 32 * K::XB));
+    T::mma(c, T::template row<K::XP>(Y + (yrow ^ (uint32_t)(ks * 32)) + jt * 32 * K::XB),
+           T::template row<K::XP>(X + (xrow ^ (uint32_t)(ks * 32)) + it * 32 * K::XB));
   const int j0 = 32 * jt + 8 * h;
   if (near) {
 #pragma unroll
@@ -638,11 +665,11 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   if (wave == kExpWave) la_exponents<C, K::kExp>(g0, REV, J.s_out, J.s_ratio, J.s_upd, exps, lane);
 
   // lane offsets of the operands in LDS
-  uint32_t xrow = n32 * K::XB + (((h * T::kHalf) ^ la_f<K::XB>(n32)) << 4);
-  uint32_t yrow = pm * K::XB + (((h * T::kHalf) ^ la_f<K::XB>(pm)) << 4);
+  uint32_t xrow = n32 * K::XB + ((h ^ la_f<K::XB>(n32)) << 4);
+  uint32_t yrow = pm * K::XB + ((h ^ la_f<K::XB>(pm)) << 4);
   uint32_t ycol = T::template col_base<K::XB>(lane, 0);
   uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
-  uint32_t prow = n32 * K::PB + (((h * T::kHalf) ^ la_f<K::PB>(n32)) << 4);
+  uint32_t prow = n32 * K::PB + ((h ^ la_f<K::PB>(n32)) << 4);
 
   const int oes = dot && J.o_f32 ? 4 : K::ES;
   char* ob = (char*)J.o.p +
@@ -715,7 +742,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
           T::template pieces<NP>(v, pp);
 #pragma unroll
           for (int p = 0; p < NP; ++p)
-            T::put(P + p * K::kP + (prow ^ (uint32_t)((2 * jt + k2) * 32 * T::kHalf)) + it * 32 * K::PB, pp[p]);
+            T::put(P + p * K::kP + (prow ^ (uint32_t)((2 * jt + k2) * 32)) + it * 32 * K::PB, pp[p]);
         }
       }
     }
@@ -735,7 +762,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
         T::template pieces<NP>(v, sp);
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
-          const F xb = T::row(X + (xrow ^ (uint32_t)((2 * t4 + k2) * 32 * T::kHalf)) + it * 32 * K::XB);
+          const F xb = T::template row<K::XP>(X + (xrow ^ (uint32_t)((2 * t4 + k2) * 32)) + it * 32 * K::XB);
 #pragma unroll
           for (int p = 0; p < NP; ++p) T::mma(o[it], sp[p], xb);
         }
@@ -753,7 +780,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     // what the chunk's own tokens give
     F zf[C / 16];
 #pragma unroll
-    for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB>(Z, zcol, 16 * js, 0);
+    for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB, K::ZP>(Z, zcol, 16 * js, 0);
     if constexpr (K::kShareP) {
       __syncthreads();
 #pragma unroll
@@ -763,7 +790,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
           if (REV ? js < 2 * it : js >= 2 * it + 2) continue;
 #pragma unroll
           for (int p = 0; p < NP; ++p)
-            T::mma(o[it], zf[js], T::row(P + p * K::kP + (prow ^ (uint32_t)(js * 32 * T::kHalf)) + it * 32 * K::PB));
+            T::mma(o[it], zf[js], T::template row<0>(P + p * K::kP + (prow ^ (uint32_t)(js * 32)) + it * 32 * K::PB));
         }
     } else {
 #pragma unroll
@@ -988,7 +1015,7 @@ pdssm_linattn_state_kernel(const LaArgs a) {
     }
     F zf[C / 16];
 #pragma unroll
-    for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB>(Z, zcol, 16 * js, 0);
+    for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB, K::ZP>(Z, zcol, 16 * js, 0);
     la_update<T, DKP, NW, true>(S, Y, ycol, zf, ew + q % PAIR * C, 1.0f, lane);
     at += (int)dir;
     n = rev ? s.len - at : C;

@@ -176,7 +176,8 @@ FwdWs fwd_ws(const pdssm_linattn_dims* d) {
   FwdWs w;
   const int bf16 = d->in_dtype == PDSSM_BF16;
   w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * pdscan::la_slabs(d->dk, d->dv, bf16),
-                             kCus * pdscan::la_resident(d->dk, d->dv, bf16, 0));
+                             kCus * pdscan::la_resident(d->dk, d->dv, bf16, 0), (long long)d->dk * d->dv,
+                             (2 * d->dk + 2 * d->dv) * (bf16 ? 2 : 4));
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -214,7 +215,8 @@ BwdWs bwd_ws(const pdssm_linattn_dims* d) {
           pdscan::la_waves(d->dk, d->dv, bf16) == pdscan::la_waves(d->dv, d->dk, bf16);
   // the launch with the most work decides: all three jobs in one, or those of q and k
   w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * (w.one ? 3 : 2) * w.qslabs,
-                             kCus * pdscan::la_resident(d->dv, d->dk, bf16, 1));
+                             kCus * pdscan::la_resident(d->dv, d->dk, bf16, 1), 2ll * d->dk * d->dv,
+                             (8 * d->dk + 7 * d->dv) * (bf16 ? 2 : 4));
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -540,11 +542,10 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
     f.cu = cu_seqlens;
     f.B = d.B; f.H = d.H; f.L = d.L; f.ratio = ratio; f.d = d.dk; f.bf16 = bf16;
     f.rows = a.rows;
-    f.part = (const float*)(ws + w.fq);
-    f.out = gq;
-    if (e == hipSuccess) e = pdscan::launch_linattn_fold(f, st);
-    f.part = (const float*)(ws + w.fk);
-    f.out = gk;
+    f.part_q = (const float*)(ws + w.fq);
+    f.part_k = (const float*)(ws + w.fk);
+    f.out_q = gq;
+    f.out_k = gk;
     if (e == hipSuccess) e = pdscan::launch_linattn_fold(f, st);
   }
   return launched(e);

@@ -8,7 +8,7 @@
 
 namespace pdscan {
 
-constexpr int kLaChunk = 64;     // tokens per step of a sequence's serial axis (32 for wide fp32 rows)
+constexpr int kLaChunk = 64;     // segments are multiples of this: one or two chunks
 constexpr int kLaMaxD = 256;     // widest key or value row
 constexpr int kLaMaxStep = 1 << 23;   // longest step stride, elements: 64 rows stay within 31 bits of bytes
 constexpr int kLaKeep = 512;     // steps of a segment between states kept for the log-decay gradient
@@ -85,8 +85,8 @@ struct LaDecayArgs {
 
 // Sum over the value heads that share a query or key head.
 struct LaFoldArgs {
-  const float* part;           // [rows][H][d]
-  LaView out;
+  const float *part_q, *part_k;   // [rows][H][d]
+  LaView out_q, out_k;
   const int32_t* cu;
   int B, H, L, ratio, d, bf16;
   long long rows;
@@ -113,9 +113,9 @@ inline constexpr int la_simd_waves(int regs, bool f32, bool bwd) {
 // and by those waves.
 inline int la_resident(int DK, int DV, int bf16, int bwd) {
   const int es = bf16 ? 2 : 4, nw = la_waves(DK, DV, bf16), d = la_pad(DK);
-  const int C = nw < 4 || (!bf16 && d == 256) ? 32 : 64;
-  const int np = bf16 ? bwd ? 3 : 2 : 1;
-  const int lds = C * es * (2 * d + 32 * nw) + (nw == 4 ? np * C * C * es : 0) + 4 * (64 / C * (8 * C + 8) + nw * C);
+  const int C = nw < 4 || !bf16 ? 32 : 64;
+  const int lds = C * (bf16 ? 2 : 6) * (2 * d + 32 * nw) + (nw == 4 && bf16 ? (bwd ? 3 : 2) * C * C * 2 : 0) +
+                  4 * (64 / C * (8 * C + 8) + nw * C);
   const int regs = (d + C) / 2 + C * es * (2 * d + 32 * nw) / (256 * nw);
   const int waves = 4 * la_simd_waves(regs, !bf16, bwd);
   const int n = 163840 / lds < waves / nw ? 163840 / lds : waves / nw;
@@ -131,19 +131,23 @@ struct LaSplit {
 // segment fills the card once (`room` workgroups).  Whole sequences where
 // they do that, and up to 256 steps: the three launches more cost what the
 // shorter chains save.  Sequences of different lengths take 7/4 of it, so that
-// no long one is left alone at the end.
+// no long one is left alone at the end.  A segment's states are written and
+// read twice; with at least a workgroup a compute unit they stay under half of
+// what its steps (`bytes` each) move.
 //   65536 steps, 16 heads, 128/128 bf16: 32 segments of 2048 434 us, of 1024 459, of 4096 506, uncut over 5000
 //   16 x 2048 steps, 24 heads, 64/32 bf16: 4 segments of 512 104 us, 8 of 256 114, uncut 131
 //   4 x 4096 steps, 8 heads, 16/64 fp32: 128 steps 53 us, 64 63, 256 71
-//   23 sequences in 12001 rows, 24 heads, 128/64 bf16: 320 steps 109 us, 640 117, 128 128
-inline LaSplit la_split(int B, int L, int packed, int width, int room) {
+//   23 sequences in 12001 rows, 24 heads, 128/64 bf16: 384 steps 102 us, 192 107, 640 117
+inline LaSplit la_split(int B, int L, int packed, int width, int room, long long state, int bytes) {
   LaSplit s;
   long long n = (long long)room / (packed ? width : (long long)B * width);   // segments of a sequence
   if (packed) n = n * 7 / 4;
-  if (n > L / kLaChunk) n = L / kLaChunk;
+  const long long least = 256 / (packed ? width : (long long)B * width), most = (long long)L * bytes / (32 * state);
+  if (n > most) n = most > least ? most : least < n ? least : n;
+  if (n > (L - 1) / kLaChunk + 1) n = (L - 1) / kLaChunk + 1;
   s.split = n > 1 && L > 256;
   const long long each = s.split ? ((long long)L + n - 1) / n : L;
-  s.seg = (int)((each + kLaChunk - 1) / kLaChunk * kLaChunk);
+  s.seg = each <= 3 * kLaChunk / 2 && s.split ? kLaChunk : (int)((each + kLaChunk - 1) / kLaChunk * kLaChunk);
   s.nseg = s.split ? (int)(((long long)L + s.seg - 1) / s.seg) : 1;
   const long long segs = !packed ? (long long)B * s.nseg : s.split ? (long long)(L / s.seg) + B : B;
   s.segs = segs > 0x7fffffffll ? 0x7fffffff : (int)segs;
