@@ -50,7 +50,7 @@ __global__ __launch_bounds__(256) void pdssm_linattn_table_kernel(const int32_t*
         e.x = b;
         e.y = t0 + i * seg;
         e.z = len - i * seg < seg ? len - i * seg : seg;
-        e.w = (i == 0 ? 1 : 0) | (i == n - 1 ? 2 : 0);
+        e.w = (i == 0 ? 1 : 0) | (i == n - 1 || at + i == segs - 1 ? 2 : 0);   // nothing is passed on behind the bound
         *(int4*)(table + 4 * (long long)(at + i)) = e;
       }
     }
@@ -106,86 +106,84 @@ __device__ __forceinline__ double block_sum(double x, double* red, int tid) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// d loss / d log a_t of one piece of a segment (kLaKeep steps) and head.
-// Pairs (key at or before t-1, query at or behind t) meet at t, so with
-// r_i = q_i . dq_i (every key before query i) and c_j = k_j . dk_j (every query
-// behind key j)
+// d loss / d log a_t of one segment and head.  Pairs (key at or before t-1,
+// query at or behind t) meet at t, so with r_i = q_i . dq_i (every key before
+// query i, its own left out) and c_j = k_j . dk_j (every query behind key j)
 //   g_t = sum_{i >= t} r_i - sum_{j >= t} c_j + <S_end, dS_end>
-// over the rest of the piece: pairs inside it cancel but for those that meet
-// at t, and the last term holds those that meet behind its end.  The sums run
-// in 64 bits, but r and c carry fp32 errors that do not cancel and grow with
-// the square root of their number: 2048 steps in one sum left 1.6e-6 of the
-// gradient, pieces of 512 half of that, for 2 states stored and read a piece.
-__global__ __launch_bounds__(256) void pdssm_linattn_decay_kernel(const LaDecayArgs a) {
-  __shared__ double red[4];
+// over the rest of the segment: pairs inside it cancel but for those that
+// meet at t, and the last term holds those that meet behind its end.  The
+// sums run in 64 bits, but r and c carry fp32 errors that do not cancel and
+// grow with the square root of their number: 2048 steps in one sum left 1.6e-6
+// of the gradient, the 512 that a segment has at most half of that.
+// One step a thread: a segment is one round of the workgroup.
+__global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaDecayArgs a) {
+  constexpr int W = kLaPiece / 64;
+  __shared__ double red[2][W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.x % a.c.H, piece = blockIdx.x / a.c.H;
-  const int sub = piece % a.subs, sid = piece / a.subs;
+  const int h = blockIdx.x % a.c.H, sid = blockIdx.x / a.c.H;
   LaSeg s;
-  double total = 0.0;
-  if (la_segment(a.c, sid, s) && sub * kLaKeep < s.len) {
-    const int lo = sub * kLaKeep, hi = lo + kLaKeep < s.len ? lo + kLaKeep : s.len;
-    const float4 *A = nullptr, *R = nullptr;
-    double x = 0.0;
-    if (hi < s.len) {
-      const long long at = (la_keep_slot(a.c, s, s.t0 + hi) * a.c.H + h) * a.c.state;
-      A = (const float4*)(a.kS + at);
-      R = (const float4*)(a.kR + at);
-    } else if (!s.last) {
-      A = (const float4*)(a.sS + ((long long)(sid + 1) * a.c.H + h) * a.c.state);
-      R = (const float4*)(a.sR + ((long long)sid * a.c.H + h) * a.c.state);
-    } else if (a.xd) {
-      for (int w = 0; w < a.xd_slabs; ++w) x += a.xd[((long long)w * a.c.segs + sid) * a.c.H + h];
-    }
-    if (A) {
-      for (int e = tid; e < a.c.state / 4; e += 256) {
-        const float4 p = A[e], q = R[e];
-        x += (double)((p.x * q.x + p.y * q.y) + (p.z * q.z + p.w * q.w));
-      }
-      x = block_sum(x, red, tid);
-    }
-    double carry = x;
-    for (int t1 = hi; t1 > lo; t1 -= 256) {
-      const int t = t1 - 1 - tid;
-      double d = 0.0;
-      if (t >= lo) {
-        const long long at = (long long)h * a.c.rows + s.row0 + t;
-        const long long slab = (long long)a.c.H * a.c.rows;
-        for (int w = 0; w < a.r_slabs; ++w) d += (double)a.r[w * slab + at];
-        for (int w = 0; w < a.k_slabs; ++w) d -= (double)a.k[w * slab + at];
-      }
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) {
-        const double up = __shfl_up(d, m, 64);
-        if (lane >= m) d += up;
-      }
-      __syncthreads();
-      if (lane == 63) red[wave] = d;
-      __syncthreads();
-      double before = carry;
-      for (int w = 0; w < wave; ++w) before += red[w];
-      carry += (red[0] + red[1]) + (red[2] + red[3]);
-      if (t >= lo) {
-        const double g = before + d;
-        if (a.per_head)
-          total += g;
-        else
-          ((float*)a.out.p)[(int64_t)s.vb * a.out.sb + (int64_t)h * a.out.sh + (int64_t)(s.t0 + t) * a.out.st] =
-              (float)g;
-      }
-    }
+  if (!la_segment(a.c, sid, s)) {
+    if (a.per_head && tid == 0) a.part[(long long)sid * a.c.H + h] = 0.0;
+    return;
   }
-  if (a.per_head) {
-    total = block_sum(total, red, tid);
-    if (tid == 0) a.part[(long long)piece * a.c.H + h] = total;
+  const int t = s.len - 1 - tid;
+  double d = 0.0, x = 0.0;
+  if (t >= 0) {
+    const long long at = (long long)h * a.c.rows + s.row0 + t;
+    const long long slab = (long long)a.c.H * a.c.rows;
+    for (int w = 0; w < a.r_slabs; ++w) d += (double)a.r[w * slab + at];
+    for (int w = 0; w < a.k_slabs; ++w) d -= (double)a.k[w * slab + at];
+  }
+  if (!s.last) {
+    const float4* A = (const float4*)(a.sS + ((long long)(sid + 1) * a.c.H + h) * a.c.state);
+    const float4* R = (const float4*)(a.sR + ((long long)sid * a.c.H + h) * a.c.state);
+    for (int e = tid; e < a.c.state / 4; e += kLaPiece) {
+      const float4 p = A[e], q = R[e];
+      x += (double)((p.x * q.x + p.y * q.y) + (p.z * q.z + p.w * q.w));
+    }
+  } else if (a.xd && tid < a.xd_slabs) {
+    x = a.xd[((long long)tid * a.c.segs + sid) * a.c.H + h];
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const double up = __shfl_up(d, m, 64);
+    if (lane >= m) d += up;
+  }
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m, 64);
+  if (lane == 63) {
+    red[0][wave] = d;
+    red[1][wave] = x;
+  }
+  __syncthreads();
+  double g = d;
+  for (int w = 0; w < W; ++w) {
+    g += red[1][w];
+    if (w < wave) g += red[0][w];
+  }
+  if (t < 0) g = 0.0;
+  if (!a.per_head) {
+    if (t >= 0)
+      ((float*)a.out.p)[(int64_t)s.vb * a.out.sb + (int64_t)h * a.out.sh + (int64_t)(s.t0 + t) * a.out.st] = (float)g;
+    return;
+  }
+#pragma unroll
+  for (int m = 32; m; m >>= 1) g += __shfl_xor(g, m, 64);
+  __syncthreads();
+  if (lane == 0) red[0][wave] = g;
+  __syncthreads();
+  if (tid == 0) {
+    double sum = 0.0;
+    for (int w = 0; w < W; ++w) sum += red[0][w];
+    a.part[(long long)sid * a.c.H + h] = sum;
   }
 }
 
-__global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int pieces) {
+__global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int segs) {
   __shared__ double red[4];
   const int h = blockIdx.x;
   double x = 0.0;
-  for (int s = threadIdx.x; s < pieces; s += 256) x += part[(long long)s * H + h];
+  for (int s = threadIdx.x; s < segs; s += 256) x += part[(long long)s * H + h];
   x = block_sum(x, red, threadIdx.x);
   if (threadIdx.x == 0) out[h] = (float)x;
 }
@@ -325,12 +323,12 @@ hipError_t launch_linattn_carry(const LaCarryArgs& a, int passes, hipStream_t st
 }
 
 hipError_t launch_linattn_decay(const LaDecayArgs& a, hipStream_t st) {
-  const long long grid = (long long)a.c.segs * a.subs * a.c.H;
+  const long long grid = (long long)a.c.segs * a.c.H;
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(pdssm_linattn_decay_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(pdssm_linattn_decay_kernel, dim3((unsigned)grid), dim3(kLaPiece), 0, st, a);
   if (a.per_head)
     hipLaunchKernelGGL(pdssm_linattn_decay_sum_kernel, dim3((unsigned)a.c.H), dim3(256), 0, st, a.part,
-                       (float*)a.out.p, a.c.H, a.c.segs * a.subs);
+                       (float*)a.out.p, a.c.H, a.c.segs);
   return hipGetLastError();
 }
 

@@ -20,10 +20,10 @@
 //
 // Precision.  bf16 inputs enter the products as they are.  What is computed
 // (the state, the weighted scores, the weighted values) is held in fp32 and
-// enters a product as two or three bf16 pieces x = x0 + x1 (+ x2), each the
-// next eight significant bits: two leave 2^-16 of a term (outputs in bf16
-// are rounded at 2^-9), three are exact but for the last bit (the state is
-// an fp32 output).  fp32 inputs use fp32 products throughout.
+// enters a product as two or three bf16 pieces, each the rest of those before
+// it: two leave 2^-18 of a term (enough for outputs that are rounded to bf16,
+// at 2^-9), three nothing (states and what the log-decay gradient is summed
+// from).  fp32 inputs are three pieces themselves.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -115,23 +115,28 @@ struct LaBf16 {
     f.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s4*)(lds + (b ^ (la_f<RB>(4) << 4)) + (r0 + 4) * RB));
     return f;
   }
-  // eight floats as bf16 pieces, cut (not rounded) so that each rest is exact
+  static __device__ __forceinline__ uint32_t round2(float x, float y) {   // nearest, ties to even
+    const la_f2 v = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, la_bf2));
+  }
+  // two floats rounded to bf16, and what is left of them (exactly)
+  static __device__ __forceinline__ uint32_t split2(float& x, float& y) {
+    const uint32_t w = round2(x, y);
+    x -= __uint_as_float(w << 16);
+    y -= __uint_as_float(w & 0xffff0000u);
+    return w;
+  }
+  // eight floats as bf16 pieces, each the rest of those before rounded to the
+  // nearest: two leave 2^-18 of a value, three nothing.  (Cut pieces cost the
+  // same, leave 2^-16 and all on one side, which adds up over long sums.)
   template <int NP>
   static __device__ __forceinline__ void pieces(const float* v, frag* out) {
-    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = v[e];
+    for (int e = 0; e < 4; ++e) {
+      float x = v[2 * e], y = v[2 * e + 1];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = __float_as_uint(x[2 * e]), hi = __float_as_uint(x[2 * e + 1]);
-        out[p].u[e] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
-        if (p + 1 < NP) {
-          x[2 * e] -= __uint_as_float(lo & 0xffff0000u);
-          x[2 * e + 1] -= __uint_as_float(hi & 0xffff0000u);
-        }
-      }
+      for (int p = 0; p + 1 < NP; ++p) out[p].u[e] = split2(x, y);
+      out[NP - 1].u[e] = round2(x, y);
     }
   }
   static __device__ __forceinline__ void put(unsigned char* a, const frag& f) { *(uint4*)a = f.w; }
@@ -139,10 +144,6 @@ struct LaBf16 {
   template <int RB, int PS>
   static __device__ __forceinline__ void put_row(unsigned char* lds, int row, int c, uint32_t x, const uint4& w) {
     *(uint4*)(lds + ((row * RB + (((c >> 3) ^ la_f<RB>(row)) << 4)) ^ x)) = w;
-  }
-  static __device__ __forceinline__ uint32_t round2(float x, float y) {   // nearest, ties to even
-    const la_f2 v = {x, y};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, la_bf2));
   }
   static __device__ __forceinline__ void store4(store* p, const float* v) {
     *(uint2*)p = make_uint2(round2(v[0], v[1]), round2(v[2], v[3]));
@@ -159,10 +160,10 @@ struct LaBf16 {
   }
 };
 
-// fp32 elements are three bf16 pieces in LDS, a plane each, cut so that their
-// sum is the element; of the nine products of two elements the six of weight
-// 2^-16 and up are formed, which leaves 2^-23 of a term.  Six bf16 products
-// take 3/8 of the time of the fp32 ones.
+// fp32 elements are three bf16 pieces in LDS, a plane each, whose sum is the
+// element; of the nine products of two elements the six of weight 2^-18 and up
+// are formed, which leaves 2^-26 of a term.  Six bf16 products take 3/8 of the
+// time of the fp32 ones.
 struct LaF32 {
   using store = float;
   static constexpr int kVec = 4;
@@ -216,15 +217,11 @@ struct LaF32 {
   template <int RB, int PS>
   static __device__ __forceinline__ void put_row(unsigned char* lds, int row, int c, uint32_t x, const uint4& w) {
     unsigned char* a = lds + ((row * RB + (((c >> 3) ^ la_f<RB>(row)) << 4) + (c & 4) * 2) ^ x);
-    uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    float v[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-      *(uint2*)(a + p * PS) = make_uint2(__builtin_amdgcn_perm(v[1], v[0], 0x07060302u),
-                                         __builtin_amdgcn_perm(v[3], v[2], 0x07060302u));
-      if (p < 2)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = __float_as_uint(__uint_as_float(v[e]) - __uint_as_float(v[e] & 0xffff0000u));
+      const uint32_t lo = LaBf16::split2(v[0], v[1]), hi = LaBf16::split2(v[2], v[3]);
+      *(uint2*)(a + p * PS) = make_uint2(lo, hi);
     }
   }
   static __device__ __forceinline__ void store4(store* p, const float* v) {
@@ -288,11 +285,6 @@ __device__ __forceinline__ bool la_unit(const LaArgs& a, unsigned id, LaUnit& u)
   u.hd = set % groups * a.ratio + member;
   u.sid = set / groups;
   return u.sid < a.segs;
-}
-
-// Place of the state kept at step t of a view's axis (every kLaKeep steps of a segment).
-__device__ __forceinline__ long long la_keep_slot(const LaArgs& a, const LaSeg& s, int t) {
-  return (long long)s.vb * ((a.L + kLaKeep - 1) / kLaKeep) + t / kLaKeep;
 }
 
 template <typename T>
@@ -446,7 +438,7 @@ struct LaTile {
   static constexpr int kExp = 4 * C + 4;         // floats of one chunk's exponents
   static constexpr size_t kX = (size_t)T::kPlanes * XP, kZ = (size_t)T::kPlanes * ZP, kP = kShareP ? (size_t)C * PB : 0;
   static constexpr int PAIR = 64 / C;            // chunks whose exponents are formed at once
-  static constexpr size_t kSmall = (size_t)(2 * PAIR * kExp + NW * C) * 4;
+  static constexpr size_t kSmall = (size_t)(2 * PAIR * kExp + (NW + 1) * C) * 4;
   static constexpr int pieces(int mode) { return kF32 ? 1 : mode == kLaQ || mode == kLaK ? 3 : 2; }
   static constexpr size_t main_bytes(int np) { return 2 * kX + kZ + np * kP + kSmall; }
   static constexpr size_t state_bytes() { return 2 * (kX + kZ) + (size_t)NW * 64 * 4; }
@@ -454,36 +446,66 @@ struct LaTile {
   using Z = LaTileIO<T, C, NW * 32, NT>;
   // registers: state, outputs and the tiles under way
   static constexpr int kRegs = 16 * (KT + IT) + 4 * (2 * X::N + Z::N);
-  static constexpr int kStateWaves = 16 * KT + 4 * (X::N + Z::N) <= 96 ? 3 : 2;
+  // rows of 256 elements: the scheduler is kept from loading more operands ahead than the registers hold
+  static constexpr bool kWide = KT == 8;
+  static constexpr bool kApart = kF32 || KT < 4 || (KT == 4 && !kShareP);
+  static constexpr int kStateWaves = 16 * KT + 4 * (X::N + Z::N) <= 64 ? 3 : 2;
   static constexpr int waves(bool bwd) { return la_simd_waves(kRegs, kF32, bwd); }
 };
 
-// S = decay S + sum_j y_j (w_j z_j)^T (KEEP: S as it is)
-template <typename T, int DKP, int NW, bool KEEP>
+// S = decay S + sum_j y_j (w_j z_j)^T (KEEP: S as it is).  The sum of 32 tokens
+// is formed apart and added once: the matrix instructions do not round their
+// sums to the nearest, and what they lose is then small beside the sum, not
+// beside the whole state (a long memory in fp32: states 5e-7 off before).  Not
+// where the registers do not hold it (APART false: bf16 rows of 128 elements
+// with four waves, 311 us instead of 175 for a gradient, and of 256): with
+// bf16 inputs half as many instructions add to a state.
+template <typename T, int DKP, int NW, bool KEEP, bool APART>
 __device__ __forceinline__ void la_update(la_f16 (&S)[DKP / 32], const unsigned char* Y, uint32_t ycol,
                                           const typename T::frag* zf, const float* ew, float decay, int lane) {
   using K = LaTile<T, DKP, NW>;
   const int h = lane >> 5;
-  if constexpr (!KEEP) {
+  if constexpr (!KEEP && !APART) {
 #pragma unroll
     for (int t = 0; t < K::KT; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) S[t][r] *= decay;
   }
 #pragma unroll
-  for (int js = 0; js < K::C / 16; ++js) {
-    float v[8];
-    const float4 w0 = *(const float4*)(ew + 16 * js + 8 * h), w1 = *(const float4*)(ew + 16 * js + 8 * h + 4);
-    const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  for (int g = 0; g < K::C / 32; ++g) {
+    typename T::frag b[2][K::NPS];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = T::get(zf[js], e) * w[e];
-    typename T::frag b[K::NPS];
-    T::template pieces<K::NPS>(v, b);
+    for (int k2 = 0; k2 < 2; ++k2) {
+      const int js = 2 * g + k2;
+      float v[8];
+      const float4 w0 = *(const float4*)(ew + 16 * js + 8 * h), w1 = *(const float4*)(ew + 16 * js + 8 * h + 4);
+      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = T::get(zf[js], e) * w[e];
+      T::template pieces<K::NPS>(v, b[k2]);
+      if constexpr (!APART) {
+#pragma unroll
+        for (int t = 0; t < K::KT; ++t) {
+          const typename T::frag y = T::template col<K::XB, K::XP>(Y, ycol, 16 * js, t);
+#pragma unroll
+          for (int p = 0; p < K::NPS; ++p) T::mma(S[t], y, b[k2][K::NPS - 1 - p]);
+          if (K::kWide) __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    if constexpr (!APART) continue;
 #pragma unroll
     for (int t = 0; t < K::KT; ++t) {
-      const typename T::frag y = T::template col<K::XB, K::XP>(Y, ycol, 16 * js, t);
+      la_f16 d = {};
 #pragma unroll
-      for (int p = 0; p < K::NPS; ++p) T::mma(S[t], y, b[p]);
+      for (int k2 = 0; k2 < 2; ++k2) {
+        const typename T::frag y = T::template col<K::XB, K::XP>(Y, ycol, 16 * (2 * g + k2), t);
+#pragma unroll
+        for (int p = 0; p < K::NPS; ++p) T::mma(d, y, b[k2][K::NPS - 1 - p]);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[t][r] = KEEP || g > 0 ? S[t][r] + d[r] : __builtin_fmaf(S[t][r], decay, d[r]);
+      if (K::kWide) __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -541,18 +563,21 @@ __device__ __forceinline__ void la_store_state(const la_f16 (&S)[KT], float* p, 
 
 // Scores of one 32 x 32 tile (rows j of y, columns i of x), weighted by the
 // decay between the two tokens (near: by the part of it that is the key's) and
-// zero on the wrong side of the diagonal.
-template <typename T, int DKP, int NW, bool REV>
+// zero on the wrong side of the diagonal.  DIAG: zero on it too, and d is the
+// diagonal's element of column i (zero in the half of the lanes without it).
+template <typename T, int DKP, int NW, bool REV, bool DIAG>
 __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsigned char* Y, uint32_t xrow,
                                             uint32_t yrow, const float* e, bool near, int jt, int it, float s_intra,
-                                            int lane) {
+                                            int lane, float& d) {
   using K = LaTile<T, DKP, NW>;
   const int h = lane >> 5, n32 = lane & 31;
   la_f16 c = {};
 #pragma unroll
-  for (int ks = 0; ks < DKP / 16; ++ks)
+  for (int ks = 0; ks < DKP / 16; ++ks) {
     T::mma(c, T::template row<K::XP>(Y + (yrow ^ (uint32_t)(ks * 32)) + jt * 32 * K::XB),
            T::template row<K::XP>(X + (xrow ^ (uint32_t)(ks * 32)) + it * 32 * K::XB));
+    if (K::kWide && ks % 2) __builtin_amdgcn_sched_barrier(0);
+  }
   const int j0 = 32 * jt + 8 * h;
   if (near) {
 #pragma unroll
@@ -575,8 +600,8 @@ __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsign
       *(float4*)&ll[4] = *(const float4*)(e + K::C + j0 + 16 * s + 4);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float d = REV ? (hh[q] - gi) + (ll[q] - gl) : (gi - hh[q]) + (gl - ll[q]);
-        c[8 * s + q] *= __builtin_amdgcn_exp2f(d) * s_intra;
+        const float x = REV ? (hh[q] - gi) + (ll[q] - gl) : (gi - hh[q]) + (gl - ll[q]);
+        c[8 * s + q] *= __builtin_amdgcn_exp2f(x) * s_intra;
       }
     }
   }
@@ -586,7 +611,8 @@ __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsign
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const int j = 16 * s + 8 * h + q;
-        if (REV ? j < n32 : j > n32) c[8 * s + q] = 0.0f;
+        if (DIAG && j == n32) d = c[8 * s + q];
+        if (REV ? DIAG ? j <= n32 : j < n32 : DIAG ? j >= n32 : j > n32) c[8 * s + q] = 0.0f;
       }
   }
   return c;
@@ -595,8 +621,7 @@ __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsign
 // o = form(x, y, z) over one segment, head and slab of 32 NW columns.
 // MODE: the forward pass, or one of the gradient's jobs.  Those of q and k
 // also give w . o per token (for the log-decay gradient, so with three pieces
-// throughout), those of q and v keep states inside the segment, that of q
-// multiplies the final state with its gradient.
+// throughout); that of q multiplies the final state with its gradient.
 template <typename T, int DKP, int NW, int MODE>
 __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const LaSeg& s, int sid, int hd, int slab,
                                         unsigned char* smem) {
@@ -605,13 +630,13 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   using F = typename T::frag;
   constexpr int C = K::C, IT = K::IT, NP = K::pieces(MODE);
   constexpr bool REV = MODE == kLaK || MODE == kLaV, dot = MODE == kLaQ || MODE == kLaK;
-  constexpr bool keep = MODE == kLaQ || MODE == kLaV;
   unsigned char* X = smem;
   unsigned char* Y = smem + K::kX;
   unsigned char* Z = smem + 2 * K::kX;
   unsigned char* P = smem + 2 * K::kX + K::kZ;
   float* exps = (float*)(smem + 2 * K::kX + K::kZ + NP * K::kP);   // of the chunks under way and the next
   float* dots = exps + 2 * K::PAIR * K::kExp;                      // [NW][C]
+  float* diag = dots + NW * C;                                     // [C]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5,
             n32 = lane & 31, pm = la_pi(n32);
   const int slab0 = slab * NW * 32;
@@ -669,6 +694,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   uint32_t yrow = pm * K::XB + ((h ^ la_f<K::XB>(pm)) << 4);
   uint32_t ycol = T::template col_base<K::XB>(lane, 0);
   uint32_t zcol = T::template col_base<K::ZB>(lane, wave * 32);
+  uint32_t zrow = n32 * K::ZB + (((wave * 4 + h) ^ la_f<K::ZB>(n32)) << 4);
   uint32_t prow = n32 * K::PB + ((h ^ la_f<K::PB>(n32)) << 4);
 
   const int oes = dot && J.o_f32 ? 4 : K::ES;
@@ -686,16 +712,10 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   int n = s.len - first;                 // steps of this chunk
   int at = first;                        // its first step in the segment
 
-  int q = 0, stop = chunks;
-  do {
-  if (keep && J.keep) {   // up to the next step whose state is kept
-    const int run = REV ? at % kLaKeep / C + 1 : kLaKeep / C - at % kLaKeep / C;
-    stop = q + run < chunks ? q + run : chunks;
-  }
-  for (; q < stop; ++q) {
+  for (int q = 0; q < chunks; ++q) {
     if (n > C) n = C;
     // the operands' places are one exclusive-or away from these: cheaper than the registers to keep them all
-    asm volatile("" : "+v"(xrow), "+v"(yrow), "+v"(ycol), "+v"(zcol), "+v"(prow));
+    asm volatile("" : "+v"(xrow), "+v"(yrow), "+v"(ycol), "+v"(zcol), "+v"(zrow), "+v"(prow));
     const float* e = exps + (q % (2 * PAIR)) * K::kExp;
     tx.commit(X, tid, n, whole && n == C);
     ty.commit(Y, tid, n, whole && n == C);
@@ -732,7 +752,12 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
         la_exponents<C, K::kExp>(gv, REV, s_out, s_ratio, s_upd, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
       const int jt = wave / IT, it = wave % IT;
       if (wave < IT * IT && (REV ? jt >= it : jt <= it)) {
-        const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, near, jt, it, s_intra, lane);
+        float d = 0.0f;
+        const la_f16 c = la_scores<T, DKP, NW, REV, dot>(X, Y, xrow, yrow, e, near, jt, it, s_intra, lane, d);
+        if (dot && jt == it) {
+          d += __shfl_xor(d, 32, 64);
+          if (h == 0) diag[32 * it + n32] = d;
+        }
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
           float v[8];
@@ -766,6 +791,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
 #pragma unroll
           for (int p = 0; p < NP; ++p) T::mma(o[it], sp[p], xb);
         }
+        if (K::kWide) __builtin_amdgcn_sched_barrier(0);
       }
     auto scale_out = [&]() {
 #pragma unroll
@@ -781,8 +807,12 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     F zf[C / 16];
 #pragma unroll
     for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB, K::ZP>(Z, zcol, 16 * js, 0);
+    float dv[IT];   // the token's own score, left out of the product where w . o is asked for
     if constexpr (K::kShareP) {
       __syncthreads();
+      if (dot)
+#pragma unroll
+        for (int it = 0; it < IT; ++it) dv[it] = diag[32 * it + n32];
 #pragma unroll
       for (int it = 0; it < IT; ++it)
 #pragma unroll
@@ -799,7 +829,9 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
         for (int jt = 0; jt < IT; ++jt) {
           if (REV ? jt < it : jt > it) continue;
           __builtin_amdgcn_sched_barrier(0);   // one tile at a time: all at once would not fit the registers
-          const la_f16 c = la_scores<T, DKP, NW, REV>(X, Y, xrow, yrow, e, near, jt, it, s_intra, lane);
+          float d = 0.0f;
+          const la_f16 c = la_scores<T, DKP, NW, REV, dot>(X, Y, xrow, yrow, e, near, jt, it, s_intra, lane, d);
+          if (dot && jt == it) dv[it] = d + __shfl_xor(d, 32, 64);
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
             float v[8];
@@ -818,25 +850,31 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
       const int i = 32 * it + n32;
-      float dsum = 0.0f;
-      if (i < n) {
-        char* oi = ob + (ooff + 32 * it * ost);
+      float dsum = 0.0f, own = 0.0f;
+      if (dot) own = near ? dv[it] * e[2 * C + i] : dv[it];
+      char* oi = ob + (ooff + 32 * it * ost);
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          if (c0 + 16 * k2 + 8 * h >= J.DV) continue;
-          float v[8];
+      for (int k2 = 0; k2 < 2; ++k2) {
+        float v[8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) v[r] = o[it][8 * k2 + r];
+        for (int r = 0; r < 8; ++r) v[r] = o[it][8 * k2 + r];
+        if (dot) {
+          // w . o without the token's own part: it is the same in the jobs of
+          // q and k and cancels in their difference, but for rounding
+          float w[8];
+          T::unpack(&wv[it][k2 * K::WV], w);
+          if (c0 + 16 * k2 + 8 * h < J.DV)
+            dsum += ((w[0] * v[0] + w[1] * v[1]) + (w[2] * v[2] + w[3] * v[3])) +
+                    ((w[4] * v[4] + w[5] * v[5]) + (w[6] * v[6] + w[7] * v[7]));
+          const F z = T::template row<K::ZP>(Z + (zrow ^ (uint32_t)(k2 * 32)) + it * 32 * K::ZB);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] += own * T::get(z, r);
+        }
+        if (i < n && c0 + 16 * k2 + 8 * h < J.DV) {
           if (dot && J.o_f32)
             LaF32::store8((float*)oi + 16 * k2, v);
           else
             T::store8((E*)oi + 16 * k2, v);
-          if (dot) {
-            float w[8];
-            T::unpack(&wv[it][k2 * K::WV], w);
-            dsum += ((w[0] * v[0] + w[1] * v[1]) + (w[2] * v[2] + w[3] * v[3])) +
-                    ((w[4] * v[4] + w[5] * v[5]) + (w[6] * v[6] + w[7] * v[7]));
-          }
         }
       }
       if (dot) {
@@ -846,7 +884,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     }
 
     __builtin_amdgcn_sched_barrier(0);
-    la_update<T, DKP, NW, false>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
+    la_update<T, DKP, NW, false, K::kApart>(S, Y, ycol, zf, e + 3 * C, e[4 * C], lane);
     if (!K::kShareP && wave == kExpWave && q + 1 < chunks && q % PAIR == PAIR - 1)
       la_exponents<C, K::kExp>(gv, REV, s_out, s_ratio, s_upd, exps + ((q + 1) % (2 * PAIR)) * K::kExp, lane);
     gv = gnext;
@@ -863,10 +901,6 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
     at += dir;
     n = REV ? C : s.len - at;
   }
-  if (keep && q < chunks)
-    la_store_state<K::KT>(S, J.keep + (la_keep_slot(a, s, s.t0 + (REV ? at + C : at)) * a.H + hd) * a.state, J.sm, J.sn,
-                          J.DK, J.DV, col, h);
-  } while (q < chunks);
 
   if (!(REV ? s.first : s.last)) return;
   if ((MODE == kLaFwd || MODE == kLaV) && J.s_fin) la_store_state<K::KT>(S, J.s_fin + unit * a.state, J.sm, J.sn, J.DK, J.DV, col, h);
@@ -1016,7 +1050,7 @@ pdssm_linattn_state_kernel(const LaArgs a) {
     F zf[C / 16];
 #pragma unroll
     for (int js = 0; js < C / 16; ++js) zf[js] = T::template col<K::ZB, K::ZP>(Z, zcol, 16 * js, 0);
-    la_update<T, DKP, NW, true>(S, Y, ycol, zf, ew + q % PAIR * C, 1.0f, lane);
+    la_update<T, DKP, NW, true, K::kApart>(S, Y, ycol, zf, ew + q % PAIR * C, 1.0f, lane);
     at += (int)dir;
     n = rev ? s.len - at : C;
     more = q + 1 < chunks;

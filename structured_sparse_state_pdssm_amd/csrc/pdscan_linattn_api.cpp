@@ -177,7 +177,7 @@ FwdWs fwd_ws(const pdssm_linattn_dims* d) {
   const int bf16 = d->in_dtype == PDSSM_BF16;
   w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * pdscan::la_slabs(d->dk, d->dv, bf16),
                              kCus * pdscan::la_resident(d->dk, d->dv, bf16, 0), (long long)d->dk * d->dv,
-                             (2 * d->dk + 2 * d->dv) * (bf16 ? 2 : 4));
+                             (2 * d->dk + 2 * d->dv) * (bf16 ? 2 : 4), 0x7fffff00);
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -200,8 +200,7 @@ FwdWs fwd_ws(const pdssm_linattn_dims* d) {
 
 struct BwdWs {
   LaSplit split;
-  size_t table, starts, segS, segR, decS, decR, keepS, keepR, r, k, xd, part, fq, fk, total;
-  int subs;                      // pieces of a segment in the log-decay gradient
+  size_t table, starts, segS, segR, decS, decR, r, k, xd, part, fq, fk, total;
   bool one;                      // all three jobs have one shape
   int qslabs, vslabs;            // slabs of the passes whose outputs are dk and dv wide
 };
@@ -216,7 +215,7 @@ BwdWs bwd_ws(const pdssm_linattn_dims* d) {
   // the launch with the most work decides: all three jobs in one, or those of q and k
   w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * (w.one ? 3 : 2) * w.qslabs,
                              kCus * pdscan::la_resident(d->dv, d->dk, bf16, 1), 2ll * d->dk * d->dv,
-                             (8 * d->dk + 7 * d->dv) * (bf16 ? 2 : 4));
+                             (8 * d->dk + 7 * d->dv) * (bf16 ? 2 : 4), pdscan::kLaPiece);
   size_t at = pdscan::kLaHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -236,18 +235,10 @@ BwdWs bwd_ws(const pdssm_linattn_dims* d) {
     w.decS = put(units * 4);
     w.decR = put(units * 4);
   }
-  // states inside the segments: none where they are short
-  w.subs = pdscan::la_subs(w.split, d->L);
-  w.keepS = w.keepR = at;
-  if (w.subs > 1) {
-    const size_t kept = (size_t)(d->packed ? 1 : d->B) * (((size_t)d->L + pdscan::kLaKeep - 1) / pdscan::kLaKeep);
-    w.keepS = put(kept * d->H * d->dk * d->dv * 4);
-    w.keepR = put(kept * d->H * d->dk * d->dv * 4);
-  }
   w.r = put((size_t)w.qslabs * d->H * rows * 4);
   w.k = put((size_t)w.qslabs * d->H * rows * 4);
   w.xd = put(units * w.qslabs * 8);
-  w.part = put(d->decay_per_head ? units * w.subs * 8 : 0);
+  w.part = put(d->decay_per_head ? units * 8 : 0);
   w.fq = w.fk = at;
   if (d->Hk != d->H) {
     w.fq = put(rows * d->H * d->dk * 4);
@@ -264,9 +255,8 @@ int launched(hipError_t e) {
 }
 
 int grid_ok(const LaSplit& s, const pdssm_linattn_dims* d) {
-  // three jobs of two slabs each, or one workgroup per piece of a segment
-  const uint64_t subs = (uint64_t)pdscan::la_subs(s, d->L);
-  if (((uint64_t)s.segs + 8) * d->H * (subs > 6 ? subs : 6) > 0x7fffffffull)
+  // up to three jobs of two slabs each
+  if (((uint64_t)s.segs + 8) * d->H * 6 > 0x7fffffffull)
     return set_error(PDSSM_EUNSUPPORTED, "too many segments and heads (%d, %d)", s.segs, d->H);
   return PDSSM_OK;
 }
@@ -475,11 +465,6 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   v_job.rev = 1;
   v_job.mode = pdscan::kLaV;
 
-  if (w.subs > 1) {
-    q_job.keep = (float*)(ws + w.keepS);
-    v_job.keep = (float*)(ws + w.keepR);
-  }
-
   hipError_t e = hipSuccess;
   if (w.split.split) {
     if (d.packed)
@@ -528,9 +513,6 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   g.k = (const float*)(ws + w.k);
   g.sS = (const float*)(ws + w.segS);
   g.sR = (const float*)(ws + w.segR);
-  g.kS = (const float*)(ws + w.keepS);
-  g.kR = (const float*)(ws + w.keepR);
-  g.subs = w.subs;
   g.xd = q_job.xd_out;
   g.part = (double*)(ws + w.part);
   g.out = gg;

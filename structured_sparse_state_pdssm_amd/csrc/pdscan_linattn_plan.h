@@ -11,7 +11,7 @@ namespace pdscan {
 constexpr int kLaChunk = 64;     // segments are multiples of this: one or two chunks
 constexpr int kLaMaxD = 256;     // widest key or value row
 constexpr int kLaMaxStep = 1 << 23;   // longest step stride, elements: 64 rows stay within 31 bits of bytes
-constexpr int kLaKeep = 512;     // steps of a segment between states kept for the log-decay gradient
+constexpr int kLaPiece = 512;    // longest segment of a gradient (see the log-decay gradient)
 constexpr double kLaNear = 24.0; // log2 of the decay over a chunk up to which it is split into factors of its tokens
 constexpr int kLaHeader = 256;   // workspace header: word 1 stays zero (nothing here waits on another workgroup)
 
@@ -36,7 +36,6 @@ struct LaJob {
   double* xd_out;              // that product [slab][segment][H]
   float* seg_out;              // (state pass) contributions [segment][H], written at the next segment
   float* seg_decay;            // (state pass) log2 decay of the segment [segment][H]
-  float* keep;                 // states inside a segment, every kLaKeep steps [row / kLaKeep][H], NULL: none
   float* dot;                  // w . o per token [slab][H][rows], NULL: none
   int sm, sn;                  // strides of a state's x-row and z-row axes
   float s_out, s_ratio, s_upd; // scale of the output, of its own tokens' part beside the state's, of the update
@@ -74,13 +73,10 @@ struct LaDecayArgs {
   const float* k;              // k . dk per token [k_slabs][H][rows]
   const float* sS;             // entering states [segment][H]
   const float* sR;             // entering adjoints [segment][H]
-  const float* kS;             // the same every kLaKeep steps inside a segment [row / kLaKeep][H]
-  const float* kR;
   const double* xd;            // final state . its gradient [xd_slabs][segment][H], NULL: zero
-  double* part;                // sums per piece of kLaKeep steps and head (one decay per head)
+  double* part;                // sums per segment and head (one decay per head)
   LaView out;
   int r_slabs, k_slabs, xd_slabs, per_head;
-  int subs;                    // pieces of kLaKeep steps of the longest segment
 };
 
 // Sum over the value heads that share a query or key head.
@@ -115,7 +111,7 @@ inline int la_resident(int DK, int DV, int bf16, int bwd) {
   const int es = bf16 ? 2 : 4, nw = la_waves(DK, DV, bf16), d = la_pad(DK);
   const int C = nw < 4 || !bf16 ? 32 : 64;
   const int lds = C * (bf16 ? 2 : 6) * (2 * d + 32 * nw) + (nw == 4 && bf16 ? (bwd ? 3 : 2) * C * C * 2 : 0) +
-                  4 * (64 / C * (8 * C + 8) + nw * C);
+                  4 * (64 / C * (8 * C + 8) + (nw + 1) * C);
   const int regs = (d + C) / 2 + C * es * (2 * d + 32 * nw) / (256 * nw);
   const int waves = 4 * la_simd_waves(regs, !bf16, bwd);
   const int n = 163840 / lds < waves / nw ? 163840 / lds : waves / nw;
@@ -133,21 +129,22 @@ struct LaSplit {
 // shorter chains save.  Sequences of different lengths take 7/4 of it, so that
 // no long one is left alone at the end.  A segment's states are written and
 // read twice; with at least a workgroup a compute unit they stay under half of
-// what its steps (`bytes` each) move.
+// what its steps (`bytes` each) move.  No segment is over `longest` steps.
 //   65536 steps, 16 heads, 128/128 bf16: 32 segments of 2048 434 us, of 1024 459, of 4096 506, uncut over 5000
 //   16 x 2048 steps, 24 heads, 64/32 bf16: 4 segments of 512 104 us, 8 of 256 114, uncut 131
 //   4 x 4096 steps, 8 heads, 16/64 fp32: 128 steps 53 us, 64 63, 256 71
 //   23 sequences in 12001 rows, 24 heads, 128/64 bf16: 384 steps 102 us, 192 107, 640 117
-inline LaSplit la_split(int B, int L, int packed, int width, int room, long long state, int bytes) {
+inline LaSplit la_split(int B, int L, int packed, int width, int room, long long state, int bytes, int longest) {
   LaSplit s;
   long long n = (long long)room / (packed ? width : (long long)B * width);   // segments of a sequence
   if (packed) n = n * 7 / 4;
   const long long least = 256 / (packed ? width : (long long)B * width), most = (long long)L * bytes / (32 * state);
   if (n > most) n = most > least ? most : least < n ? least : n;
   if (n > (L - 1) / kLaChunk + 1) n = (L - 1) / kLaChunk + 1;
+  if (n < ((long long)L + longest - 1) / longest) n = ((long long)L + longest - 1) / longest;
   s.split = n > 1 && L > 256;
   const long long each = s.split ? ((long long)L + n - 1) / n : L;
-  s.seg = each <= 3 * kLaChunk / 2 && s.split ? kLaChunk : (int)((each + kLaChunk - 1) / kLaChunk * kLaChunk);
+  s.seg = each <= 5 * kLaChunk / 4 && s.split ? kLaChunk : (int)((each + kLaChunk - 1) / kLaChunk * kLaChunk);
   s.nseg = s.split ? (int)(((long long)L + s.seg - 1) / s.seg) : 1;
   const long long segs = !packed ? (long long)B * s.nseg : s.split ? (long long)(L / s.seg) + B : B;
   s.segs = segs > 0x7fffffffll ? 0x7fffffff : (int)segs;
@@ -162,8 +159,6 @@ inline long long la_grid(const LaArgs& a) {
   const long long sets = (long long)a.segs * (a.H / a.ratio);
   return (sets + a.dies - 1) / a.dies * a.dies * a.ratio * a.slabs * a.njobs;
 }
-
-inline int la_subs(const LaSplit& s, int L) { return ((s.seg < L ? s.seg : L) - 1) / kLaKeep + 1; }
 
 inline size_t la_align(size_t n) { return (n + 255) / 256 * 256; }
 
