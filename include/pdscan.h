@@ -363,11 +363,14 @@ int pdssm_dict_hardmax(int32_t H, int32_t K, int32_t N, const float* M, int32_t*
  *   - The workspace header's error word stays zero: no call here waits for
  *     another workgroup.
  *   - Shape limits (else PDSSM_EUNSUPPORTED): dk and dv multiples of 8, at
- *     most 256.
- * Precision: products of bf16 inputs are exact and summed in fp32; decay
- * sums, states and weights are fp32 or better, and enter matrix products as
- * two bf16 pieces or more (relative error 2^-16 of a term in o, none to speak
- * of in states and gradients).  fp32 inputs use fp32 products. */
+ *     most 256; step strides at most 2^23 elements, and H * dk likewise where
+ *     the gradient sums over shared heads.
+ * Precision: decay sums are held in 64 bits, states, weights and sums in
+ * fp32.  On the matrix cores bf16 inputs are exact; what is computed enters
+ * as two bf16 pieces where a bf16 output comes of it (2^-18 of a term) and as
+ * three (24 bits) where an fp32 one does; fp32 inputs are three pieces, of
+ * whose nine products the six largest are formed (2^-26 of a term is left).
+ * Values under about 1e-30 in size lose digits there. */
 typedef struct {
   int32_t B;               /* sequences */
   int32_t H, Hk;           /* value heads; query / key heads (Hk divides H) */

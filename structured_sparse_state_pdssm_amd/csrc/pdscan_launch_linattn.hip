@@ -131,8 +131,7 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
   if (t >= 0) {
     const long long at = (long long)h * a.c.rows + s.row0 + t;
     const long long slab = (long long)a.c.H * a.c.rows;
-    for (int w = 0; w < a.r_slabs; ++w) d += (double)a.r[w * slab + at];
-    for (int w = 0; w < a.k_slabs; ++w) d -= (double)a.k[w * slab + at];
+    for (int w = 0; w < a.slabs; ++w) d += (double)a.r[w * slab + at] - (double)a.k[w * slab + at];
   }
   if (!s.last) {
     const float4* A = (const float4*)(a.sS + ((long long)(sid + 1) * a.c.H + h) * a.c.state);
@@ -141,7 +140,7 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
       const float4 p = A[e], q = R[e];
       x += (double)((p.x * q.x + p.y * q.y) + (p.z * q.z + p.w * q.w));
     }
-  } else if (a.xd && tid < a.xd_slabs) {
+  } else if (a.xd && tid < a.slabs) {
     x = a.xd[((long long)tid * a.c.segs + sid) * a.c.H + h];
   }
 #pragma unroll
@@ -345,9 +344,7 @@ hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
 }
 
 // The product kernels, by type, x-row width and waves.
-hipError_t launch_linattn_form(const LaArgs& args, int bf16, int pass, hipStream_t st) {
-  LaArgs a = args;
-  a.dies = la_dies((long long)a.segs * (a.H / a.ratio));
+hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pass, hipStream_t st) {
   const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DK, a.job[0].DV, bf16);
   const long long grid = la_grid(a);
   if (grid > 0x7fffffffll) return hipErrorInvalidValue;

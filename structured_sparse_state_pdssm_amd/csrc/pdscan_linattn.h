@@ -213,7 +213,6 @@ struct LaF32 {
   static __device__ __forceinline__ void pieces(const float* v, frag* out) {
     LaBf16::pieces<3>(v, out[0].p);
   }
-  static __device__ __forceinline__ void put(unsigned char*, const frag&) {}
   template <int RB, int PS>
   static __device__ __forceinline__ void put_row(unsigned char* lds, int row, int c, uint32_t x, const uint4& w) {
     unsigned char* a = lds + ((row * RB + (((c >> 3) ^ la_f<RB>(row)) << 4) + (c & 4) * 2) ^ x);
@@ -271,20 +270,14 @@ struct LaUnit {
   int job, slab, hd, sid;
 };
 
-// What workgroup `id` works on: `dies` sets of workgroups that share rows are
-// interleaved, the members of a set one after the other on its die.
-__device__ __forceinline__ bool la_unit(const LaArgs& a, unsigned id, LaUnit& u) {
-  const unsigned die = id % a.dies;
-  id /= a.dies;
+// What workgroup `id` works on: those that share rows follow one another.
+__device__ __forceinline__ void la_unit(const LaArgs& a, unsigned id, LaUnit& u) {
   u.job = id % a.njobs;
   id /= a.njobs;
   u.slab = id % a.slabs;
   id /= a.slabs;
-  const unsigned member = id % a.ratio;
-  const unsigned set = id / a.ratio * a.dies + die, groups = a.H / a.ratio;
-  u.hd = set % groups * a.ratio + member;
-  u.sid = set / groups;
-  return u.sid < a.segs;
+  u.hd = id % a.H;
+  u.sid = id / a.H;
 }
 
 template <typename T>
@@ -939,7 +932,7 @@ __global__ __launch_bounds__(NW * 64)
   const unsigned id = blockIdx.x;
   if (id == 0 && threadIdx.x < 2) a.header[threadIdx.x] = 0;
   LaUnit u;
-  if (!la_unit(a, id, u)) return;
+  la_unit(a, id, u);
   const LaJob& J = a.job[u.job];
   LaSeg s;
   if (!la_segment(a, u.sid, s)) return;
@@ -971,7 +964,7 @@ pdssm_linattn_state_kernel(const LaArgs a) {
             n32 = lane & 31;
   float* ew = (float*)(smem + 2 * (K::kX + K::kZ)) + wave * 64;   // this wave's own copy of the weights
   LaUnit u;
-  if (!la_unit(a, blockIdx.x, u)) return;
+  la_unit(a, blockIdx.x, u);
   const int slab = u.slab, hd = u.hd, sid = u.sid;
   const LaJob& J = a.job[u.job];
   LaSeg s;

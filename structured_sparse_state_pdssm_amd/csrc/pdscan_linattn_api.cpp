@@ -256,7 +256,7 @@ int launched(hipError_t e) {
 
 int grid_ok(const LaSplit& s, const pdssm_linattn_dims* d) {
   // up to three jobs of two slabs each
-  if (((uint64_t)s.segs + 8) * d->H * 6 > 0x7fffffffull)
+  if ((uint64_t)s.segs * d->H * 6 > 0x7fffffffull)
     return set_error(PDSSM_EUNSUPPORTED, "too many segments and heads (%d, %d)", s.segs, d->H);
   return PDSSM_OK;
 }
@@ -269,8 +269,6 @@ LaArgs common(const pdssm_linattn_dims* d, const LaView& g, const int32_t* cu, c
   a.table = (cu && s.split) ? (const int32_t*)(ws + table) : nullptr;
   a.header = (uint32_t*)ws;
   a.B = d->B; a.H = d->H; a.L = d->L;
-  a.ratio = d->H / d->Hk;
-  a.dies = 1;
   a.nseg = s.nseg; a.seg = s.seg; a.segs = s.segs;
   a.rows = (long long)(d->packed ? 1 : d->B) * d->L;
   a.state = (long long)d->dk * d->dv;
@@ -398,6 +396,9 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   }
   out[4] = dense("g_h0", g_h0, state);
   out[5] = dense("workspace", workspace, w.total);
+  if (d.H != d.Hk && (long long)d.H * d.dk > pdscan::kLaMaxStep)   // partial gradients, [rows][H][dk]
+    return set_error(PDSSM_EUNSUPPORTED, "H * dk = %lld above %d with shared heads", (long long)d.H * d.dk,
+                     pdscan::kLaMaxStep);
   if (!d.packed && cu_seqlens) return set_error(PDSSM_EINVAL, "cu_seqlens given with packed = 0");
   if ((rc = dense_ok(in[4], d.packed, 4)) || (rc = dense_ok(in[5], false, 16)) || (rc = dense_ok(in[7], false, 16)) ||
       (rc = dense_ok(out[4], false, 16)) || (rc = dense_ok(out[5], true, 16)))
@@ -516,7 +517,7 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   g.xd = q_job.xd_out;
   g.part = (double*)(ws + w.part);
   g.out = gg;
-  g.r_slabs = g.k_slabs = g.xd_slabs = w.qslabs;
+  g.slabs = w.qslabs;
   g.per_head = d.decay_per_head;
   if (e == hipSuccess) e = pdscan::launch_linattn_decay(g, st);
   if (fold) {
@@ -561,9 +562,10 @@ int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, cons
   a.B = d.B; a.H = d.H; a.qd = d.H / d.Hk; a.dk = d.dk; a.dv = d.dv; a.slots = n_slots;
   a.scale = d.scale;
   a.bf16 = d.in_dtype == PDSSM_BF16;
-  // columns per workgroup: whole rows, halved while the card is not full (16 at least: 64 bytes of a row)
+  // Columns per workgroup: whole rows (16 states of 128/128 6.1 us, 264 of 16/64 4.1), halved down to 16 (64
+  // bytes of a row) while there is not a workgroup for every compute unit (the 16 5.7 us; the 264 in quarters 6.8).
   a.cols = d.dv;
-  while (a.cols >= 32 && a.cols % 16 == 0 && (long long)d.B * d.H * (d.dv / a.cols) < 1024) a.cols /= 2;
+  while (a.cols >= 32 && a.cols % 16 == 0 && (long long)d.B * d.H * (d.dv / a.cols) < kCus) a.cols /= 2;
   if ((long long)d.B * d.H * ((d.dv + a.cols - 1) / a.cols) > 0x7fffffffll)
     return set_error(PDSSM_EUNSUPPORTED, "too many rows and heads (%d, %d)", d.B, d.H);
   return launched(pdscan::launch_linattn_step(a, (hipStream_t)stream));

@@ -9,8 +9,8 @@ absolute values).  A term passes through at most
   and one multiplication per chunk,
 so fp32 work is off by at most (dk + dv + L + 128) 2^-24 mag.  bf16 outputs add
 half a step of bf16 (2^-8 of the value) and two pieces of 8 bits for the state
-and for the weighted scores (each cut below 2^-16 of a term: 2^-15 mag).  States
-and gradients of bf16 inputs use three pieces, cut below 2^-23.  The log-decay
+and for the weighted scores (each within 2^-16 of a term: 2^-15 mag).  States
+and gradients of bf16 inputs use three pieces, within 2^-23.  The log-decay
 gradient is a difference of sums, so its `mag` is the sum of what they hold.
 """
 
@@ -138,6 +138,9 @@ SHAPES = [
     (1, 1, 1, 700, 64, 64, False, True),      # few rows: the step axis is cut into segments
     (1, 2, 1, 1100, 96, 160, False, False),
     (1, 1, 1, 513, 16, 256, True, True),
+    (1, 2, 1, 300, 256, 192, False, True),
+    (1, 1, 1, 530, 192, 256, True, False),
+    (2, 1, 1, 600, 128, 128, False, True),    # a gradient's segments are never over 512 steps
 ]
 
 
@@ -323,21 +326,141 @@ def test_layouts_agree(dt):
 
 
 @pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
-def test_decays_at_their_ends(dt):
-    """No decay, a decay that forgets at once, minus infinity (the state starts anew) and strong decays
-    before weak ones (differences of large sums)."""
-    x = make(1, 4, 4, 200, 32, 32, dt)
+@pytest.mark.parametrize("L,dk,dv", [(200, 32, 32), (140, 128, 128), (600, 64, 40), (100, 256, 64)])
+def test_decays_at_their_ends(L, dk, dv, dt):
+    """No decay, a decay that forgets at once, minus infinity (the state starts anew), strong decays
+    before weak ones (differences of large sums), and a chunk at the border between both kinds of weights."""
+    x = make(1, 5, 5, L, dk, dv, dt)
     g = x["log_decay"]
     g[:, 0] = 0.0
     g[:, 1] = -200.0
     g[:, 2, ::37] = float("-inf")
     g[:, 3, ::3] = -60.0
+    g[:, 4] = -24.0 * np.log(2.0) / 32 * (1 + 0.001 * torch.randn(L, generator=torch.Generator().manual_seed(1)).cuda())
+    print(f"[gpu] linattn decays {L} {dk} {dv} {dt}", flush=True)
     o, hL = fwd(x, scale=1.0)
     check_fwd(x, o, hL, 1.0)
     check_bwd(x, bwd(x, scale=1.0), 1.0)
-    x["log_decay"] = torch.tensor([0.0, -1e-4, float("-inf"), -90.0]).cuda()
+    x["log_decay"] = torch.tensor([0.0, -1e-4, float("-inf"), -90.0, -0.52]).cuda()
     check_fwd(x, *fwd(x, scale=1.0), 1.0)
     check_bwd(x, bwd(x, scale=1.0), 1.0)
+
+
+def test_sequences_of_one_step_have_no_decay_gradient():
+    """Without a state before it a token's decay meets nothing: exactly zero."""
+    x, cu = packed([1, 1, 1], 3, 1, 64, 96, BF, tail=0, state=False)
+    assert (bwd(x, cu_seqlens=cu)["g_log_decay"] == 0).all()
+
+
+def test_many_sequences_around_a_long_one():
+    """More sequences than a round of the segment table, one of them cut into segments."""
+    lens = [int(v) for v in np.random.default_rng(0).integers(0, 5, 150)] + [900] + [2] * 150 + [333]
+    x, cu = packed(lens, 1, 1, 32, 32, BF, tail=3)
+    o, hL = fwd(x, scale=0.4, cu_seqlens=cu)
+    r = bwd(x, scale=0.4, cu_seqlens=cu)
+    for i in (0, 1, 77, 149, 150, 151, 299, 300, 301):
+        y, a, b = part(x, cu, i)
+        if a == b:
+            assert torch.equal(hL[i], x["h0"][i])
+            continue
+        check_fwd(y, o[:, :, a:b], hL[i:i + 1], 0.4)
+        s = {n: r[n][:, :, a:b] for n in ("g_q", "g_k", "g_v", "g_log_decay")}
+        check_bwd(y, dict(s, g_h0=r["g_h0"][i:i + 1]), 0.4)
+
+
+@pytest.mark.parametrize("bad", [[0, 40, 30, 700, 1000], [-5, 100, 90, 2000, 1 << 30], [900, 800, 700, 0, 5],
+                                 [0, 1000, 0, 1000, 0, 1000, 0, 1000, 0, 1000]])
+def test_offsets_out_of_order_touch_nothing_outside(bad):
+    """Offsets outside the rows or out of order are cut: rows of the buffers around the tensors stay, and a
+    sequence whose own bounds are in order and apart from the others' is right."""
+    L = 1000
+    x = make(1, 2, 1, L, 32, 32, BF, state=False)
+    cu = torch.tensor(bad, dtype=torch.int32).cuda()
+    n = len(bad) - 1
+    guard = {m: torch.full((1, 2 if m in ("o", "g_v") else 1, L + 2000, 32), 5.0, dtype=BF, device="cuda") for m in ("o", "g_q", "g_k", "g_v")}
+    gl = torch.full((1, 2, L + 2000), 5.0, device="cuda")
+    view = {m: t[:, :, 1000:1000 + L] for m, t in guard.items()}
+    hs = torch.full((n + 2, 2, 32, 32), 5.0, device="cuda")
+    print(f"[gpu] linattn offsets {bad}", flush=True)
+    fwd(x, cu_seqlens=cu, out={"o": view["o"], "h_L": hs[1:-1]})
+    bwd(x, cu_seqlens=cu, out={**{m: view[m] for m in ("g_q", "g_k", "g_v")}, "g_log_decay": gl[:, :, 1000:1000 + L]})
+    torch.cuda.synchronize()
+    for t in (*guard.values(), gl):
+        assert (t[:, :, :1000] == 5).all() and (t[:, :, 1000 + L:] == 5).all()
+    assert (hs[0] == 5).all() and (hs[-1] == 5).all()
+    if bad[:2] == [0, 40]:
+        y = {m: (t[:, :, :40] if t is not None else None) for m, t in x.items()}
+        ro = linattn_fwd(f64(y["q"]), f64(y["k"]), f64(y["v"]), decays(y), None, 32 ** -0.5)[0]
+        assert np.abs(f64(view["o"][:, :, :30]) - ro[:, :, :30]).max() < 0.05
+
+
+def test_offsets_past_32_bits():
+    """Batch strides over 2^31 elements and a pool of states over 2^32 bytes."""
+    P = lib()
+    B, H, L, d = 2, 1, 70, 32
+    far = (1 << 31) + 64
+    buf = torch.empty(far + 4 * L * d, dtype=BF, device="cuda")
+    x = make(B, H, H, L, d, d, BF)
+    y = dict(x)
+    for i, n in enumerate(("q", "k", "v", "g_o")):
+        y[n] = buf.as_strided((B, H, L, d), (far, L * d, d, 1), i * L * d)
+        y[n].copy_(x[n])
+    a, b = fwd(x), fwd(y)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga, gb = bwd(x), bwd(y)
+    assert all(torch.equal(ga[n], gb[n]) for n in ga)
+    del buf, y
+    slots = (1 << 32) // (128 * 128 * 4) + 40
+    pool = torch.zeros(slots, 1, 128, 128, device="cuda")
+    t = make(2, 1, 1, 1, 128, 128, BF)
+    idx = torch.tensor([slots - 1, 3], dtype=torch.int32).cuda()
+    pool[idx.long()] = t["h0"]
+    o = P.pdssm_linattn_step(t["q"][:, :, 0], t["k"][:, :, 0], t["v"][:, :, 0], t["log_decay"][:, :, 0], pool, state_idx=idx)
+    small = t["h0"].clone()
+    o2 = P.pdssm_linattn_step(t["q"][:, :, 0], t["k"][:, :, 0], t["v"][:, :, 0], t["log_decay"][:, :, 0], small)
+    assert torch.equal(o, o2) and torch.equal(pool[idx.long()], small)
+    assert int((pool != 0).any(-1).any(-1).sum()) == 2
+
+
+def test_gradient_by_differences():
+    """The gradient of a scalar loss along random directions against central differences of the GPU's own
+    forward pass.  A step of 2^-5 leaves (2^-5)^2 / 6 of the third derivative; the loss is a polynomial of degree
+    three in q, k, v and h0 together (four with two factors of k and v, smooth in the decays), so its error
+    is under 2^-10 of the sums' size, and the fp32 losses add 2^-24 / 2^-5 of theirs."""
+    x = make(1, 4, 2, 90, 32, 24, F32, decay=-2.0)
+    r = bwd(x, scale=0.7)
+    gen = torch.Generator().manual_seed(3)
+
+    def loss(y):
+        o, hL = fwd(y, scale=0.7)
+        return float((o.double() * x["g_o"].double()).sum() + (hL.double() * x["g_hL"].double()).sum())
+
+    for n in ("q", "k", "v", "log_decay", "h0"):
+        d = torch.randn(x[n].shape, generator=gen).cuda()
+        if n == "log_decay":
+            d = d * x[n]          # in proportion: no decay becomes positive
+        e = 2.0 ** -5
+        num = (loss(dict(x, **{n: x[n] + e * d})) - loss(dict(x, **{n: x[n] - e * d}))) / (2 * e)
+        got = float((r["g_" + n].double() * d.double()).sum())
+        size = float((r["g_" + n].double() * d.double()).abs().sum())
+        assert abs(num - got) <= 2.0 ** -10 * size, (n, num, got, size)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with workspaces of their own, running together."""
+    a, b = make(1, 2, 1, 900, 64, 64, BF, seed=1), make(1, 2, 1, 900, 64, 64, BF, seed=2)
+    want = [(fwd(x), bwd(x)) for x in (a, b)]
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(s[i]):
+                got[i].append((fwd(x), bwd(x)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for f, g in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(f, want[i][0])) and all(torch.equal(g[n], want[i][1][n]) for n in g)
 
 
 def test_scale_zero_and_negative():

@@ -128,6 +128,31 @@ def test_abi_refusals(P):
         assert _fwd(P, e) == code, (f, v)
 
 
+def test_limits_of_strides(P):
+    """Step strides, and the partial gradients' of shared heads, that a lane's 32-bit offsets would not hold."""
+    from structured_sparse_state_pdssm_amd import _lib
+    P._lib = _lib
+    V = _lib.PdssmView
+    at = lambda i: 0x7f0000000000 + (i << 36)  # noqa: E731
+    d = P.linattn_dims(1, 4, 10, 32, 64, Hk=4)
+    far = 1 << 23
+    for n, i in (("q", 0), ("k", 1), ("v", 2), ("o", 5)):
+        assert _fwd(P, d, n=255, **{n: V(at(i), 0, 64, far)}) == -3       # every check passed but the workspace's size
+        assert _fwd(P, d, n=255, **{n: V(at(i), 0, 64, far + 4)}) == -2 and n.encode() in P.lib.pdssm_last_error()
+    assert _fwd(P, d, n=255, g=V(at(3), 0, 1, far + 4)) == -3              # the decays' is not bounded
+    one = P.linattn_dims(1, 4, 1, 32, 64, Hk=4)
+    assert _fwd(P, one, n=255, q=V(at(0), 0, 64, far + 4)) == -3           # one step: not looked at
+    wide = V(at(0), 0, 256, 256)
+    rest = [V(at(i), 0, 256, 256) for i in range(1, 9)]
+
+    def bwd(H, Hk):
+        e = P.linattn_dims(1, H, 1, 256, 8, Hk=Hk, bf16=True)
+        return P.lib.pdssm_linattn_bwd(e, wide, rest[0], rest[1], V(at(9), 0, 1, 0), None, None, rest[2], None, rest[3],
+                                       rest[4], rest[5], V(at(10), 0, 1, 0), None, at(11), 255, None)
+
+    assert bwd(1 << 15, 1) == -3 and bwd((1 << 15) + 2, 2) == -2 and b"shared heads" in P.lib.pdssm_last_error()
+
+
 def test_step_abi_refusals(P):
     from structured_sparse_state_pdssm_amd import _lib
     V = _lib.PdssmView
