@@ -12,7 +12,7 @@ namespace pdscan {
 // Segments of packed sequences, in order: {sequence, first row, rows,
 // first | last << 1}, then the first segment of every sequence.  Every
 // sequence has at least one segment (an empty one passes its state through);
-// entries behind the last hold -1 rows.
+// entries behind the last hold -1 rows.  One workgroup, 3 to 5 us: its launch.
 __global__ __launch_bounds__(256) void pdssm_linattn_table_kernel(const int32_t* cu, int32_t* table,
                                                                   int32_t* starts, int B, int L, int seg, int segs) {
   __shared__ int wsum[4];
@@ -62,7 +62,10 @@ __global__ __launch_bounds__(256) void pdssm_linattn_table_kernel(const int32_t*
 }
 
 // Entering states of all segments of a sequence and head from the segments'
-// contributions, in place, four state elements a thread.
+// contributions, in place, four state elements a thread and eight segments'
+// loads at once.  It moves every segment's state twice, at the rate of the
+// cache behind the L2s (65536 steps in 32 segments, 16 heads, 128/128: 67 MB in
+// 11.7 us).
 __global__ __launch_bounds__(256) void pdssm_linattn_carry_kernel(LaCarryArgs a) {
   const LaCarry& c = a.c[blockIdx.z];
   const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -115,7 +118,8 @@ __device__ __forceinline__ double block_sum(double x, double* red, int tid) {
 // sums run in 64 bits, but r and c carry fp32 errors that do not cancel and
 // grow with the square root of their number: 2048 steps in one sum left 1.6e-6
 // of the gradient, the 512 that a segment has at most half of that.
-// One step a thread: a segment is one round of the workgroup.
+// One step a thread: a segment is one round of the workgroup.  It reads two
+// floats a step and two states a segment (24 heads, 16 x 2048 steps, 64/32: 14 us).
 __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaDecayArgs a) {
   constexpr int W = kLaPiece / 64;
   __shared__ double red[2][W];
@@ -187,7 +191,8 @@ __global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const doub
   if (threadIdx.x == 0) out[h] = (float)x;
 }
 
-// Sum over the value heads of a query or key head, of g_q (y = 0) and g_k.
+// Sum over the value heads of a query or key head, of g_q (y = 0) and g_k:
+// each partial gradient read once (8190 rows, 16 heads on 4, 128: 151 MB in 25 us).
 template <typename T>
 __global__ __launch_bounds__(256) void pdssm_linattn_fold_kernel(const LaFoldArgs a) {
   const float* part = blockIdx.y ? a.part_k : a.part_q;
@@ -218,7 +223,9 @@ __global__ __launch_bounds__(256) void pdssm_linattn_fold_kernel(const LaFoldArg
 
 // One token: S = a S + k v^T in place, o = s S^T q.  One workgroup owns `cols`
 // value columns of one row and head; a thread owns four columns of every
-// nr-th state row.  The state is read and written once, which is all the time.
+// nr-th state row.  The state is read and written once, which is all the time
+// (250 rows, 16 heads, 128/128: 532 MB in 95 us, 5.6 TB/s; one row: 5.7 us, of
+// which the loads' way there and back is most).
 template <typename T>
 __global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArgs a) {
   __shared__ float qs[kLaMaxD], ks[kLaMaxD];
