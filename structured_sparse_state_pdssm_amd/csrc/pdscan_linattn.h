@@ -414,7 +414,7 @@ template <typename T, int DKP, int NW>
 struct LaTile {
   static constexpr bool kF32 = sizeof(typename T::store) == 4;
   // Tokens of a chunk.  64 where four waves share the scores (bf16); else 32, which
-  // halves the registers and the LDS of a workgroup (two to three waves a SIMD
+  // halves the registers and the LDS of a workgroup (two waves a SIMD
   // instead of one: 24 heads of 64/32 at 16 x 2048 tokens 122 -> 104 us).
   static constexpr int C = NW < 4 || kF32 ? 32 : 64;
   static constexpr int NT = NW * 64;
@@ -437,13 +437,12 @@ struct LaTile {
   static constexpr size_t state_bytes() { return 2 * (kX + kZ) + (size_t)NW * 64 * 4; }
   using X = LaTileIO<T, C, DKP, NT>;
   using Z = LaTileIO<T, C, NW * 32, NT>;
-  // registers: state, outputs and the tiles under way
-  static constexpr int kRegs = 16 * (KT + IT) + 4 * (2 * X::N + Z::N);
   // rows of 256 elements: the scheduler is kept from loading more operands ahead than the registers hold
   static constexpr bool kWide = KT == 8;
   static constexpr bool kApart = kF32 || KT < 4 || (KT == 4 && !kShareP);
-  static constexpr int kStateWaves = 16 * KT + 4 * (X::N + Z::N) <= 64 ? 3 : 2;
-  static constexpr int waves(bool bwd) { return la_simd_waves(kRegs, kF32, bwd); }
+  static constexpr int kWaves = la_simd_waves(la_regs(KT + IT, 2 * X::N + Z::N, kF32));
+  // (fp32 rows of 256 spill at two: 2 x 2048 steps, 8 heads, 256/256 232 us instead of 174 for the whole pass)
+  static constexpr int kStateWaves = kWide && kF32 ? 1 : 2;
 };
 
 // S = decay S + sum_j y_j (w_j z_j)^T (KEEP: S as it is).  The sum of 32 tokens
@@ -938,7 +937,7 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
 // JOBS: the modes of its jobs, a bit each.
 template <typename T, int DKP, int NW, int JOBS>
 __global__ __launch_bounds__(NW * 64)
-    __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::waves(JOBS != 1 << kLaFwd)))) void
+    __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
     pdssm_linattn_kernel(const LaArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const unsigned id = blockIdx.x;

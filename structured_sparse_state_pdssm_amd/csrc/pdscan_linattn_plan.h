@@ -98,11 +98,16 @@ inline int la_slabs(int DK, int DV, int bf16) {
   const int w = 32 * la_waves(DK, DV, bf16);
   return (DV + w - 1) / w;
 }
-// Waves of the product kernel on a SIMD, by the registers of a lane that its
-// state, outputs and tiles under way take (the compiler's spills confirm it).
-inline constexpr int la_simd_waves(int regs, bool f32, bool bwd) {
-  return regs <= (bwd ? f32 ? 0 : 56 : 72) ? 3 : regs <= 150 ? 2 : 1;
-}
+// Registers of a lane that the state and the outputs (`tiles` of 32 x 32 a
+// wave) and the tiles under way (`units` of 16 bytes a lane) take; an fp32 unit
+// counts its pieces on their way to LDS too.
+inline constexpr int la_regs(int tiles, int units, bool f32) { return 16 * tiles + (f32 ? 11 * units / 2 : 4 * units); }
+// Waves of the product kernel on a SIMD: two, and one where two would spill.
+// 65536 steps of 128/128 bf16 (144 registers by that count) 262 us with two, 369
+// with one; 8 x 2048 steps, 12 heads in fp32: 128/128 (146) 255 and 305, the
+// gradient of 32/64 (158) 245 and 193; 2 x 2048 steps, 8 heads, 256/256 bf16 (216)
+// 115 and 91.  Three change nothing where they fit.
+inline constexpr int la_simd_waves(int regs) { return regs <= 150 ? 2 : 1; }
 // Workgroups of the product kernel that a compute unit holds, by LDS (160 KiB)
 // and by those waves.
 inline int la_resident(int DK, int DV, int bf16, int bwd) {
@@ -110,8 +115,7 @@ inline int la_resident(int DK, int DV, int bf16, int bwd) {
   const int C = nw < 4 || !bf16 ? 32 : 64;
   const int lds = C * (bf16 ? 2 : 6) * (2 * d + 32 * nw) + (nw == 4 && bf16 ? (bwd ? 3 : 2) * C * C * 2 : 0) +
                   4 * (64 / C * (8 * C + 8) + (nw + 1) * C);
-  const int regs = (d + C) / 2 + C * es * (2 * d + 32 * nw) / (256 * nw);
-  const int waves = 4 * la_simd_waves(regs, !bf16, bwd);
+  const int waves = 4 * la_simd_waves(la_regs((d + C) / 32, C * es * (2 * d + 32 * nw) / (1024 * nw), !bf16));
   const int n = 163840 / lds < waves / nw ? 163840 / lds : waves / nw;
   return n < 1 ? 1 : n;
 }
