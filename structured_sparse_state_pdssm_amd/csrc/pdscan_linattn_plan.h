@@ -4,7 +4,6 @@
 
 #include <cstddef>
 #include <cstdint>
-#include <cstdlib>
 
 namespace pdscan {
 
@@ -132,10 +131,11 @@ struct LaSplit {
 // no long one is left alone at the end.  A segment's states are written and
 // read twice; with at least a workgroup a compute unit they stay under half of
 // what its steps (`bytes` each) move.  No segment is over `longest` steps.
-//   65536 steps, 16 heads, 128/128 bf16: 32 segments of 2048 434 us, of 1024 459, of 4096 506, uncut over 5000
-//   16 x 2048 steps, 24 heads, 64/32 bf16: 4 segments of 512 104 us, 8 of 256 114, uncut 131
-//   4 x 4096 steps, 8 heads, 16/64 fp32: 128 steps 53 us, 64 63, 256 71
-//   23 sequences in 12001 rows, 24 heads, 128/64 bf16: 384 steps 102 us, 192 107, 640 117
+//   65536 steps, 16 heads, 128/128 bf16: 2048 steps 405 us, 1024 449, 4096 423, uncut over 5000
+//   16 x 2048 steps, 24 heads, 64/32 bf16: 448 steps 111 us (512 103, 256 119), uncut 125
+//   4 x 4096 steps, 8 heads, 16/64 fp32: 128 steps 46 us, 64 62, 256 63
+//   23 sequences in 12001 rows, 24 heads, 128/64 bf16: 384 steps 105 us, 192 117, 640 124
+//   gradient of 9 in 8190 rows, 16 heads, 128/128 bf16: 512 steps 243 us, 384 254, 256 275
 inline LaSplit la_split(int B, int L, int packed, int width, int room, long long state, int bytes, int longest) {
   LaSplit s;
   long long n = (long long)room / (packed ? width : (long long)B * width);   // segments of a sequence
