@@ -104,8 +104,9 @@ int check_dims(const pdssm_linattn_dims* d, bool step) {
     return set_error(PDSSM_EINVAL, "a step has L=1 and packed=0 (got L=%d packed=%d)", d->L, d->packed);
   if (d->L > 0x7fffff00) return set_error(PDSSM_EUNSUPPORTED, "L=%d is too long", d->L);
   const uint64_t units = (uint64_t)d->B * d->H;
-  if (units > 0x7fffffffull || (uint64_t)d->B * d->H * (d->packed ? 1 : d->L) > (1ull << 40))
-    return set_error(PDSSM_EUNSUPPORTED, "B*H or B*H*L is too large");
+  // (packed: L counts the rows of all sequences)
+  if (units > 0x7fffffffull || (uint64_t)(d->packed ? 1 : d->B) * d->H * d->L > (1ull << 40))
+    return set_error(PDSSM_EUNSUPPORTED, "B*H or the heads' rows are too many");
   return PDSSM_OK;
 }
 
@@ -121,7 +122,8 @@ int view_span(Span& s, LaView& v, const char* name, const pdssm_view* a, const p
   if ((uintptr_t)a->data & 3) return set_error(PDSSM_EINVAL, "%s is not 4-byte aligned", name);
   for (int i = 0; i < 3; ++i) {
     if (ext[i] == 1) continue;   // an axis of one element has no step
-    if (str[i] < 0 || str[i] > (1ll << 40)) return set_error(PDSSM_EINVAL, "%s has a negative or huge stride", name);
+    // three such axes stay within 64 bits of bytes
+    if (str[i] < 0 || str[i] > (1ll << 40) || str[i] > (1ll << 60) / (es * (ext[i] - 1))) return set_error(PDSSM_EINVAL, "%s has a negative or huge stride", name);
     if (width > 1 && (str[i] * es) % 16)
       return set_error(PDSSM_EINVAL, "%s has a stride of %lld elements, not a multiple of 16 bytes", name,
                        (long long)str[i]);
@@ -543,6 +545,7 @@ int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, cons
   if (n_slots < 1) return set_error(PDSSM_EINVAL, "n_slots must be >= 1 (got %d)", n_slots);
   if (!state_idx && n_slots < d.B)
     return set_error(PDSSM_EINVAL, "n_slots=%d < B=%d without state_idx", n_slots, d.B);
+  if ((uint64_t)n_slots * d.H > (1ull << 40)) return set_error(PDSSM_EUNSUPPORTED, "n_slots * H is too large");
   const int es = d.in_dtype == PDSSM_BF16 ? 2 : 4;
   Span in[5], out[2];
   LaView vq, vk, vv, vg, vo;

@@ -103,6 +103,21 @@ int main() {
     w.stride_h = s;
     expect(pdssm_linattn_fwd(&d, &q, &k, &v, &g, nullptr, nullptr, &w, (float*)at(11), at(14), 1 << 20, nullptr), PDSSM_EINVAL, "o stride");
   }
+  // sizes and strides whose product passes 64 bits
+  d = dims(1, 1, 1, 0x7fffff00, 8, 8);
+  pdssm_linattn_workspace_bytes(&d, &n);
+  {
+    pdssm_view a = view(0, d, 1, 8), b = view(1, d, 1, 8), c = view(2, d, 1, 8), e = view(3, d, 1, 8), w = view(4, d, 1, 1);
+    w.stride_t = (int64_t)1 << 40;
+    expect(pdssm_linattn_fwd(&d, &a, &b, &c, &w, nullptr, nullptr, &e, (float*)at(11), at(14), n, nullptr), PDSSM_EINVAL, "long stride");
+  }
+  d = dims(1, 1 << 20, 1, 1 << 30, 8, 8, 1);
+  expect(pdssm_linattn_workspace_bytes(&d, &n), PDSSM_EUNSUPPORTED, "packed H*L");
+  d = dims(1, 1 << 20, 1 << 20, 1, 256, 256);
+  {
+    pdssm_view a = view(0, d, 1 << 20, 256), b = view(1, d, 1 << 20, 256), c = view(2, d, 1 << 20, 256), e = view(3, d, 1 << 20, 256), w = view(4, d, 1 << 20, 1);
+    expect(pdssm_linattn_step(&d, &a, &b, &c, &w, (const int32_t*)at(9), 0x7fffffff, (float*)at(11), &e, nullptr), PDSSM_EUNSUPPORTED, "huge pool");
+  }
   if (g_launches != reached) ++g_fail;
   // the stride of an axis of one element is not looked at
   d = dims(1, 1, 1, 1, 8, 8);
