@@ -536,6 +536,57 @@ def test_two_graphs_replayed():
         assert torch.equal(so, es) and torch.equal(pool, want_pool), turn
 
 
+def test_captured_packed_call_follows_its_offsets():
+    """The segment table is made on the device: a replay sees the offsets that are there then."""
+    x, cu = packed([500, 300, 0, 203], 2, 1, 64, 32, BF, tail=0)
+    fwd(x, cu_seqlens=cu), bwd(x, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, hL = fwd(x, cu_seqlens=cu)
+        g = bwd(x, cu_seqlens=cu)
+    for lens in ([500, 300, 0, 203], [1, 0, 1001, 1], [0, 1003, 0, 0], [250, 251, 251, 251]):
+        cu.copy_(torch.tensor([0] + lens).cumsum(0))
+        graph.replay()
+        torch.cuda.synchronize()
+        eo, eh = fwd(x, cu_seqlens=cu)
+        eg = bwd(x, cu_seqlens=cu)
+        torch.cuda.synchronize()
+        assert torch.equal(o, eo) and torch.equal(hL, eh), lens
+        assert all(torch.equal(g[n], eg[n]) for n in g), lens
+        for i in range(4):
+            y, a, b = part(x, cu, i)
+            if a != b:
+                check_fwd(y, eo[:, :, a:b], eh[i:i + 1], 64 ** -0.5)
+
+
+def test_step_of_many_rows():
+    """More rows than a round of the search for an earlier row of the slot, in any order, some of them empty or again."""
+    P = lib()
+    n, slots = 3001, 3500
+    x = make(n, 1, 1, 1, 8, 8, BF)
+    gen = torch.Generator().manual_seed(5)
+    idx = torch.randperm(slots, generator=gen)[:n].to(torch.int32)
+    idx[::97] = -1
+    idx[2999] = idx[1500]
+    idx[1700] = idx[5]
+    pool = torch.randn(slots, 1, 8, 8, generator=gen).cuda()
+    new = pool.clone()
+    row = lambda t: t[:, :, 0]  # noqa: E731
+    o = P.pdssm_linattn_step(row(x["q"]), row(x["k"]), row(x["v"]), row(x["log_decay"]), new, state_idx=idx.cuda())
+    ok = idx >= 0
+    ok[2999] = ok[1700] = False
+    at = idx[ok].long().cuda()
+    use = ok.cuda()
+    own = pool[at].clone()
+    want = P.pdssm_linattn_step(*(row(x[m])[use].contiguous() for m in ("q", "k", "v", "log_decay")), own)
+    assert torch.equal(o[use], want) and torch.equal(new[at], own)
+    assert (o[(idx < 0).cuda()] == 0).all() and torch.isnan(o[[1700, 2999]].float()).all()
+    rest = torch.ones(slots, dtype=torch.bool)
+    rest[at.cpu()] = False
+    assert torch.equal(new[rest.cuda()], pool[rest.cuda()])
+
+
 def test_prompt_then_tokens_then_gradient():
     """As they are used together: packed prompts fill a pool, tokens follow, and the gradient of the whole
     prompt equals the one of its two halves joined at the state."""
