@@ -224,7 +224,7 @@ __global__ __launch_bounds__(256) void pdssm_linattn_fold_kernel(const LaFoldArg
 // One token: S = a S + k v^T in place, o = s S^T q.  One workgroup owns `cols`
 // value columns of one row and head; a thread owns four columns of every
 // nr-th state row.  The state is read and written once, which is all the time
-// (250 rows, 16 heads, 128/128: 532 MB in 95 us, 5.6 TB/s; one row: 5.7 us, of
+// (250 rows, 16 heads, 128/128: 532 MB in 95 us, 5.6 TB/s; one row: 5.0 us, of
 // which the loads' way there and back is most).
 template <typename T>
 __global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArgs a) {
@@ -292,9 +292,23 @@ __global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArg
     *(float4*)(red + 4 * tid) = make_float4(o[0], o[1], o[2], o[3]);
   }
   __syncthreads();
+  // The nr partial sums of a column: more than 16 in two rounds, by eight
+  // threads in the first (64 of them 5.7 -> 5.0 us for the call; 16 4.1 -> 4.4).
+  int parts = nr;
+  if (nr > 16) {
+    parts = 8;
+    if (rg < parts) {
+      for (int g = rg + parts; g < nr; g += parts) {
+        const float4 p = *(const float4*)(red + 4 * (g * W + c / 4));
+        o[0] += p.x; o[1] += p.y; o[2] += p.z; o[3] += p.w;
+      }
+      *(float4*)(red + 4 * tid) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+    __syncthreads();
+  }
   if (tid < W) {
     float x[4] = {0, 0, 0, 0};
-    for (int g = 0; g < nr; ++g) {
+    for (int g = 0; g < parts; ++g) {
       const float4 p = *(const float4*)(red + 4 * (g * W + tid));
       x[0] += p.x; x[1] += p.y; x[2] += p.z; x[3] += p.w;
     }

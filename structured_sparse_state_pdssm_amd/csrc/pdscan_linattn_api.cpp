@@ -566,7 +566,7 @@ int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, cons
   a.scale = d.scale;
   a.bf16 = d.in_dtype == PDSSM_BF16;
   // Columns per workgroup: whole rows (16 states of 128/128 6.1 us, 264 of 16/64 4.1), halved down to 16 (64
-  // bytes of a row) while there is not a workgroup for every compute unit (the 16 5.7 us; the 264 in quarters 6.8).
+  // bytes of a row) while there is not a workgroup for every compute unit (the 16 5.0 us; the 264 in quarters 6.8).
   a.cols = d.dv;
   while (a.cols >= 32 && a.cols % 16 == 0 && (long long)d.B * d.H * (d.dv / a.cols) < kCus) a.cols /= 2;
   if ((long long)d.B * d.H * ((d.dv + a.cols - 1) / a.cols) > 0x7fffffffll)
