@@ -177,7 +177,7 @@ struct FwdWs {
 FwdWs fwd_ws(const pdssm_linattn_dims* d) {
   FwdWs w;
   const int bf16 = d->in_dtype == PDSSM_BF16;
-  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * pdscan::la_slabs(d->dk, d->dv, bf16),
+  w.split = pdscan::la_split(d->B, d->L, d->packed, (long long)d->H * pdscan::la_slabs(d->dk, d->dv, bf16),
                              kCus * pdscan::la_resident(d->dk, d->dv, bf16, 0), (long long)d->dk * d->dv,
                              (2 * d->dk + 2 * d->dv) * (bf16 ? 2 : 4), 0x7fffff00);
   size_t at = pdscan::kLaHeader;
@@ -215,7 +215,7 @@ BwdWs bwd_ws(const pdssm_linattn_dims* d) {
   w.one = pdscan::la_pad(d->dk) == pdscan::la_pad(d->dv) && w.qslabs == w.vslabs &&
           pdscan::la_waves(d->dk, d->dv, bf16) == pdscan::la_waves(d->dv, d->dk, bf16);
   // the launch with the most work decides: all three jobs in one, or those of q and k
-  w.split = pdscan::la_split(d->B, d->L, d->packed, d->H * (w.one ? 3 : 2) * w.qslabs,
+  w.split = pdscan::la_split(d->B, d->L, d->packed, (long long)d->H * (w.one ? 3 : 2) * w.qslabs,
                              kCus * pdscan::la_resident(d->dv, d->dk, bf16, 1), 2ll * d->dk * d->dv,
                              (8 * d->dk + 7 * d->dv) * (bf16 ? 2 : 4), pdscan::kLaPiece);
   size_t at = pdscan::kLaHeader;

@@ -136,11 +136,11 @@ struct LaSplit {
 //   4 x 4096 steps, 8 heads, 16/64 fp32: 128 steps 46 us, 64 62, 256 63
 //   23 sequences in 12001 rows, 24 heads, 128/64 bf16: 384 steps 105 us, 192 117, 640 124
 //   gradient of 9 in 8190 rows, 16 heads, 128/128 bf16: 512 steps 243 us, 384 254, 256 275
-inline LaSplit la_split(int B, int L, int packed, int width, int room, long long state, int bytes, int longest) {
+inline LaSplit la_split(int B, int L, int packed, long long width, int room, long long state, int bytes, int longest) {
   LaSplit s;
-  long long n = (long long)room / (packed ? width : (long long)B * width);   // segments of a sequence
+  long long n = (long long)room / (packed ? width : B * width);   // segments of a sequence
   if (packed) n = n * 7 / 4;
-  const long long least = 256 / (packed ? width : (long long)B * width), most = (long long)L * bytes / (32 * state);
+  const long long least = 256 / (packed ? width : B * width), most = (long long)L * bytes / (32 * state);
   if (n > most) n = most > least ? most : least < n ? least : n;
   if (n > (L - 1) / kLaChunk + 1) n = (L - 1) / kLaChunk + 1;
   if (n < ((long long)L + longest - 1) / longest) n = ((long long)L + longest - 1) / longest;

@@ -1,0 +1,37 @@
+"""The linear-attention calls at the ends of what their arguments can name, on
+the host: plans, limits and the kernels that a call can reach, built with g++
+and the host sanitizers against stand-in launchers."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "structured_sparse_state_pdssm_amd", "csrc")
+SAN = os.path.join(ROOT, "tests", "sanitize")
+HIP_INC = "/opt/rocm/include"
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir(HIP_INC),
+                                reason="needs g++ and the HIP headers")
+
+
+def run(tmp_path, name, *more, std="c++17"):
+    """Build tests/sanitize/<name>.cpp (with the C ABI where asked for) and run it; its output."""
+    exe = str(tmp_path / name)
+    cmd = ["g++", f"-std={std}", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+           "-D__HIP_PLATFORM_AMD__", f"-I{HIP_INC}", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}", *more,
+           os.path.join(SAN, name + ".cpp"), "-o", exe]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "ok: 0 failures" in r.stdout, r.stdout + r.stderr
+    return r.stdout
+
+
+API = os.path.join(CSRC, "pdscan_linattn_api.cpp")
+
+
+def test_workspace_queries_of_extreme_sizes(tmp_path):
+    """Jobs, slabs and heads multiply past 32 bits: refused, not divided by what is left of the product."""
+    run(tmp_path, "linattn_sizes", API)
