@@ -23,7 +23,7 @@ SOURCES = ["pdscan_api.cpp", "pdscan_launch_select.hip", "pdscan_launch_scan.hip
 HEADERS = ["pdscan_plan.h", "pdscan_device.h", "pdscan_launch_general.h", "pdscan_bwd_plan.h", "pdscan_bwd.h",
            "pdscan_sens_plan.h", "pdscan_sens.h", "pdscan_soft_plan.h", "pdscan_soft.h", "pdscan_gemm_sel.h", "pdscan_gemm_sel_plan.h",
            "pdscan_error.h", "pdscan_linattn_plan.h", "pdscan_linattn.h", "pdscan_linattn_launch.h",
-           "pdscan_linattn_inst.h"]
+           "pdscan_linattn_inst.h", "pdscan_linattn_table.h"]
 
 COMPILE_FLAGS = [
     "-O3", "-std=c++17", "-fPIC",

@@ -35,3 +35,9 @@ API = os.path.join(CSRC, "pdscan_linattn_api.cpp")
 def test_workspace_queries_of_extreme_sizes(tmp_path):
     """Jobs, slabs and heads multiply past 32 bits: refused, not divided by what is left of the product."""
     run(tmp_path, "linattn_sizes", API)
+
+
+def test_segment_table_of_any_offsets(tmp_path):
+    """The table's kernel lane by lane: entries of offsets in order, and nothing written outside the table where the
+    offsets ask for more segments than 32 bits count."""
+    run(tmp_path, "linattn_table", "-pthread", std="c++20")
