@@ -364,7 +364,9 @@ int pdssm_dict_hardmax(int32_t H, int32_t K, int32_t N, const float* M, int32_t*
  *     another workgroup.
  *   - Shape limits (else PDSSM_EUNSUPPORTED): dk and dv multiples of 8, at
  *     most 256; step strides at most 2^23 elements, and H * dk likewise where
- *     the gradient sums over shared heads.
+ *     the gradient sums over shared heads; H times the sequences (or the
+ *     segments, of 64 steps and more, that few long ones are cut into) at most
+ *     (2^31 - 1) / 6.  The workspace queries apply the last of these too.
  * Precision: decay sums are held in 64 bits, states, weights and sums in
  * fp32.  On the matrix cores bf16 inputs are exact; what is computed enters
  * as two bf16 pieces where a bf16 output comes of it (2^-18 of a term) and as

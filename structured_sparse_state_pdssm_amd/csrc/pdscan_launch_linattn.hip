@@ -16,10 +16,11 @@ namespace pdscan {
 // cache behind the L2s (65536 steps in 32 segments, 16 heads, 128/128: 67 MB in
 // 11.7 us).
 __global__ __launch_bounds__(256) void pdssm_linattn_carry_kernel(LaCarryArgs a) {
-  const LaCarry& c = a.c[blockIdx.z];
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const long long e = ((long long)blockIdx.y * 256 + threadIdx.x) * 4;
-  if (e >= a.state) return;
+  const LaCarry& c = a.c[blockIdx.z / a.tiles];
+  const unsigned unit = la_block();
+  const int b = unit / a.H, h = unit % a.H;
+  const long long e = ((long long)(blockIdx.z % a.tiles) * 256 + threadIdx.x) * 4;
+  if (b >= a.B || e >= a.state) return;
   const int s0 = a.starts ? a.starts[b] : b * a.nseg;
   const int s1 = a.starts ? a.starts[b + 1] : s0 + a.nseg;
   const int n = s1 - s0 - 1;
@@ -73,7 +74,9 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
   constexpr int W = kLaPiece / 64;
   __shared__ double red[2][W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.x % a.c.H, sid = blockIdx.x / a.c.H;
+  const unsigned id = la_block();
+  const int h = id % a.c.H, sid = id / a.c.H;
+  if (sid >= a.c.segs) return;
   LaSeg s;
   if (!la_segment(a.c, sid, s)) {
     if (a.per_head && tid == 0) a.part[(long long)sid * a.c.H + h] = 0.0;
@@ -133,7 +136,8 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
 
 __global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int segs) {
   __shared__ double red[4];
-  const int h = blockIdx.x;
+  const unsigned h = la_block();
+  if (h >= (unsigned)H) return;
   double x = 0.0;
   for (int s = threadIdx.x; s < segs; s += 256) x += part[(long long)s * H + h];
   x = block_sum(x, red, threadIdx.x);
@@ -182,10 +186,11 @@ __global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArg
   __shared__ int dup;
   const int tid = threadIdx.x;
   const int tiles = (a.dv + a.cols - 1) / a.cols;
-  unsigned id = blockIdx.x;
+  unsigned id = la_block();
   const int tile = id % tiles;
   id /= tiles;
   const int h = id % a.H, b = id / a.H;
+  if (b >= a.B) return;
   const int c0 = tile * a.cols;
   const int cols = a.dv - c0 < a.cols ? a.dv - c0 : a.cols;
   using E = typename T::store;
@@ -268,12 +273,11 @@ __global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArg
 
 hipError_t launch_linattn_step(const LaStepArgs& a, hipStream_t st) {
   const int tiles = (a.dv + a.cols - 1) / a.cols;
-  const long long grid = (long long)a.B * a.H * tiles;
-  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  const LaGrid g = la_grid_rows((long long)a.B * a.H * tiles, 256);
   if (a.bf16)
-    hipLaunchKernelGGL(pdssm_linattn_step_kernel<LaBf16>, dim3((unsigned)grid), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(pdssm_linattn_step_kernel<LaBf16>, dim3(g.x, g.y), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL(pdssm_linattn_step_kernel<LaF32>, dim3((unsigned)grid), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(pdssm_linattn_step_kernel<LaF32>, dim3(g.x, g.y), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -284,20 +288,19 @@ hipError_t launch_linattn_table(const int32_t* cu, int32_t* table, int32_t* star
 }
 
 hipError_t launch_linattn_carry(const LaCarryArgs& a, int passes, hipStream_t st) {
-  const long long grid = (long long)a.B * a.H;
-  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(pdssm_linattn_carry_kernel, dim3((unsigned)grid, (unsigned)((a.state / 4 + 255) / 256), passes),
-                     dim3(256), 0, st, a);
+  const LaGrid g = la_grid_rows((long long)a.B * a.H, 256);
+  hipLaunchKernelGGL(pdssm_linattn_carry_kernel, dim3(g.x, g.y, a.tiles * passes), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
 hipError_t launch_linattn_decay(const LaDecayArgs& a, hipStream_t st) {
-  const long long grid = (long long)a.c.segs * a.c.H;
-  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(pdssm_linattn_decay_kernel, dim3((unsigned)grid), dim3(kLaPiece), 0, st, a);
-  if (a.per_head)
-    hipLaunchKernelGGL(pdssm_linattn_decay_sum_kernel, dim3((unsigned)a.c.H), dim3(256), 0, st, a.part,
-                       (float*)a.out.p, a.c.H, a.c.segs);
+  LaGrid g = la_grid_rows((long long)a.c.segs * a.c.H, kLaPiece);
+  hipLaunchKernelGGL(pdssm_linattn_decay_kernel, dim3(g.x, g.y), dim3(kLaPiece), 0, st, a);
+  if (a.per_head) {
+    g = la_grid_rows(a.c.H, 256);
+    hipLaunchKernelGGL(pdssm_linattn_decay_sum_kernel, dim3(g.x, g.y), dim3(256), 0, st, a.part, (float*)a.out.p, a.c.H,
+                       a.c.segs);
+  }
   return hipGetLastError();
 }
 
@@ -316,17 +319,16 @@ hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
 // The product kernels, by type, x-row width and waves.
 hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pass, hipStream_t st) {
   const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DK, a.job[0].DV, bf16);
-  const long long grid = la_grid(a);
-  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  const LaGrid g = la_grid_rows(la_grid(a), 64 * nw);
   if (bf16)
-    return dk == 32    ? la_bf16_32(a, nw, pass, (unsigned)grid, st)
-           : dk == 64  ? la_bf16_64(a, nw, pass, (unsigned)grid, st)
-           : dk == 128 ? la_bf16_128(a, nw, pass, (unsigned)grid, st)
-                       : la_bf16_256(a, nw, pass, (unsigned)grid, st);
-  return dk == 32    ? la_f32_32(a, nw, pass, (unsigned)grid, st)
-         : dk == 64  ? la_f32_64(a, nw, pass, (unsigned)grid, st)
-         : dk == 128 ? la_f32_128(a, nw, pass, (unsigned)grid, st)
-                     : la_f32_256(a, nw, pass, (unsigned)grid, st);
+    return dk == 32    ? la_bf16_32(a, nw, pass, g, st)
+           : dk == 64  ? la_bf16_64(a, nw, pass, g, st)
+           : dk == 128 ? la_bf16_128(a, nw, pass, g, st)
+                       : la_bf16_256(a, nw, pass, g, st);
+  return dk == 32    ? la_f32_32(a, nw, pass, g, st)
+         : dk == 64  ? la_f32_64(a, nw, pass, g, st)
+         : dk == 128 ? la_f32_128(a, nw, pass, g, st)
+                     : la_f32_256(a, nw, pass, g, st);
 }
 
 }  // namespace pdscan

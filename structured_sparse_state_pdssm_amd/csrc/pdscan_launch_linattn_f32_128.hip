@@ -2,7 +2,7 @@
 #include "pdscan_linattn_inst.h"
 
 namespace pdscan {
-hipError_t la_f32_128(const LaArgs& a, int nw, int pass, unsigned grid, hipStream_t st) {
-  return la_launch<LaF32, 128>(a, nw, pass, grid, st);
+hipError_t la_f32_128(const LaArgs& a, int nw, int pass, LaGrid g, hipStream_t st) {
+  return la_launch<LaF32, 128>(a, nw, pass, g, st);
 }
 }  // namespace pdscan

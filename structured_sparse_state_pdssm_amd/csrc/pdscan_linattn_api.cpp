@@ -257,7 +257,7 @@ int launched(hipError_t e) {
 }
 
 int grid_ok(const LaSplit& s, const pdssm_linattn_dims* d) {
-  // up to three jobs of two slabs each
+  // workgroups are numbered in 31 bits: up to three jobs of two slabs each
   if ((uint64_t)s.segs * d->H * 6 > 0x7fffffffull)
     return set_error(PDSSM_EUNSUPPORTED, "too many segments and heads (%d, %d)", s.segs, d->H);
   return PDSSM_OK;
@@ -360,7 +360,7 @@ int pdssm_linattn_fwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
     pdscan::LaCarryArgs c = {};
     c.c[0].seg = J.seg_out; c.c[0].decay = J.seg_decay; c.c[0].user = h0; c.c[0].rev = 0;
     c.starts = d.packed ? (const int32_t*)(ws + w.starts) : nullptr;
-    c.B = d.B; c.H = d.H; c.nseg = w.split.nseg; c.state = a.state;
+    c.B = d.B; c.H = d.H; c.nseg = w.split.nseg; c.state = a.state; c.tiles = (int)((a.state + 1023) / 1024);
     if (e == hipSuccess) e = pdscan::launch_linattn_carry(c, 1, st);
   }
   if (e == hipSuccess) e = pdscan::launch_linattn_form(a, bf16, pdscan::kLaPassFwd, st);
@@ -491,7 +491,7 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
     c.c[0].seg = s.job[0].seg_out; c.c[0].decay = s.job[0].seg_decay; c.c[0].user = h0; c.c[0].rev = 0;
     c.c[1].seg = s.job[1].seg_out; c.c[1].decay = s.job[1].seg_decay; c.c[1].user = g_hL; c.c[1].rev = 1;
     c.starts = d.packed ? (const int32_t*)(ws + w.starts) : nullptr;
-    c.B = d.B; c.H = d.H; c.nseg = w.split.nseg; c.state = a.state;
+    c.B = d.B; c.H = d.H; c.nseg = w.split.nseg; c.state = a.state; c.tiles = (int)((a.state + 1023) / 1024);
     if (e == hipSuccess) e = pdscan::launch_linattn_carry(c, 2, st);
   }
   LaArgs m = a;

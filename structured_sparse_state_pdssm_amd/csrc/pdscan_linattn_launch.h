@@ -16,7 +16,7 @@ struct LaCarry {
 struct LaCarryArgs {
   LaCarry c[2];
   const int32_t* starts; // packed: first segment of every sequence
-  int B, H, nseg;
+  int B, H, nseg, tiles;   // tiles: workgroups of a state, 1024 elements each
   long long state;
 };
 
@@ -29,7 +29,7 @@ hipError_t launch_linattn_decay(const LaDecayArgs& a, hipStream_t st);
 hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st);
 hipError_t launch_linattn_step(const LaStepArgs& a, hipStream_t st);
 
-#define PDSCAN_LA_LAUNCHER(name) hipError_t name(const LaArgs& a, int nw, int pass, unsigned grid, hipStream_t st)
+#define PDSCAN_LA_LAUNCHER(name) hipError_t name(const LaArgs& a, int nw, int pass, LaGrid g, hipStream_t st)
 PDSCAN_LA_LAUNCHER(la_bf16_32);
 PDSCAN_LA_LAUNCHER(la_bf16_64);
 PDSCAN_LA_LAUNCHER(la_bf16_128);

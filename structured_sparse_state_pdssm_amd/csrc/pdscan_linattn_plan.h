@@ -160,6 +160,18 @@ inline LaSplit la_split(int B, int L, int packed, long long width, int room, lon
 // or not: 179 us so against 189 and 178, 216 / 214, 70 / 70, 68 / 66).
 inline long long la_grid(const LaArgs& a) { return (long long)a.segs * a.H * a.slabs * a.njobs; }
 
+// A launch has fewer than 2^32 threads along an axis, which is 2^23 workgroups
+// of 512: more take rows of equal length along y, in the same order.  Numbers
+// at or behind `blocks` (fewer than y of them) have nothing to do.
+struct LaGrid {
+  unsigned x, y;
+};
+inline LaGrid la_grid_rows(long long blocks, int threads) {
+  const long long most = 0xffffffffll / threads;
+  const long long y = (blocks + most - 1) / most;
+  return LaGrid{(unsigned)((blocks + y - 1) / y), (unsigned)y};
+}
+
 inline size_t la_align(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace pdscan

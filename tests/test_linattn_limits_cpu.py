@@ -41,3 +41,9 @@ def test_segment_table_of_any_offsets(tmp_path):
     """The table's kernel lane by lane: entries of offsets in order, and nothing written outside the table where the
     offsets ask for more segments than 32 bits count."""
     run(tmp_path, "linattn_table", "-pthread", std="c++20")
+
+
+def test_grids_of_the_largest_calls(tmp_path):
+    """No launch of 2^32 threads along an axis, whatever the sizes; query and call agree; what is refused is refused
+    before its first launch."""
+    run(tmp_path, "linattn_grids", API)
