@@ -195,6 +195,18 @@ def _workspace(nbytes, dev, workspace):
     return workspace
 
 
+def _given(out, names):
+    """The caller's outputs, by name: a misspelt one would be left as it is."""
+    if out is None:
+        return {}
+    if not isinstance(out, dict):
+        raise TypeError(f"out must be a dict (got {type(out).__name__})")
+    for n in out:
+        if n not in names:
+            raise ValueError(f"out has no {n!r}: {', '.join(names)}")
+    return out
+
+
 def pdssm_linattn_fwd(q, k, v, log_decay, h0=None, scale=None, cu_seqlens=None, workspace=None, out=None):
     """Prompts.  Returns (o [B,H,L,dv], h_L [B,H,dk,dv]).  ``scale`` is
     dk ** -0.5 when not given; ``out`` may hold "o" and "h_L" to write to."""
@@ -202,9 +214,8 @@ def pdssm_linattn_fwd(q, k, v, log_decay, h0=None, scale=None, cu_seqlens=None, 
     B, H, Hk, L, dk, dv, _, _, per_head, _ = d
     dt, index = v.dtype, q.get_device()
     kshape, vshape, sshape = (rows, Hk, L, dk), (rows, H, L, dv), (B, H, dk, dv)
-    o = hL = None
-    if out:
-        o, hL = out.get("o"), out.get("h_L")
+    given = _given(out, ("o", "h_L"))
+    o, hL = given.get("o"), given.get("h_L")
     _verify([(q, "q", kshape, dt, _ROWS), (k, "k", kshape, dt, _ROWS), (v, "v", vshape, dt, _ROWS),
              (log_decay, "log_decay", (H,) if per_head else (rows, H, L), _f32, _WHOLE if per_head else _ANY),
              (h0, "h0", sshape, _f32, _WHOLE), (cu_seqlens, "cu_seqlens", (B + 1,), _i32, _WHOLE),
@@ -226,14 +237,15 @@ def pdssm_linattn_bwd(q, k, v, log_decay, g_o, h0=None, g_hL=None, scale=None, c
                       workspace=None, out=None):
     """Gradient of pdssm_linattn_fwd, given the gradients of o and (optional)
     h_L.  Returns dict(g_q, g_k, g_v, g_log_decay[, g_h0]), shaped and typed
-    as their inputs; g_h0 is dLoss/dh0 also where h0 is left out (zero)."""
+    as their inputs; g_h0 is dLoss/dh0 also where h0 is left out (zero).
+    ``out`` may hold any of them to write to (g_h0 only with want_h0)."""
     d, rows = _dims(q, k, v, log_decay, scale, cu_seqlens)
     B, H, Hk, L, dk, dv, _, _, per_head, _ = d
     dt, index = v.dtype, q.get_device()
     kshape, vshape, sshape = (rows, Hk, L, dk), (rows, H, L, dv), (B, H, dk, dv)
     gshape = (H,) if per_head else (rows, H, L)
     glayout = _WHOLE if per_head else _ANY
-    given = out or {}
+    given = _given(out, ("g_q", "g_k", "g_v", "g_log_decay", "g_h0"))
     res = {n: given.get(n) for n in ("g_q", "g_k", "g_v", "g_log_decay")}
     if want_h0:
         res["g_h0"] = given.get("g_h0")
