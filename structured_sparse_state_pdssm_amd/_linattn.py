@@ -240,6 +240,8 @@ def pdssm_linattn_bwd(q, k, v, log_decay, g_o, h0=None, g_hL=None, scale=None, c
     as their inputs; g_h0 is dLoss/dh0 also where h0 is left out (zero).
     ``out`` may hold any of them to write to (g_h0 only with want_h0)."""
     d, rows = _dims(q, k, v, log_decay, scale, cu_seqlens)
+    if not isinstance(g_o, torch.Tensor):
+        raise TypeError("g_o must be a torch.Tensor")
     B, H, Hk, L, dk, dv, _, _, per_head, _ = d
     dt, index = v.dtype, q.get_device()
     kshape, vshape, sshape = (rows, Hk, L, dk), (rows, H, L, dv), (B, H, dk, dv)

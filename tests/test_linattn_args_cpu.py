@@ -35,3 +35,12 @@ def test_unknown_outputs(P):
             P.pdssm_linattn_fwd(**args(), out=out)
     with pytest.raises(ValueError, match="device tensor"):   # left alone, as asked for
         P.pdssm_linattn_bwd(**args(g_o=g_o), want_h0=False, out={"g_h0": None})
+
+
+def test_required_tensors(P):
+    """None where a tensor is required is named, whatever the argument."""
+    for n in ("q", "k", "v", "log_decay"):
+        with pytest.raises(TypeError, match=f"{n} must be a torch.Tensor"):
+            P.pdssm_linattn_fwd(**args(**{n: None}))
+    with pytest.raises(TypeError, match="g_o must be a torch.Tensor"):
+        P.pdssm_linattn_bwd(**args(), g_o=None)
