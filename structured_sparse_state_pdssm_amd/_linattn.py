@@ -32,7 +32,7 @@ _WHOLE, _ROWS, _ANY = range(3)   # layouts: contiguous, contiguous last axis, an
 # time: arguments go as packed bytes (pdssm_linattn_dims, pdssm_view) through
 # functions of their own, and the checks run as one expression whose failure
 # is explained by the slower ones.
-_pack_dims = struct.Struct("9if").pack
+_struct_dims = struct.Struct("9if").pack
 _pack_view = struct.Struct("Pqqq").pack
 
 
@@ -92,6 +92,13 @@ def _verify(specs, dev):
                                   and t.get_device() == dev
                                   and (layout is _ANY or (t.stride(-1) == 1 if layout is _ROWS else t.is_contiguous()))):
             return _explain(specs)
+
+
+def _pack_dims(*fields):
+    try:
+        return _struct_dims(*fields)
+    except (struct.error, OverflowError):
+        raise ValueError(f"scale {fields[-1]!r} or a size in {fields[:6]} (B, H, Hk, L, dk, dv) does not fit 32 bits") from None
 
 
 def _view(t):

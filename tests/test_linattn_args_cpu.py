@@ -44,3 +44,14 @@ def test_required_tensors(P):
             P.pdssm_linattn_fwd(**args(**{n: None}))
     with pytest.raises(TypeError, match="g_o must be a torch.Tensor"):
         P.pdssm_linattn_bwd(**args(), g_o=None)
+
+
+def test_sizes_and_scales_past_32_bits():
+    """What pdssm_linattn_dims cannot hold is a ValueError that shows it."""
+    from tests._libutil import ensure_built
+    ensure_built()
+    from structured_sparse_state_pdssm_amd import _linattn as A
+    assert len(A._pack_dims(1, 2, 1, (1 << 31) - 1, 8, 8, 1, True, False, 0.5)) == 40
+    for f in ((1, 2, 1, 1 << 31, 8, 8, 1, 0, 0, 0.5), (1, 2, 1, 9, 8, 8, 1, 0, 0, 1e300), (1, 2, 1, 9, 8, 8, 1, 0, 0, "x")):
+        with pytest.raises(ValueError, match="32 bits"):
+            A._pack_dims(*f)
