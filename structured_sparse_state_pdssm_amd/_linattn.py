@@ -97,8 +97,8 @@ def _verify(specs, dev):
 def _pack_dims(*fields):
     try:
         return _struct_dims(*fields)
-    except (struct.error, OverflowError):
-        raise ValueError(f"scale {fields[-1]!r} or a size in {fields[:6]} (B, H, Hk, L, dk, dv) does not fit 32 bits") from None
+    except struct.error:
+        raise ValueError(f"scale {fields[-1]!r} or a size in {fields[:6]} (B, H, Hk, L, dk, dv) is no number of 32 bits") from None
 
 
 def _view(t):
