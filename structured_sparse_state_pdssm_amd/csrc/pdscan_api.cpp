@@ -36,21 +36,9 @@ hipError_t noalloc_scratch(void** ptr, size_t* bytes);
 
 using pdscan::Plan;
 
-namespace {
-
-thread_local char g_err[512] = "";
-
-int fail(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-}  // namespace
-
 namespace pdscan {
+static thread_local char g_err[512] = "";
+
 int set_error(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -60,6 +48,9 @@ int set_error(int code, const char* fmt, ...) {
 }
 void clear_error() { g_err[0] = 0; }
 }  // namespace pdscan
+
+using pdscan::g_err;
+using pdscan::set_error;
 
 namespace {
 
@@ -77,23 +68,23 @@ bool overlap(const Range& a, const Range& b) {
 
 // Shape checks common to all entry points.  `chunk` < 0 means "not used".
 int check_dims(const pdssm_dims* d, int32_t chunk) {
-  if (!d) return fail(PDSSM_EINVAL, "dims is NULL");
+  if (!d) return set_error(PDSSM_EINVAL, "dims is NULL");
   if (d->B < 1 || d->H < 1 || d->L < 1 || d->N < 1 || d->K < 1 || d->d_in < 1)
-    return fail(PDSSM_EINVAL, "dims must be >= 1 (B=%d H=%d L=%d N=%d K=%d d_in=%d)", d->B, d->H,
-                d->L, d->N, d->K, d->d_in);
+    return set_error(PDSSM_EINVAL, "dims must be >= 1 (B=%d H=%d L=%d N=%d K=%d d_in=%d)", d->B, d->H,
+                     d->L, d->N, d->K, d->d_in);
   if (d->u_shared != 0 && d->u_shared != 1)
-    return fail(PDSSM_EINVAL, "u_shared must be 0 or 1 (got %d)", d->u_shared);
+    return set_error(PDSSM_EINVAL, "u_shared must be 0 or 1 (got %d)", d->u_shared);
   if (d->in_dtype != PDSSM_F32 && d->in_dtype != PDSSM_BF16)
-    return fail(PDSSM_EINVAL, "in_dtype must be PDSSM_F32 or PDSSM_BF16 (got %d)", d->in_dtype);
-  if (chunk != -1 && chunk < 1) return fail(PDSSM_EINVAL, "chunk must be >= 1 (got %d)", chunk);
-  if (d->N > 64) return fail(PDSSM_EUNSUPPORTED, "N=%d > 64 (one lane owns one state row)", d->N);
-  if (d->K > 64) return fail(PDSSM_EUNSUPPORTED, "K=%d > 64", d->K);
-  if (d->K + d->N > 128) return fail(PDSSM_EUNSUPPORTED, "K+N=%d > 128", d->K + d->N);
-  if (d->d_in % 8 != 0) return fail(PDSSM_EUNSUPPORTED, "d_in=%d is not a multiple of 8", d->d_in);
-  if (d->d_in > 8192) return fail(PDSSM_EUNSUPPORTED, "d_in=%d > 8192", d->d_in);
+    return set_error(PDSSM_EINVAL, "in_dtype must be PDSSM_F32 or PDSSM_BF16 (got %d)", d->in_dtype);
+  if (chunk != -1 && chunk < 1) return set_error(PDSSM_EINVAL, "chunk must be >= 1 (got %d)", chunk);
+  if (d->N > 64) return set_error(PDSSM_EUNSUPPORTED, "N=%d > 64 (one lane owns one state row)", d->N);
+  if (d->K > 64) return set_error(PDSSM_EUNSUPPORTED, "K=%d > 64", d->K);
+  if (d->K + d->N > 128) return set_error(PDSSM_EUNSUPPORTED, "K+N=%d > 128", d->K + d->N);
+  if (d->d_in % 8 != 0) return set_error(PDSSM_EUNSUPPORTED, "d_in=%d is not a multiple of 8", d->d_in);
+  if (d->d_in > 8192) return set_error(PDSSM_EUNSUPPORTED, "d_in=%d > 8192", d->d_in);
   const uint64_t rows = (uint64_t)d->B * d->H * d->L;
   if (rows > 0x7fffffffull)
-    return fail(PDSSM_EUNSUPPORTED, "B*H*L=%llu exceeds 2^31-1", (unsigned long long)rows);
+    return set_error(PDSSM_EUNSUPPORTED, "B*H*L=%llu exceeds 2^31-1", (unsigned long long)rows);
   return PDSSM_OK;
 }
 
@@ -135,11 +126,11 @@ int build_plan(Plan& p, int mode, const pdssm_dims* d, int32_t chunk, int fold_b
   const int c = (mode == pdscan::kModeSelect) ? pdscan::kSelectRows : chunk;
   if (!pdscan::make_plan(p, mode, d->B, d->H, d->L, d->N, d->K, d->d_in, d->u_shared,
                          d->in_dtype == PDSSM_BF16, c, fold_bu, step16, n_out))
-    return fail(PDSSM_EUNSUPPORTED,
-                "chunk=%d with N=%d needs %d bytes of on-chip memory per workgroup (limit %d)", c,
-                d->N, p.lds_bytes, p.lds_limit);
+    return set_error(PDSSM_EUNSUPPORTED,
+                     "chunk=%d with N=%d needs %d bytes of on-chip memory per workgroup (limit %d)", c,
+                     d->N, p.lds_bytes, p.lds_limit);
   if ((uint64_t)p.nC * d->B * d->H > 0x7fffffffull)
-    return fail(PDSSM_EUNSUPPORTED, "too many chunks");
+    return set_error(PDSSM_EUNSUPPORTED, "too many chunks");
   if (mode == pdscan::kModeFused && !p.fused16) {
     int hg = pdscan::xcd_head_groups(p.B, p.H, p.L, p.N, p.K, p.d, p.u_shared, p.in_bf16, p.fold_bu, p.nC);
     const int forced = xcd_groups_hook();
@@ -185,24 +176,24 @@ int check_ptrs(const Range* in, int nin, const Range* out, int nout, const char*
   for (int r = 0; required[r]; ++r) {
     for (int q = 0; q < nin; ++q)
       if (!strcmp(in[q].name, required[r]) && !in[q].p)
-        return fail(PDSSM_EINVAL, "%s is NULL", in[q].name);
+        return set_error(PDSSM_EINVAL, "%s is NULL", in[q].name);
     for (int q = 0; q < nout; ++q)
       if (!strcmp(out[q].name, required[r]) && !out[q].p)
-        return fail(PDSSM_EINVAL, "%s is NULL", out[q].name);
+        return set_error(PDSSM_EINVAL, "%s is NULL", out[q].name);
   }
   for (int q = 0; q < nin; ++q)
     if (in[q].p && ((uintptr_t)in[q].p & 15))
-      return fail(PDSSM_EINVAL, "%s is not 16-byte aligned", in[q].name);
+      return set_error(PDSSM_EINVAL, "%s is not 16-byte aligned", in[q].name);
   for (int q = 0; q < nout; ++q)
     if (out[q].p && ((uintptr_t)out[q].p & 15))
-      return fail(PDSSM_EINVAL, "%s is not 16-byte aligned", out[q].name);
+      return set_error(PDSSM_EINVAL, "%s is not 16-byte aligned", out[q].name);
   for (int q = 0; q < nout; ++q) {
     for (int r = 0; r < nin; ++r)
       if (overlap(out[q], in[r]))
-        return fail(PDSSM_EINVAL, "output %s overlaps input %s", out[q].name, in[r].name);
+        return set_error(PDSSM_EINVAL, "output %s overlaps input %s", out[q].name, in[r].name);
     for (int r = q + 1; r < nout; ++r)
       if (overlap(out[q], out[r]))
-        return fail(PDSSM_EINVAL, "outputs %s and %s overlap", out[q].name, out[r].name);
+        return set_error(PDSSM_EINVAL, "outputs %s and %s overlap", out[q].name, out[r].name);
   }
   return PDSSM_OK;
 }
@@ -212,7 +203,7 @@ int dispatch(int mode, const pdscan::Args& a, void* stream) {
   const hipError_t e = mode == pdscan::kModeSelect ? pdscan::launch_select(a, st)
                        : mode == pdscan::kModeScan ? pdscan::launch_scan(a, st)
                                                    : pdscan::launch_fused(a, st);
-  if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
   g_err[0] = 0;
   return PDSSM_OK;
 }
@@ -221,19 +212,19 @@ int sens_plan(pdscan::SensPlan& q, const pdssm_dims* dims, int32_t chunk) {
   int rc = check_dims(dims, chunk);
   if (rc) return rc;
   if (dims->u_shared)
-    return fail(PDSSM_EUNSUPPORTED, "impulse sensitivity: u shared by the heads is not supported");
+    return set_error(PDSSM_EUNSUPPORTED, "impulse sensitivity: u shared by the heads is not supported");
   if (dims->N > 16)
-    return fail(PDSSM_EUNSUPPORTED, "impulse sensitivity: N=%d > 16", dims->N);
+    return set_error(PDSSM_EUNSUPPORTED, "impulse sensitivity: N=%d > 16", dims->N);
   if (dims->d_in % 16 || dims->d_in > pdscan::kSensMaxD)
-    return fail(PDSSM_EUNSUPPORTED, "impulse sensitivity: d_in=%d must be a multiple of 16, at most %d",
-                dims->d_in, pdscan::kSensMaxD);
+    return set_error(PDSSM_EUNSUPPORTED, "impulse sensitivity: d_in=%d must be a multiple of 16, at most %d",
+                     dims->d_in, pdscan::kSensMaxD);
   if (!pdscan::make_sens_plan(q, dims->B, dims->H, dims->L, dims->N, dims->K, dims->d_in,
                               dims->in_dtype == PDSSM_BF16, chunk))
-    return fail(PDSSM_EUNSUPPORTED, "impulse sensitivity: chunk=%d with d_in=%d needs %d steps per lane "
-                "group (at most %d: chunk <= 512) and %d bytes of on-chip memory (at most %d)", chunk,
-                dims->d_in, q.S, pdscan::kSensMaxS, q.bytes, pdscan::kMaxLds);
+    return set_error(PDSSM_EUNSUPPORTED, "impulse sensitivity: chunk=%d with d_in=%d needs %d steps per lane "
+                     "group (at most %d: chunk <= 512) and %d bytes of on-chip memory (at most %d)", chunk,
+                     dims->d_in, q.S, pdscan::kSensMaxS, q.bytes, pdscan::kMaxLds);
   if ((uint64_t)q.nC * dims->B * dims->H > 0x7fffffffull)
-    return fail(PDSSM_EUNSUPPORTED, "too many chunks");
+    return set_error(PDSSM_EUNSUPPORTED, "too many chunks");
   if (lookback_giveup_hook()) {
     q.force_giveup = 1;
     q.spin_limit = 2;
@@ -279,8 +270,8 @@ int scan_fwd_impl(const pdssm_dims* dims, int32_t chunk, int32_t n_out, const in
   Plan p;
   if ((rc = build_plan(p, pdscan::kModeScan, dims, chunk, 0, 1, n_out))) return rc;
   if (workspace_bytes < p.ws_bytes)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
-                p.ws_bytes);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
+                     p.ws_bytes);
   const Sizes z = sizes(dims);
   const Range in[] = {{"k_star", k_star, z.k}, {"dict_idx", dict_idx, z.dict}, {"D", D, z.D},
                       {"Bu", Bu, z.Bu}, {"C", C, z.C * n_out}, {"h0", h0, z.h0}};
@@ -312,7 +303,7 @@ int fwd_wb_impl(const pdssm_dims* dims, int32_t chunk, int32_t n_out, const void
     // selection GEMM, drive GEMM, then the scan (with n_out rows of C)
     const TwoPassWs w = two_pass_ws(dims, q);
     if (workspace_bytes < w.total)
-      return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
+      return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
     const Range out[] = {{"k_star", k_star, z.k}, {"D", D, z.D}, {"y", y, z.y * n_out},
                          {"h_L", h_L, z.hL},      {"workspace", workspace, w.total}};
     if ((rc = check_ptrs(in, 8, out, 5, req))) return rc;
@@ -324,7 +315,7 @@ int fwd_wb_impl(const pdssm_dims* dims, int32_t chunk, int32_t n_out, const void
     a.D_out = D ? D : (float*)(ws + w.D);
     hipError_t e = pdscan::launch_gemm_sel(a, (hipStream_t)stream);
     if (e == hipSuccess) e = pdscan::launch_gemm_drive(a, (float*)(ws + w.Bu), (hipStream_t)stream);
-    if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     pdscan::Args b = {};
     b.p = q;
     b.dict = dict_idx; b.k_in = a.k_out; b.D_in = a.D_out; b.Bu = (const float*)(ws + w.Bu); b.C = C;
@@ -335,14 +326,14 @@ int fwd_wb_impl(const pdssm_dims* dims, int32_t chunk, int32_t n_out, const void
   Plan p;
   if ((rc = build_plan(p, pdscan::kModeFused, dims, chunk, 1, 0, n_out))) return rc;
   if (!p.fold_bu)
-    return fail(PDSSM_EUNSUPPORTED,
-                "the drive term cannot be folded for this shape: the selection GEMM would need more "
-                "column tiles than the kernel holds (K + 2N <= 128, or with bf16 d >= 256 at most %d "
-                "tiles of 16; got N=%d K=%d d=%d %s)", pdscan::kFoldMaxTiles, dims->N, dims->K,
-                dims->d_in, dims->in_dtype == PDSSM_BF16 ? "bf16" : "fp32");
+    return set_error(PDSSM_EUNSUPPORTED,
+                     "the drive term cannot be folded for this shape: the selection GEMM would need more "
+                     "column tiles than the kernel holds (K + 2N <= 128, or with bf16 d >= 256 at most %d "
+                     "tiles of 16; got N=%d K=%d d=%d %s)", pdscan::kFoldMaxTiles, dims->N, dims->K,
+                     dims->d_in, dims->in_dtype == PDSSM_BF16 ? "bf16" : "fp32");
   if (workspace_bytes < p.ws_bytes)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
-                p.ws_bytes);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
+                     p.ws_bytes);
   const Range out[] = {{"k_star", k_star, z.k}, {"D", D, z.D}, {"y", y, z.y * n_out},
                        {"h_L", h_L, z.hL},      {"workspace", workspace, p.ws_bytes}};
   if ((rc = check_ptrs(in, 8, out, 5, req))) return rc;
@@ -356,7 +347,7 @@ int fwd_wb_impl(const pdssm_dims* dims, int32_t chunk, int32_t n_out, const void
 
 int check_n_out(int32_t n_out) {
   if (n_out < 1 || n_out > pdscan::kMaxOut)
-    return fail(PDSSM_EINVAL, "n_out=%d outside [1, %d]", n_out, pdscan::kMaxOut);
+    return set_error(PDSSM_EINVAL, "n_out=%d outside [1, %d]", n_out, pdscan::kMaxOut);
   return PDSSM_OK;
 }
 
@@ -367,14 +358,14 @@ extern "C" {
 int pdssm_abi_version(void) { return PDSSM_ABI_VERSION; }
 
 int pdssm_workspace_status(const void* workspace, size_t workspace_bytes, uint32_t* status, void* stream) {
-  if (!workspace) return fail(PDSSM_EINVAL, "workspace is NULL");
-  if (!status) return fail(PDSSM_EINVAL, "status is NULL");
-  if ((uintptr_t)workspace & 15) return fail(PDSSM_EINVAL, "workspace is not 16-byte aligned");
-  if ((uintptr_t)status & 3) return fail(PDSSM_EINVAL, "status is not 4-byte aligned");
+  if (!workspace) return set_error(PDSSM_EINVAL, "workspace is NULL");
+  if (!status) return set_error(PDSSM_EINVAL, "status is NULL");
+  if ((uintptr_t)workspace & 15) return set_error(PDSSM_EINVAL, "workspace is not 16-byte aligned");
+  if ((uintptr_t)status & 3) return set_error(PDSSM_EINVAL, "status is not 4-byte aligned");
   if (workspace_bytes < 256)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes is smaller than its 256-byte header", workspace_bytes);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes is smaller than its 256-byte header", workspace_bytes);
   const hipError_t e = pdscan::launch_status(workspace, status, (hipStream_t)stream);
-  if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
   g_err[0] = 0;
   return PDSSM_OK;
 }
@@ -397,7 +388,7 @@ int pdssm_select(const pdssm_dims* dims, const void* u, const void* W_sel,
                  float* D, int32_t* P_idx, void* stream) {
   int rc = check_dims(dims, -1);
   if (rc) return rc;
-  if (P_idx && !dict_idx) return fail(PDSSM_EINVAL, "P_idx requested but dict_idx is NULL");
+  if (P_idx && !dict_idx) return set_error(PDSSM_EINVAL, "P_idx requested but dict_idx is NULL");
   const Sizes z = sizes(dims);
   const Range in[] = {{"u", u, z.u}, {"W_sel", W_sel, z.Wsel}, {"W_d", W_d, z.Wd},
                       {"b_d", b_d, z.bd}, {"dict_idx", dict_idx, z.dict}};
@@ -415,7 +406,7 @@ int pdssm_select(const pdssm_dims* dims, const void* u, const void* W_sel,
     // u shared by the heads: one GEMM over all tokens, the heads of a token
     // tile on one die
     const hipError_t e = pdscan::launch_gemm_sel(a, (hipStream_t)stream);
-    if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     g_err[0] = 0;
     return PDSSM_OK;
   }
@@ -425,7 +416,7 @@ int pdssm_select(const pdssm_dims* dims, const void* u, const void* W_sel,
 int pdssm_scan_workspace_bytes(const pdssm_dims* dims, int32_t chunk, size_t* bytes) {
   int rc = check_dims(dims, chunk);
   if (rc) return rc;
-  if (!bytes) return fail(PDSSM_EINVAL, "bytes is NULL");
+  if (!bytes) return set_error(PDSSM_EINVAL, "bytes is NULL");
   Plan p;
   if ((rc = build_plan(p, pdscan::kModeScan, dims, chunk))) return rc;
   *bytes = p.ws_bytes;
@@ -435,7 +426,7 @@ int pdssm_scan_workspace_bytes(const pdssm_dims* dims, int32_t chunk, size_t* by
 int pdssm_fwd_workspace_bytes(const pdssm_dims* dims, int32_t chunk, size_t* bytes) {
   int rc = check_dims(dims, chunk);
   if (rc) return rc;
-  if (!bytes) return fail(PDSSM_EINVAL, "bytes is NULL");
+  if (!bytes) return set_error(PDSSM_EINVAL, "bytes is NULL");
   // The size depends only on the chunk count; the shape is accepted when
   // any of the fused calls that take this workspace (pdssm_fwd, pdssm_fwd_wb,
   // pdssm_fwd_wb_multi) can run it, whose on-chip budgets differ.
@@ -499,7 +490,7 @@ int pdssm_fwd(const pdssm_dims* dims, int32_t chunk, const void* u, const void* 
   if (fwd_two_pass(dims) && build_plan(q, pdscan::kModeScan, dims, chunk, 0, 1) == PDSSM_OK) {
     const TwoPassWs w = two_pass_ws(dims, q);
     if (workspace_bytes < w.total)
-      return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
+      return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
     const Range out[] = {{"k_star", k_star, z.k}, {"D", D, z.D}, {"y", y, z.y},
                          {"h_L", h_L, z.hL},      {"workspace", workspace, w.total}};
     if ((rc = check_ptrs(in, 8, out, 5, req))) return rc;
@@ -510,7 +501,7 @@ int pdssm_fwd(const pdssm_dims* dims, int32_t chunk, const void* u, const void* 
     a.k_out = k_star ? k_star : (int32_t*)(ws + w.k);
     a.D_out = D ? D : (float*)(ws + w.D);
     hipError_t e = pdscan::launch_gemm_sel(a, (hipStream_t)stream);
-    if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     pdscan::Args b = {};
     b.p = q;
     b.dict = dict_idx; b.k_in = a.k_out; b.D_in = a.D_out; b.Bu = Bu; b.C = C; b.h0 = h0;
@@ -519,8 +510,8 @@ int pdssm_fwd(const pdssm_dims* dims, int32_t chunk, const void* u, const void* 
   }
   g_err[0] = 0;
   if (workspace_bytes < p.ws_bytes)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
-                p.ws_bytes);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
+                     p.ws_bytes);
   const Range out[] = {{"k_star", k_star, z.k}, {"D", D, z.D}, {"y", y, z.y},
                        {"h_L", h_L, z.hL},      {"workspace", workspace, p.ws_bytes}};
   if ((rc = check_ptrs(in, 8, out, 5, req))) return rc;
@@ -541,10 +532,10 @@ int pdssm_fwd_noalloc(const pdssm_dims* dims, int32_t chunk, const void* u, cons
   Plan p;
   if ((rc = build_plan(p, pdscan::kModeFused, dims, chunk))) return rc;
   if (p.ws_bytes > (size_t)PDSSM_NOALLOC_SCRATCH_BYTES)
-    return fail(PDSSM_EUNSUPPORTED, "this call needs %zu bytes of look-back scratch, more than the %zu the "
-                "allocation-free entry point holds per device (use pdssm_fwd with a workspace, or a longer "
-                "chunk)", p.ws_bytes, (size_t)PDSSM_NOALLOC_SCRATCH_BYTES);
-  if (status && ((uintptr_t)status & 3)) return fail(PDSSM_EINVAL, "status is not 4-byte aligned");
+    return set_error(PDSSM_EUNSUPPORTED, "this call needs %zu bytes of look-back scratch, more than the %zu the "
+                     "allocation-free entry point holds per device (use pdssm_fwd with a workspace, or a longer "
+                     "chunk)", p.ws_bytes, (size_t)PDSSM_NOALLOC_SCRATCH_BYTES);
+  if (status && ((uintptr_t)status & 3)) return set_error(PDSSM_EINVAL, "status is not 4-byte aligned");
   const Sizes z = sizes(dims);
   const Range in[] = {{"u", u, z.u},         {"W_sel", W_sel, z.Wsel}, {"dict_idx", dict_idx, z.dict},
                       {"W_d", W_d, z.Wd},    {"b_d", b_d, z.bd},       {"Bu", Bu, z.Bu},
@@ -553,14 +544,14 @@ int pdssm_fwd_noalloc(const pdssm_dims* dims, int32_t chunk, const void* u, cons
   static const char* const req[] = {"u", "W_sel", "dict_idx", "W_d", "b_d", "Bu", "C", "y", "h_L", nullptr};
   if ((rc = check_ptrs(in, 8, out, 4, req))) return rc;
   for (const Range& r : in)
-    if (overlap({"status", status, 4}, r)) return fail(PDSSM_EINVAL, "status overlaps input %s", r.name);
+    if (overlap({"status", status, 4}, r)) return set_error(PDSSM_EINVAL, "status overlaps input %s", r.name);
   for (const Range& r : out)
-    if (overlap({"status", status, 4}, r)) return fail(PDSSM_EINVAL, "status overlaps output %s", r.name);
+    if (overlap({"status", status, 4}, r)) return set_error(PDSSM_EINVAL, "status overlaps output %s", r.name);
   void* scratch = nullptr;
   size_t cap = 0;
   hipError_t e = pdscan::noalloc_scratch(&scratch, &cap);
-  if (e != hipSuccess) return fail(PDSSM_EHIP, "device scratch lookup failed: %s", hipGetErrorString(e));
-  if (p.ws_bytes > cap) return fail(PDSSM_EUNSUPPORTED, "scratch of %zu bytes < %zu needed", cap, p.ws_bytes);
+  if (e != hipSuccess) return set_error(PDSSM_EHIP, "device scratch lookup failed: %s", hipGetErrorString(e));
+  if (p.ws_bytes > cap) return set_error(PDSSM_EUNSUPPORTED, "scratch of %zu bytes < %zu needed", cap, p.ws_bytes);
   pdscan::Args a = {};
   a.p = p;
   a.u = u; a.W_sel = W_sel; a.W_d = W_d; a.b_d = b_d; a.dict = dict_idx;
@@ -569,7 +560,7 @@ int pdssm_fwd_noalloc(const pdssm_dims* dims, int32_t chunk, const void* u, cons
   if ((rc = dispatch(pdscan::kModeFused, a, stream))) return rc;
   if (status) {
     e = pdscan::launch_status(scratch, status, (hipStream_t)stream);
-    if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
   }
   return PDSSM_OK;
 }
@@ -595,7 +586,7 @@ int pdssm_fwd_wb_multi(const pdssm_dims* dims, int32_t chunk, int32_t n_out, con
 int pdssm_scan_fwd_pidx(const pdssm_dims* dims, int32_t chunk, const int32_t* P_idx, const float* D,
                         const float* Bu, const float* C, const float* h0, float* y, float* h_L,
                         void* workspace, size_t workspace_bytes, void* stream) {
-  if (!dims) return fail(PDSSM_EINVAL, "dims is NULL");
+  if (!dims) return set_error(PDSSM_EINVAL, "dims is NULL");
   pdssm_dims dd = *dims;
   dd.K = 1;                                        // no dictionary: one map per step
   int rc = check_dims(&dd, chunk);
@@ -608,15 +599,15 @@ int pdssm_scan_fwd_pidx(const pdssm_dims* dims, int32_t chunk, const int32_t* P_
   dd.K = sm ? 1 : T;
   if (!pdscan::make_plan(p, pdscan::kModeScan, dd.B, dd.H, dd.L, dd.N, dd.K, dd.d_in, dd.u_shared,
                          dd.in_dtype == PDSSM_BF16, chunk, 0, sm ? 1 : 0))
-    return fail(PDSSM_EUNSUPPORTED, "chunk=%d with N=%d needs %d bytes of on-chip memory with per-step "
-                "maps (limit %d); use a shorter chunk", chunk, dd.N, p.lds_bytes, pdscan::kMaxLds);
+    return set_error(PDSSM_EUNSUPPORTED, "chunk=%d with N=%d needs %d bytes of on-chip memory with per-step "
+                     "maps (limit %d); use a shorter chunk", chunk, dd.N, p.lds_bytes, pdscan::kMaxLds);
   if (lookback_giveup_hook()) {
     p.force_giveup = 1;
     p.spin_limit = 2;
   }
   if (workspace_bytes < p.ws_bytes)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
-                p.ws_bytes);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
+                     p.ws_bytes);
   const Sizes z = sizes(dims);
   const Range in[] = {{"P_idx", P_idx, z.D}, {"D", D, z.D}, {"Bu", Bu, z.Bu}, {"C", C, z.C},
                       {"h0", h0, z.h0}};
@@ -639,8 +630,8 @@ int pdssm_scan_states(const pdssm_dims* dims, int32_t chunk, const int32_t* k_st
   Plan p;
   if ((rc = build_plan(p, pdscan::kModeScan, dims, chunk, 0, 2))) return rc;
   if (workspace_bytes < p.ws_bytes)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
-                p.ws_bytes);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes,
+                     p.ws_bytes);
   const Sizes z = sizes(dims);
   const Range in[] = {{"k_star", k_star, z.k}, {"dict_idx", dict_idx, z.dict}, {"D", D, z.D},
                       {"Bu", Bu, z.Bu}, {"C", C, z.C}, {"h0", h0, z.h0}};
@@ -659,13 +650,13 @@ int pdssm_scan_states(const pdssm_dims* dims, int32_t chunk, const int32_t* k_st
 int pdssm_scan_bwd_workspace_bytes(const pdssm_dims* dims, int32_t chunk, size_t* bytes) {
   int rc = check_dims(dims, chunk);
   if (rc) return rc;
-  if (!bytes) return fail(PDSSM_EINVAL, "bytes is NULL");
+  if (!bytes) return set_error(PDSSM_EINVAL, "bytes is NULL");
   Plan p;
   if ((rc = build_plan(p, pdscan::kModeScan, dims, chunk))) return rc;
   pdscan::BwdLds l;
   if (!pdscan::make_bwd_lds(p, l))
-    return fail(PDSSM_EUNSUPPORTED, "chunk=%d with N=%d K=%d needs %d bytes of on-chip memory in the "
-                "gradient pass (limit %d)", p.chunk, dims->N, dims->K, l.bytes, pdscan::kMaxLds);
+    return set_error(PDSSM_EUNSUPPORTED, "chunk=%d with N=%d K=%d needs %d bytes of on-chip memory in the "
+                     "gradient pass (limit %d)", p.chunk, dims->N, dims->K, l.bytes, pdscan::kMaxLds);
   *bytes = pdscan::bwd_ws_bytes(p);
   return PDSSM_OK;
 }
@@ -681,11 +672,11 @@ int pdssm_scan_bwd(const pdssm_dims* dims, int32_t chunk, const int32_t* k_star,
   if ((rc = build_plan(p, pdscan::kModeScan, dims, chunk))) return rc;
   pdscan::BwdLds l;
   if (!pdscan::make_bwd_lds(p, l))
-    return fail(PDSSM_EUNSUPPORTED, "chunk=%d with N=%d K=%d needs %d bytes of on-chip memory in the "
-                "gradient pass (limit %d)", p.chunk, dims->N, dims->K, l.bytes, pdscan::kMaxLds);
+    return set_error(PDSSM_EUNSUPPORTED, "chunk=%d with N=%d K=%d needs %d bytes of on-chip memory in the "
+                     "gradient pass (limit %d)", p.chunk, dims->N, dims->K, l.bytes, pdscan::kMaxLds);
   const size_t need = pdscan::bwd_ws_bytes(p);
   if (workspace_bytes < need)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
   const Sizes z = sizes(dims);
   const Range in[] = {{"k_star", k_star, z.k}, {"dict_idx", dict_idx, z.dict}, {"D", D, z.D},
                       {"C", C, z.C},           {"h0", h0, z.h0},           {"H_all", H_all, z.D},
@@ -703,7 +694,7 @@ int pdssm_scan_bwd(const pdssm_dims* dims, int32_t chunk, const int32_t* k_star,
   a.g_y = g_y; a.g_hL = g_hL; a.g_Bu = g_Bu; a.g_D = g_D; a.g_h0 = g_h0;
   a.ws = (unsigned char*)workspace;
   const hipError_t e = pdscan::launch_bwd(a, g_C, (hipStream_t)stream);
-  if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
   g_err[0] = 0;
   return PDSSM_OK;
 }
@@ -712,7 +703,7 @@ int pdssm_impulse_sens_workspace_bytes(const pdssm_dims* dims, int32_t chunk, si
   pdscan::SensPlan q;
   int rc = sens_plan(q, dims, chunk);
   if (rc) return rc;
-  if (!bytes) return fail(PDSSM_EINVAL, "bytes is NULL");
+  if (!bytes) return set_error(PDSSM_EINVAL, "bytes is NULL");
   *bytes = q.ws_bytes;
   return PDSSM_OK;
 }
@@ -725,7 +716,7 @@ int pdssm_impulse_sens(const pdssm_dims* dims, int32_t chunk, const int32_t* k_s
   int rc = sens_plan(q, dims, chunk);
   if (rc) return rc;
   if (workspace_bytes < q.ws_bytes)
-    return fail(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, q.ws_bytes);
+    return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, q.ws_bytes);
   const Sizes z = sizes(dims);
   const size_t ydz = (size_t)dims->B * dims->H * dims->L * dims->d_in * 4;
   const Range in[] = {{"k_star", k_star, z.k}, {"dict_idx", dict_idx, z.dict}, {"D", D, z.D},
@@ -740,7 +731,7 @@ int pdssm_impulse_sens(const pdssm_dims* dims, int32_t chunk, const int32_t* k_s
   a.k_star = k_star; a.dict = dict_idx; a.D = D; a.W_d = W_d; a.W_b = W_b; a.C = C; a.h0 = h0;
   a.dY = dY; a.ws = (unsigned char*)workspace;
   const hipError_t e = pdscan::launch_sens(a, (hipStream_t)stream);
-  if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
   g_err[0] = 0;
   return PDSSM_OK;
 }
@@ -753,8 +744,8 @@ int pdssm_soft_select(const pdssm_dims* dims, const void* u, const void* W_sel, 
   pdscan::SoftPlan q;
   if (!pdscan::make_soft_plan(q, dims->B, dims->H, dims->L, dims->N, dims->K, dims->d_in, dims->u_shared,
                               dims->in_dtype == PDSSM_BF16))
-    return fail(PDSSM_EUNSUPPORTED, "soft selection: N=%d K=%d d_in=%d (N, K at most %d, %d; d_in one of "
-                "16, 32, 64, 128)", dims->N, dims->K, dims->d_in, pdscan::kSoftMaxN, pdscan::kSoftMaxK);
+    return set_error(PDSSM_EUNSUPPORTED, "soft selection: N=%d K=%d d_in=%d (N, K at most %d, %d; d_in one of "
+                     "16, 32, 64, 128)", dims->N, dims->K, dims->d_in, pdscan::kSoftMaxN, pdscan::kSoftMaxK);
   const Sizes z = sizes(dims);
   const size_t mz = (size_t)dims->H * dims->K * dims->N * dims->N * 4;
   const size_t mtz = (size_t)dims->B * dims->H * dims->L * dims->N * dims->N * 4;
@@ -767,14 +758,14 @@ int pdssm_soft_select(const pdssm_dims* dims, const void* u, const void* W_sel, 
   a.q = q;
   a.u = u; a.W_sel = W_sel; a.M = M; a.W_d = W_d; a.b_d = b_d; a.M_t = M_t; a.P_idx = P_idx; a.D = D;
   const hipError_t e = pdscan::launch_soft(a, (hipStream_t)stream);
-  if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
   g_err[0] = 0;
   return PDSSM_OK;
 }
 
 int pdssm_dict_hardmax(int32_t H, int32_t K, int32_t N, const float* M, int32_t* dict_idx, void* stream) {
-  if (H < 1 || K < 1 || N < 1) return fail(PDSSM_EINVAL, "H, K, N must be >= 1 (got %d %d %d)", H, K, N);
-  if (N > 64) return fail(PDSSM_EUNSUPPORTED, "N=%d > 64", N);
+  if (H < 1 || K < 1 || N < 1) return set_error(PDSSM_EINVAL, "H, K, N must be >= 1 (got %d %d %d)", H, K, N);
+  if (N > 64) return set_error(PDSSM_EUNSUPPORTED, "N=%d > 64", N);
   const size_t mz = (size_t)H * K * N * N * 4, dz = (size_t)H * K * N * 4;
   const Range in[] = {{"M", M, mz}};
   const Range out[] = {{"dict_idx", dict_idx, dz}};
@@ -782,7 +773,7 @@ int pdssm_dict_hardmax(int32_t H, int32_t K, int32_t N, const float* M, int32_t*
   int rc = check_ptrs(in, 1, out, 1, req);
   if (rc) return rc;
   const hipError_t e = pdscan::launch_dict_hardmax(M, dict_idx, H * K, N, (hipStream_t)stream);
-  if (e != hipSuccess) return fail(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return set_error(PDSSM_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
   g_err[0] = 0;
   return PDSSM_OK;
 }
