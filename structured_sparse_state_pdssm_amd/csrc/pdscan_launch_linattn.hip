@@ -84,7 +84,12 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
   }
   const int t = s.len - 1 - tid;
   double d = 0.0, x = 0.0;
+  // Where the decay is zero in fp32 (e^-104 < 2^-150), or no state lies before
+  // the token, the product is zero: not left to what the sums' errors leave.
+  bool none = t < 0 || (t == 0 && s.first && !a.h0);
   if (t >= 0) {
+    none |= ((const float*)a.c.g.p)[(int64_t)s.vb * a.c.g.sb + (int64_t)h * a.c.g.sh + (int64_t)(s.t0 + t) * a.c.g.st] <
+            -104.0f;
     const long long at = (long long)h * a.c.rows + s.row0 + t;
     const long long slab = (long long)a.c.H * a.c.rows;
     for (int w = 0; w < a.slabs; ++w) d += (double)a.r[w * slab + at] - (double)a.k[w * slab + at];
@@ -116,7 +121,7 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
     g += red[1][w];
     if (w < wave) g += red[0][w];
   }
-  if (t < 0) g = 0.0;
+  if (none) g = 0.0;
   if (!a.per_head) {
     if (t >= 0)
       ((float*)a.out.p)[(int64_t)s.vb * a.out.sb + (int64_t)h * a.out.sh + (int64_t)(s.t0 + t) * a.out.st] = (float)g;

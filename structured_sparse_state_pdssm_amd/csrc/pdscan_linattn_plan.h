@@ -73,7 +73,7 @@ struct LaDecayArgs {
   const double* xd;            // final state . its gradient [slabs][segment][H], NULL: zero
   double* part;                // sums per segment and head (one decay per head)
   LaView out;
-  int slabs, per_head;
+  int slabs, per_head, h0;     // h0: 1 where the sequences start from a state
 };
 
 // Sum over the value heads that share a query or key head.

@@ -55,3 +55,38 @@ def test_gradient_of_more_sequences_than_a_launch_has_along_an_axis(const):
         # the same terms in 64 bits (2^23 additions lose under 2^-29 of a typical sum), each of the three sums rounded once
         whole = r["g_log_decay"].double()
         assert ((whole - total).abs() <= 2.0 ** -23 * (whole.abs() + held)).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("L,dk,dv", [(200, 32, 32), (1100, 128, 128)])
+def test_decays_of_zero_have_no_gradient(L, dk, dv, dt):
+    """exp(log_decay) is zero: so is its gradient, and not the rounding of the sums that it is a difference of; the
+    steps around it keep theirs."""
+    P = lib()
+    H, n = 3, normals(3)
+    x = dict(q=n(1, H, L, dk, dt=dt), k=n(1, H, L, dk, dt=dt), v=n(1, H, L, dv, dt=dt), g_o=n(1, H, L, dv, dt=dt),
+             h0=n(1, H, dk, dv), g_hL=n(1, H, dk, dv), log_decay=n(1, H, L).sub_(3.0).exp_().neg_())
+    at = torch.zeros(1, H, L, dtype=torch.bool, device="cuda")
+    at[:, 0, ::37] = at[:, 1, 5::64] = at[:, 2, L - 1] = at[:, 2, 0] = True
+    x["log_decay"][at] = torch.tensor([float("-inf"), -104.5, torch.finfo(F32).min, -1e4] * L, device="cuda")[:int(at.sum())]
+    g = P.pdssm_linattn_bwd(**x)["g_log_decay"]
+    assert (g[at] == 0).all() and (g[~at] != 0).float().mean() > 0.99
+    x["log_decay"] = torch.tensor([float("-inf"), -0.01, -1e30], device="cuda")
+    g = P.pdssm_linattn_bwd(**x)["g_log_decay"]
+    assert g[0] == 0 and g[2] == 0 and g[1] != 0
+
+
+def test_first_tokens_without_a_state_have_no_decay_gradient():
+    """The state before the first token of every sequence is zero, batched and packed, in one segment and in several."""
+    P = lib()
+    H, L, n = 2, 1300, normals(4)
+    x = dict(q=n(1, H, L, 64, dt=BF), k=n(1, H, L, 64, dt=BF), v=n(1, H, L, 32, dt=BF), g_o=n(1, H, L, 32, dt=BF),
+             log_decay=n(1, H, L).sub_(3.0).exp_().neg_())
+    g = P.pdssm_linattn_bwd(**x, g_hL=n(1, H, 64, 32))["g_log_decay"]
+    assert (g[:, :, 0] == 0).all() and (g[:, :, 1:] != 0).float().mean() > 0.99
+    cu = torch.tensor([0, 7, 7, 700, 1300], dtype=torch.int32, device="cuda")
+    first = [0, 7, 700]
+    r = P.pdssm_linattn_bwd(**x, g_hL=n(4, H, 64, 32), cu_seqlens=cu)["g_log_decay"]
+    assert (r[:, :, first] == 0).all()
+    r = P.pdssm_linattn_bwd(**x, h0=n(4, H, 64, 32), cu_seqlens=cu)["g_log_decay"]
+    assert (r[:, :, first] != 0).any()
