@@ -90,3 +90,51 @@ def test_first_tokens_without_a_state_have_no_decay_gradient():
     assert (r[:, :, first] == 0).all()
     r = P.pdssm_linattn_bwd(**x, h0=n(4, H, 64, 32), cu_seqlens=cu)["g_log_decay"]
     assert (r[:, :, first] != 0).any()
+
+
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("decay", [-3.0, -0.5, 1.0, 2.3])
+@pytest.mark.parametrize("L,dk,dv", [(150, 64, 32), (1100, 32, 128)])
+def test_log_decay_gradient_is_as_good_as_its_sums(L, dk, dv, decay, dt):
+    """The bound of the sums that g_log_decay is a difference of: r_i = q_i . dq_i and c_j = k_j . dk_j without the
+    token's own pair, over the rest of a segment (at most 512 steps), and what meets behind its end.  Each is an fp32
+    sum of products of magnitude `mag`, through at most n = dk + dv + 512 + 128 roundings of up to 2^-24 of it, of
+    either sign: their sum is within 4 sqrt(n) 2^-24 mag (seven times its root mean square), and those of the terms
+    add in squares.  Where the decays are strong (e^-10) the own pair is 10^4 times the rest, so a gradient
+    that held its rounding would be out of the bound."""
+    import numpy as np
+
+    from oracle.linattn_oracle import linattn_bwd
+    from tests.test_gpu_linattn import bwd, decays, f64, make
+    H, scale = 3, 0.3
+    x = make(1, H, H, L, dk, dv, dt, seed=L + dk)
+    x["log_decay"] = -torch.exp(0.3 * x["log_decay"].neg().log() + decay + 0.9)
+    g = decays(x)
+    a = {n: np.abs(f64(t)) for n, t in x.items()}
+    ref = linattn_bwd(f64(x["q"]), f64(x["k"]), f64(x["v"]), g, f64(x["g_o"]), f64(x["h0"]), f64(x["g_hL"]), scale)["g_g"]
+    m = linattn_bwd(a["q"], a["k"], a["v"], g, a["g_o"], a["h0"], a["g_hL"], scale)
+    own = scale * (a["q"] * a["k"]).sum(-1) * (a["v"] * a["g_o"]).sum(-1)
+    # (the magnitudes of q's and of k's terms)
+    held = (a["q"] * m["g_q"]).sum(-1) - own + (a["k"] * m["g_k"]).sum(-1) - own
+    rest = np.stack([(held[..., t:t + 512] ** 2).sum(-1) for t in range(L)], -1)
+    # <S, dS> at a segment's end lies in the rest, or is the state's at the sequence's
+    ends = [(s * d).sum((-1, -2)) for s, d in zip(*state_pairs(a, g, scale))]
+    end = np.stack([np.max(ends[t:t + 512], axis=0) for t in range(L)], -1)
+    bound = 4 * (dk + dv + 640) ** 0.5 * 2.0 ** -24 * np.sqrt(rest + end ** 2) + 2.0 ** -24 * np.abs(ref)
+    got = f64(bwd(x, scale=scale)["g_log_decay"])
+    worst = float((np.abs(got - ref) / bound).max())
+    print(f"[gpu] linattn log-decay gradient {L} {dk} {dv} {decay} {dt}: {worst:.2g} of the bound", flush=True)
+    assert worst <= 1.0, worst
+
+
+def state_pairs(a, g, scale):
+    """States behind every step and their adjoints just behind them, of the inputs' magnitudes."""
+    import numpy as np
+
+    from oracle.linattn_oracle import linattn_fwd
+    S = linattn_fwd(a["q"], a["k"], a["v"], g, a["h0"], scale)[2][1:]
+    D, out = a["g_hL"], []
+    for t in reversed(range(g.shape[-1])):
+        out.append(D)     # dLoss / d(the state behind step t), of the steps behind t
+        D = np.exp(g[:, :, t, None, None]) * (D + scale * a["q"][:, :, t, :, None] * a["g_o"][:, :, t, None, :])
+    return S, out[::-1]
