@@ -212,8 +212,7 @@ BwdWs bwd_ws(const pdssm_linattn_dims* d) {
   const int bf16 = d->in_dtype == PDSSM_BF16;
   w.qslabs = pdscan::la_slabs(d->dv, d->dk, bf16);
   w.vslabs = pdscan::la_slabs(d->dk, d->dv, bf16);
-  w.one = pdscan::la_pad(d->dk) == pdscan::la_pad(d->dv) && w.qslabs == w.vslabs &&
-          pdscan::la_waves(d->dk, d->dv, bf16) == pdscan::la_waves(d->dv, d->dk, bf16);
+  w.one = pdscan::la_one(d->dk, d->dv, bf16);
   // the launch with the most work decides: all three jobs in one, or those of q and k
   w.split = pdscan::la_split(d->B, d->L, d->packed, (long long)d->H * (w.one ? 3 : 2) * w.qslabs,
                              kCus * pdscan::la_resident(d->dv, d->dk, bf16, 1), 2ll * d->dk * d->dv,

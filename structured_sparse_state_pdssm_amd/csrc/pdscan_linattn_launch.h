@@ -20,7 +20,6 @@ struct LaCarryArgs {
   long long state;
 };
 
-enum { kLaPassState, kLaPassFwd, kLaPassQK, kLaPassV, kLaPassQKV };
 hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pass, hipStream_t st);
 hipError_t launch_linattn_table(const int32_t* cu, int32_t* table, int32_t* starts, int B, int L, int seg, int segs,
                                 hipStream_t st);

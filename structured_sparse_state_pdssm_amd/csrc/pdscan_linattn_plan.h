@@ -85,17 +85,36 @@ struct LaFoldArgs {
   long long rows;
 };
 
-inline int la_pad(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+inline constexpr int la_pad(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // Waves of a workgroup, 32 columns each, for x rows of DK and z rows of DV
 // elements.  Rows of more than 128 elements take more waves than columns need
 // where fewer would not hold the tiles under way in their registers.
-inline int la_waves(int DK, int DV, int bf16) {
+inline constexpr int la_waves(int DK, int DV, int bf16) {
   const int w = DV <= 32 ? 1 : DV <= 64 ? 2 : 4;
   return DK <= 128 ? w : bf16 ? (w < 2 ? 2 : w) : 4;
 }
-inline int la_slabs(int DK, int DV, int bf16) {
+inline constexpr int la_slabs(int DK, int DV, int bf16) {
   const int w = 32 * la_waves(DK, DV, bf16);
   return (DV + w - 1) / w;
+}
+// Passes of the product and state kernels.
+enum { kLaPassState, kLaPassFwd, kLaPassQK, kLaPassV, kLaPassQKV };
+// Whether the three jobs of a gradient have one shape and go in one launch.
+inline constexpr bool la_one(int dk, int dv, int bf16) {
+  return la_pad(dk) == la_pad(dv) && la_slabs(dv, dk, bf16) == la_slabs(dk, dv, bf16) &&
+         la_waves(dk, dv, bf16) == la_waves(dv, dk, bf16);
+}
+// Whether any dk and dv take a pass to the kernel of x rows of up to `pad`
+// elements and `waves` waves.
+inline constexpr bool la_reached(int pass, int pad, int waves, int bf16) {
+  for (int dk = 8; dk <= kLaMaxD; dk += 8)
+    for (int dv = 8; dv <= kLaMaxD; dv += 8) {
+      const bool one = la_one(dk, dv, bf16);
+      if ((pass == kLaPassQKV && !one) || ((pass == kLaPassQK || pass == kLaPassV) && one)) continue;
+      const bool q = pass == kLaPassQK || pass == kLaPassQKV;   // x rows of dv, z rows of dk
+      if (la_pad(q ? dv : dk) == pad && la_waves(q ? dv : dk, q ? dk : dv, bf16) == waves) return true;
+    }
+  return false;
 }
 // Registers of a lane that the state and the outputs (`tiles` of 32 x 32 a
 // wave) and the tiles under way (`units` of 16 bytes a lane) take; an fp32 unit

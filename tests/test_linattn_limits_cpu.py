@@ -47,3 +47,15 @@ def test_grids_of_the_largest_calls(tmp_path):
     """No launch of 2^32 threads along an axis, whatever the sizes; query and call agree; what is refused is refused
     before its first launch."""
     run(tmp_path, "linattn_grids", API)
+
+
+@pytest.mark.skipif(shutil.which("nm") is None, reason="needs nm")
+def test_every_kernel_built_is_reached(tmp_path):
+    """The library holds the product and state kernels that some call launches, and no others."""
+    import re
+
+    from tests._libutil import ensure_built
+    reached = {ln for ln in run(tmp_path, "linattn_reached", API).splitlines() if "kernel<" in ln}
+    names = subprocess.run(["nm", "-C", ensure_built()], capture_output=True, text=True, timeout=60).stdout
+    built = {re.sub(r"pdscan::", "", m) for m in re.findall(r"__device_stub__pdssm_linattn_((?:state_)?kernel<(?:pdscan::La)[^>]*>)", names)}
+    assert built == reached, (sorted(built - reached), sorted(reached - built))
