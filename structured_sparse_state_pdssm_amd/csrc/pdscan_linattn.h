@@ -416,10 +416,7 @@ __device__ __forceinline__ void la_exponents(float g, int rev, float s_out, floa
 template <typename T, int DKP, int NW>
 struct LaTile {
   static constexpr bool kF32 = sizeof(typename T::store) == 4;
-  // Tokens of a chunk.  64 where four waves share the scores (bf16); else 32, which
-  // halves the registers and the LDS of a workgroup (two waves a SIMD
-  // instead of one: 24 heads of 64/32 at 16 x 2048 tokens 122 -> 104 us).
-  static constexpr int C = NW < 4 || kF32 ? 32 : 64;
+  static constexpr int C = la_chunk(NW, !kF32);  // tokens of a chunk
   static constexpr int NT = NW * 64;
   static constexpr int IT = C / 32;              // 32-token tiles of a chunk
   static constexpr int KT = DKP / 32;            // 32-row tiles of the state
@@ -437,6 +434,8 @@ struct LaTile {
   static constexpr size_t kSmall = (size_t)(2 * PAIR * kExp + (NW + 1) * C) * 4;
   static constexpr int pieces(int mode) { return kF32 ? 1 : mode == kLaQ || mode == kLaK ? 3 : 2; }
   static constexpr size_t main_bytes(int np) { return 2 * kX + kZ + np * kP + kSmall; }
+  static_assert(main_bytes(2) == (size_t)la_lds(DKP, NW, !kF32, 2) && main_bytes(3) == (size_t)la_lds(DKP, NW, !kF32, 3),
+                "what the plan counts");
   static constexpr size_t state_bytes() { return 2 * (kX + kZ) + (size_t)NW * 64 * 4; }
   using X = LaTileIO<T, C, DKP, NT>;
   using Z = LaTileIO<T, C, NW * 32, NT>;

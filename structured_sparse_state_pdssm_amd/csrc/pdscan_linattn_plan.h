@@ -126,13 +126,22 @@ inline constexpr int la_regs(int tiles, int units, bool f32) { return 16 * tiles
 // gradient of 32/64 (158) 245 and 193; 2 x 2048 steps, 8 heads, 256/256 bf16 (216)
 // 115 and 91.  Three change nothing where they fit.
 inline constexpr int la_simd_waves(int regs) { return regs <= 150 ? 2 : 1; }
+// Tokens of a chunk.  64 where four waves share the scores (bf16); else 32, which
+// halves the registers and the LDS of a workgroup (two waves a SIMD
+// instead of one: 24 heads of 64/32 at 16 x 2048 tokens 122 -> 104 us).
+inline constexpr int la_chunk(int waves, int bf16) { return waves < 4 || !bf16 ? 32 : 64; }
+// Bytes of LDS that a workgroup of the product kernel takes with scores of
+// `pieces` pieces (LaTile lays them out).
+inline constexpr int la_lds(int pad, int waves, int bf16, int pieces) {
+  const int C = la_chunk(waves, bf16);
+  return C * (bf16 ? 2 : 6) * (2 * pad + 32 * waves) + (waves == 4 && bf16 ? pieces * C * C * 2 : 0) +
+         4 * (64 / C * (8 * C + 8) + (waves + 1) * C);
+}
 // Workgroups of the product kernel that a compute unit holds, by LDS (160 KiB)
 // and by those waves.
 inline int la_resident(int DK, int DV, int bf16, int bwd) {
-  const int es = bf16 ? 2 : 4, nw = la_waves(DK, DV, bf16), d = la_pad(DK);
-  const int C = nw < 4 || !bf16 ? 32 : 64;
-  const int lds = C * (bf16 ? 2 : 6) * (2 * d + 32 * nw) + (nw == 4 && bf16 ? (bwd ? 3 : 2) * C * C * 2 : 0) +
-                  4 * (64 / C * (8 * C + 8) + (nw + 1) * C);
+  const int es = bf16 ? 2 : 4, nw = la_waves(DK, DV, bf16), d = la_pad(DK), C = la_chunk(nw, bf16);
+  const int lds = la_lds(d, nw, bf16, bwd ? 3 : 2);
   const int waves = 4 * la_simd_waves(la_regs((d + C) / 32, C * es * (2 * d + 32 * nw) / (1024 * nw), !bf16));
   const int n = 163840 / lds < waves / nw ? 163840 / lds : waves / nw;
   return n < 1 ? 1 : n;
