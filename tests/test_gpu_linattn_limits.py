@@ -138,3 +138,47 @@ def state_pairs(a, g, scale):
         out.append(D)     # dLoss / d(the state behind step t), of the steps behind t
         D = np.exp(g[:, :, t, None, None]) * (D + scale * a["q"][:, :, t, :, None] * a["g_o"][:, :, t, None, :])
     return S, out[::-1]
+
+
+@pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 128), (BF, 256), (F32, 128)])
+def test_long_memories_round_to_both_sides(dt, d):
+    """8192 same-signed steps without decay, in one segment: the additions to the state are all the error there is.
+    At most 24 roundings for 32 tokens, so n = 6144, each uniform within 2^-24 of the state at that time, which
+    grows in proportion: the root mean square of their sum is sqrt(n / 9) 2^-24 of the state (a third for the
+    uniform error, a third for the growth).  Six times of it is allowed, and a d-th of that for the mean over
+    d^2 elements.  Half a step lost to one side at each would be n / 4 2^-24."""
+    P = lib()
+    B, H, L, n = 32, 16 if d < 256 else 8, 8192, normals(5)
+    k, v = (n(B, H, L, d).abs_().mul_(d ** -0.25).to(dt) for _ in range(2))
+    print(f"[gpu] linattn long memory {d} {dt}", flush=True)
+    _, hL = P.pdssm_linattn_fwd(k, k, v, torch.zeros(H, device="cuda"))
+    rms = 6144 ** 0.5 / 3 * 2.0 ** -24
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        want = k[b, h].double().t().contiguous() @ v[b, h].double()
+        err = (hL[b, h].double() - want) / want
+        assert err.abs().max() <= 6 * rms, float(err.abs().max())
+        assert err.mean().abs() <= 6 * rms / d, float(err.mean())
+
+
+@pytest.mark.parametrize("rate", [2.0 ** -9, 2.0 ** -13])
+@pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 128), (BF, 256), (F32, 128)])
+def test_long_memories_with_a_decay(dt, d, rate):
+    """A constant decay over far more steps than it remembers: the error is that of the memory, not of the length.
+    A chunk of 32 tokens multiplies the state with a decay that is off by up to 2^-23 (its rounding and the
+    exponential's), the same in every chunk: 1 / (32 rate) of them.  The additions, 24 roundings a chunk, of
+    either sign, are allowed six times sqrt(24 / (64 rate)) 2^-24 (their squares decay twice as fast)."""
+    P = lib()
+    B, H, L, n = 8, 16, 16384, normals(6)
+    k, v = (n(B, H, L, d).abs_().mul_(d ** -0.25).to(dt) for _ in range(2))
+    la = torch.full((H,), rate, dtype=torch.float64, device="cuda").neg_().log1p_().float()
+    print(f"[gpu] linattn long memory {d} {dt} {rate}", flush=True)
+    _, hL = P.pdssm_linattn_fwd(k, k, v, la)
+    r = P.pdssm_linattn_bwd(k, k, v, la, v, scale=1.0)["g_h0"]
+    bound = 2.0 ** -23 / (32 * rate) + 6 * (24 / (64 * rate)) ** 0.5 * 2.0 ** -24 + 2.0 ** -22
+    steps = torch.arange(L, dtype=torch.float64, device="cuda")
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        behind, before = (((L - 1 - steps) * la[h].double()).exp(), ((steps + 1) * la[h].double()).exp())
+        for got, w in ((hL[b, h], behind), (r[b, h], before)):
+            want = (k[b, h].double() * w[:, None]).t().contiguous() @ v[b, h].double()
+            err = ((got.double() - want) / want).abs().max()
+            assert err <= bound, (float(err), bound)
