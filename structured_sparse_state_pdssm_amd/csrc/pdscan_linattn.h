@@ -14,9 +14,11 @@
 //
 // One workgroup owns one segment of a sequence, one head and 32 columns of z
 // per wave; the state stays in the accumulators of its matrix instructions.
-// Every exponent is a difference of sums that ends at or below zero, held as
-// two floats (the sums are formed in 64 bits), so a strong decay does not
-// spoil the differences behind it.
+// Exponents are differences of sums formed in 64 bits.  Where the decay over a
+// chunk is moderate, a pair's weight is a factor of its query (2^A) times one of its
+// key (2^-A, up to 2^24); else it is the power of the pair's own difference,
+// at or below zero, of sums held as two floats, so a strong decay does not spoil
+// the differences behind it.
 //
 // Precision.  bf16 inputs enter the products as they are.  What is computed
 // (the state, the weighted scores, the weighted values) is held in fp32 and
@@ -443,8 +445,11 @@ struct LaTile {
   static constexpr bool kWide = KT == 8;
   static constexpr bool kApart = kF32 || KT < 4 || (KT == 4 && !kShareP);
   static constexpr int kWaves = la_simd_waves(la_regs(KT + IT, 2 * X::N + Z::N, kF32));
-  // (fp32 rows of 256 spill at two: 2 x 2048 steps, 8 heads, 256/256 232 us instead of 174 for the whole pass)
-  static constexpr int kStateWaves = kWide && kF32 ? 1 : 2;
+  // The state kernel's, by the same count of its own registers in fp32.  Forward passes: 65536 steps, 4 heads, 128/32
+  // (174) 214 us instead of 235 at two, where it spills 30; 2 x 2048 steps, 8 heads, 256/256 (194) 174 instead of
+  // 232.  bf16 stays at two: rows of 256 with four waves spill 2 there and take the same (4 x 2048 steps, 12 heads,
+  // 256/256 208 us either way, its gradient 640 against 645).
+  static constexpr int kStateWaves = kF32 ? la_simd_waves(la_regs(KT, X::N + Z::N, true)) : 2;
 };
 
 // S = decay S + sum_j y_j (w_j z_j)^T (KEEP: S as it is).  A matrix instruction
@@ -937,7 +942,8 @@ __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const L
   }
 }
 
-// JOBS: the modes of its jobs, a bit each.
+// JOBS: the modes of its jobs, a bit each.  With those of q and k the compiler
+// keeps 83 to 135 scalar registers, mostly the jobs' arguments, in lanes of vector ones (forwards 0 to 8).
 template <typename T, int DKP, int NW, int JOBS>
 __global__ __launch_bounds__(NW * 64)
     __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void

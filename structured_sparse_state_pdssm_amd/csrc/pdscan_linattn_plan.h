@@ -34,7 +34,7 @@ struct LaJob {
   const float* xd_with;        // state to dot the final state with [B][H], NULL: none
   double* xd_out;              // that product [slab][segment][H]
   float* seg_out;              // (state pass) contributions [segment][H], written at the next segment
-  float* seg_decay;            // (state pass) log2 decay of the segment [segment][H]
+  float* seg_decay;            // (state pass) the segment's decay [segment][H]
   float* dot;                  // w . o per token [slab][H][rows], NULL: none
   int sm, sn;                  // strides of a state's x-row and z-row axes
   float s_out, s_ratio, s_upd; // scale of the output, of its own tokens' part beside the state's, of the update
@@ -120,11 +120,13 @@ inline constexpr bool la_reached(int pass, int pad, int waves, int bf16) {
 // wave) and the tiles under way (`units` of 16 bytes a lane) take; an fp32 unit
 // counts its pieces on their way to LDS too.
 inline constexpr int la_regs(int tiles, int units, bool f32) { return 16 * tiles + (f32 ? 11 * units / 2 : 4 * units); }
-// Waves of the product kernel on a SIMD: two, and one where two would spill.
-// 65536 steps of 128/128 bf16 (144 registers by that count) 262 us with two, 369
-// with one; 8 x 2048 steps, 12 heads in fp32: 128/128 (146) 255 and 305, the
-// gradient of 32/64 (158) 245 and 193; 2 x 2048 steps, 8 heads, 256/256 bf16 (216)
-// 115 and 91.  Three change nothing where they fit.
+// Waves of a product kernel on a SIMD: two, and one where two spill more than
+// the second hides.  One count for all jobs of a width, by the forward pass: 65536 steps
+// of 128/128 bf16 (144 registers) 262 us with two, 369 with one; 8 x 2048 steps,
+// 12 heads in fp32: 128/128 (146) 239 and 291 forwards, where two spill nothing,
+// and 667 and 762 for the gradient, whose jobs spill 8 to 44; the gradient of
+// 32/64 (158) 245 and 193; 2 x 2048 steps, 8 heads, 256/256 bf16 (216) 115 and 91.
+// Three change nothing where they fit.
 inline constexpr int la_simd_waves(int regs) { return regs <= 150 ? 2 : 1; }
 // Tokens of a chunk.  64 where four waves share the scores (bf16); else 32, which
 // halves the registers and the LDS of a workgroup (two waves a SIMD

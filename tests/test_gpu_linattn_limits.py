@@ -182,3 +182,14 @@ def test_long_memories_with_a_decay(dt, d, rate):
             want = (k[b, h].double() * w[:, None]).t().contiguous() @ v[b, h].double()
             err = ((got.double() - want) / want).abs().max()
             assert err <= bound, (float(err), bound)
+
+
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(128, 24), (24, 128), (256, 40), (200, 256)])
+def test_segments_of_every_width(dk, dv, dt):
+    """Wide and narrow rows over more than one segment, forwards and backwards."""
+    from tests.test_gpu_linattn import bwd, check_bwd, check_fwd, fwd, make
+    x = make(1, 2, 1, 777, dk, dv, dt, seed=dk)
+    print(f"[gpu] linattn segments {dk} {dv} {dt}", flush=True)
+    check_fwd(x, *fwd(x, scale=0.2), 0.2)
+    check_bwd(x, bwd(x, scale=0.2), 0.2)
