@@ -411,12 +411,14 @@ int pdssm_linattn_fwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
  *   (out, required); g_h0 [B,H,dk,dv] (out, optional)
  * g_log_decay is a difference of sums over the rest of t's segment (512 steps
  * at most) of q . g_q and k . g_k, each without the token's own key and query,
- * and of a product of states.  Its error is theirs: 2^-23 of the root of their
- * squares' sum, 3e-7 to 1.5e-6 of the gradient's norm.  An element that is
- * small beside its neighbours' (a strong decay between weak ones) has fewer
- * digits: at decays around e^-0.02 the median element is good to 4e-7 of
- * itself and one in a hundred to 4e-5 or worse, around e^-3 to 1e-5, and what
- * is under 1e-6 of them has none.  Exactly zero where the decay is zero, and
+ * and of a product of states; what the sums miss at the segment's other end is
+ * taken out along it (at a sequence's start: where h0 is NULL or g_h0 is asked
+ * for).  Its error is theirs: 2^-23 of the root of the sum of their squares,
+ * 2e-7 to 9e-7 of the gradient's norm.  An element that is small beside its
+ * neighbours (a strong decay between weak ones) has fewer digits: at decays
+ * around e^-0.02 the median element is good to 4e-7 of itself and one in a
+ * hundred to 3e-5 or worse, around e^-3 the median to 6e-6, and what is below
+ * 1e-7 of the neighbours has none.  Exactly zero where the decay is zero, and
  * for a first token without a state before it. */
 int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const pdssm_view* k,
                       const pdssm_view* v, const pdssm_view* log_decay, const int32_t* cu_seqlens,

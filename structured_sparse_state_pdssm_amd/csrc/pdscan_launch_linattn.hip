@@ -59,6 +59,17 @@ __device__ __forceinline__ double block_sum(double x, double* red, int tid) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
+// This thread's part of the product of two states.
+__device__ __forceinline__ double la_dot_states(const float* a, const float* b, long long n, int tid) {
+  double x = 0.0;
+#pragma unroll 4
+  for (int e = tid; e < (int)(n / 4); e += kLaPiece) {
+    const float4 p = ((const float4*)a)[e], q = ((const float4*)b)[e];
+    x += (double)((p.x * q.x + p.y * q.y) + (p.z * q.z + p.w * q.w));
+  }
+  return x;
+}
+
 // d loss / d log a_t of one segment and head.  Pairs (key at or before t-1,
 // query at or behind t) meet at t, so with r_i = q_i . dq_i (every key before
 // query i, its own left out) and c_j = k_j . dk_j (every query behind key j)
@@ -66,13 +77,22 @@ __device__ __forceinline__ double block_sum(double x, double* red, int tid) {
 // over the rest of the segment: pairs inside it cancel but for those that
 // meet at t, and the last term holds those that meet behind its end.  The
 // sums run in 64 bits, but r and c carry fp32 errors that do not cancel and
-// grow with the square root of their number: 2048 steps in one sum left 1.6e-6
-// of the gradient, the 512 that a segment has at most half of that.
-// One step a thread: a segment is one round of the workgroup.  It reads two
-// floats a step and two states a segment (24 heads, 16 x 2048 steps, 64/32: 14 us).
+// grow with the square root of their number: hence the at most 512 steps of a segment.
+//
+// Over the whole segment the sum is <S_start, dS_start>, the product of the states
+// before it.  What it differs by is the errors' sum; it is taken out along the
+// segment in proportion to the squares of the terms, which leaves the
+// errors of a walk held at both ends (a third of their squares on average, a
+// quarter in the sum over t that a decay per head has).  Without h0's gradient
+// the start of a sequence with an h0 is not known, and its first segment is held at its end alone.
+// Errors of the norm so, and held at the end alone: 4 x 1024 steps, 4 heads, 64/32 bf16 2.4e-7
+// and 4.1e-7, 8190 packed rows of 128/128 5.6e-7 and 8.0e-7.
+//
+// One step a thread: a segment is one round of the workgroup.  It reads three
+// floats a step and four states a segment (24 heads, 16 x 2048 steps, 64/32: 22 us).
 __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaDecayArgs a) {
   constexpr int W = kLaPiece / 64;
-  __shared__ double red[2][W];
+  __shared__ double red[4][W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const unsigned id = la_block();
   const int h = id % a.c.H, sid = id / a.c.H;
@@ -83,7 +103,8 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
     return;
   }
   const int t = s.len - 1 - tid;
-  double d = 0.0, x = 0.0;
+  const long long n = a.c.state, unit = (long long)s.b * a.c.H + h, seg = (long long)sid * a.c.H + h;
+  double d = 0.0, v = 0.0, x = 0.0, y = 0.0;   // r - c, their squares, the products at the end and at the start
   // Where the decay is zero in fp32 (e^-104 < 2^-150), or no state lies before
   // the token, the product is zero: not left to what the sums' errors leave.
   bool none = t < 0 || (t == 0 && s.first && !a.h0);
@@ -92,35 +113,59 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
             -104.0f;
     const long long at = (long long)h * a.c.rows + s.row0 + t;
     const long long slab = (long long)a.c.H * a.c.rows;
-    for (int w = 0; w < a.slabs; ++w) d += (double)a.r[w * slab + at] - (double)a.k[w * slab + at];
-  }
-  if (!s.last) {
-    const float4* A = (const float4*)(a.sS + ((long long)(sid + 1) * a.c.H + h) * a.c.state);
-    const float4* R = (const float4*)(a.sR + ((long long)sid * a.c.H + h) * a.c.state);
-    for (int e = tid; e < a.c.state / 4; e += kLaPiece) {
-      const float4 p = A[e], q = R[e];
-      x += (double)((p.x * q.x + p.y * q.y) + (p.z * q.z + p.w * q.w));
+    double r = 0.0, c = 0.0;
+    for (int w = 0; w < a.slabs; ++w) {
+      r += (double)a.r[w * slab + at];
+      c += (double)a.k[w * slab + at];
     }
-  } else if (a.xd && tid < a.slabs) {
-    x = a.xd[((long long)tid * a.c.segs + sid) * a.c.H + h];
+    d = r - c;
+    v = r * r + c * c;
   }
+  if (!s.last)
+    x = la_dot_states(a.sS + (seg + a.c.H) * n, a.sR + seg * n, n, tid);
+  else if (a.xd && tid < a.slabs)
+    x = a.xd[((long long)tid * a.c.segs + sid) * a.c.H + h];
+  const bool held = !s.first || !a.h0 || a.g_h0;
+  if (!s.first)
+    y = la_dot_states(a.sS + seg * n, a.sR + (seg - a.c.H) * n, n, tid);
+  else if (a.h0 && a.g_h0)
+    y = la_dot_states(a.h0 + unit * n, a.g_h0 + unit * n, n, tid);
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
-    const double up = __shfl_up(d, m, 64);
-    if (lane >= m) d += up;
+    const double up = __shfl_up(d, m, 64), uv = __shfl_up(v, m, 64);
+    if (lane >= m) {
+      d += up;
+      v += uv;
+    }
   }
 #pragma unroll
-  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m, 64);
+  for (int m = 32; m; m >>= 1) {
+    x += __shfl_xor(x, m, 64);
+    y += __shfl_xor(y, m, 64);
+  }
   if (lane == 63) {
     red[0][wave] = d;
-    red[1][wave] = x;
+    red[1][wave] = v;
+    red[2][wave] = x;
+    red[3][wave] = y;
   }
   __syncthreads();
-  double g = d;
+  double all = 0.0, squares = 0.0;
+  x = y = 0.0;
   for (int w = 0; w < W; ++w) {
-    g += red[1][w];
-    if (w < wave) g += red[0][w];
+    if (w < wave) {
+      d += red[0][w];
+      v += red[1][w];
+    }
+    all += red[0][w];
+    squares += red[1][w];
+    x += red[2][w];
+    y += red[3][w];
   }
+  double g = d + x;
+  const double off = all + x - y;
+  squares += x * x + y * y;
+  if (held && squares > 0.0) g -= off * ((v + x * x) / squares);
   if (none) g = 0.0;
   if (!a.per_head) {
     if (t >= 0)
@@ -135,7 +180,7 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
   if (tid == 0) {
     double sum = 0.0;
     for (int w = 0; w < W; ++w) sum += red[0][w];
-    a.part[(long long)sid * a.c.H + h] = sum;
+    a.part[seg] = sum;
   }
 }
 

@@ -520,7 +520,8 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
   g.out = gg;
   g.slabs = w.qslabs;
   g.per_head = d.decay_per_head;
-  g.h0 = h0 != nullptr;
+  g.h0 = h0;
+  g.g_h0 = g_h0;
   if (e == hipSuccess) e = pdscan::launch_linattn_decay(g, st);
   if (fold) {
     pdscan::LaFoldArgs f = {};

@@ -73,7 +73,8 @@ struct LaDecayArgs {
   const double* xd;            // final state . its gradient [slabs][segment][H], NULL: zero
   double* part;                // sums per segment and head (one decay per head)
   LaView out;
-  int slabs, per_head, h0;     // h0: 1 where the sequences start from a state
+  const float *h0, *g_h0;      // states before the sequences and their gradients [B][H], NULL: zero, not asked for
+  int slabs, per_head;
 };
 
 // Sum over the value heads that share a query or key head.

@@ -193,3 +193,21 @@ def test_segments_of_every_width(dk, dv, dt):
     print(f"[gpu] linattn segments {dk} {dv} {dt}", flush=True)
     check_fwd(x, *fwd(x, scale=0.2), 0.2)
     check_bwd(x, bwd(x, scale=0.2), 0.2)
+
+
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+def test_log_decay_gradient_meets_the_state_at_the_start(dt):
+    """The first token's is the product of h0 with its gradient, not what 500 steps' sums leave of it: p products in
+    fp32, four and four added in fp32 (three roundings of 2^-24 each, of either sign, so within 6 sqrt(3) 2^-24 of
+    the root of their squares' sum), rounded once."""
+    P = lib()
+    B, H, L, d, n = 4, 16, 500, 64, normals(7)
+    x = dict(q=n(B, H, L, d, dt=dt), k=n(B, H, L, d, dt=dt), v=n(B, H, L, d, dt=dt), g_o=n(B, H, L, d, dt=dt),
+             h0=n(B, H, d, d), g_hL=n(B, H, d, d), log_decay=n(B, H, L).sub_(6.0).exp_().neg_())
+    r = P.pdssm_linattn_bwd(**x, scale=1.0)
+    p = x["h0"].double() * r["g_h0"].double()
+    want = p.sum((-1, -2))
+    bound = 6 * 3 ** 0.5 * 2.0 ** -24 * (p ** 2).sum((-1, -2)).sqrt() + 2.0 ** -24 * want.abs()
+    worst = float(((r["g_log_decay"][:, :, 0].double() - want).abs() / bound).max())
+    print(f"[gpu] linattn first token's decay gradient {dt}: {worst:.2g} of the bound", flush=True)
+    assert worst <= 1.0
