@@ -17,7 +17,7 @@ namespace pdscan {
 // 11.7 us).
 __global__ __launch_bounds__(256) void pdssm_linattn_carry_kernel(LaCarryArgs a) {
   const LaCarry& c = a.c[blockIdx.z / a.tiles];
-  const unsigned unit = la_block();
+  const unsigned unit = la_block(a.row);
   const int b = unit / a.H, h = unit % a.H;
   const long long e = ((long long)(blockIdx.z % a.tiles) * 256 + threadIdx.x) * 4;
   if (b >= a.B || e >= a.state) return;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
   constexpr int W = kLaPiece / 64;
   __shared__ double red[4][W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const unsigned id = la_block();
+  const unsigned id = la_block(a.c.row);
   const int h = id % a.c.H, sid = id / a.c.H;
   if (sid >= a.c.segs) return;
   LaSeg s;
@@ -184,9 +184,10 @@ __global__ __launch_bounds__(kLaPiece) void pdssm_linattn_decay_kernel(const LaD
   }
 }
 
-__global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int segs) {
+__global__ __launch_bounds__(256) void pdssm_linattn_decay_sum_kernel(const double* part, float* out, int H, int segs,
+                                                                      unsigned row) {
   __shared__ double red[4];
-  const unsigned h = la_block();
+  const unsigned h = la_block(row);
   if (h >= (unsigned)H) return;
   double x = 0.0;
   for (int s = threadIdx.x; s < segs; s += 256) x += part[(long long)s * H + h];
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArg
   __shared__ int dup;
   const int tid = threadIdx.x;
   const int tiles = (a.dv + a.cols - 1) / a.cols;
-  unsigned id = la_block();
+  unsigned id = la_block(a.row);
   const int tile = id % tiles;
   id /= tiles;
   const int h = id % a.H, b = id / a.H;
@@ -321,9 +322,11 @@ __global__ __launch_bounds__(256) void pdssm_linattn_step_kernel(const LaStepArg
   }
 }
 
-hipError_t launch_linattn_step(const LaStepArgs& a, hipStream_t st) {
+hipError_t launch_linattn_step(const LaStepArgs& args, hipStream_t st) {
+  LaStepArgs a = args;
   const int tiles = (a.dv + a.cols - 1) / a.cols;
   const LaGrid g = la_grid_rows((long long)a.B * a.H * tiles, 256);
+  a.row = g.x;
   if (a.bf16)
     hipLaunchKernelGGL(pdssm_linattn_step_kernel<LaBf16>, dim3(g.x, g.y), dim3(256), 0, st, a);
   else
@@ -337,19 +340,23 @@ hipError_t launch_linattn_table(const int32_t* cu, int32_t* table, int32_t* star
   return hipGetLastError();
 }
 
-hipError_t launch_linattn_carry(const LaCarryArgs& a, int passes, hipStream_t st) {
+hipError_t launch_linattn_carry(const LaCarryArgs& args, int passes, hipStream_t st) {
+  LaCarryArgs a = args;
   const LaGrid g = la_grid_rows((long long)a.B * a.H, 256);
+  a.row = g.x;
   hipLaunchKernelGGL(pdssm_linattn_carry_kernel, dim3(g.x, g.y, a.tiles * passes), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-hipError_t launch_linattn_decay(const LaDecayArgs& a, hipStream_t st) {
+hipError_t launch_linattn_decay(const LaDecayArgs& args, hipStream_t st) {
+  LaDecayArgs a = args;
   LaGrid g = la_grid_rows((long long)a.c.segs * a.c.H, kLaPiece);
+  a.c.row = g.x;
   hipLaunchKernelGGL(pdssm_linattn_decay_kernel, dim3(g.x, g.y), dim3(kLaPiece), 0, st, a);
   if (a.per_head) {
     g = la_grid_rows(a.c.H, 256);
     hipLaunchKernelGGL(pdssm_linattn_decay_sum_kernel, dim3(g.x, g.y), dim3(256), 0, st, a.part, (float*)a.out.p, a.c.H,
-                       a.c.segs);
+                       a.c.segs, g.x);
   }
   return hipGetLastError();
 }
@@ -367,9 +374,11 @@ hipError_t launch_linattn_fold(const LaFoldArgs& a, hipStream_t st) {
 }
 
 // The product kernels, by type, x-row width and waves.
-hipError_t launch_linattn_form(const LaArgs& a, int bf16, int pass, hipStream_t st) {
+hipError_t launch_linattn_form(const LaArgs& args, int bf16, int pass, hipStream_t st) {
+  LaArgs a = args;
   const int dk = la_pad(a.job[0].DK), nw = la_waves(a.job[0].DK, a.job[0].DV, bf16);
   const LaGrid g = la_grid_rows(la_grid(a), 64 * nw);
+  a.row = g.x;
   if (bf16)
     return dk == 32    ? la_bf16_32(a, nw, pass, g, st)
            : dk == 64  ? la_bf16_64(a, nw, pass, g, st)

@@ -268,8 +268,8 @@ __device__ __forceinline__ bool la_segment(const LaArgs& a, int sid, LaSeg& s) {
   return true;
 }
 
-// This workgroup's number in a grid of la_grid_rows.
-__device__ __forceinline__ unsigned la_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+// This workgroup's number in a grid of la_grid_rows, `row` of them along x.
+__device__ __forceinline__ unsigned la_block(unsigned row) { return blockIdx.y * row + blockIdx.x; }
 
 struct LaUnit {
   int job, slab, hd, sid;
@@ -949,7 +949,7 @@ __global__ __launch_bounds__(NW * 64)
     __attribute__((amdgpu_waves_per_eu(LaTile<T, DKP, NW>::kWaves))) void
     pdssm_linattn_kernel(const LaArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  const unsigned id = la_block();
+  const unsigned id = la_block(a.row);
   if (id == 0 && threadIdx.x < 2) a.header[threadIdx.x] = 0;
   LaUnit u;
   la_unit(a, id, u);
@@ -987,7 +987,7 @@ pdssm_linattn_state_kernel(const LaArgs a) {
             n32 = lane & 31;
   float* ew = (float*)(smem + 2 * (K::kX + K::kZ)) + wave * 64;   // this wave's own copy of the weights
   LaUnit u;
-  la_unit(a, la_block(), u);
+  la_unit(a, la_block(a.row), u);
   if (u.sid >= a.segs) return;
   const int slab = u.slab, hd = u.hd, sid = u.sid;
   const LaJob& J = a.job[u.job];

@@ -17,6 +17,7 @@ struct LaCarryArgs {
   LaCarry c[2];
   const int32_t* starts; // packed: first segment of every sequence
   int B, H, nseg, tiles;   // tiles: workgroups of a state, 1024 elements each
+  unsigned row;            // workgroups along x of the launch
   long long state;
 };
 

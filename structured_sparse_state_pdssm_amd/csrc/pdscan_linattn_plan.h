@@ -50,6 +50,7 @@ struct LaArgs {
   uint32_t* header;            // workspace header
   int B, H, L, nseg, seg, segs;   // nseg per sequence (not packed), steps per segment, segments in all (bound)
   int slabs, njobs;
+  unsigned row;                // workgroups along x of the launch
   long long rows, state;       // token rows in all; elements of one state
   LaJob job[3];
 };
@@ -59,6 +60,7 @@ struct LaStepArgs {
   float* state;
   const int32_t* idx;
   int B, H, qd, dk, dv, slots, cols;   // cols: value columns per workgroup
+  unsigned row;                // workgroups along x of the launch
   float scale;
   int bf16;
 };
