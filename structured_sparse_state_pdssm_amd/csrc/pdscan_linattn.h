@@ -625,15 +625,17 @@ __device__ __forceinline__ la_f16 la_scores(const unsigned char* X, const unsign
 //
 // A chunk's tiles are loaded once, a chunk ahead, and everything but o stays in
 // registers and LDS, so few rows of input are waited for at once and the work
-// of a chunk is a chain: scores, their pieces, the products, the state.  What
-// bounds it is memory where the rows are short (64/32: 3.6 of the 4.7 TB/s that
-// a large copy has) and that chain where they are long or carry three pieces:
-//   forward  16 x 2048, 24 heads, 64/32 bf16    70 us (matrix 9, VALU 19)
-//            65536 steps, 16 heads, 128/128    262 us (matrix 84, VALU 77)
-//            4 x 4096, 8 heads, 16/64 fp32      26 us (matrix 5, VALU 10)
-//   dq and dk of the first of these            203 us (matrix 26, VALU 95), dv 70 us
-//   dq, dk, dv of 8190 rows, 16 heads, 128/128 177 us (matrix 38, VALU 45)
-// (matrix, VALU: the SIMD time of those instructions alone.)
+// of a chunk is a chain: scores, their pieces, the products, the state.  In most
+// sizes memory bounds it: whole 128-byte lines move behind the L2s, more than once where
+// heads that share them run on several dies (a large copy has 4.7 TB/s, reads and writes;
+// what is above comes from the cache there).  With three pieces of 128-wide rows it is that chain.
+//   forward  16 x 2048, 24 heads, 64/32 bf16    70 us, 396 MB at 5.6 TB/s (matrix 9, VALU 19, LDS 8)
+//            65536 steps, 16 heads, 128/128    264 us, 1145 MB at 4.3 (matrix 84, VALU 77, LDS 47)
+//            4 x 4096, 8 heads, 16/64 fp32      25 us, 105 MB at 4.1 (matrix 5, VALU 10, LDS 3)
+//   dq and dk of the first of these            209 us, 1067 MB at 5.1 (matrix 26, VALU 94, LDS 22), dv 70 us
+//   dq, dk, dv of 8190 rows, 16 heads, 128/128 179 us, 627 MB at 3.5 (matrix 38, VALU 45, LDS 21)
+// (matrix, VALU, LDS: the time that those alone take of a SIMD or an LDS.)  A call
+// of few steps is its start-up: 5 to 7 us, and 2 to 6 for a chunk of 32 (64/64).
 template <typename T, int DKP, int NW, int MODE>
 __device__ __forceinline__ void la_body(const LaArgs& a, const LaJob& J, const LaSeg& s, int sid, int hd, int slab,
                                         unsigned char* smem) {
@@ -968,8 +970,8 @@ __global__ __launch_bounds__(NW * 64)
 
 // Contribution of one segment to the state behind it (before it, for a
 // reversed job), written at that segment's place.  Reading y and z is its time
-// (16 x 2048 steps, 24 heads, 64/32 bf16: 35 us, 4.3 TB/s; 65536 steps, 16 heads,
-// 128/128: 117 us, 4.6 TB/s; two chunks under way instead of one: the same).  The last segment in the
+// (16 x 2048 steps, 24 heads, 64/32 bf16: 35 us, 212 MB behind the L2s at 6.0 TB/s; 65536 steps,
+// 16 heads, 128/128: 120 us, 587 MB at 4.9; two chunks under way instead of one: the same).  The last segment in the
 // job's direction has none behind it and does nothing.
 //
 // It goes through its chunks from that end on, each weighted with the decay f
