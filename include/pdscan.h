@@ -372,7 +372,9 @@ int pdssm_dict_hardmax(int32_t H, int32_t K, int32_t N, const float* M, int32_t*
  * as two bf16 pieces where a bf16 output comes of it (2^-18 of a term) and as
  * three (24 bits) where an fp32 one does; fp32 inputs are three pieces, of
  * whose nine products the six largest are formed (2^-26 of a term is left).
- * Values under about 1e-30 in size lose digits there. */
+ * Values under about 1e-30 in size lose digits there.  The decay over a chunk
+ * is rounded to fp32; a constant decay is off to the same side in every chunk:
+ * 1e-6 of a state that remembers 8192 steps. */
 typedef struct {
   int32_t B;               /* sequences */
   int32_t H, Hk;           /* value heads; query / key heads (Hk divides H) */
@@ -434,7 +436,8 @@ int pdssm_linattn_bwd(const pdssm_linattn_dims* dims, const pdssm_view* q, const
  *   state_idx [B] int32 on the device: row b's slot; NULL: slot b (B <= n_slots)
  * A negative slot marks an empty row: its o is zero and no state is touched.
  * A slot >= n_slots, or one that an earlier row of the call has, gives NaN in
- * that row's o and touches no state. */
+ * that row's o and touches no state.  The search for an earlier row reads B / 2
+ * indices a row and head on average: for batches up to some ten thousand rows. */
 int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, const pdssm_view* k,
                        const pdssm_view* v, const pdssm_view* log_decay, const int32_t* state_idx,
                        int32_t n_slots, float* state, const pdssm_view* o, void* stream);
