@@ -351,7 +351,8 @@ int pdssm_dict_hardmax(int32_t H, int32_t K, int32_t N, const float* M, int32_t*
  *     exponential is zero).  Not checked on the device.
  *   - q, k, v, g_o and the states are finite (as everywhere in this library:
  *     not checked).  A token that is not finite can spoil every output of
- *     its chunk of 64 tokens, and of the rest of its sequence.
+ *     its chunk of 64 tokens, and of the rest of its sequence; in a gradient
+ *     also g_log_decay over its segment of up to 512 steps.
  *   - packed = 1: one step axis of L rows holds B sequences end to end;
  *     sequence b has the rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (device,
  *     int32 [B+1], not decreasing, within [0, L]; lengths of 0 pass h0 on).

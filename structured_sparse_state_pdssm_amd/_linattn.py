@@ -19,6 +19,7 @@ outputs are made here they hold whatever the memory held.
 
 import ctypes
 import struct
+from collections.abc import Mapping
 
 import torch
 
@@ -206,7 +207,7 @@ def _given(out, names):
     """The caller's outputs, by name: a misspelt one would be left as it is."""
     if out is None:
         return {}
-    if not isinstance(out, dict):
+    if not isinstance(out, Mapping):
         raise TypeError(f"out must be a dict (got {type(out).__name__})")
     for n in out:
         if n not in names:

@@ -1,5 +1,7 @@
 """Arguments of the linear-attention calls that the binding refuses on the host, no GPU."""
 
+from types import MappingProxyType
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -30,7 +32,7 @@ def test_unknown_outputs(P):
         P.pdssm_linattn_bwd(**args(g_o=g_o), out={"g_q": torch.zeros(B, H, L, dk), "g_decay": torch.zeros(B, H, L)})
     with pytest.raises(TypeError, match="out must be a dict"):
         P.pdssm_linattn_fwd(**args(), out=torch.zeros(B, H, L, dv))
-    for out in ({}, None, {"o": torch.zeros(B, H, L, dv)}, {"o": None}):
+    for out in ({}, None, {"o": torch.zeros(B, H, L, dv)}, {"o": None}, MappingProxyType({"o": None})):
         with pytest.raises(ValueError, match="device tensor"):
             P.pdssm_linattn_fwd(**args(), out=out)
     with pytest.raises(ValueError, match="device tensor"):   # left alone, as asked for
