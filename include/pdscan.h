@@ -443,6 +443,127 @@ int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, cons
                        const pdssm_view* v, const pdssm_view* log_decay, const int32_t* state_idx,
                        int32_t n_slots, float* state, const pdssm_view* o, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Selective state-space layer: a short causal convolution of every channel, a
+ * scan whose decay depends on the input, the channel and the state, and the
+ * norm around a block.  Where PD-SSM selects a permutation and linear attention has
+ * one decay a head, this scan's transition is a diagonal of its own at every
+ * step; the layer is mixed with both.
+ *
+ * Conventions of these calls: those of the linattn calls above, with
+ *   - channels as the last, contiguous axis of a view, a multiple of 8 of them; a view
+ *     without heads (x, dt, z, y [B,L,D] and their gradients) does not look at stride_h;
+ *   - inputs and outputs of one type, in_dtype; weights, scan states and
+ *     the gradients of both fp32 and contiguous; a convolution's states hold
+ *     inputs as they are, in in_dtype;
+ *   - packed = 1, cu_seqlens, rows outside the sequences, offsets out of order:
+ *     as there.  L, and B L, at most 2^31 - 257;
+ *   - everything is finite (not checked).  What is not spoils its own channel, from its
+ *     token on, and in a scan and its gradients what its tile of up to 64 tokens and
+ *     its segment share. */
+typedef struct {
+  int32_t B;               /* sequences */
+  int32_t L;               /* steps per sequence; packed: rows of the step axis */
+  int32_t D;               /* channels */
+  int32_t W;               /* taps, 2 to 4 */
+  int32_t in_dtype;        /* pdssm_dtype of x, y, the states and their gradients */
+  int32_t packed;          /* 1: cu_seqlens holds the sequences' bounds */
+  int32_t silu;            /* 1: y = v / (1 + e^-v) of the sum v; 0: y = v */
+} pdssm_conv_dims;
+
+/* Short causal convolution: y_t = act(bias + sum_j w[:,j] x_{t-W+1+j}).
+ *   x, y [B,L,D] (views); w [D,W], bias [D] or NULL (fp32)
+ *   x0 [B,W-1,D] or NULL (zero): the rows before each sequence, the oldest first
+ *   x_L [B,W-1,D] (out, required): its last rows, those of x0 among them where it
+ *     is shorter: x0 of what follows */
+int pdssm_conv_fwd(const pdssm_conv_dims* dims, const pdssm_view* x, const float* w, const float* bias,
+                   const int32_t* cu_seqlens, const void* x0, const pdssm_view* y, void* x_L, void* stream);
+
+/* Its gradient, given g_y [B,L,D] and g_xL [B,W-1,D] (NULL: zero).
+ *   g_x [B,L,D], g_w [D,W], g_bias [D] (out, required); g_x0 [B,W-1,D] (out, optional) */
+int pdssm_conv_bwd_workspace_bytes(const pdssm_conv_dims* dims, size_t* bytes);
+int pdssm_conv_bwd(const pdssm_conv_dims* dims, const pdssm_view* x, const float* w, const float* bias,
+                   const int32_t* cu_seqlens, const void* x0, const pdssm_view* g_y, const void* g_xL,
+                   const pdssm_view* g_x, float* g_w, float* g_bias, void* g_x0, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* One token of every row on a pool of states, updated in place.
+ *   dims: L = 1, packed = 0.  x, y [B,D] (views; the step stride is not looked at)
+ *   state [n_slots,W-1,D] (in and out); state_idx [B] or NULL, as in pdssm_linattn_step:
+ *   a negative slot gives zeros, one past the pool or of an earlier row NaN. */
+int pdssm_conv_step(const pdssm_conv_dims* dims, const pdssm_view* x, const float* w, const float* bias,
+                    const int32_t* state_idx, int32_t n_slots, void* state, const pdssm_view* y, void* stream);
+
+typedef struct {
+  int32_t B, L, D;         /* as above */
+  int32_t N;               /* state values of a channel: a multiple of 8, at most 64 */
+  int32_t G;               /* groups of channels that share B and C: D / G is a multiple of 8 */
+  int32_t in_dtype, packed;
+  int32_t softplus;        /* 1: steps d = log(1 + e^(dt + bias)); 0: d = dt + bias */
+} pdssm_selscan_dims;
+
+/* Selective scan, per sequence, channel d (of group d / (D / G)) and state n:
+ *   h_t = exp(d_t A) h_{t-1} + d_t x_t B_t,   y_t = (C_t . h_t + skip x_t) silu(z_t),   h_{-1} = h0
+ *   x, dt, z, y [B,L,D], Bm, Cm [B,G,L,N] (views; z NULL: no gate)
+ *   A [D,N]; skip, dt_bias [D] or NULL (zero); h0 [B,D,N] or NULL (zero)
+ *   h_L [B,D,N] (out, required)
+ * Steps d_t >= 0 and A <= 0 (not checked; exp(d A) past fp32 overflows).
+ * Precision: fp32 throughout, sums of steps over more than a tile in 64 bits;
+ * an exponential is good to two steps of fp32.  Decays below 2^-126 are zero. */
+int pdssm_selscan_workspace_bytes(const pdssm_selscan_dims* dims, size_t* bytes);
+int pdssm_selscan_fwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const pdssm_view* dt, const float* A,
+                      const pdssm_view* Bm, const pdssm_view* Cm, const float* skip, const pdssm_view* z,
+                      const float* dt_bias, const int32_t* cu_seqlens, const float* h0, const pdssm_view* y,
+                      float* h_L, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient, given g_y [B,L,D] and g_hL [B,D,N] (NULL: zero).  Nothing of
+ * the forward pass is kept: the states are formed again, from states at every 32nd step
+ * that the workspace holds (D N / 8 bytes a row, and N / 4 a row and channel block for sums).
+ *   g_x, g_dt, g_z [B,L,D] (g_z NULL with z), g_B, g_C [B,G,L,N] (views)
+ *   g_A [D,N], g_skip [D], g_bias [D] (out, required); g_h0 [B,D,N] (out, optional) */
+int pdssm_selscan_bwd_workspace_bytes(const pdssm_selscan_dims* dims, size_t* bytes);
+int pdssm_selscan_bwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const pdssm_view* dt, const float* A,
+                      const pdssm_view* Bm, const pdssm_view* Cm, const float* skip, const pdssm_view* z,
+                      const float* dt_bias, const int32_t* cu_seqlens, const float* h0, const pdssm_view* g_y,
+                      const float* g_hL, const pdssm_view* g_x, const pdssm_view* g_dt, float* g_A,
+                      const pdssm_view* g_B, const pdssm_view* g_C, float* g_skip, const pdssm_view* g_z,
+                      float* g_bias, float* g_h0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every row on a pool of states, updated in place.
+ *   dims: L = 1, packed = 0.  x, dt, z, y [B,D], Bm, Cm [B,G,N] (views; the step stride is not looked at)
+ *   state [n_slots,D,N] (in and out); state_idx [B] or NULL, as in pdssm_linattn_step. */
+int pdssm_selscan_step(const pdssm_selscan_dims* dims, const pdssm_view* x, const pdssm_view* dt, const float* A,
+                       const pdssm_view* Bm, const pdssm_view* Cm, const float* skip, const pdssm_view* z,
+                       const float* dt_bias, const int32_t* state_idx, int32_t n_slots, float* state,
+                       const pdssm_view* y, void* stream);
+
+typedef enum { PDSSM_GATE_NONE = 0, PDSSM_GATE_BEFORE = 1, PDSSM_GATE_AFTER = 2 } pdssm_gate;
+
+typedef struct {
+  int32_t B, H, L;         /* rows */
+  int32_t d;               /* elements of a row: a multiple of 8, at most 8192 */
+  int32_t in_dtype;        /* pdssm_dtype of x, z, the residual, y and their gradients */
+  int32_t gate;            /* pdssm_gate: where silu(z) is multiplied in */
+  int32_t per_head;        /* 0: w and res_scale [d]; 1: [H,d] */
+  float eps;               /* > 0, a normal number */
+} pdssm_norm_dims;
+
+/* Norm before or behind a block, over the last axis of every row:
+ *   y = residual + res_scale (w u / sqrt(mean(u^2) + eps)) [silu(z) with PDSSM_GATE_AFTER]
+ *   u = x, or x silu(z) with PDSSM_GATE_BEFORE
+ *   x, z, residual, y [B,H,L,d] (views; z NULL without a gate; residual NULL: zero)
+ *   w, res_scale [H,d] or [d] (res_scale NULL: one) */
+int pdssm_norm_fwd(const pdssm_norm_dims* dims, const pdssm_view* x, const float* w, const pdssm_view* z,
+                   const pdssm_view* residual, const float* res_scale, const pdssm_view* y, void* stream);
+
+/* Its gradient, given g_y [B,H,L,d]; the residual's is g_y itself.
+ *   g_x, g_z [B,H,L,d] (views; g_z NULL without a gate), g_w and g_res_scale
+ *   [H,d] or [d] (summed over the heads then; g_res_scale NULL with res_scale) */
+int pdssm_norm_bwd_workspace_bytes(const pdssm_norm_dims* dims, size_t* bytes);
+int pdssm_norm_bwd(const pdssm_norm_dims* dims, const pdssm_view* x, const float* w, const pdssm_view* z,
+                   const float* res_scale, const pdssm_view* g_y, const pdssm_view* g_x, float* g_w,
+                   const pdssm_view* g_z, float* g_res_scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* pdssm_status_str(int status);
 

@@ -16,6 +16,8 @@ Entry points (same names as the C ABI):
     -> dict(y, h_L[, k_star][, D])
 * ``pdssm_linattn_fwd``, ``pdssm_linattn_bwd``, ``pdssm_linattn_step``:
   linear attention with a decay for each head (see ``_linattn.py``)
+* ``pdssm_conv_{fwd,bwd,step}``, ``pdssm_selscan_{fwd,bwd,step}``,
+  ``pdssm_norm_{fwd,bwd}``: the selective state-space layer (see ``_ssm.py``)
 
 Shapes: u [B,H,L,d] (per head) or [B,L,d] (shared by all heads, detected by
 its rank); W_sel [H,K,d]; W_d [H,N,d]; b_d [H,N]; dict_idx [H,K,N] int32;
@@ -532,3 +534,17 @@ from ._linattn import (  # noqa: E402,F401
 
 __all__ += ["linattn_dims", "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "pdssm_linattn_fwd",
             "pdssm_linattn_bwd", "pdssm_linattn_step"]
+
+from ._ssm import (  # noqa: E402,F401
+    pdssm_conv_bwd,
+    pdssm_conv_fwd,
+    pdssm_conv_step,
+    pdssm_norm_bwd,
+    pdssm_norm_fwd,
+    pdssm_selscan_bwd,
+    pdssm_selscan_fwd,
+    pdssm_selscan_step,
+)
+
+__all__ += ["pdssm_conv_fwd", "pdssm_conv_bwd", "pdssm_conv_step", "pdssm_selscan_fwd", "pdssm_selscan_bwd",
+            "pdssm_selscan_step", "pdssm_norm_fwd", "pdssm_norm_bwd"]

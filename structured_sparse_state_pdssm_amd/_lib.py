@@ -72,6 +72,19 @@ def _load():
         "pdssm_linattn_fwd": [ldp, wp, wp, wp, wp, vp, vp, wp, vp, vp, sz, vp],
         "pdssm_linattn_bwd": [ldp, wp, wp, wp, wp, vp, vp, wp, vp, wp, wp, wp, wp, vp, vp, sz, vp],
         "pdssm_linattn_step": [ldp, wp, wp, wp, wp, vp, i32, vp, wp, vp],
+        "pdssm_conv_fwd": [vp, wp, vp, vp, vp, vp, wp, vp, vp],
+        "pdssm_conv_bwd_workspace_bytes": [vp, ctypes.POINTER(sz)],
+        "pdssm_conv_bwd": [vp, wp, vp, vp, vp, vp, wp, vp, wp, vp, vp, vp, vp, sz, vp],
+        "pdssm_conv_step": [vp, wp, vp, vp, vp, i32, vp, wp, vp],
+        "pdssm_selscan_workspace_bytes": [vp, ctypes.POINTER(sz)],
+        "pdssm_selscan_fwd": [vp, wp, wp, vp, wp, wp, vp, wp, vp, vp, vp, wp, vp, vp, sz, vp],
+        "pdssm_selscan_bwd_workspace_bytes": [vp, ctypes.POINTER(sz)],
+        "pdssm_selscan_bwd": [vp, wp, wp, vp, wp, wp, vp, wp, vp, vp, vp, wp, vp, wp, wp, vp, wp, wp, vp, wp, vp, vp, vp,
+                              sz, vp],
+        "pdssm_selscan_step": [vp, wp, wp, vp, wp, wp, vp, wp, vp, vp, i32, vp, wp, vp],
+        "pdssm_norm_fwd": [vp, wp, vp, wp, wp, vp, wp, vp],
+        "pdssm_norm_bwd_workspace_bytes": [vp, ctypes.POINTER(sz)],
+        "pdssm_norm_bwd": [vp, wp, vp, wp, vp, wp, wp, vp, wp, vp, vp, sz, vp],
         "pdssm_status_str": [ctypes.c_int],
         "pdssm_last_error": [],
         "pdssm_abi_version": [],

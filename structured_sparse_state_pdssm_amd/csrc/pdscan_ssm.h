@@ -1,0 +1,170 @@
+// Element types, rounding and the few functions that the kernels of the
+// selective scan, the convolution and the norm share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "pdscan_ssm_plan.h"
+
+namespace pdscan {
+
+typedef __bf16 ss_bf2 __attribute__((ext_vector_type(2)));
+typedef float ss_f2 __attribute__((ext_vector_type(2)));
+
+// V neighbouring elements, loaded and stored at once.
+template <typename E, int V>
+struct alignas(sizeof(E) * V > 16 ? 16 : sizeof(E) * V) SsVec {
+  E e[V];
+};
+
+struct SsF32 {
+  using E = float;
+  static __device__ __forceinline__ float get(float x) { return x; }
+  template <int V>
+  static __device__ __forceinline__ void put(SsVec<E, V>& o, const float* x) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.e[i] = x[i];
+  }
+};
+struct SsBf16 {
+  using E = uint16_t;
+  static __device__ __forceinline__ float get(uint16_t x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }
+  // rounded to the nearest, once, from the fp32 value
+  template <int V>
+  static __device__ __forceinline__ void put(SsVec<E, V>& o, const float* x) {
+    if constexpr (V == 1) {
+      o.e[0] = __builtin_bit_cast(uint16_t, (__bf16)x[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(ss_f2{x[i], x[i + 1]}, ss_bf2));
+        o.e[i] = (uint16_t)u;
+        o.e[i + 1] = (uint16_t)(u >> 16);
+      }
+    }
+  }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ SsVec<typename T::E, V> ss_load(const void* p, int64_t at) {
+  return *(const SsVec<typename T::E, V>*)((const typename T::E*)p + at);
+}
+template <typename T, int V>
+__device__ __forceinline__ void ss_store(void* p, int64_t at, const float* x) {
+  SsVec<typename T::E, V> o;
+  T::template put<V>(o, x);
+  *(SsVec<typename T::E, V>*)((typename T::E*)p + at) = o;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float ss_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// e^-|x|, with what the product by log2 e lost put back (two steps of fp32
+// instead of |x| of them).
+__device__ __forceinline__ float ss_decay(float x) {
+  constexpr float kLo = 1.925963033500011e-08f;   // log2 e behind its fp32 value
+  const float n = -fabsf(x), t = kLog2e * n;
+  const float r = __builtin_fmaf(n, kLo, __builtin_fmaf(n, kLog2e, -t)), e = ss_exp2(t);
+  return __builtin_fmaf(e * kLn2, r, e);
+}
+// 1 / (1 + e^-x) from e = e^-|x|.
+__device__ __forceinline__ float ss_sigmoid_of(float x, float e) {
+  return (x >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+__device__ __forceinline__ float ss_sigmoid(float x) { return ss_sigmoid_of(x, ss_decay(x)); }
+
+// log(1 + e^x) = max(x, 0) + log1p(e) with e = e^-|x|, the latter as
+// log(w) e / (w - 1) with w = 1 + e rounded (Kahan's form: the rounding of w
+// cancels), so that small steps keep their digits.
+__device__ __forceinline__ float ss_softplus_of(float x, float e) {
+  const float w = 1.0f + e;
+  const float l = kLn2 * __builtin_amdgcn_logf(w) * e * __builtin_amdgcn_rcpf(w - 1.0f);
+  return (x > 0.0f ? x : 0.0f) + (w == 1.0f ? e : l);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float ss_dpp(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppRor4 = 0x124, kDppRor8 = 0x128;
+
+// Sums over the lanes 32 apart of a (lower half of the result) and of b (upper
+// half): the instruction exchanges a's upper half and b's lower one.  By hand,
+// as the compiler's builtin gives the first result twice; it waits for the
+// two states that the exchange has to be behind what wrote its operands.
+__device__ __forceinline__ float ss_fold32(float a, float b) {
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b));
+  return a + b;
+}
+// Sums over the rows of 16 lanes next to each other: of a in even rows, of b
+// in odd ones (a's odd rows and b's even ones change places).
+__device__ __forceinline__ float ss_fold16(float a, float b) {
+  asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a), "+v"(b));
+  return a + b;
+}
+// Sums over the four rows of 16 lanes: row r of the result has v_r's.
+__device__ __forceinline__ float ss_fold_rows(float v0, float v1, float v2, float v3) {
+  return ss_fold16(ss_fold32(v0, v2), ss_fold32(v1, v3));
+}
+
+// Sum over P lanes next to each other, in every one of them (P: up to 64).
+template <int P>
+__device__ __forceinline__ float ss_sum(float x) {
+  if constexpr (P >= 2) x += ss_dpp<kDppXor1>(x);
+  if constexpr (P >= 4) x += ss_dpp<kDppXor2>(x);
+  if constexpr (P >= 8) x += ss_dpp<kDppHalfMirror>(x);
+  if constexpr (P >= 16) x += ss_dpp<kDppRor8>(x);
+  if constexpr (P >= 32) x = ss_fold16(x, x);
+  if constexpr (P >= 64) x = ss_fold32(x, x);
+  return x;
+}
+
+// The workgroup's number, in a launch of la_grid_rows.
+__device__ __forceinline__ unsigned ss_block(unsigned row) { return blockIdx.y * row + blockIdx.x; }
+
+// Workgroups go to the eight dies in turn; this numbers them so that a die
+// has neighbours: they share rows' cache lines and, in a scan, B and C.
+__device__ __forceinline__ long long ss_near(unsigned id, long long n) {
+  const long long per = (n + 7) / 8;
+  return (long long)(id % 8) * per + id / 8;   // at or past n: nothing to do
+}
+
+struct SsSeg {
+  int b, t0, len;                // sequence; first row of the step axis, rows
+  int64_t vb;                    // row of the batch axis
+  bool first, last;
+};
+
+__device__ __forceinline__ bool ss_segment(const SsSegs& g, int sid, SsSeg& s) {
+  if (g.table) {
+    const int4 e = *(const int4*)(g.table + 4 * (int64_t)sid);
+    if (e.z < 0) return false;
+    s.b = e.x;
+    s.t0 = e.y;
+    s.len = e.z;
+    s.first = e.w & 1;
+    s.last = e.w >> 1;
+    s.vb = 0;
+  } else if (g.cu) {
+    s.b = sid;
+    int t0 = g.cu[sid], t1 = g.cu[sid + 1];
+    t0 = t0 < 0 ? 0 : t0 > g.L ? g.L : t0;
+    t1 = t1 < t0 ? t0 : t1 > g.L ? g.L : t1;
+    s.t0 = t0;
+    s.len = t1 - t0;
+    s.first = s.last = true;
+    s.vb = 0;
+  } else {
+    s.b = sid / g.nseg;
+    const int i = sid % g.nseg;
+    s.t0 = i * g.seg;
+    s.len = g.L - s.t0 < g.seg ? g.L - s.t0 : g.seg;
+    s.first = i == 0;
+    s.last = i == g.nseg - 1;
+    s.vb = s.b;
+  }
+  return true;
+}
+
+}  // namespace pdscan

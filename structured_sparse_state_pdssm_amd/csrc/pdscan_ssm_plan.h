@@ -1,0 +1,185 @@
+// Argument blocks and host-side planning of the selective scan, the short
+// causal convolution and the norm around a block (pdssm_selscan_*,
+// pdssm_conv_*, pdssm_norm_*): shared by the C ABI (host only) and the kernels.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "pdscan_linattn_plan.h"
+
+namespace pdscan {
+
+constexpr int kSsMaxN = 64;      // state values of a channel
+constexpr int kSsMaxD = 1 << 20; // channels
+constexpr int kCvMinW = 2, kCvMaxW = 4;
+
+// The sequences of a call, cut into segments where there are few.
+struct SsSegs {
+  const int32_t* cu;             // packed: B+1 row offsets, NULL: B sequences of L steps
+  const int32_t* table;          // packed and split: {sequence, first row, rows, first | last << 1} per segment
+  int B, L, nseg, seg, segs;     // nseg per sequence (not packed), steps per segment, segments in all (bound)
+};
+
+// One pass of the selective scan.  Element (b, t, d) of x, dt, z, y and their
+// gradients is at sb b + st t + d; B and C have a head axis of G groups.
+struct SsArgs {
+  LaView x, dt, z, Bm, Cm, y;    // z.p NULL: no gate
+  LaView gy, gx, gdt, gz;        // (gradient) gz.p NULL with z.p
+  const float *A, *skip, *bias;  // [D][N]; [D] or NULL
+  const float *h0, *ghL;         // [B][D][N] or NULL: zero
+  float *hL, *gh0;               // gh0 may be NULL
+  SsSegs s;
+  float *seg, *adj;              // [segments][D][N]: contributions of segments, then entering (adjoint) states
+  float *sum;                    // [segments][D]: sums of the steps d_t of a segment
+  float *ckpt, *cum;             // states at the tiles' starts, each segment from zero, and the sums up to there
+  float *part;                   // partial g_B and g_C [2][blocks of all groups][rows][N]
+  float *partA, *partD;          // [segments][D][N]; [segments][2][D]: g_skip, g_bias
+  uint32_t* header;              // workspace header
+  int D, N, G, softplus;
+  unsigned row;                  // workgroups along x of the launch
+  long long rows;                // token rows in all
+};
+
+struct SsCarryArgs {
+  const float *A, *user;         // user: state before the first segment in this direction [B][D][N], NULL: zero
+  float *seg;
+  const float *sum;
+  const int32_t* starts;         // packed: first segment of every sequence
+  int B, D, N, nseg, rev, blocks;
+  unsigned row;
+};
+
+// Sums that finish a gradient: over channel blocks into g_B and g_C, over segments into the parameters'.
+struct SsFoldArgs {
+  const float* part;
+  LaView out[2];
+  const int32_t* cu;
+  int B, L, N, G, blocks;        // blocks per group
+  long long rows;
+};
+// Sums of `parts` rows of `width` columns: the first `first` go to out, the others to out2 (NULL: nowhere).
+struct SsSumArgs {
+  const float* part;
+  float *out, *out2;
+  float* mid;                    // [kSsSumMid][width] where there are more than kSsSumMost parts
+  int parts;
+  int64_t width, first;
+};
+constexpr int kSsSumMost = 256, kSsSumMid = 64;
+
+struct SsStepArgs {
+  LaView x, dt, z, Bm, Cm, y;
+  const float *A, *skip, *bias;
+  float* state;
+  const int32_t* idx;
+  int B, D, N, G, slots, softplus;
+  unsigned row;
+};
+
+// States of a lane and lanes of a channel, by the state count: a wave holds
+// 64 / lanes channels whole.
+struct SsShape {
+  int S, NS;
+};
+inline constexpr SsShape ss_shape(int N) {
+  return N <= 8 ? SsShape{2, 4} : N <= 16 ? SsShape{4, 4} : N <= 32 ? SsShape{8, 4} : SsShape{8, 8};
+}
+inline constexpr int ss_channels(int N) { return 64 / ss_shape(N).NS; }   // of a wave
+inline int ss_blocks(int K, int per) { return (K + per - 1) / per; }        // channel blocks of a group of K
+
+// Steps of a tile: forwards four waves of 64 / S steps (at most 16) each, backwards four of 8.
+inline constexpr int ss_fwd_steps(int N) { return ss_shape(N).S >= 8 ? 8 : 16; }
+constexpr int kSsBwdSteps = 8, kSsTimeWaves = 4, kSsBwdTile = kSsBwdSteps * kSsTimeWaves;
+constexpr int kSsBwdGroups = 2;  // channel groups (waves side by side) of a gradient's workgroup
+constexpr int kSsStateGroups = 4;
+
+struct SsSplit {
+  int seg, nseg, segs;
+  bool split;
+};
+
+// Cuts the step axis into segments where `width` workgroups a sequence leave
+// the card idle: `room` of them fill it.
+inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, int least, int unit) {
+  SsSplit s;
+  const long long have = packed ? width * 2 : B * width;   // (sequences of different lengths: the longest counts)
+  long long n = have * 2 >= room ? 1 : (room + have - 1) / have;
+  if (n > L / least) n = L / least;
+  s.split = n > 1;
+  const long long each = s.split ? ((long long)L + n - 1) / n : L;
+  s.seg = s.split ? (int)((each + unit - 1) / unit * unit) : L;
+  s.nseg = s.split ? (int)(((long long)L + s.seg - 1) / s.seg) : 1;
+  const long long segs = !packed ? (long long)B * s.nseg : s.split ? (long long)(L / s.seg) + B : B;
+  s.segs = segs > 0x7fffffffll ? 0x7fffffff : (int)segs;
+  return s;
+}
+
+struct CvArgs {
+  LaView x, y, gy, gx;
+  const float *w, *bias;         // [D][W]; [D] or NULL
+  const void *x0, *gxL;          // [B][W-1][D] or NULL: zero
+  void *xL, *gx0;                // gx0 may be NULL
+  const int32_t* cu;
+  float* part;                   // [parts][D][W], [D]
+  uint32_t* header;              // workspace header
+  int B, L, D, W, silu, strips;  // strips: of a sequence (packed: of all rows)
+  int parts;
+  unsigned units;                // threads with rows to do, before those of the states
+  unsigned row;
+};
+struct CvStepArgs {
+  LaView x, y;
+  const float *w, *bias;
+  void* state;                   // [slots][W-1][D]
+  const int32_t* idx;
+  int B, D, W, silu, slots;
+  unsigned row;
+};
+constexpr int kCvRows = 16;      // rows of a thread, forwards
+inline long long cv_units(const CvArgs& a, int bf16) {
+  return (long long)(a.cu ? 1 : a.B) * ((a.L + kCvRows - 1) / kCvRows) * (a.D / (bf16 ? 8 : 4));
+}
+constexpr int kCvBwdRows = 32;   // backwards
+constexpr int kCvBwdStrips = 4;  // strips of a workgroup, backwards
+
+// Lanes of a row and 16-byte vectors of a lane, by the row's length.
+struct NmShape {
+  int P, K;                      // P: 1 .. 64, or 256 (a whole workgroup)
+};
+inline constexpr NmShape nm_shape(int d, int bf16) {
+  const int n = d / (bf16 ? 8 : 4);
+  if (n > 256) return NmShape{256, n <= 512 ? 2 : n <= 1024 ? 4 : 8};
+  if (n > 64) return NmShape{64, n <= 128 ? 2 : 4};
+  int p = 1;
+  while (p < n) p *= 2;
+  return NmShape{p, 1};
+}
+constexpr int kNmMaxD = 8192;
+
+struct NmArgs {
+  LaView x, z, r, y;             // [B][H][L][d]; z.p, r.p may be NULL
+  LaView gy, gx, gz;
+  const float *w, *s;            // [H][d] or [d]; s may be NULL
+  float *partw, *parts;          // (gradient) [chunks][H][d]
+  uint32_t* header;              // workspace header
+  int B, H, L, d, gate, per_head;
+  int cols, slots, tiles;        // lanes of a workgroup side by side in (head, row), rows at once, tiles of the former
+  int chunks;                    // workgroups along the rows
+  float eps;
+  long long rows;                // B L: of a head
+  unsigned row;
+};
+// Heads side by side where they lie so (`near`: the head stride is below the step's), else one head a workgroup.
+inline void nm_plan(NmArgs& a, int bf16, bool near, int each, int most) {
+  const int P = nm_shape(a.d, bf16).P;
+  const long long all = (long long)a.H * P;
+  a.cols = !near ? P : all < 256 ? (int)all : 256;
+  a.slots = 256 / a.cols;
+  a.tiles = (int)((all + a.cols - 1) / a.cols);
+  long long n = (a.rows + (long long)a.slots * each - 1) / ((long long)a.slots * each);
+  if (most && n > most) n = most;
+  a.chunks = (int)(n > 0x7fffffff ? 0x7fffffff : n);
+}
+
+}  // namespace pdscan
