@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void pdssm_conv_kernel(const CvArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float p = cv_pre<T, W, V>(win + i, w, bias[v], v);
-          o[v] = a.silu ? p * ss_sigmoid(p) : p;
+          o[v] = a.silu ? p * ss_sigmoid<T>(p) : p;
         }
         ss_store<T, V>(a.y.p, yp + i * a.y.st, o);
       }
@@ -151,7 +151,7 @@ __device__ __forceinline__ void cv_grad(float (&p)[V], const SsVec<typename T::E
     const float x = cv_pre<T, W, V>(win, w, bias[v], v);
     p[v] = T::get(gy.e[v]);
     if (silu) {
-      const float k = ss_sigmoid(x);
+      const float k = ss_sigmoid<T>(x);
       p[v] *= k * __builtin_fmaf(x, 1.0f - k, 1.0f);
     }
   }
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(256) void pdssm_conv_step_kernel(const CvStepArgs a
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const float p = cv_pre<T, W, V>(win, w, bias[v], v);
-    o[v] = a.silu ? p * ss_sigmoid(p) : p;
+    o[v] = a.silu ? p * ss_sigmoid<T>(p) : p;
   }
   ss_store<T, V>(a.y.p, yp, o);
 #pragma unroll

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void pdssm_norm_kernel(const NmArgs a) {
         gate[k][v] = 1.0f;
         if (a.gate != kNmNone) {
           const float z = T::get(zv[k].e[v]);
-          gate[k][v] = z * ss_sigmoid(z);
+          gate[k][v] = z * ss_sigmoid<T>(z);
           if (a.gate == kNmBefore) u[k][v] *= gate[k][v];
         }
         q = __builtin_fmaf(u[k][v], u[k][v], q);
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(256) void pdssm_norm_bwd_kernel(const NmArgs a) {
         u[k][v] = T::get(xv[k].e[v]);
         float g = T::get(gv[k].e[v]) * s[k][v];
         if (a.gate != kNmNone) {
-          const float z = T::get(zv[k].e[v]), gate = z * ss_sigmoid(z);
+          const float z = T::get(zv[k].e[v]), gate = z * ss_sigmoid<T>(z);
           if (a.gate == kNmBefore) u[k][v] *= gate;
           else g *= gate;
         }
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(256) void pdssm_norm_bwd_kernel(const NmArgs a) {
         const float gy = T::get(gv[k].e[v]), kk = u[k][v] * rms;
         float g = gy * s[k][v], n = kk * w[k][v], gate = 1.0f, slope = 0.0f;
         if (a.gate != kNmNone) {
-          const float z = T::get(zv[k].e[v]), sig = ss_sigmoid(z);
+          const float z = T::get(zv[k].e[v]), sig = ss_sigmoid<T>(z);
           gate = z * sig;
           slope = sig * __builtin_fmaf(z, 1.0f - sig, 1.0f);
         }

@@ -91,81 +91,98 @@ __device__ __forceinline__ bool ss_unit(const SsArgs& a, int per, SsUnit& u) {
   return true;
 }
 
-// The tile of a gradient at step t of segment s: tiles of different segments do not meet.
-__device__ __forceinline__ int64_t ss_tile(const SsArgs& a, const SsSeg& s, int sid, int t) {
+// The first piece of the run that segment s is.
+__device__ __forceinline__ int ss_piece(const SsArgs& a, const SsSeg& s, int sid) {
+  if (!a.s.cu) return s.b * a.npiece + s.t0 / a.piece;
+  if (!a.pieces) return s.b;
+  return __builtin_amdgcn_readfirstlane(a.pieces[s.b] + (a.runs ? (sid - a.runs[s.b]) * a.run : 0));
+}
+
+// The gradient's tile at step t of piece `at` of sequence b, which starts at
+// row t0: tiles of different pieces do not meet.
+__device__ __forceinline__ int64_t ss_tile(const SsArgs& a, int b, int at, int t0, int t) {
   const int per = (a.s.L + kSsBwdTile - 1) / kSsBwdTile;
-  return (a.s.cu ? (int64_t)sid : (int64_t)s.b * per) + s.t0 / kSsBwdTile + t / kSsBwdTile;
+  return (a.s.cu ? (int64_t)at + t0 / kSsBwdTile : (int64_t)b * per + t0 / kSsBwdTile) + t / kSsBwdTile;
 }
 
 // ---- prompts
 
 template <typename T, int S, int NS, int TS>
-__global__ __launch_bounds__(256) void pdssm_selscan_kernel(const SsArgs a) {
+__global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(const SsArgs a) {
   constexpr int W = kSsTimeWaves, CW = 64 / NS, TT = W * TS, NP = S * NS;
   constexpr int V = TS * CW / 64, VB = TS * NP / 64;   // elements of a thread when a tile is staged
-  using E = typename T::E;
   __shared__ __align__(16) float2 du[TT][CW];          // step, step times input
   __shared__ __align__(16) float Bs[TT][NP], Cs[TT][NP];
-  __shared__ __align__(16) float ys[TT][CW];
-  __shared__ __align__(16) float Es[W][S * 64], Ps[W][S * 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __align__(16) float ys[TT][CW], pars[2][CW];
+  __shared__ __align__(16) float Es[W - 1][S * 64], Ps[W - 1][S * 64], Hs[2][S * 64];   // Hs: the state that enters a tile
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (ss_block(a.row) == 0 && tid < 2 && a.header) a.header[tid] = 0;
   SsUnit u;
   SsSeg s;
   if (!ss_unit(a, CW, u) || !ss_segment(a.s, u.sid, s)) return;
   const int c = lane % CW, q = lane / CW, ch = u.c0 + c;
   const bool ok = ch < u.end;
-  float A2[S], H[S];
+  float A2[S];
   ss_load_A(A2, a.A, ch, q * S, a.N, ok);
-  if (s.first)
-    ss_load_state(H, a.h0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
-  else
-    ss_load_state(H, a.seg, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
+  if (wave == W - 1) {
+    float H[S];
+    if (a.seg)
+      ss_load_state(H, a.seg, (int64_t)ss_piece(a, s, u.sid) * a.D + ch, q * S, a.N, ok);
+    else
+      ss_load_state(H, a.h0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+    ss_lane_put(Hs[0], H, lane);
+  }
 
   // this thread's part of a tile: V channels of one step, VB states of one step
   const int st = tid * V / CW, sc = tid * V % CW, bt = tid * VB / NP, bn = tid * VB % NP;
   const bool sok = u.c0 + sc < u.end, bok = bn < a.N;   // whole vectors: sizes are multiples of 8
-  const int64_t row0 = s.t0;
-  const int64_t xat = s.vb * a.x.sb + (row0 + st) * a.x.st + u.c0 + sc, dat = s.vb * a.dt.sb + (row0 + st) * a.dt.st + u.c0 + sc;
-  const int64_t zat = s.vb * a.z.sb + (row0 + st) * a.z.st + u.c0 + sc, yat = s.vb * a.y.sb + (row0 + st) * a.y.st + u.c0 + sc;
-  const int64_t Bat = s.vb * a.Bm.sb + u.g * a.Bm.sh + (row0 + bt) * a.Bm.st + bn, Cat = s.vb * a.Cm.sb + u.g * a.Cm.sh + (row0 + bt) * a.Cm.st + bn;
-  float bias[V], skip[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    bias[v] = a.bias && sok ? a.bias[u.c0 + sc + v] : 0.0f;
-    skip[v] = a.skip && sok ? a.skip[u.c0 + sc + v] : 0.0f;
+  const uint32_t xo = ss_off<T>(a.x, st, sc), dto = ss_off<T>(a.dt, st, sc), zo = ss_off<T>(a.z, st, sc), yo = ss_off<T>(a.y, st, sc);
+  const uint32_t Bo = ss_off<T>(a.Bm, bt, bn), Co = ss_off<T>(a.Cm, bt, bn);
+  if (tid < CW) {
+    pars[0][tid] = a.bias && ok ? a.bias[ch] : 0.0f;
+    pars[1][tid] = a.skip && ok ? a.skip[ch] : 0.0f;
   }
+  __syncthreads();
   const bool gated = a.z.p != nullptr;
-  SsVec<E, V> xn = {}, dn = {}, zn = {};
-  SsVec<E, VB> Bn = {}, Cn = {};
-  auto fetch = [&](int t) {
+  SsRaw<T, V> xn = {}, dn = {}, zn = {};
+  SsRaw<T, VB> Bn = {}, Cn = {};
+  const char *xp = ss_tile_at<T>(a.x, s.vb, s.t0, u.c0), *dp = ss_tile_at<T>(a.dt, s.vb, s.t0, u.c0), *zp = ss_tile_at<T>(a.z, s.vb, s.t0, u.c0);
+  const char *Bp = ss_tile_at<T>(a.Bm, s.vb, s.t0, u.g * a.Bm.sh), *Cp = ss_tile_at<T>(a.Cm, s.vb, s.t0, u.g * a.Cm.sh);
+  char* yp = ss_tile_at<T>(a.y, s.vb, s.t0, u.c0);
+  auto fetch = [&](int t) {   // and the pointers on to the tile behind it
     if (sok && t + st < s.len) {
-      xn = ss_load<T, V>(a.x.p, xat + (int64_t)t * a.x.st);
-      dn = ss_load<T, V>(a.dt.p, dat + (int64_t)t * a.dt.st);
-      if (gated) zn = ss_load<T, V>(a.z.p, zat + (int64_t)t * a.z.st);
+      ss_load_at(xn, xp, xo);
+      ss_load_at(dn, dp, dto);
+      if (gated) ss_load_at(zn, zp, zo);
     }
     if (bok && t + bt < s.len) {
-      Bn = ss_load<T, VB>(a.Bm.p, Bat + (int64_t)t * a.Bm.st);
-      Cn = ss_load<T, VB>(a.Cm.p, Cat + (int64_t)t * a.Cm.st);
+      ss_load_at(Bn, Bp, Bo);
+      ss_load_at(Cn, Cp, Co);
     }
+    xp += ss_rows<T>(a.x, TT);
+    dp += ss_rows<T>(a.dt, TT);
+    zp += ss_rows<T>(a.z, TT);
+    Bp += ss_rows<T>(a.Bm, TT);
+    Cp += ss_rows<T>(a.Cm, TT);
   };
   fetch(0);
-  for (int t0 = 0; t0 < s.len; t0 += TT) {
+  int turn = 0;
+  for (int t0 = 0; t0 < s.len; t0 += TT, turn ^= 1) {
     // stage: steps behind the end have d = 0, which leaves the state as it is
     const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
-    const SsVec<E, V> xc = xn, zc = zn;
+    const SsRaw<T, V> xc = xn, zc = zn;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float raw = T::get(dn.e[v]) + bias[v];
+      const float raw = dn.get(v) + pars[0][sc + v];
       const float d = !live ? 0.0f : a.softplus ? ss_softplus_of(raw, ss_decay(raw)) : raw;
-      du[st][sc + v] = make_float2(d, live ? d * T::get(xc.e[v]) : 0.0f);
+      du[st][sc + v] = make_float2(d, d * xc.get(v));
     }
     {
       SsVec<float, VB> b, k;
 #pragma unroll
       for (int v = 0; v < VB; ++v) {
-        b.e[v] = blive ? T::get(Bn.e[v]) : 0.0f;
-        k.e[v] = blive ? T::get(Cn.e[v]) : 0.0f;
+        b.e[v] = blive ? Bn.get(v) : 0.0f;
+        k.e[v] = blive ? Cn.get(v) : 0.0f;
       }
       *(SsVec<float, VB>*)&Bs[bt][bn] = b;
       *(SsVec<float, VB>*)&Cs[bt][bn] = k;
@@ -178,87 +195,109 @@ __global__ __launch_bounds__(256) void pdssm_selscan_kernel(const SsArgs a) {
 #pragma unroll
     for (int j = 0; j < S; ++j) h[j] = 0.0f;
 #pragma unroll
-    for (int t = 0; t < TS; ++t) {
-      const float2 w = du[wave * TS + t][c];
-      float b[S];
-      ss_row_get(b, &Bs[wave * TS + t][q * S]);
-      sum += w.x;
+    for (int t4 = 0; t4 < TS; t4 += 4) {
+      float2 w[4];
+      float b[4][S];
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        dec[t][j] = ss_exp2(w.x * A2[j]);
-        drv[t][j] = w.y * b[j];
-        h[j] = __builtin_fmaf(dec[t][j], h[j], drv[t][j]);
+      for (int i = 0; i < 4; ++i) {
+        w[i] = du[wave * TS + t4 + i][c];
+        ss_row_get(b[i], &Bs[wave * TS + t4 + i][q * S]);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = t4 + i;
+        sum += w[i].x;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          dec[t][j] = ss_exp2(w[i].x * A2[j]);
+          drv[t][j] = w[i].y * b[i][j];
+          h[j] = __builtin_fmaf(dec[t][j], h[j], drv[t][j]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int j = 0; j < S; ++j) P[j] = ss_exp2(sum * A2[j]);
-    ss_lane_put(Es[wave], h, lane);
-    ss_lane_put(Ps[wave], P, lane);
+    if (wave < W - 1) {
+      ss_lane_put(Es[wave], h, lane);
+      ss_lane_put(Ps[wave], P, lane);
+    }
     __syncthreads();
-    // the state that enters them, and the one behind the tile
+    // the state that enters them; the last wave's is behind the tile then
+    float own[S];
 #pragma unroll
-    for (int j = 0; j < S; ++j) h[j] = H[j];
+    for (int j = 0; j < S; ++j) own[j] = h[j];
+    ss_lane_get(h, Hs[turn], lane);
 #pragma unroll
-    for (int v = 0; v < W; ++v) {
-      float e[S], p[S];
-      ss_lane_get(e, Es[v], lane);
-      ss_lane_get(p, Ps[v], lane);
+    for (int v = 0; v < W - 1; ++v) {
+      if (v < wave) {
+        float e[S], p[S];
+        ss_lane_get(e, Es[v], lane);
+        ss_lane_get(p, Ps[v], lane);
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        if (v == wave) h[j] = H[j];
-        H[j] = __builtin_fmaf(p[j], H[j], e[j]);
+        for (int j = 0; j < S; ++j) h[j] = __builtin_fmaf(p[j], h[j], e[j]);
       }
+    }
+    if (wave == W - 1) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) own[j] = __builtin_fmaf(P[j], h[j], own[j]);
+      ss_lane_put(Hs[turn ^ 1], own, lane);
     }
     // and the steps again
 #pragma unroll
     for (int t4 = 0; t4 < TS; t4 += 4) {
-      float y[4];
+      float y[4], k[4][S];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss_row_get(k[i], &Cs[wave * TS + t4 + i][q * S]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = t4 + i;
-        float k[S];
-        ss_row_get(k, &Cs[wave * TS + t][q * S]);
         y[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < S; ++j) {
           h[j] = __builtin_fmaf(dec[t][j], h[j], drv[t][j]);
-          y[i] = __builtin_fmaf(k[j], h[j], y[i]);
+          y[i] = __builtin_fmaf(k[i][j], h[j], y[i]);
         }
       }
       // four steps' sums over the states, one step a row of 16 lanes
       float r = ss_fold_rows(y[0], y[1], y[2], y[3]);
       if constexpr (NS == 8) r += ss_dpp<kDppRor8>(r);
       if (NS == 4 || (lane & 15) < CW) ys[wave * TS + t4 + (lane >> 4)][lane & (CW - 1)] = r;
+      __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
     if (live) {
       float o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        o[v] = __builtin_fmaf(skip[v], T::get(xc.e[v]), ys[st][sc + v]);
+        o[v] = __builtin_fmaf(pars[1][sc + v], xc.get(v), ys[st][sc + v]);
         if (gated) {
-          const float z = T::get(zc.e[v]);
-          o[v] *= z * ss_sigmoid(z);
+          const float z = zc.get(v);
+          o[v] *= z * ss_sigmoid<T>(z);
         }
       }
-      ss_store<T, V>(a.y.p, yat + (int64_t)t0 * a.y.st, o);
+      ss_store_at<T, V>(yp, yo, o);
     }
+    yp += ss_rows<T>(a.y, TT);
   }
-  if (s.last && wave == 0) ss_store_state(H, a.hL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+  if (s.last && wave == W - 1) {
+    float H[S];
+    ss_lane_get(H, Hs[turn], lane);
+    ss_store_state(H, a.hL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+  }
 }
 
-// ---- contributions of segments
+// ---- contributions of pieces
 //
-// The state that a segment adds, from zero, and the sum of its steps; a wave
-// takes its channels through the segment alone.  With ckpt it also writes the
+// The state that a piece adds, from zero, and the sum of its steps; a wave
+// takes its channels through the piece alone.  With ckpt it also writes the
 // state and the sum at the start of every tile of the gradient.  Backwards
-// (REV) it is the adjoint state that flows out of the segment's start,
+// (REV) it is the adjoint state that flows out of the piece's start,
 // l = a_t (l + g_t C_t), with g the gradient of y before its gate.
 template <typename T, int S, int NS, bool REV>
 __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a) {
   constexpr int CG = kSsStateGroups, CW = 64 / NS, CC = CG * CW, NP = S * NS, TT = 16;
   constexpr int V = TT * CC / 256, VB = TT * NP / 64 < 8 ? TT * NP / 64 : 8, BT = TT * NP / VB;   // B by BT threads
-  using E = typename T::E;
   __shared__ __align__(16) float2 du[2][TT][CC];
   __shared__ __align__(16) float Bs[2][TT][NP];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -275,22 +314,27 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
   const int st = tid * V / CC, sc = tid * V % CC, bt = tid * VB / NP, bn = tid * VB % NP;
   const bool sok = u.c0 + sc < u.end, bok = tid < BT && bn < a.N, gated = REV && a.z.p;
   const LaView &vx = REV ? a.gy : a.x, &vb = REV ? a.Cm : a.Bm;
-  const int64_t row0 = s.t0;
-  const int64_t xat = s.vb * vx.sb + (row0 + st) * vx.st + u.c0 + sc, dat = s.vb * a.dt.sb + (row0 + st) * a.dt.st + u.c0 + sc;
-  const int64_t zat = s.vb * a.z.sb + (row0 + st) * a.z.st + u.c0 + sc, Bat = s.vb * vb.sb + u.g * vb.sh + (row0 + bt) * vb.st + bn;
+  const uint32_t xo = ss_off<T>(vx, st, sc), dto = ss_off<T>(a.dt, st, sc), zo = ss_off<T>(a.z, st, sc), Bo = ss_off<T>(vb, bt, bn);
   float bias[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) bias[v] = a.bias && sok ? a.bias[u.c0 + sc + v] : 0.0f;
-  SsVec<E, V> xn = {}, dn = {}, zn = {};
-  SsVec<E, VB> Bn = {};
+  SsRaw<T, V> xn = {}, dn = {}, zn = {};
+  SsRaw<T, VB> Bn = {};
   const int tiles = (s.len + TT - 1) / TT;
+  const int t1 = s.t0 + (REV && tiles ? (tiles - 1) * TT : 0), way = REV ? -TT : TT;
+  const char *xp = ss_tile_at<T>(vx, s.vb, t1, u.c0), *dp = ss_tile_at<T>(a.dt, s.vb, t1, u.c0), *zp = ss_tile_at<T>(a.z, s.vb, t1, u.c0);
+  const char* Bp = ss_tile_at<T>(vb, s.vb, t1, u.g * vb.sh);
   auto fetch = [&](int t) {
     if (sok && t + st < s.len) {
-      xn = ss_load<T, V>(vx.p, xat + (int64_t)t * vx.st);
-      dn = ss_load<T, V>(a.dt.p, dat + (int64_t)t * a.dt.st);
-      if (gated) zn = ss_load<T, V>(a.z.p, zat + (int64_t)t * a.z.st);
+      ss_load_at(xn, xp, xo);
+      ss_load_at(dn, dp, dto);
+      if (gated) ss_load_at(zn, zp, zo);
     }
-    if (bok && t + bt < s.len) Bn = ss_load<T, VB>(vb.p, Bat + (int64_t)t * vb.st);
+    if (bok && t + bt < s.len) ss_load_at(Bn, Bp, Bo);
+    xp += ss_rows<T>(vx, way);
+    dp += ss_rows<T>(a.dt, way);
+    zp += ss_rows<T>(a.z, way);
+    Bp += ss_rows<T>(vb, way);
   };
   auto at = [&](int i) { return (REV ? tiles - 1 - i : i) * TT; };
   if (tiles) fetch(at(0));
@@ -302,26 +346,26 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
     const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float raw = T::get(dn.e[v]) + bias[v];
+      const float raw = dn.get(v) + bias[v];
       const float d = !live ? 0.0f : a.softplus ? ss_softplus_of(raw, ss_decay(raw)) : raw;
-      float x = live ? T::get(xn.e[v]) : 0.0f;
-      if (!REV) x = live ? d * x : 0.0f;
+      float x = live ? xn.get(v) : 0.0f;
+      if (!REV) x *= d;
       if (gated && live) {
-        const float z = T::get(zn.e[v]);
-        x *= z * ss_sigmoid(z);
+        const float z = zn.get(v);
+        x *= z * ss_sigmoid<T>(z);
       }
       du[p][st][sc + v] = make_float2(d, x);
     }
     if (tid < BT) {
       SsVec<float, VB> b;
 #pragma unroll
-      for (int v = 0; v < VB; ++v) b.e[v] = blive ? T::get(Bn.e[v]) : 0.0f;
+      for (int v = 0; v < VB; ++v) b.e[v] = blive ? Bn.get(v) : 0.0f;
       *(SsVec<float, VB>*)&Bs[p][bt][bn] = b;
     }
     __syncthreads();
     if (i + 1 < tiles) fetch(at(i + 1));
     if (!REV && a.ckpt && t0 % kSsBwdTile == 0) {
-      const int64_t tile = ss_tile(a, s, u.sid, t0);
+      const int64_t tile = ss_tile(a, s.b, u.sid, s.t0, t0);
       if (wblk < nblk) ss_lane_put(a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), h, lane);
       if (ok && q == 0) a.cum[tile * a.D + ch] = (float)total;
     }
@@ -353,28 +397,37 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 //   g_d = x (l . B) + sum_n A q h_{t-1}                q = a_t l_t
 //   g_A = sum_t d q h_{t-1}
 //
-// Tiles of 32 steps from the segment's end, each from the state at its start
-// (written by the state pass): four waves take eight steps each, forwards and
-// backwards from zero first, then, with what enters at both ends, again on the
-// decays and states in registers.  Two such rows of waves, side by side in
-// the channels, share a workgroup so that half as many partial sums of g_B and g_C are left.
+// Tiles of 32 steps from the run's end, each from the state at its start
+// (the state pass wrote it, from its piece's start): four waves take eight
+// steps each, forwards and backwards from zero first, then, with what enters
+// at both ends, again on the decays and states in registers.
+//
+// Sums over the channels (g_B, g_C) are the part that crosses lanes: for every
+// step and state, over the 16 lanes that hold channels.  A matrix instruction adds the
+// four rows of 16 lanes: v is its 4 x 16 operand, the other one has ones in
+// one of its 16 rows, so that steps and both sums pile up in one accumulator
+// per state, fp32 throughout; what is left, four lanes of a row, is added once a tile.
 template <typename T, int S, int NS>
-__global__ __launch_bounds__(512) void pdssm_selscan_bwd_kernel(const SsArgs a) {
+__global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_selscan_bwd_kernel(const SsArgs a) {
   constexpr int W = kSsTimeWaves, CG = kSsBwdGroups, TS = kSsBwdSteps, TT = W * TS, CW = 64 / NS, CC = CG * CW, NP = S * NS;
-  constexpr int V = TT * CC / 512;
-  constexpr int VB = TT * NP / 256 < 1 ? 1 : TT * NP / 256;   // B by the first four waves, C by the others
-  using E = typename T::E;
-  __shared__ __align__(16) float4 pre[TT][CC];     // d, d x, g
+  constexpr int NT = 256 * CG, V = TT * CC / NT;
+  constexpr int BT = NT / 2, VB = TT * NP / BT < 8 ? TT * NP / BT : 8, BR = TT * NP / BT / VB;   // B by one half of the threads, C by the other
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  static_assert(TS == 8, "rows of an accumulator: eight steps of g_B, eight of g_C");
+  __shared__ __align__(16) float4 pre[TT][CC];     // d, d x, g, slope of d
+  __shared__ __align__(16) float gzs[TT][CC];      // slope of the gate times g_y
   __shared__ __align__(16) float Bs[TT][NP], Cs[TT][NP];
   __shared__ __align__(16) float outs[3][TT][CC];  // C . h, l . B, sum A q h
-  __shared__ __align__(16) float gBs[CG][TT][NP], gCs[CG][TT][NP];
+  __shared__ __align__(16) float gs[2][CG][TT][NP];   // g_B, g_C
   __shared__ __align__(16) float Es[CG * W][S * 64], Ps[CG * W][S * 64], Rs[CG * W][S * 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = (tid >> 6) % W, cg = (tid >> 6) / W;
+  __shared__ __align__(16) float Rt[2][CG][S * 64];   // the adjoint state that enters a tile, from its end
+  __shared__ __align__(16) float pars[2][CC];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6) % W, cg = __builtin_amdgcn_readfirstlane(tid >> 6) / W;
   if (ss_block(a.row) == 0 && tid < 2) a.header[tid] = 0;
   SsUnit u;
   if (!ss_unit(a, CC, u)) return;
   SsSeg s;
-  const int c = lane / NS, q = lane % NS, ch = u.c0 + cg * CW + c;
+  const int c = lane / NS, q = lane % NS, lc = cg * CW + c, ch = u.c0 + lc;
   const bool ok = ch < u.end;
   const bool found = ss_segment(a.s, u.sid, s);
   if (!found || s.len <= 0) {   // no rows: nothing but sums of none and what passes through
@@ -390,204 +443,230 @@ __global__ __launch_bounds__(512) void pdssm_selscan_bwd_kernel(const SsArgs a) 
     }
     return;
   }
-  float A2[S], An[S], R[S], H0[S], gA[S];
+  const int piece0 = ss_piece(a, s, u.sid);
+  float A2[S], gA[S];
   ss_load_A(A2, a.A, ch, q * S, a.N, ok);
-  ss_load_state(An, a.A, ch, q * S, a.N, ok);
-  if (s.last)
-    ss_load_state(R, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
-  else
-    ss_load_state(R, a.adj, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
-  if (s.first)
-    ss_load_state(H0, a.h0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
-  else
-    ss_load_state(H0, a.seg, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
-  const bool enters = !s.first || a.h0;
+  if (wave == 0) {
+    float R[S];
+    if (s.last)
+      ss_load_state(R, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+    else
+      ss_load_state(R, a.adj, (int64_t)(piece0 + (s.len - 1) / a.piece) * a.D + ch, q * S, a.N, ok);
+    ss_lane_put(Rt[0][cg], R, lane);
+  }
 #pragma unroll
   for (int j = 0; j < S; ++j) gA[j] = 0.0f;
 
   const int st = tid * V / CC, sc = tid * V % CC;
-  const int btid = tid & 255, bt = btid * VB / NP, bn = btid * VB % NP;
-  const bool second = tid >= 256, sok = u.c0 + sc < u.end, bok = bt < TT && bn < a.N, gated = a.z.p != nullptr;
+  const bool second = tid >= BT, sok = u.c0 + sc < u.end, gated = a.z.p != nullptr;
+  const int bt = tid % BT * VB / NP, bn = tid % BT * VB % NP;   // and rows BT VB / NP further on
+  const bool bok = bn < a.N;
   const LaView& vbc = second ? a.Cm : a.Bm;
-  const int64_t row0 = s.t0, r = row0 + st, cc = u.c0 + sc;
-  const int64_t xat = s.vb * a.x.sb + r * a.x.st + cc, dat = s.vb * a.dt.sb + r * a.dt.st + cc, zat = s.vb * a.z.sb + r * a.z.st + cc;
-  const int64_t gat = s.vb * a.gy.sb + r * a.gy.st + cc;
-  const int64_t gxat = s.vb * a.gx.sb + r * a.gx.st + cc, gdat = s.vb * a.gdt.sb + r * a.gdt.st + cc, gzat = s.vb * a.gz.sb + r * a.gz.st + cc;
-  const int64_t Bat = s.vb * vbc.sb + u.g * vbc.sh + (row0 + bt) * vbc.st + bn;
-  float bias[V], skip[V], gD[V], gb[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    bias[v] = a.bias && sok ? a.bias[cc + v] : 0.0f;
-    skip[v] = a.skip && sok ? a.skip[cc + v] : 0.0f;
-    gD[v] = gb[v] = 0.0f;
+  const uint32_t xo = ss_off<T>(a.x, st, sc), dto = ss_off<T>(a.dt, st, sc), zo = ss_off<T>(a.z, st, sc), go = ss_off<T>(a.gy, st, sc);
+  const uint32_t gxo = ss_off<T>(a.gx, st, sc), gdo = ss_off<T>(a.gdt, st, sc), gzo = ss_off<T>(a.gz, st, sc);
+  constexpr int BS = BT * VB / NP;
+  const uint32_t Bo = ss_off<T>(vbc, bt, bn);
+  if (tid < CC) {
+    const int k = u.c0 + tid;
+    pars[0][tid] = a.bias && k < u.end ? a.bias[k] : 0.0f;
+    pars[1][tid] = a.skip && k < u.end ? a.skip[k] : 0.0f;
   }
-  const int wblk = u.c0 % (a.D / a.G) / CW + cg, nblk = (a.D / a.G + CW - 1) / CW;
-  SsVec<E, V> xn = {}, dn = {}, zn = {}, gn = {};
-  SsVec<E, VB> Bn = {};
-  float hn[S], cumn = 0.0f;
-  auto fetch = [&](int t) {
-    if (sok && t + st < s.len) {
-      xn = ss_load<T, V>(a.x.p, xat + (int64_t)t * a.x.st);
-      dn = ss_load<T, V>(a.dt.p, dat + (int64_t)t * a.dt.st);
-      gn = ss_load<T, V>(a.gy.p, gat + (int64_t)t * a.gy.st);
-      if (gated) zn = ss_load<T, V>(a.z.p, zat + (int64_t)t * a.z.st);
-    }
-    if (bok && t + bt < s.len) Bn = ss_load<T, VB>(vbc.p, Bat + (int64_t)t * vbc.st);
-    const int64_t tile = ss_tile(a, s, u.sid, t);
-    if (wblk < nblk) ss_lane_get(hn, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), lane);
-    cumn = ok ? a.cum[tile * a.D + ch] : 0.0f;
-  };
+  __syncthreads();
+  float gD[V], gb[V];
 #pragma unroll
-  for (int j = 0; j < S; ++j) hn[j] = 0.0f;
-  const int last = (s.len - 1) / TT * TT;
+  for (int v = 0; v < V; ++v) gD[v] = gb[v] = 0.0f;
+  const int wblk = u.c0 % (a.D / a.G) / CW + cg, nblk = (a.D / a.G + CW - 1) / CW;
+  SsRaw<T, V> xn = {}, dn = {}, zn = {}, gn = {};
+  SsRaw<T, VB> Bn[BR] = {};
+  const int last = (s.len - 1) / TT * TT, t1 = s.t0 + last;
+  const char *xp = ss_tile_at<T>(a.x, s.vb, t1, u.c0), *dp = ss_tile_at<T>(a.dt, s.vb, t1, u.c0), *zp = ss_tile_at<T>(a.z, s.vb, t1, u.c0);
+  const char *gp = ss_tile_at<T>(a.gy, s.vb, t1, u.c0), *Bp = ss_tile_at<T>(vbc, s.vb, t1, u.g * vbc.sh);
+  char *gxp = ss_tile_at<T>(a.gx, s.vb, t1, u.c0), *gdp = ss_tile_at<T>(a.gdt, s.vb, t1, u.c0), *gzp = ss_tile_at<T>(a.gz, s.vb, t1, u.c0);
+  auto fetch = [&](int t) {   // and the pointers back to the tile before it
+    if (sok && t + st < s.len) {
+      ss_load_at(xn, xp, xo);
+      ss_load_at(dn, dp, dto);
+      ss_load_at(gn, gp, go);
+      if (gated) ss_load_at(zn, zp, zo);
+    }
+#pragma unroll
+    for (int i = 0; i < BR; ++i)
+      if (bok && t + bt + i * BS < s.len) ss_load_at(Bn[i], Bp + ss_rows<T>(vbc, i * BS), Bo);
+    xp -= ss_rows<T>(a.x, TT);
+    dp -= ss_rows<T>(a.dt, TT);
+    gp -= ss_rows<T>(a.gy, TT);
+    zp -= ss_rows<T>(a.z, TT);
+    Bp -= ss_rows<T>(vbc, TT);
+  };
+  int pc = (s.len - 1) / a.piece, turn = 0;   // piece of the tile
   fetch(last);
-  for (int t0 = last; t0 >= 0; t0 -= TT) {
-    const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
-    float x[V], d[V], g[V], sg[V], gz[V];   // input, step, gradient behind the gate, slope of the step, of the gate
+  for (int t0 = last; t0 >= 0; t0 -= TT, turn ^= 1) {
+    const bool live = sok && t0 + st < s.len;
+    const SsRaw<T, V> xc = xn;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float raw = T::get(dn.e[v]) + bias[v], e = ss_decay(raw);
-      x[v] = live ? T::get(xn.e[v]) : 0.0f;
-      d[v] = !live ? 0.0f : a.softplus ? ss_softplus_of(raw, e) : raw;
-      sg[v] = a.softplus ? ss_sigmoid_of(raw, e) : 1.0f;
-      g[v] = live ? T::get(gn.e[v]) : 0.0f;
-      gz[v] = 0.0f;
-      if (gated && live) {
-        const float z = T::get(zn.e[v]), k = ss_sigmoid(z);
-        gz[v] = g[v] * k * __builtin_fmaf(z, 1.0f - k, 1.0f);
-        g[v] *= z * k;
+      const float raw = dn.get(v) + pars[0][sc + v], e = ss_decay(raw);
+      const float d = !live ? 0.0f : a.softplus ? ss_softplus_of(raw, e) : raw;
+      float g = live ? gn.get(v) : 0.0f;
+      if (gated) {
+        const float z = zn.get(v), k = ss_sigmoid<T>(z);
+        gzs[st][sc + v] = g * k * __builtin_fmaf(z, 1.0f - k, 1.0f);
+        g *= z * k;
       }
-      pre[st][sc + v] = make_float4(d[v], d[v] * x[v], g[v], 0.0f);
+      pre[st][sc + v] = make_float4(d, d * xc.get(v), g, a.softplus ? ss_sigmoid_of(raw, e) : 1.0f);
     }
-    if (bt < TT) {
+#pragma unroll
+    for (int i = 0; i < BR; ++i) {
+      const int t = bt + i * BS;
+      const bool blive = bok && t0 + t < s.len;
       SsVec<float, VB> b;
 #pragma unroll
-      for (int v = 0; v < VB; ++v) b.e[v] = blive ? T::get(Bn.e[v]) : 0.0f;
-      *(SsVec<float, VB>*)(second ? &Cs[bt][bn] : &Bs[bt][bn]) = b;
+      for (int v = 0; v < VB; ++v) b.e[v] = blive ? Bn[i].get(v) : 0.0f;
+      *(SsVec<float, VB>*)(second ? &Cs[t][bn] : &Bs[t][bn]) = b;
     }
-    float H[S];
-#pragma unroll
-    for (int j = 0; j < S; ++j) H[j] = enters ? __builtin_fmaf(ss_exp2(cumn * A2[j]), H0[j], hn[j]) : hn[j];
     __syncthreads();
     if (t0) fetch(t0 - TT);
+    // the state at the tile's start: what it was from its piece's start, and what entered there
+    if (t0 < pc * a.piece) --pc;
+    const int64_t tile = ss_tile(a, s.b, piece0 + pc, s.t0 + pc * a.piece, t0 - pc * a.piece);
+    float hin[S] = {}, H0[S];
+    if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), lane);
+    const float cum = ok ? a.cum[tile * a.D + ch] : 0.0f;
+    ss_load_state(H0, a.seg ? a.seg : a.h0, (int64_t)(a.seg ? piece0 + pc : s.b) * a.D + ch, q * S, a.N, ok);
 
     // from zero, forwards and backwards
-    const int me = cg * W + wave, tw = wave * TS, lc = cg * CW + c;
+    const int me = cg * W + wave, tw = wave * TS;
     float dec[TS][S], hs[TS][S], h[S], l[S], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < S; ++j) h[j] = l[j] = 0.0f;
 #pragma unroll
-    for (int t = 0; t < TS; ++t) {
-      const float4 w = pre[tw + t][lc];
-      float b[S];
-      ss_row_get(b, &Bs[tw + t][q * S]);
-      sum += w.x;
+    for (int t4 = 0; t4 < TS; t4 += 4) {
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        dec[t][j] = ss_exp2(w.x * A2[j]);
-        hs[t][j] = w.y * b[j];
-        h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
+      for (int i = 0; i < 4; ++i) {
+        const int t = t4 + i;
+        const float4 w = pre[tw + t][lc];
+        float b[S];
+        ss_row_get(b, &Bs[tw + t][q * S]);
+        sum += w.x;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          dec[t][j] = ss_exp2(w.x * A2[j]);
+          hs[t][j] = w.y * b[j];
+          h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
     ss_lane_put(Es[me], h, lane);
 #pragma unroll
     for (int j = 0; j < S; ++j) h[j] = ss_exp2(sum * A2[j]);
     ss_lane_put(Ps[me], h, lane);
 #pragma unroll
-    for (int t = TS - 1; t >= 0; --t) {
-      const float g1 = pre[tw + t][lc].z;
-      float k[S];
-      ss_row_get(k, &Cs[tw + t][q * S]);
+    for (int t4 = TS - 4; t4 >= 0; t4 -= 4) {
 #pragma unroll
-      for (int j = 0; j < S; ++j) l[j] = dec[t][j] * __builtin_fmaf(g1, k[j], l[j]);
+      for (int i = 3; i >= 0; --i) {
+        const int t = t4 + i;
+        const float g1 = pre[tw + t][lc].z;
+        float k[S];
+        ss_row_get(k, &Cs[tw + t][q * S]);
+#pragma unroll
+        for (int j = 0; j < S; ++j) l[j] = dec[t][j] * __builtin_fmaf(g1, k[j], l[j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     ss_lane_put(Rs[me], l, lane);
     __syncthreads();
-    // what enters at both ends of this wave's steps, and at the tile's start
+    // what enters at both ends of this wave's steps; the first wave's adjoint leaves the tile then
 #pragma unroll
-    for (int j = 0; j < S; ++j) h[j] = H[j];
+    for (int j = 0; j < S; ++j) hin[j] = __builtin_fmaf(ss_exp2(cum * A2[j]), H0[j], hin[j]);
 #pragma unroll
     for (int v = 0; v < W - 1; ++v) {
-      float e[S], p[S];
-      ss_lane_get(e, Es[cg * W + v], lane);
-      ss_lane_get(p, Ps[cg * W + v], lane);
+      if (v < wave) {
+        float e[S], p[S];
+        ss_lane_get(e, Es[cg * W + v], lane);
+        ss_lane_get(p, Ps[cg * W + v], lane);
 #pragma unroll
-      for (int j = 0; j < S; ++j)
-        if (v < wave) h[j] = __builtin_fmaf(p[j], h[j], e[j]);
-    }
-#pragma unroll
-    for (int v = W - 1; v >= 0; --v) {
-      float e[S], p[S];
-      ss_lane_get(e, Rs[cg * W + v], lane);
-      ss_lane_get(p, Ps[cg * W + v], lane);
-#pragma unroll
-      for (int j = 0; j < S; ++j) {
-        if (v == wave) l[j] = R[j];
-        R[j] = __builtin_fmaf(p[j], R[j], e[j]);
+        for (int j = 0; j < S; ++j) hin[j] = __builtin_fmaf(p[j], hin[j], e[j]);
       }
     }
-    float hin[S];
+    {
+      float r[S], p[S];   // own contribution and decay, for the first wave
 #pragma unroll
-    for (int j = 0; j < S; ++j) hin[j] = h[j];
+      for (int j = 0; j < S; ++j) {
+        r[j] = l[j];
+        p[j] = h[j];
+      }
+      ss_lane_get(l, Rt[turn][cg], lane);
+#pragma unroll
+      for (int v = W - 1; v > 0; --v) {
+        if (v > wave) {
+          float e[S], f[S];
+          ss_lane_get(e, Rs[cg * W + v], lane);
+          ss_lane_get(f, Ps[cg * W + v], lane);
+#pragma unroll
+          for (int j = 0; j < S; ++j) l[j] = __builtin_fmaf(f[j], l[j], e[j]);
+        }
+      }
+      if (wave == 0) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) r[j] = __builtin_fmaf(p[j], l[j], r[j]);
+        ss_lane_put(Rt[turn ^ 1][cg], r, lane);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < S; ++j) h[j] = hin[j];
 #pragma unroll
     for (int t = 0; t < TS; ++t)
 #pragma unroll
       for (int j = 0; j < S; ++j) hs[t][j] = h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
+    f4 acc[S] = {};   // rows 0 .. 7: steps of g_B, 8 .. 15: of g_C
+    float row = (lane & 15) == TS - 1 ? 1.0f : 0.0f;   // ones in row t
 #pragma unroll
-    for (int t4 = TS - 4; t4 >= 0; t4 -= 4) {
-      float vB[4][S], vC[4][S];
-#pragma unroll
-      for (int i = 3; i >= 0; --i) {
-        const int t = t4 + i;
-        const float4 w = pre[tw + t][lc];
-        float b[S], k[S], y = 0.0f, lb = 0.0f, pa = 0.0f;
-        ss_row_get(b, &Bs[tw + t][q * S]);
-        ss_row_get(k, &Cs[tw + t][q * S]);
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          l[j] = __builtin_fmaf(w.z, k[j], l[j]);
-          vB[i][j] = w.y * l[j];
-          vC[i][j] = w.z * hs[t][j];
-          y = __builtin_fmaf(k[j], hs[t][j], y);
-          lb = __builtin_fmaf(b[j], l[j], lb);
-          l[j] *= dec[t][j];
-          const float p = l[j] * (t ? hs[t ? t - 1 : 0][j] : hin[j]);
-          pa = __builtin_fmaf(An[j], p, pa);
-          gA[j] = __builtin_fmaf(w.x, p, gA[j]);
-        }
-        // over the states: lanes next to each other
-        y += ss_dpp<kDppXor1>(y);
-        lb += ss_dpp<kDppXor1>(lb);
-        pa += ss_dpp<kDppXor1>(pa);
-        y += ss_dpp<kDppXor2>(y);
-        lb += ss_dpp<kDppXor2>(lb);
-        pa += ss_dpp<kDppXor2>(pa);
-        if constexpr (NS == 8) {
-          y += ss_dpp<kDppHalfMirror>(y);
-          lb += ss_dpp<kDppHalfMirror>(lb);
-          pa += ss_dpp<kDppHalfMirror>(pa);
-        }
-        if (q < 3) outs[q][tw + t][lc] = q == 0 ? y : q == 1 ? lb : pa;
-      }
-      // over the channels: four steps' sums, one step a row of 16 lanes
-      float rB[S], rC[S];
+    for (int t = TS - 1; t >= 0; --t) {
+      const float4 w = pre[tw + t][lc];
+      const float rowC = ss_dpp<kDppRor8>(row);
+      float b[S], k[S], y = 0.0f, lb = 0.0f, pa = 0.0f;
+      ss_row_get(b, &Bs[tw + t][q * S]);
+      ss_row_get(k, &Cs[tw + t][q * S]);
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        rB[j] = ss_fold_rows(vB[0][j], vB[1][j], vB[2][j], vB[3][j]);
-        rC[j] = ss_fold_rows(vC[0][j], vC[1][j], vC[2][j], vC[3][j]);
-        rB[j] += ss_dpp<kDppRor8>(rB[j]);
-        rC[j] += ss_dpp<kDppRor8>(rC[j]);
-        if constexpr (NS == 4) {
-          rB[j] += ss_dpp<kDppRor4>(rB[j]);
-          rC[j] += ss_dpp<kDppRor4>(rC[j]);
-        }
+        l[j] = __builtin_fmaf(w.z, k[j], l[j]);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(row, w.y * l[j], acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(rowC, w.z * hs[t][j], acc[j], 0, 0, 0);
+        y = __builtin_fmaf(k[j], hs[t][j], y);
+        lb = __builtin_fmaf(b[j], l[j], lb);
+        l[j] *= dec[t][j];
+        const float p = l[j] * (t ? hs[t ? t - 1 : 0][j] : hin[j]);
+        pa = __builtin_fmaf(A2[j], p, pa);
+        gA[j] = __builtin_fmaf(w.x, p, gA[j]);
       }
-      if ((lane & 15) < NS) {
+      row = ss_dpp<kDppShl1>(row);
+      // over the states, lanes next to each other: the sum of y ends in lane 0 of four, of lb in 1, of pa in 2
+      const bool odd = q & 1, high = q & 2;
+      const float r1 = (odd ? lb : y) + ss_dpp<kDppXor1>(odd ? y : lb);
+      const float r2 = pa + ss_dpp<kDppXor1>(pa);
+      float r = (high ? r2 : r1) + ss_dpp<kDppXor2>(high ? r1 : r2);
+      if constexpr (NS == 8) r += ss_dpp<kDppShl4>(r);
+      if (q < 3) outs[q][tw + t][lc] = r;
+      if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+    }
+    // over the channels of a row of 16 lanes
 #pragma unroll
-        for (int j = 0; j < S; ++j) {
-          gBs[cg][tw + t4 + (lane >> 4)][q * S + j] = rB[j];
-          gCs[cg][tw + t4 + (lane >> 4)][q * S + j] = rC[j];
-        }
+    for (int i = 0; i < 4; ++i) {
+      SsVec<float, S < 4 ? S : 4> o[S < 4 ? 1 : S / 4];
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        float r = acc[j][i];
+        r += ss_dpp<kDppRor8>(r);
+        if constexpr (NS == 4) r += ss_dpp<kDppRor4>(r);
+        o[j / 4].e[j % 4] = r;
+      }
+      const int at = (lane >> 4) * 4 + i;   // row of the accumulator
+      if ((lane & 15) < NS) {
+        float* to = &gs[at >> 3][cg][tw + (at & 7)][q * S];
+#pragma unroll
+        for (int j = 0; j < S; j += S < 4 ? S : 4) *(SsVec<float, S < 4 ? S : 4>*)(to + j) = o[j / 4];
       }
     }
     __syncthreads();
@@ -595,34 +674,47 @@ __global__ __launch_bounds__(512) void pdssm_selscan_bwd_kernel(const SsArgs a) 
       float ox[V], od[V], oz[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float y = outs[0][st][sc + v], lb = outs[1][st][sc + v], pa = outs[2][st][sc + v];
-        ox[v] = __builtin_fmaf(d[v], lb, g[v] * skip[v]);
-        od[v] = __builtin_fmaf(x[v], lb, pa) * sg[v];
-        oz[v] = gz[v] * __builtin_fmaf(skip[v], x[v], y);
-        gD[v] = __builtin_fmaf(g[v], x[v], gD[v]);
+        const float4 w = pre[st][sc + v];
+        const float y = outs[0][st][sc + v], lb = outs[1][st][sc + v], pa = kLn2 * outs[2][st][sc + v];
+        const float x = xc.get(v), skip = pars[1][sc + v];
+        ox[v] = __builtin_fmaf(w.x, lb, w.z * skip);
+        od[v] = __builtin_fmaf(x, lb, pa) * w.w;
+        oz[v] = gated ? gzs[st][sc + v] * __builtin_fmaf(skip, x, y) : 0.0f;
+        gD[v] = __builtin_fmaf(w.z, x, gD[v]);
         gb[v] += od[v];
       }
-      ss_store<T, V>(a.gx.p, gxat + (int64_t)t0 * a.gx.st, ox);
-      ss_store<T, V>(a.gdt.p, gdat + (int64_t)t0 * a.gdt.st, od);
-      if (gated) ss_store<T, V>(a.gz.p, gzat + (int64_t)t0 * a.gz.st, oz);
+      ss_store_at<T, V>(gxp, gxo, ox);
+      ss_store_at<T, V>(gdp, gdo, od);
+      if (gated) ss_store_at<T, V>(gzp, gzo, oz);
     }
+    gxp -= ss_rows<T>(a.gx, TT);
+    gdp -= ss_rows<T>(a.gdt, TT);
+    gzp -= ss_rows<T>(a.gz, TT);
     // this workgroup's part of g_B (first half of the threads) and g_C
-    if (bt < TT && bn < a.N && t0 + bt < s.len) {
-      const float(*src)[TT][NP] = second ? gCs : gBs;
+#pragma unroll
+    for (int i = 0; i < BR; ++i) {
+      const int t = bt + i * BS;
+      if (!bok || t0 + t >= s.len) continue;
       const int nb = a.G * ((a.D / a.G + CC - 1) / CC);
-      const int64_t row = s.vb * a.s.L + s.t0 + t0 + bt;
-      float* o = a.part + ((((int64_t)(second ? nb : 0) + u.block) * a.rows) + row) * a.N + bn;
+      const int64_t r = s.vb * a.s.L + s.t0 + t0 + t;
+      float* o = a.part + ((((int64_t)(second ? nb : 0) + u.block) * a.rows) + r) * a.N + bn;
       SsVec<float, VB> v;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) v.e[j] = src[0][bt][bn + j] + src[1][bt][bn + j];
+      for (int j = 0; j < VB; ++j) {
+        v.e[j] = gs[second][0][t][bn + j];
+        if constexpr (CG == 2) v.e[j] += gs[second][CG - 1][t][bn + j];
+      }
       *(SsVec<float, VB>*)o = v;
     }
   }
-  if (s.first && wave == 0 && a.gh0) ss_store_state(R, a.gh0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+  if (s.first && wave == 0 && a.gh0) {
+    float R[S];
+    ss_lane_get(R, Rt[turn][cg], lane);
+    ss_store_state(R, a.gh0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+  }
   // sums over this workgroup's steps: the four waves', then the staging threads' of every channel
   __syncthreads();
-  const int me = cg * W + wave;
-  ss_lane_put(Es[me], gA, lane);
+  ss_lane_put(Es[cg * W + wave], gA, lane);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     outs[0][st][sc + v] = gD[v];
@@ -640,7 +732,7 @@ __global__ __launch_bounds__(512) void pdssm_selscan_bwd_kernel(const SsArgs a) 
     ss_store_state(sumA, a.partA, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
     if (ok && q < 2) {
       float o = 0.0f;
-      for (int t = 0; t < TT; ++t) o += outs[q][t][cg * CW + c];
+      for (int t = 0; t < TT; ++t) o += outs[q][t][lc];
       a.partD[((int64_t)u.sid * 2 + q) * a.D + ch] = o;
     }
   }
@@ -710,7 +802,7 @@ __global__ __launch_bounds__(256) void pdssm_selscan_step_kernel(const SsStepArg
     y = __builtin_fmaf(a.skip ? a.skip[ch] : 0.0f, x, y);
     if (a.z.p) {
       const float z = T::get(((const typename T::E*)a.z.p)[(int64_t)b * a.z.sb + ch]);
-      y *= z * ss_sigmoid(z);
+      y *= z * ss_sigmoid<T>(z);
     }
     ss_store<T, 1>(a.y.p, (int64_t)b * a.y.sb + ch, &y);
   }

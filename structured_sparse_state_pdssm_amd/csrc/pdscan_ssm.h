@@ -56,38 +56,88 @@ __device__ __forceinline__ void ss_store(void* p, int64_t at, const float* x) {
   *(SsVec<typename T::E, V>*)((typename T::E*)p + at) = o;
 }
 
+// V neighbouring elements on their way, as the words that they come in: what
+// unpacks them stays behind the wait for them.
+template <typename T, int V>
+struct SsRaw {
+  static constexpr int kBytes = V * (int)sizeof(typename T::E), kWords = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(typename T::E) == 4) return __builtin_bit_cast(float, w[i]);
+    return __builtin_bit_cast(float, i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+// Addressed by one uniform pointer, which walks with the tiles, and this
+// lane's 32 bits of offset (kept from being added up ahead of the loop: half the
+// registers of a pointer a lane).
+template <typename T, int V>
+__device__ __forceinline__ void ss_load_at(SsRaw<T, V>& r, const char* tile, uint32_t off) {
+  asm("" : "+v"(off));
+  if constexpr (SsRaw<T, V>::kBytes == 2) {
+    r.w[0] = *(const uint16_t*)(tile + off);
+  } else {
+    using Q = SsVec<uint32_t, SsRaw<T, V>::kWords>;
+    const Q q = *(const Q*)(tile + off);
+#pragma unroll
+    for (int i = 0; i < SsRaw<T, V>::kWords; ++i) r.w[i] = q.e[i];
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void ss_store_at(char* tile, uint32_t off, const float* x) {
+  asm("" : "+v"(off));
+  SsVec<typename T::E, V> o;
+  T::template put<V>(o, x);
+  *(SsVec<typename T::E, V>*)(tile + off) = o;
+}
+template <typename T>
+__device__ __forceinline__ char* ss_tile_at(const LaView& v, int64_t vb, int64_t row, int64_t c) {
+  return (char*)v.p + (vb * v.sb + row * v.st + c) * (int64_t)sizeof(typename T::E);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t ss_off(const LaView& v, int row, int c) {
+  return ((uint32_t)row * (uint32_t)v.st + (uint32_t)c) * (uint32_t)sizeof(typename T::E);
+}
+// Bytes of `rows` rows.
+template <typename T>
+__device__ __forceinline__ int64_t ss_rows(const LaView& v, int rows) {
+  return v.st * rows * (int64_t)sizeof(typename T::E);
+}
+
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float ss_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// e^-|x|, with what the product by log2 e lost put back (two steps of fp32
-// instead of |x| of them).
+// e^-|x|, with what the product by log2 e lost put back (a step of fp32 or
+// two, instead of |x| of them).
 __device__ __forceinline__ float ss_decay(float x) {
-  constexpr float kLo = 1.925963033500011e-08f;   // log2 e behind its fp32 value
-  const float n = -fabsf(x), t = kLog2e * n;
-  const float r = __builtin_fmaf(n, kLo, __builtin_fmaf(n, kLog2e, -t)), e = ss_exp2(t);
-  return __builtin_fmaf(e * kLn2, r, e);
+  const float n = -fabsf(x), t = kLog2e * n, e = ss_exp2(t);
+  return __builtin_fmaf(e, kLn2 * __builtin_fmaf(n, kLog2e, -t), e);
 }
 // 1 / (1 + e^-x) from e = e^-|x|.
 __device__ __forceinline__ float ss_sigmoid_of(float x, float e) {
   return (x >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
 }
-__device__ __forceinline__ float ss_sigmoid(float x) { return ss_sigmoid_of(x, ss_decay(x)); }
+// The gate's: bf16 takes the short way, off by |x| steps of fp32 at most (x = -20: 2^-20).
+template <typename T>
+__device__ __forceinline__ float ss_sigmoid(float x) {
+  if constexpr (sizeof(typename T::E) == 2) return __builtin_amdgcn_rcpf(1.0f + ss_exp2(-kLog2e * x));
+  return ss_sigmoid_of(x, ss_decay(x));
+}
 
-// log(1 + e^x) = max(x, 0) + log1p(e) with e = e^-|x|, the latter as
-// log(w) e / (w - 1) with w = 1 + e rounded (Kahan's form: the rounding of w
-// cancels), so that small steps keep their digits.
+// log(1 + e^x) = max(x, 0) + log1p(e) with e = e^-|x|.  log1p(e) is log(w),
+// w = 1 + e rounded, and what the rounding dropped, e - (w - 1): small steps keep
+// their digits (dividing that by w would change less than 2^-24 of e).
 __device__ __forceinline__ float ss_softplus_of(float x, float e) {
   const float w = 1.0f + e;
-  const float l = kLn2 * __builtin_amdgcn_logf(w) * e * __builtin_amdgcn_rcpf(w - 1.0f);
-  return (x > 0.0f ? x : 0.0f) + (w == 1.0f ? e : l);
+  return fmaxf(x, 0.0f) + __builtin_fmaf(kLn2, __builtin_amdgcn_logf(w), e - (w - 1.0f));
 }
 
 template <int CTRL>
 __device__ __forceinline__ float ss_dpp(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
-constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppRor4 = 0x124, kDppRor8 = 0x128;
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppRor4 = 0x124, kDppRor8 = 0x128,
+              kDppShl1 = 0x101, kDppShl4 = 0x104;
 
 // Sums over the lanes 32 apart of a (lower half of the result) and of b (upper
 // half): the instruction exchanges a's upper half and b's lower one.  By hand,
@@ -137,18 +187,19 @@ struct SsSeg {
 };
 
 __device__ __forceinline__ bool ss_segment(const SsSegs& g, int sid, SsSeg& s) {
+  auto one = [](int x) { return __builtin_amdgcn_readfirstlane(x); };   // (the same in every lane)
   if (g.table) {
     const int4 e = *(const int4*)(g.table + 4 * (int64_t)sid);
-    if (e.z < 0) return false;
-    s.b = e.x;
-    s.t0 = e.y;
-    s.len = e.z;
-    s.first = e.w & 1;
-    s.last = e.w >> 1;
+    if (one(e.z) < 0) return false;
+    s.b = one(e.x);
+    s.t0 = one(e.y);
+    s.len = one(e.z);
+    s.first = one(e.w) & 1;
+    s.last = one(e.w) >> 1;
     s.vb = 0;
   } else if (g.cu) {
     s.b = sid;
-    int t0 = g.cu[sid], t1 = g.cu[sid + 1];
+    int t0 = one(g.cu[sid]), t1 = one(g.cu[sid + 1]);
     t0 = t0 < 0 ? 0 : t0 > g.L ? g.L : t0;
     t1 = t1 < t0 ? t0 : t1 > g.L ? g.L : t1;
     s.t0 = t0;

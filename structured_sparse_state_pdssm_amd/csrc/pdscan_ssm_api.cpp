@@ -153,36 +153,45 @@ int check_scan(const pdssm_selscan_dims* d, bool step) {
 // Workgroups of the widest launch over so many segments: channel blocks of the fewest channels.
 int scan_grid(const pdssm_selscan_dims* d, const SsSplit& s) {
   const int64_t blocks = (int64_t)d->G * pdscan::ss_blocks(d->D / d->G, pdscan::ss_channels(d->N));
-  if (s.segs * blocks > kMost / 2 || (int64_t)d->B * (((int64_t)d->D * d->N + 1023) / 1024) > kMost)
-    return set_error(PDSSM_EUNSUPPORTED, "too many segments and channels (%d, %d)", s.segs, d->D);
+  if (s.pieces * blocks > kMost / 2 || (int64_t)d->B * (((int64_t)d->D * d->N + 1023) / 1024) > kMost)
+    return set_error(PDSSM_EUNSUPPORTED, "too many pieces and channels (%d, %d)", s.pieces, d->D);
   return PDSSM_OK;
 }
 
 struct ScanWs {
   SsSplit split;
-  size_t table, starts, seg, adj, sum, ckpt, cum, part, partA, partD, mid, total;
+  size_t table, pieces, run_table, runs, seg, adj, sum, ckpt, cum, part, partA, partD, mid, total;
   int blocks;                          // (gradient) channel blocks of a group
 };
 
-void put_segments(ScanWs& w, Layout& l, const pdssm_selscan_dims* d, bool adj) {
-  const size_t state = (size_t)w.split.segs * d->D * d->N * 4;
-  w.table = w.starts = w.seg = w.adj = w.sum = l.at;
-  if (!w.split.split) return;
+// Tables of packed sequences, contributions of pieces and their sums.
+void put_pieces(ScanWs& w, Layout& l, const pdssm_selscan_dims* d, bool bwd) {
+  const SsSplit& p = w.split;
+  const size_t state = (size_t)p.pieces * d->D * d->N * 4;
+  w.table = w.pieces = w.run_table = w.runs = w.seg = w.adj = w.sum = l.at;
+  if (!p.states) return;
   if (d->packed) {
-    w.table = l.put((size_t)w.split.segs * 16);
-    w.starts = l.put(((size_t)d->B + 1) * 4);
+    w.table = l.put((size_t)p.pieces * 16);
+    w.pieces = l.put(((size_t)d->B + 1) * 4);
+    if (p.cut) {
+      w.run_table = l.put((size_t)p.segs * 16);
+      w.runs = l.put(((size_t)d->B + 1) * 4);
+    }
   }
   w.seg = l.put(state);
-  if (adj) w.adj = l.put(state);
-  w.sum = l.put((size_t)w.split.segs * d->D * 4);
+  if (bwd && p.cut) w.adj = l.put(state);
+  w.sum = l.put((size_t)p.pieces * d->D * 4);
+}
+
+int64_t scan_blocks(const pdssm_selscan_dims* d, int groups) {
+  return (int64_t)d->G * pdscan::ss_blocks(d->D / d->G, pdscan::ss_channels(d->N) * groups);
 }
 
 ScanWs scan_ws(const pdssm_selscan_dims* d) {
   ScanWs w = {};
-  const int64_t blocks = (int64_t)d->G * pdscan::ss_blocks(d->D / d->G, pdscan::ss_channels(d->N));
-  w.split = pdscan::ss_split(d->B, d->L, d->packed, blocks, 2 * kCus, 256, 64);
+  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, 1), 3 * kCus, scan_blocks(d, pdscan::kSsStateGroups), false);
   Layout l;
-  put_segments(w, l, d, false);
+  put_pieces(w, l, d, false);
   w.total = l.at;
   return w;
 }
@@ -192,13 +201,14 @@ ScanWs scan_bwd_ws(const pdssm_selscan_dims* d) {
   const int per = pdscan::ss_channels(d->N);
   const size_t rows = (size_t)(d->packed ? 1 : d->B) * d->L;
   w.blocks = pdscan::ss_blocks(d->D / d->G, per * pdscan::kSsBwdGroups);
-  w.split = pdscan::ss_split(d->B, d->L, d->packed, (int64_t)d->G * w.blocks, kCus, 128, 64);
+  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, pdscan::kSsBwdGroups), 3 * kCus / pdscan::kSsBwdGroups,
+                             scan_blocks(d, pdscan::kSsStateGroups), true);
   Layout l;
-  put_segments(w, l, d, true);
+  put_pieces(w, l, d, true);
   const size_t perseq = ((size_t)d->L + pdscan::kSsBwdTile - 1) / pdscan::kSsBwdTile;
-  const size_t tiles = d->packed ? (size_t)w.split.segs + perseq : d->B * perseq;
+  const size_t tiles = d->packed ? (size_t)w.split.pieces + perseq : d->B * perseq;
   const pdscan::SsShape shape = pdscan::ss_shape(d->N);
-  w.ckpt = l.put(tiles * d->G * pdscan::ss_blocks(d->D / d->G, per) * shape.S * 64 * 4);
+  w.ckpt = l.put(tiles * scan_blocks(d, 1) * shape.S * 64 * 4);
   w.cum = l.put(tiles * d->D * 4);
   w.part = l.put(2 * (size_t)d->G * w.blocks * rows * d->N * 4);
   w.partA = l.put((size_t)w.split.segs * d->D * d->N * 4);
@@ -231,32 +241,57 @@ void scan_in(Args& c, SsArgs& a, const pdssm_selscan_dims* d, const ScanIn& i) {
   a.rows = c.B * c.L;
 }
 
-// Segment table and contributions: what the passes of a split call read.
-hipError_t scan_segments(SsArgs& a, const pdssm_selscan_dims* d, const ScanWs& w, const int32_t* cu, unsigned char* ws,
-                         hipStream_t st) {
-  a.s.cu = cu;
-  a.s.B = d->B; a.s.L = d->L;
-  a.s.nseg = w.split.nseg; a.s.seg = w.split.seg; a.s.segs = w.split.segs;
+// The launches before a scan's last: tables, states at the pieces' starts (and,
+// for a gradient, at the tiles'), the adjoint's at the runs' ends.  Leaves in
+// `a` what the last one reads.
+hipError_t scan_states(SsArgs& a, const pdssm_selscan_dims* d, const ScanWs& w, const int32_t* cu, unsigned char* ws,
+                       bool bwd, hipStream_t st) {
+  const SsSplit& p = w.split;
+  const int bf16 = d->in_dtype == PDSSM_BF16;
   a.header = (uint32_t*)ws;
-  if (!w.split.split) return hipSuccess;
-  a.seg = (float*)(ws + w.seg);
-  a.sum = (float*)(ws + w.sum);
-  if (!cu) return hipSuccess;
-  a.s.table = (const int32_t*)(ws + w.table);
-  return pdscan::launch_linattn_table(cu, (int32_t*)(ws + w.table), (int32_t*)(ws + w.starts), d->B, d->L, w.split.seg,
-                                      w.split.segs, st);
-}
-
-hipError_t scan_carry(const SsArgs& a, const pdssm_selscan_dims* d, const ScanWs& w, unsigned char* ws, int rev,
-                      hipStream_t st) {
-  pdscan::SsCarryArgs c = {};
-  c.A = a.A;
-  c.user = rev ? a.ghL : a.h0;
-  c.seg = rev ? a.adj : a.seg;
-  c.sum = a.sum;
-  c.starts = d->packed ? (const int32_t*)(ws + w.starts) : nullptr;
-  c.B = d->B; c.D = d->D; c.N = d->N; c.nseg = w.split.nseg; c.rev = rev;
-  return pdscan::launch_selscan_carry(c, st);
+  a.piece = p.piece; a.npiece = p.npiece; a.run = p.run;
+  pdscan::SsSegs pieces = {cu, nullptr, d->B, d->L, p.npiece, p.piece, p.pieces};
+  pdscan::SsSegs runs = {cu, nullptr, d->B, d->L, p.nseg, p.seg, p.segs};
+  hipError_t e = hipSuccess;
+  if (p.states) {
+    a.seg = (float*)(ws + w.seg);
+    a.sum = (float*)(ws + w.sum);
+    if (bwd && p.cut) a.adj = (float*)(ws + w.adj);
+    if (cu) {
+      pieces.table = (const int32_t*)(ws + w.table);
+      a.pieces = (const int32_t*)(ws + w.pieces);
+      e = pdscan::launch_linattn_table(cu, (int32_t*)(ws + w.table), (int32_t*)(ws + w.pieces), d->B, d->L, p.piece, p.pieces, st);
+      if (p.cut) {
+        runs.table = (const int32_t*)(ws + w.run_table);
+        a.runs = (const int32_t*)(ws + w.runs);
+        if (e == hipSuccess)
+          e = pdscan::launch_linattn_table(cu, (int32_t*)(ws + w.run_table), (int32_t*)(ws + w.runs), d->B, d->L, p.seg, p.segs, st);
+      }
+    }
+  }
+  if (p.states || bwd) {
+    a.s = pieces;
+    if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, 0, st);
+  }
+  if (p.states) {
+    pdscan::SsCarryArgs c = {};
+    c.A = a.A;
+    c.user = a.h0;
+    c.seg = a.seg;
+    c.sum = a.sum;
+    c.starts = a.pieces;
+    c.B = d->B; c.D = d->D; c.N = d->N; c.nseg = p.npiece;
+    if (e == hipSuccess) e = pdscan::launch_selscan_carry(c, st);
+    if (a.adj) {
+      if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, 1, st);
+      c.user = a.ghL;
+      c.seg = a.adj;
+      c.rev = 1;
+      if (e == hipSuccess) e = pdscan::launch_selscan_carry(c, st);
+    }
+  }
+  a.s = runs;
+  return e;
 }
 
 // ---- norm
@@ -474,11 +509,7 @@ int pdssm_selscan_fwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const
   const hipStream_t st = (hipStream_t)stream;
   unsigned char* ws = (unsigned char*)workspace;
   const int bf16 = d.in_dtype == PDSSM_BF16;
-  hipError_t e = scan_segments(a, dims, w, cu_seqlens, ws, st);
-  if (w.split.split) {
-    if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, 0, st);
-    if (e == hipSuccess) e = scan_carry(a, dims, w, ws, 0, st);
-  }
+  hipError_t e = scan_states(a, dims, w, cu_seqlens, ws, false, st);
   if (e == hipSuccess) e = pdscan::launch_selscan_fwd(a, bf16, st);
   return launched(e);
 }
@@ -520,20 +551,12 @@ int pdssm_selscan_bwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const
   const hipStream_t st = (hipStream_t)stream;
   unsigned char* ws = (unsigned char*)workspace;
   const int bf16 = d.in_dtype == PDSSM_BF16;
-  hipError_t e = scan_segments(a, dims, w, cu_seqlens, ws, st);
-  a.adj = (float*)(ws + w.adj);
   a.ckpt = (float*)(ws + w.ckpt);
   a.cum = (float*)(ws + w.cum);
   a.part = (float*)(ws + w.part);
   a.partA = (float*)(ws + w.partA);
   a.partD = (float*)(ws + w.partD);
-  // states from every segment's start, and what it adds; then the adjoint's, from its end
-  if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, 0, st);
-  if (w.split.split) {
-    if (e == hipSuccess) e = scan_carry(a, dims, w, ws, 0, st);
-    if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, 1, st);
-    if (e == hipSuccess) e = scan_carry(a, dims, w, ws, 1, st);
-  }
+  hipError_t e = scan_states(a, dims, w, cu_seqlens, ws, true, st);
   if (e == hipSuccess) e = pdscan::launch_selscan_bwd(a, bf16, st);
   pdscan::SsFoldArgs f = {};
   f.part = a.part;

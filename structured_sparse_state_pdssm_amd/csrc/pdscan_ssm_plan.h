@@ -29,10 +29,12 @@ struct SsArgs {
   const float *A, *skip, *bias;  // [D][N]; [D] or NULL
   const float *h0, *ghL;         // [B][D][N] or NULL: zero
   float *hL, *gh0;               // gh0 may be NULL
-  SsSegs s;
-  float *seg, *adj;              // [segments][D][N]: contributions of segments, then entering (adjoint) states
-  float *sum;                    // [segments][D]: sums of the steps d_t of a segment
-  float *ckpt, *cum;             // states at the tiles' starts, each segment from zero, and the sums up to there
+  SsSegs s;                      // of this launch: pieces in the state pass, runs of `run` pieces in the others
+  const int32_t *pieces, *runs;  // packed: first piece and first run of every sequence (runs NULL: whole sequences)
+  int piece, npiece, run;        // steps of a piece, pieces of a sequence (not packed)
+  float *seg, *adj;              // [pieces][D][N]: contributions of pieces, then entering (adjoint) states; NULL: one piece
+  float *sum;                    // [pieces][D]: sums of the steps d_t of a piece
+  float *ckpt, *cum;             // states at the tiles' starts, each piece from zero, and the sums up to there
   float *part;                   // partial g_B and g_C [2][blocks of all groups][rows][N]
   float *partA, *partD;          // [segments][D][N]; [segments][2][D]: g_skip, g_bias
   uint32_t* header;              // workspace header
@@ -88,30 +90,49 @@ inline constexpr SsShape ss_shape(int N) {
 inline constexpr int ss_channels(int N) { return 64 / ss_shape(N).NS; }   // of a wave
 inline int ss_blocks(int K, int per) { return (K + per - 1) / per; }        // channel blocks of a group of K
 
-// Steps of a tile: forwards four waves of 64 / S steps (at most 16) each, backwards four of 8.
-inline constexpr int ss_fwd_steps(int N) { return ss_shape(N).S >= 8 ? 8 : 16; }
+// A tile is four waves of eight steps each.
+constexpr int kSsFwdSteps = 8;
 constexpr int kSsBwdSteps = 8, kSsTimeWaves = 4, kSsBwdTile = kSsBwdSteps * kSsTimeWaves;
-constexpr int kSsBwdGroups = 2;  // channel groups (waves side by side) of a gradient's workgroup
+constexpr int kSsBwdGroups = 1;   // channel groups (waves side by side) of a gradient's workgroup
 constexpr int kSsStateGroups = 4;
 
+// How a call cuts the step axis.  A piece is what a wave of the state pass
+// takes; a run of pieces is what a workgroup of the others takes.
 struct SsSplit {
-  int seg, nseg, segs;
-  bool split;
+  int piece, npiece, pieces;     // steps, of a sequence (not packed), in all (bound)
+  int run, seg, nseg, segs;      // pieces of a run, its steps, runs of a sequence, in all (bound)
+  bool cut;                      // sequences take more than one run
+  bool states;                   // and more than one piece
 };
 
-// Cuts the step axis into segments where `width` workgroups a sequence leave
-// the card idle: `room` of them fill it.
-inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, int least, int unit) {
+// `width` workgroups take a run, `room` of them fill the card; `states`
+// workgroups take a piece of the state pass (its waves are light: eight times the card).
+inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, long long states, bool always) {
   SsSplit s;
-  const long long have = packed ? width * 2 : B * width;   // (sequences of different lengths: the longest counts)
+  constexpr int kUnit = 64, kLeast = 128;
+  const long long seqs = packed ? 1 : B;
+  const long long have = packed ? width * 2 : B * width;   // (of sequences of different lengths the longest counts)
   long long n = have * 2 >= room ? 1 : (room + have - 1) / have;
-  if (n > L / least) n = L / least;
-  s.split = n > 1;
-  const long long each = s.split ? ((long long)L + n - 1) / n : L;
-  s.seg = s.split ? (int)((each + unit - 1) / unit * unit) : L;
-  s.nseg = s.split ? (int)(((long long)L + s.seg - 1) / s.seg) : 1;
-  const long long segs = !packed ? (long long)B * s.nseg : s.split ? (long long)(L / s.seg) + B : B;
-  s.segs = segs > 0x7fffffffll ? 0x7fffffff : (int)segs;
+  if (n > L / (2 * kLeast)) n = L / (2 * kLeast);
+  s.cut = n > 1;
+  long long m = (s.cut || always) ? (8 * 256 + seqs * states - 1) / (seqs * states) : 1;   // pieces
+  if (m > L / kLeast) m = L / kLeast;
+  if (m < n) m = n;
+  if (m < 1) m = 1;
+  s.run = s.cut ? (int)((m + n - 1) / n) : 0x7fffffff;
+  if (s.cut) m = n * s.run;
+  s.piece = m > 1 ? (int)(((L + m - 1) / m + kUnit - 1) / kUnit * kUnit) : L;
+  s.npiece = (int)(((long long)L + s.piece - 1) / s.piece);
+  s.states = s.npiece > 1;
+  if (!s.states) s.cut = false;
+  s.seg = s.cut ? s.piece * s.run : L;
+  s.nseg = s.cut ? (int)(((long long)L + s.seg - 1) / s.seg) : 1;
+  auto all = [&](int len, int each, bool more) {
+    const long long k = !packed ? (long long)B * each : more ? (long long)(L / len) + B : B;
+    return k > 0x7fffffffll ? 0x7fffffff : (int)k;
+  };
+  s.pieces = all(s.piece, s.npiece, s.states);
+  s.segs = all(s.seg, s.nseg, s.cut);
   return s;
 }
 
