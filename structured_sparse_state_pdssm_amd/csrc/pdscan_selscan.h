@@ -403,21 +403,21 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 // at both ends, again on the decays and states in registers.
 //
 // Sums over the channels (g_B, g_C) are the part that crosses lanes: for every
-// step and state, over the 16 lanes that hold channels.  A matrix instruction adds the
-// four rows of 16 lanes: v is its 4 x 16 operand, the other one has ones in
-// one of its 16 rows, so that steps and both sums pile up in one accumulator
-// per state, fp32 throughout; what is left, four lanes of a row, is added once a tile.
+// step and state, over the 16 lanes that hold channels.  Exchanges halve what is
+// left of four steps' products twice, so that only a quarter of them is added
+// up inside the rows of 16 lanes.  (On the matrix cores, as products with a row
+// of ones, they took 32 cycles each, 660 us for the whole kernel at 16 x 2048 x
+// 768 in bf16.)
 template <typename T, int S, int NS>
 __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_selscan_bwd_kernel(const SsArgs a) {
   constexpr int W = kSsTimeWaves, CG = kSsBwdGroups, TS = kSsBwdSteps, TT = W * TS, CW = 64 / NS, CC = CG * CW, NP = S * NS;
   constexpr int NT = 256 * CG, V = TT * CC / NT;
   constexpr int BT = NT / 2, VB = TT * NP / BT < 8 ? TT * NP / BT : 8, BR = TT * NP / BT / VB;   // B by one half of the threads, C by the other
-  typedef float f4 __attribute__((ext_vector_type(4)));
-  static_assert(TS == 8, "rows of an accumulator: eight steps of g_B, eight of g_C");
+  static_assert(TS % 4 == 0, "sums over the channels take four steps at once");
   __shared__ __align__(16) float4 pre[TT][CC];     // d, d x, g, slope of d
   __shared__ __align__(16) float gzs[TT][CC];      // slope of the gate times g_y
   __shared__ __align__(16) float Bs[TT][NP], Cs[TT][NP];
-  __shared__ __align__(16) float outs[3][TT][CC];  // C . h, l . B, sum A q h
+  __shared__ float outs[3 * (TT * CC + 16)];       // C . h, l . B, sum A q h: 16 banks apart
   __shared__ __align__(16) float gs[2][CG][TT][NP];   // g_B, g_C
   __shared__ __align__(16) float Es[CG * W][S * 64], Ps[CG * W][S * 64], Rs[CG * W][S * 64];
   __shared__ __align__(16) float Rt[2][CG][S * 64];   // the adjoint state that enters a tile, from its end
@@ -620,20 +620,18 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     for (int t = 0; t < TS; ++t)
 #pragma unroll
       for (int j = 0; j < S; ++j) hs[t][j] = h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
-    f4 acc[S] = {};   // rows 0 .. 7: steps of g_B, 8 .. 15: of g_C
-    float row = (lane & 15) == TS - 1 ? 1.0f : 0.0f;   // ones in row t
+    float far[2][2 * S];   // products of the two steps before: g_B's S, then g_C's
 #pragma unroll
     for (int t = TS - 1; t >= 0; --t) {
       const float4 w = pre[tw + t][lc];
-      const float rowC = ss_dpp<kDppRor8>(row);
-      float b[S], k[S], y = 0.0f, lb = 0.0f, pa = 0.0f;
+      float b[S], k[S], y = 0.0f, lb = 0.0f, pa = 0.0f, v[2 * S];
       ss_row_get(b, &Bs[tw + t][q * S]);
       ss_row_get(k, &Cs[tw + t][q * S]);
 #pragma unroll
       for (int j = 0; j < S; ++j) {
         l[j] = __builtin_fmaf(w.z, k[j], l[j]);
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(row, w.y * l[j], acc[j], 0, 0, 0);
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(rowC, w.z * hs[t][j], acc[j], 0, 0, 0);
+        v[j] = w.y * l[j];
+        v[S + j] = w.z * hs[t][j];
         y = __builtin_fmaf(k[j], hs[t][j], y);
         lb = __builtin_fmaf(b[j], l[j], lb);
         l[j] *= dec[t][j];
@@ -641,33 +639,41 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
         pa = __builtin_fmaf(A2[j], p, pa);
         gA[j] = __builtin_fmaf(w.x, p, gA[j]);
       }
-      row = ss_dpp<kDppShl1>(row);
       // over the states, lanes next to each other: the sum of y ends in lane 0 of four, of lb in 1, of pa in 2
       const bool odd = q & 1, high = q & 2;
       const float r1 = (odd ? lb : y) + ss_dpp<kDppXor1>(odd ? y : lb);
       const float r2 = pa + ss_dpp<kDppXor1>(pa);
       float r = (high ? r2 : r1) + ss_dpp<kDppXor2>(high ? r1 : r2);
       if constexpr (NS == 8) r += ss_dpp<kDppShl4>(r);
-      if (q < 3) outs[q][tw + t][lc] = r;
+      if (q < 3) outs[q * (TT * CC + 16) + (tw + t) * CC + lc] = r;
+      // over the channels: lanes 32 apart, rows, then what is left of a row; four steps end in a row each
+      if (t % 4 >= 2) {
+#pragma unroll
+        for (int j = 0; j < 2 * S; ++j) far[t & 1][j] = v[j];
+      } else {
+        ss_fold32(far[t & 1], v, far[t & 1]);
+      }
+      if (t % 4 == 0) {
+        float g[2 * S];
+        ss_fold16(g, far[0], far[1]);
+        const int at = tw + t + (lane >> 4);
+#pragma unroll
+        for (int j = 0; j < 2 * S; ++j) {
+          g[j] += ss_dpp<kDppRor8>(g[j]);
+          if constexpr (NS == 4) g[j] += ss_dpp<kDppRor4>(g[j]);
+        }
+        if ((lane & 15) < NS) {
+          constexpr int U = S < 4 ? S : 4;
+#pragma unroll
+          for (int j = 0; j < 2 * S; j += U) {
+            SsVec<float, U> o;
+#pragma unroll
+            for (int i = 0; i < U; ++i) o.e[i] = g[j + i];
+            *(SsVec<float, U>*)&gs[j / S][cg][at][q * S + j % S] = o;
+          }
+        }
+      }
       if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-    }
-    // over the channels of a row of 16 lanes
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      SsVec<float, S < 4 ? S : 4> o[S < 4 ? 1 : S / 4];
-#pragma unroll
-      for (int j = 0; j < S; ++j) {
-        float r = acc[j][i];
-        r += ss_dpp<kDppRor8>(r);
-        if constexpr (NS == 4) r += ss_dpp<kDppRor4>(r);
-        o[j / 4].e[j % 4] = r;
-      }
-      const int at = (lane >> 4) * 4 + i;   // row of the accumulator
-      if ((lane & 15) < NS) {
-        float* to = &gs[at >> 3][cg][tw + (at & 7)][q * S];
-#pragma unroll
-        for (int j = 0; j < S; j += S < 4 ? S : 4) *(SsVec<float, S < 4 ? S : 4>*)(to + j) = o[j / 4];
-      }
     }
     __syncthreads();
     if (live) {
@@ -675,7 +681,8 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float4 w = pre[st][sc + v];
-        const float y = outs[0][st][sc + v], lb = outs[1][st][sc + v], pa = kLn2 * outs[2][st][sc + v];
+        const float* o = outs + st * CC + sc + v;
+        const float y = o[0], lb = o[TT * CC + 16], pa = kLn2 * o[2 * (TT * CC + 16)];
         const float x = xc.get(v), skip = pars[1][sc + v];
         ox[v] = __builtin_fmaf(w.x, lb, w.z * skip);
         od[v] = __builtin_fmaf(x, lb, pa) * w.w;
@@ -717,8 +724,8 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   ss_lane_put(Es[cg * W + wave], gA, lane);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    outs[0][st][sc + v] = gD[v];
-    outs[1][st][sc + v] = gb[v];
+    outs[st * CC + sc + v] = gD[v];
+    outs[TT * CC + 16 + st * CC + sc + v] = gb[v];
   }
   __syncthreads();
   if (wave == 0) {
@@ -732,7 +739,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     ss_store_state(sumA, a.partA, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
     if (ok && q < 2) {
       float o = 0.0f;
-      for (int t = 0; t < TT; ++t) o += outs[q][t][lc];
+      for (int t = 0; t < TT; ++t) o += outs[q * (TT * CC + 16) + t * CC + lc];
       a.partD[((int64_t)u.sid * 2 + q) * a.D + ch] = o;
     }
   }

@@ -139,23 +139,55 @@ __device__ __forceinline__ float ss_dpp(float x) {
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppRor4 = 0x124, kDppRor8 = 0x128,
               kDppShl1 = 0x101, kDppShl4 = 0x104;
 
-// Sums over the lanes 32 apart of a (lower half of the result) and of b (upper
-// half): the instruction exchanges a's upper half and b's lower one.  By hand,
-// as the compiler's builtin gives the first result twice; it waits for the
-// two states that the exchange has to be behind what wrote its operands.
+// Exchanges across a wave, by hand, as the compiler's builtins give the first
+// result twice; each waits for the two states that it has to be behind what wrote
+// its operands, four exchanges at a time where there are as many.
+//   32: a's upper half and b's lower one change places;
+//   16: a's odd rows of 16 lanes and b's even ones.
+// So a + b is then the sum over lanes 32 apart of a in the lower half, of b in
+// the upper; over rows next to each other of a in even rows, of b in odd ones.
 __device__ __forceinline__ float ss_fold32(float a, float b) {
   asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b));
   return a + b;
 }
-// Sums over the rows of 16 lanes next to each other: of a in even rows, of b
-// in odd ones (a's odd rows and b's even ones change places).
 __device__ __forceinline__ float ss_fold16(float a, float b) {
   asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a), "+v"(b));
   return a + b;
 }
+// r[i] = fold(a[i], b[i]), N even.
+template <int N>
+__device__ __forceinline__ void ss_fold32(float (&r)[N], float (&a)[N], float (&b)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += N < 4 ? 2 : 4) {
+    if constexpr (N < 4)
+      asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\tv_permlane32_swap_b32 %2, %3" : "+v"(a[i]), "+v"(b[i]), "+v"(a[i + 1]), "+v"(b[i + 1]));
+    else
+      asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\tv_permlane32_swap_b32 %2, %3\n\t"
+          "v_permlane32_swap_b32 %4, %5\n\tv_permlane32_swap_b32 %6, %7"
+          : "+v"(a[i]), "+v"(b[i]), "+v"(a[i + 1]), "+v"(b[i + 1]), "+v"(a[i + 2]), "+v"(b[i + 2]), "+v"(a[i + 3]), "+v"(b[i + 3]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = a[i] + b[i];
+}
+template <int N>
+__device__ __forceinline__ void ss_fold16(float (&r)[N], float (&a)[N], float (&b)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += N < 4 ? 2 : 4) {
+    if constexpr (N < 4)
+      asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\tv_permlane16_swap_b32 %2, %3" : "+v"(a[i]), "+v"(b[i]), "+v"(a[i + 1]), "+v"(b[i + 1]));
+    else
+      asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\tv_permlane16_swap_b32 %2, %3\n\t"
+          "v_permlane16_swap_b32 %4, %5\n\tv_permlane16_swap_b32 %6, %7"
+          : "+v"(a[i]), "+v"(b[i]), "+v"(a[i + 1]), "+v"(b[i + 1]), "+v"(a[i + 2]), "+v"(b[i + 2]), "+v"(a[i + 3]), "+v"(b[i + 3]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = a[i] + b[i];
+}
 // Sums over the four rows of 16 lanes: row r of the result has v_r's.
 __device__ __forceinline__ float ss_fold_rows(float v0, float v1, float v2, float v3) {
-  return ss_fold16(ss_fold32(v0, v2), ss_fold32(v1, v3));
+  float r[2], a[2] = {v0, v1}, b[2] = {v2, v3};
+  ss_fold32(r, a, b);
+  return ss_fold16(r[0], r[1]);
 }
 
 // Sum over P lanes next to each other, in every one of them (P: up to 64).
