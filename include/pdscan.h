@@ -509,7 +509,9 @@ typedef struct {
  *   h_L [B,D,N] (out, required)
  * Steps d_t >= 0 and A <= 0 (not checked; exp(d A) past fp32 overflows).
  * Precision: fp32 throughout, sums of steps over more than a tile in 64 bits;
- * an exponential is good to two steps of fp32.  Decays below 2^-126 are zero. */
+ * an exponential is good to two steps of fp32.  Decays below 2^-126 are zero.
+ * Where the query answers 0 (enough sequences and channels to run each
+ * sequence in one) workspace may be NULL. */
 int pdssm_selscan_workspace_bytes(const pdssm_selscan_dims* dims, size_t* bytes);
 int pdssm_selscan_fwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const pdssm_view* dt, const float* A,
                       const pdssm_view* Bm, const pdssm_view* Cm, const float* skip, const pdssm_view* z,

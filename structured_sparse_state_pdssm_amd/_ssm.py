@@ -113,8 +113,13 @@ def _sequences(rows, cu_seqlens):
     return cu_seqlens.shape[0] - 1
 
 
-def _new(t, shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+def _new(t, shape, dtype, like):
+    """The caller's output, or a contiguous one (made the quickest way: a small call's time is the host's)."""
+    if t is not None:
+        return t
+    if like.dtype is dtype:
+        return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
+    return like.new_empty(shape, dtype=dtype)
 
 
 # ---- convolution
@@ -140,7 +145,7 @@ def pdssm_conv_fwd(x, w, bias=None, x0=None, silu=True, cu_seqlens=None, out=Non
     index, dt = x.get_device(), x.dtype
     _verify(specs + [(y, "y", x.shape, dt, _ROWS), (xL, "x_L", sshape, dt, _WHOLE)], index)
     dims = _pack(_struct_conv, *d)
-    y, xL = _new(y, x.shape, dt, x.device), _new(xL, sshape, dt, x.device)
+    y, xL = _new(y, x.shape, dt, x), _new(xL, sshape, dt, x)
     _check(_call(index, lambda stream: _conv_fwd(
         dims, _rows_view(x), w.data_ptr(), _ptr(bias), _ptr(cu_seqlens), _ptr(x0), _rows_view(y), xL.data_ptr(), stream)))
     return y, xL
@@ -164,7 +169,7 @@ def pdssm_conv_bwd(x, w, g_y, bias=None, x0=None, g_xL=None, silu=True, cu_seqle
     dims = _pack(_struct_conv, *d)
     for _, n, shape, dtype, _ in outs:
         if n in res:
-            res[n] = _new(res[n], shape, dtype, dev)
+            res[n] = _new(res[n], shape, dtype, x)
     ws = _workspace(_bytes(_conv_bytes, dims), dev, workspace)
     _check(_call(index, lambda stream: _conv_bwd(
         dims, _rows_view(x), w.data_ptr(), _ptr(bias), _ptr(cu_seqlens), _ptr(x0), _rows_view(g_y), _ptr(g_xL),
@@ -186,7 +191,7 @@ def pdssm_conv_step(x, w, state, bias=None, state_idx=None, silu=True, out=None)
     _verify([(x, "x", (B, D), dt, _ROWS), (w, "w", (D, W), _f32, _WHOLE), (state, "state", (slots, W - 1, D), dt, _WHOLE),
              (bias, "bias", (D,), _f32, _WHOLE), (state_idx, "state_idx", (B,), _i32, _WHOLE),
              (out, "out", (B, D), dt, _ROWS)], index)
-    out = _new(out, (B, D), dt, x.device)
+    out = _new(out, x.shape, dt, x)
     dims = _pack(_struct_conv, B, 1, D, W, _FLOATS[dt], 0, bool(silu))
     _check(_call(index, lambda stream: _conv_step(
         dims, _row_view(x), w.data_ptr(), _ptr(bias), _ptr(state_idx), slots, state.data_ptr(), _row_view(out), stream)))
@@ -222,11 +227,15 @@ def pdssm_selscan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=T
     index, ty, dev = x.get_device(), x.dtype, x.device
     _verify(specs + [(y, "y", x.shape, ty, _ROWS), (hL, "h_L", sshape, _f32, _WHOLE)], index)
     dims = _pack(_struct_scan, *d)
-    y, hL = _new(y, x.shape, ty, dev), _new(hL, sshape, _f32, dev)
-    ws = _workspace(_bytes(_scan_bytes, dims), dev, workspace)
+    y, hL = _new(y, x.shape, ty, x), _new(hL, sshape, _f32, x if h0 is None else h0)
+    nbytes = _bytes(_scan_bytes, dims)   # none where the sequences are not cut
+    ws, room = None, 0
+    if nbytes or workspace is not None:
+        ws = _workspace(nbytes, dev, workspace)
+        room = ws.numel()
     _check(_call(index, lambda stream: _scan_fwd(
         dims, _rows_view(x), _rows_view(dt), A.data_ptr(), _view(Bm), _view(Cm), _ptr(D), _opt(_rows_view, z),
-        _ptr(dt_bias), _ptr(cu_seqlens), _ptr(h0), _rows_view(y), hL.data_ptr(), ws.data_ptr(), ws.numel(), stream)))
+        _ptr(dt_bias), _ptr(cu_seqlens), _ptr(h0), _rows_view(y), hL.data_ptr(), _ptr(ws), room, stream)))
     return y, hL
 
 
@@ -252,7 +261,7 @@ def pdssm_selscan_bwd(x, dt, A, Bm, Cm, g_y, D=None, z=None, dt_bias=None, softp
     dims = _pack(_struct_scan, *d)
     for t, n, shape, dtype, _ in outs:
         if n in res and t is None:
-            res[n] = _like(Bm if n == "g_B" else Cm, shape, dev) if n in ("g_B", "g_C") else _new(None, shape, dtype, dev)
+            res[n] = _like(Bm if n == "g_B" else Cm, shape, dev) if n in ("g_B", "g_C") else _new(None, shape, dtype, x)
     ws = _workspace(_bytes(_scan_bwd_bytes, dims), dev, workspace)
     _check(_call(index, lambda stream: _scan_bwd(
         dims, _rows_view(x), _rows_view(dt), A.data_ptr(), _view(Bm), _view(Cm), _ptr(D), _opt(_rows_view, z),
@@ -279,7 +288,7 @@ def pdssm_selscan_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, so
              (state, "state", (slots, K, N), _f32, _WHOLE), (D, "D", (K,), _f32, _WHOLE), (z, "z", (B, K), ty, _ROWS),
              (dt_bias, "dt_bias", (K,), _f32, _WHOLE), (state_idx, "state_idx", (B,), _i32, _WHOLE),
              (out, "out", (B, K), ty, _ROWS)], index)
-    out = _new(out, (B, K), ty, x.device)
+    out = _new(out, x.shape, ty, x)
     dims = _pack(_struct_scan, B, 1, K, N, G, _FLOATS[ty], 0, bool(softplus))
     _check(_call(index, lambda stream: _scan_step(
         dims, _row_view(x), _row_view(dt), A.data_ptr(), _view1(Bm), _view1(Cm), _ptr(D), _opt(_row_view, z),
@@ -314,7 +323,7 @@ def _norm_view(t):
 
 
 def _norm_like(t):
-    return _like(t, t.shape, t.device) if t.dim() == 4 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return _like(t, t.shape, t.device) if t.dim() == 4 and not t.is_contiguous() else _new(None, t.shape, t.dtype, t)
 
 
 def pdssm_norm_fwd(x, w, z=None, gate=None, residual=None, res_scale=None, eps=1e-5, out=None):
@@ -351,7 +360,7 @@ def pdssm_norm_bwd(x, w, g_y, z=None, gate=None, res_scale=None, eps=1e-5, works
     dims = _pack(_struct_norm, *d)
     for n in names:
         if res[n] is None:
-            res[n] = _norm_like(x if n == "g_x" else z) if n in ("g_x", "g_z") else _new(None, wshape, _f32, dev)
+            res[n] = _norm_like(x if n == "g_x" else z) if n in ("g_x", "g_z") else _new(None, wshape, _f32, w)
     ws = _workspace(_bytes(_norm_bytes, dims), dev, workspace)
     _check(_call(index, lambda stream: _norm_bwd(
         dims, _norm_view(x), w.data_ptr(), _opt(_norm_view, z), _ptr(res_scale), _norm_view(g_y), _norm_view(res["g_x"]),

@@ -48,36 +48,46 @@ __device__ __forceinline__ CvSeq cv_seq(const CvArgs& a, int b) {
 
 // V channels of row r of sequence s, or of the state before it.
 template <typename T, int W, int V>
-__device__ __forceinline__ SsVec<typename T::E, V> cv_row(const CvArgs& a, const CvSeq& s, int64_t vb, int r, int c) {
-  if (r >= s.t0) return ss_load<T, V>(a.x.p, vb * a.x.sb + (int64_t)r * a.x.st + c);
+__device__ __forceinline__ SsRaw<T, V> cv_row(const CvArgs& a, const CvSeq& s, int64_t vb, int r, int c) {
+  SsRaw<T, V> x = {};
   const int i = W - 1 + r - s.t0;
-  if (a.x0 && i >= 0) return ss_load<T, V>(a.x0, ((int64_t)s.b * (W - 1) + i) * a.D + c);
-  return SsVec<typename T::E, V>{};
+  if (r >= s.t0)
+    ss_load_raw(x, a.x.p, vb * a.x.sb + (int64_t)r * a.x.st + c);
+  else if (a.x0 && i >= 0)
+    ss_load_raw(x, a.x0, ((int64_t)s.b * (W - 1) + i) * a.D + c);
+  return x;
 }
 
 template <int W, int V>
 __device__ __forceinline__ void cv_weights(float (&w)[W][V], float (&bias)[V], const float* wp, const float* bp, int c) {
+  constexpr int U = 4;   // (c is a multiple of it)
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
+  for (int i = 0; i < V * W; i += U) {
+    const auto x = ss_load<SsF32, U>(wp, (int64_t)c * W + i);
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][v] = wp[(int64_t)(c + v) * W + j];
-    bias[v] = bp ? bp[c + v] : 0.0f;
+    for (int k = 0; k < U; ++k) w[(i + k) % W][(i + k) / W] = x.e[k];
+  }
+#pragma unroll
+  for (int v = 0; v < V; v += U) {
+    SsVec<float, U> x = {};
+    if (bp) x = ss_load<SsF32, U>(bp, c + v);
+#pragma unroll
+    for (int k = 0; k < U; ++k) bias[v + k] = x.e[k];
   }
 }
 
 // y of the last row of win, whose rows end at the current one.
 template <typename T, int W, int V>
-__device__ __forceinline__ float cv_pre(const SsVec<typename T::E, V>* win, const float (&w)[W][V], float bias, int v) {
+__device__ __forceinline__ float cv_pre(const SsRaw<T, V>* win, const float (&w)[W][V], float bias, int v) {
   float p = bias;
 #pragma unroll
-  for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][v], T::get(win[j].e[v]), p);
+  for (int j = 0; j < W; ++j) p = __builtin_fmaf(w[j][v], win[j].get(v), p);
   return p;
 }
 
 template <typename T, int W>
 __global__ __launch_bounds__(256) void pdssm_conv_kernel(const CvArgs a) {
-  using E = typename T::E;
-  constexpr int V = 16 / sizeof(E), U = 4;
+  constexpr int V = 16 / sizeof(typename T::E), U = 4;   // rows under way
   const int nv = a.D / V;
   unsigned id = ss_block(a.row) * 256 + threadIdx.x;   // (the host keeps threads below 2^31)
   if (id >= a.units) {
@@ -89,8 +99,7 @@ __global__ __launch_bounds__(256) void pdssm_conv_kernel(const CvArgs a) {
     const int64_t b = id / (W - 1);
     if (b >= a.B) return;
     const CvSeq s = cv_seq(a, (int)b);
-    *(SsVec<E, V>*)((E*)a.xL + (b * (W - 1) + j) * a.D + c) =
-        cv_row<T, W, V>(a, s, a.cu ? 0 : b, s.t1 - (W - 1) + j, c);
+    ss_store_raw(a.xL, (b * (W - 1) + j) * a.D + c, cv_row<T, W, V>(a, s, a.cu ? 0 : b, s.t1 - (W - 1) + j, c));
     return;
   }
   const int c = (int)(id % nv) * V;
@@ -113,15 +122,15 @@ __global__ __launch_bounds__(256) void pdssm_conv_kernel(const CvArgs a) {
       r = e;
       continue;
     }
-    SsVec<E, V> win[W - 1 + U];
+    SsRaw<T, V> win[W - 1 + U];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) win[j] = cv_row<T, W, V>(a, s, vb, r - (W - 1) + j, c);
-    const E* xp = (const E*)a.x.p + vb * a.x.sb + (int64_t)r * a.x.st + c;
+    int64_t xp = vb * a.x.sb + (int64_t)r * a.x.st + c;
     int64_t yp = vb * a.y.sb + (int64_t)r * a.y.st + c;
     for (; r < e; r += U) {
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        if (r + i < e) win[W - 1 + i] = *(const SsVec<E, V>*)(xp + i * a.x.st);
+        if (r + i < e) ss_load_raw(win[W - 1 + i], a.x.p, xp + i * a.x.st);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         if (r + i >= e) break;
@@ -144,12 +153,12 @@ __global__ __launch_bounds__(256) void pdssm_conv_kernel(const CvArgs a) {
 
 // p of one row: the gradient before act, V channels.
 template <typename T, int W, int V>
-__device__ __forceinline__ void cv_grad(float (&p)[V], const SsVec<typename T::E, V>* win, const SsVec<typename T::E, V>& gy,
+__device__ __forceinline__ void cv_grad(float (&p)[V], const SsRaw<T, V>* win, const SsRaw<T, V>& gy,
                                         const float (&w)[W][V], const float (&bias)[V], int silu) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const float x = cv_pre<T, W, V>(win, w, bias[v], v);
-    p[v] = T::get(gy.e[v]);
+    p[v] = gy.get(v);
     if (silu) {
       const float k = ss_sigmoid<T>(x);
       p[v] *= k * __builtin_fmaf(x, 1.0f - k, 1.0f);
@@ -161,7 +170,6 @@ __device__ __forceinline__ void cv_grad(float (&p)[V], const SsVec<typename T::E
 // rows past its end.  The strips' sums of g_w and g_bias meet in LDS.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void pdssm_conv_bwd_kernel(const CvArgs a) {
-  using E = typename T::E;
   constexpr int V = 4;
   __shared__ float red[kCvBwdStrips - 1][(W + 1) * V][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -192,54 +200,67 @@ __global__ __launch_bounds__(256) void pdssm_conv_bwd_kernel(const CvArgs a) {
         r = e;
         continue;
       }
-      // win: rows t - W + 1 .. t of x; gp: p of those rows
-      SsVec<E, V> win[W];
+      // win: rows t - W + 1 .. t + U - 1 of x; gp: p of the last W rows
+      constexpr int U = 4;
+      SsRaw<T, V> win[W - 1 + U] = {}, gy[U] = {};
       float gp[W][V] = {};
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) win[j + 1] = cv_row<T, W, V>(a, s, vb, r - (W - 1) + j, c);
-      const E* xp = (const E*)a.x.p + vb * a.x.sb + c;
-      const E* gyp = (const E*)a.gy.p + vb * a.gy.sb + c;
+      for (int j = 0; j < W - 1; ++j) win[j] = cv_row<T, W, V>(a, s, vb, r - (W - 1) + j, c);
+      int64_t xp = vb * a.x.sb + (int64_t)r * a.x.st + c, gyp = vb * a.gy.sb + (int64_t)r * a.gy.st + c;
+      int64_t gxp = vb * a.gx.sb + (int64_t)(r - (W - 1)) * a.gx.st + c;
       const int stop = e + W - 1;
-#pragma unroll 4
-      for (int t = r; t < stop; ++t) {
+      for (int t0 = r; t0 < stop; t0 += U) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-          win[j] = win[j + 1];
+        for (int i = 0; i < U; ++i)
+          if (t0 + i < s.t1 && t0 + i < stop) {
+            ss_load_raw(win[W - 1 + i], a.x.p, xp + i * a.x.st);
+            ss_load_raw(gy[i], a.gy.p, gyp + i * a.gy.st);
+          }
 #pragma unroll
-          for (int v = 0; v < V; ++v) gp[j][v] = gp[j + 1][v];
-        }
-        if (t < s.t1) {
-          win[W - 1] = *(const SsVec<E, V>*)(xp + (int64_t)t * a.x.st);
-          cv_grad<T, W, V>(gp[W - 1], win, *(const SsVec<E, V>*)(gyp + (int64_t)t * a.gy.st), w, bias, a.silu);
-        } else {
+        for (int i = 0; i < U; ++i) {
+          const int t = t0 + i;
+          if (t >= stop) break;
 #pragma unroll
-          for (int v = 0; v < V; ++v) gp[W - 1][v] = 0.0f;
-        }
-        if (t < e) {
+          for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
+            for (int v = 0; v < V; ++v) gp[j][v] = gp[j + 1][v];
+          if (t < s.t1) {
+            cv_grad<T, W, V>(gp[W - 1], win + i, gy[i], w, bias, a.silu);
+          } else {
 #pragma unroll
-            for (int j = 0; j < W; ++j) gw[j][v] = __builtin_fmaf(gp[W - 1][v], T::get(win[j].e[v]), gw[j][v]);
-            gb[v] += gp[W - 1][v];
+            for (int v = 0; v < V; ++v) gp[W - 1][v] = 0.0f;
+          }
+          if (t < e) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+              for (int j = 0; j < W; ++j) gw[j][v] = __builtin_fmaf(gp[W - 1][v], win[i + j].get(v), gw[j][v]);
+              gb[v] += gp[W - 1][v];
+            }
+          }
+          const int to = t - (W - 1);
+          if (to >= r) {
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              o[v] = 0.0f;
+#pragma unroll
+              for (int j = 0; j < W; ++j) o[v] = __builtin_fmaf(w[j][v], gp[W - 1 - j][v], o[v]);
+            }
+            const int k = to - (s.t1 - (W - 1));
+            if (k >= 0 && a.gxL) {   // one of the last rows: they are the state behind the sequence too
+              const auto g = ss_load<T, V>(a.gxL, ((int64_t)s.b * (W - 1) + k) * a.D + c);
+#pragma unroll
+              for (int v = 0; v < V; ++v) o[v] += T::get(g.e[v]);
+            }
+            ss_store<T, V>(a.gx.p, gxp + i * a.gx.st, o);
           }
         }
-        const int to = t - (W - 1);
-        if (to >= r) {
-          float o[V];
+        xp += U * a.x.st;
+        gyp += U * a.gy.st;
+        gxp += U * a.gx.st;
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            o[v] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < W; ++j) o[v] = __builtin_fmaf(w[j][v], gp[W - 1 - j][v], o[v]);
-          }
-          const int k = to - (s.t1 - (W - 1));
-          if (k >= 0 && a.gxL) {   // one of the last rows: they are the state behind the sequence too
-            const auto g = ss_load<T, V>(a.gxL, ((int64_t)s.b * (W - 1) + k) * a.D + c);
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += T::get(g.e[v]);
-          }
-          ss_store<T, V>(a.gx.p, vb * a.gx.sb + (int64_t)to * a.gx.st + c, o);
-        }
+        for (int j = 0; j < W - 1; ++j) win[j] = win[j + U];
       }
       r = e;
     }
@@ -268,7 +289,6 @@ __global__ __launch_bounds__(256) void pdssm_conv_bwd_kernel(const CvArgs a) {
 // state behind it where it is shorter than the window, have of it.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void pdssm_conv_state_bwd_kernel(const CvArgs a) {
-  using E = typename T::E;
   constexpr int V = 4;
   const int nv = a.D / V;
   const unsigned id = ss_block(a.row) * 256 + threadIdx.x;
@@ -283,10 +303,11 @@ __global__ __launch_bounds__(256) void pdssm_conv_state_bwd_kernel(const CvArgs 
 #pragma unroll
   for (int t = 0; t < W - 1; ++t) {
     if (t < len) {
-      SsVec<E, V> win[W];
+      SsRaw<T, V> win[W], gy;
 #pragma unroll
       for (int j = 0; j < W; ++j) win[j] = cv_row<T, W, V>(a, s, vb, s.t0 + t - (W - 1) + j, c);
-      cv_grad<T, W, V>(gp[t], win, ss_load<T, V>(a.gy.p, vb * a.gy.sb + (int64_t)(s.t0 + t) * a.gy.st + c), w, bias, a.silu);
+      ss_load_raw(gy, a.gy.p, vb * a.gy.sb + (int64_t)(s.t0 + t) * a.gy.st + c);
+      cv_grad<T, W, V>(gp[t], win, gy, w, bias, a.silu);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) gp[t][v] = 0.0f;
@@ -313,7 +334,6 @@ __global__ __launch_bounds__(256) void pdssm_conv_state_bwd_kernel(const CvArgs 
 // One token of every row on a pool of states, which moves up one row in place.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void pdssm_conv_step_kernel(const CvStepArgs a) {
-  using E = typename T::E;
   constexpr int V = 4;
   __shared__ int dup;
   const int tid = threadIdx.x, nb = (a.D / V + 255) / 256;
@@ -340,11 +360,11 @@ __global__ __launch_bounds__(256) void pdssm_conv_step_kernel(const CvStepArgs a
     ss_store<T, V>(a.y.p, yp, o);
     return;
   }
-  E* sp = (E*)a.state + (int64_t)slot * (W - 1) * a.D + c;
-  SsVec<E, V> win[W];
+  const int64_t sp = (int64_t)slot * (W - 1) * a.D + c;
+  SsRaw<T, V> win[W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) win[j] = *(const SsVec<E, V>*)(sp + (int64_t)j * a.D);
-  win[W - 1] = ss_load<T, V>(a.x.p, (int64_t)b * a.x.sb + c);
+  for (int j = 0; j < W - 1; ++j) ss_load_raw(win[j], a.state, sp + (int64_t)j * a.D);
+  ss_load_raw(win[W - 1], a.x.p, (int64_t)b * a.x.sb + c);
   float w[W][V], bias[V], o[V];
   cv_weights(w, bias, a.w, a.bias, c);
 #pragma unroll
@@ -354,7 +374,7 @@ __global__ __launch_bounds__(256) void pdssm_conv_step_kernel(const CvStepArgs a
   }
   ss_store<T, V>(a.y.p, yp, o);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) *(SsVec<E, V>*)(sp + (int64_t)j * a.D) = win[j + 1];
+  for (int j = 0; j < W - 1; ++j) ss_store_raw(a.state, sp + (int64_t)j * a.D, win[j + 1]);
 }
 
 #define PDSCAN_CONV(kernel, grid)                                                                            \

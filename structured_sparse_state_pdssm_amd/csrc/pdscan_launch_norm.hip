@@ -212,7 +212,7 @@ __global__ __launch_bounds__(256) void pdssm_norm_bwd_kernel(const NmArgs a) {
         for (int i = 0; i < a.slots; ++i)
 #pragma unroll
           for (int v = 0; v < V; ++v) o[v] += part[(i * a.cols + tid) * V + v];
-        float* to = (which ? a.parts : a.partw) + ((int64_t)l.chunk * a.H + l.h) * a.d + (k * P + l.p) * V;
+        float* to = a.part + l.chunk * a.part_chunk + l.h * a.part_head + which * a.part_s + (k * P + l.p) * V;
 #pragma unroll
         for (int v = 0; v < V; ++v) to[v] = o[v];
       }

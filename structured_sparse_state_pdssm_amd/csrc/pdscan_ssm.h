@@ -83,6 +83,21 @@ __device__ __forceinline__ void ss_load_at(SsRaw<T, V>& r, const char* tile, uin
   }
 }
 template <typename T, int V>
+__device__ __forceinline__ void ss_load_raw(SsRaw<T, V>& r, const void* p, int64_t at) {
+  using Q = SsVec<uint32_t, SsRaw<T, V>::kWords>;
+  const Q q = *(const Q*)((const typename T::E*)p + at);
+#pragma unroll
+  for (int i = 0; i < SsRaw<T, V>::kWords; ++i) r.w[i] = q.e[i];
+}
+template <typename T, int V>
+__device__ __forceinline__ void ss_store_raw(void* p, int64_t at, const SsRaw<T, V>& r) {
+  using Q = SsVec<uint32_t, SsRaw<T, V>::kWords>;
+  Q q;
+#pragma unroll
+  for (int i = 0; i < SsRaw<T, V>::kWords; ++i) q.e[i] = r.w[i];
+  *(Q*)((typename T::E*)p + at) = q;
+}
+template <typename T, int V>
 __device__ __forceinline__ void ss_store_at(char* tile, uint32_t off, const float* x) {
   asm("" : "+v"(off));
   SsVec<typename T::E, V> o;

@@ -66,8 +66,8 @@ struct Args {
   }
   int check(void* workspace = nullptr, size_t have = 0, size_t need = 0) {
     if (rc) return rc;
-    if (need) {
-      flat(true, "workspace", workspace, need, true);
+    if (need || (workspace && have)) {
+      flat(true, "workspace", workspace, need ? need : have, true);
       if (rc) return rc;
       if (have < need) return set_error(PDSSM_EWORKSPACE, "workspace of %zu bytes < %zu needed", have, need);
     }
@@ -187,12 +187,15 @@ int64_t scan_blocks(const pdssm_selscan_dims* d, int groups) {
   return (int64_t)d->G * pdscan::ss_blocks(d->D / d->G, pdscan::ss_channels(d->N) * groups);
 }
 
+// Workgroups of four waves that the card holds: three a compute unit, two where a lane has eight states.
+int room(const pdssm_selscan_dims* d) { return (pdscan::ss_shape(d->N).S >= 8 ? 2 : 3) * kCus; }
+
 ScanWs scan_ws(const pdssm_selscan_dims* d) {
   ScanWs w = {};
-  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, 1), 3 * kCus, scan_blocks(d, pdscan::kSsStateGroups), false);
+  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, 1), room(d), scan_blocks(d, pdscan::kSsStateGroups), false);
   Layout l;
   put_pieces(w, l, d, false);
-  w.total = l.at;
+  w.total = w.split.states ? l.at : 0;
   return w;
 }
 
@@ -201,7 +204,7 @@ ScanWs scan_bwd_ws(const pdssm_selscan_dims* d) {
   const int per = pdscan::ss_channels(d->N);
   const size_t rows = (size_t)(d->packed ? 1 : d->B) * d->L;
   w.blocks = pdscan::ss_blocks(d->D / d->G, per * pdscan::kSsBwdGroups);
-  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, pdscan::kSsBwdGroups), 3 * kCus / pdscan::kSsBwdGroups,
+  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, pdscan::kSsBwdGroups), room(d),
                              scan_blocks(d, pdscan::kSsStateGroups), true);
   Layout l;
   put_pieces(w, l, d, true);
@@ -245,10 +248,10 @@ void scan_in(Args& c, SsArgs& a, const pdssm_selscan_dims* d, const ScanIn& i) {
 // for a gradient, at the tiles'), the adjoint's at the runs' ends.  Leaves in
 // `a` what the last one reads.
 hipError_t scan_states(SsArgs& a, const pdssm_selscan_dims* d, const ScanWs& w, const int32_t* cu, unsigned char* ws,
-                       bool bwd, hipStream_t st) {
+                       size_t bytes, bool bwd, hipStream_t st) {
   const SsSplit& p = w.split;
   const int bf16 = d->in_dtype == PDSSM_BF16;
-  a.header = (uint32_t*)ws;
+  a.header = ws && bytes >= pdscan::kLaHeader ? (uint32_t*)ws : nullptr;
   a.piece = p.piece; a.npiece = p.npiece; a.run = p.run;
   pdscan::SsSegs pieces = {cu, nullptr, d->B, d->L, p.npiece, p.piece, p.pieces};
   pdscan::SsSegs runs = {cu, nullptr, d->B, d->L, p.nseg, p.seg, p.segs};
@@ -323,18 +326,14 @@ int norm_most(const pdssm_norm_dims* d) {
 }
 
 struct NormWs {
-  int64_t width;                       // of a part: all heads' rows
-  size_t w, s, mid, total;
+  size_t part, mid, total;
 };
-NormWs norm_ws(const pdssm_norm_dims* d) {
+NormWs norm_ws(const pdssm_norm_dims* d) {   // (room for the sums of res_scale in any case)
   NormWs n;
-  n.width = (int64_t)d->H * d->d;
-  const int most = norm_most(d);
-  const int64_t sums = d->per_head ? most : (int64_t)most * d->H;   // parts of the last sum
+  const int64_t most = norm_most(d), sums = d->per_head ? most : most * d->H;   // parts of the last sum
   Layout l;
-  n.w = l.put((size_t)most * n.width * 4);
-  n.s = l.put((size_t)most * n.width * 4);
-  n.mid = l.put(sums > pdscan::kSsSumMost ? (size_t)pdscan::kSsSumMid * (d->per_head ? n.width : d->d) * 4 : 0);
+  n.part = l.put((size_t)most * d->H * d->d * 8);
+  n.mid = l.put(sums > pdscan::kSsSumMost ? (size_t)pdscan::kSsSumMid * (d->per_head ? d->H : 1) * d->d * 8 : 0);
   n.total = l.at;
   return n;
 }
@@ -509,7 +508,7 @@ int pdssm_selscan_fwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const
   const hipStream_t st = (hipStream_t)stream;
   unsigned char* ws = (unsigned char*)workspace;
   const int bf16 = d.in_dtype == PDSSM_BF16;
-  hipError_t e = scan_states(a, dims, w, cu_seqlens, ws, false, st);
+  hipError_t e = scan_states(a, dims, w, cu_seqlens, ws, workspace_bytes, false, st);
   if (e == hipSuccess) e = pdscan::launch_selscan_fwd(a, bf16, st);
   return launched(e);
 }
@@ -556,7 +555,7 @@ int pdssm_selscan_bwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const
   a.part = (float*)(ws + w.part);
   a.partA = (float*)(ws + w.partA);
   a.partD = (float*)(ws + w.partD);
-  hipError_t e = scan_states(a, dims, w, cu_seqlens, ws, true, st);
+  hipError_t e = scan_states(a, dims, w, cu_seqlens, ws, workspace_bytes, true, st);
   if (e == hipSuccess) e = pdscan::launch_selscan_bwd(a, bf16, st);
   pdscan::SsFoldArgs f = {};
   f.part = a.part;
@@ -652,23 +651,24 @@ int pdssm_norm_bwd(const pdssm_norm_dims* dims, const pdssm_view* x, const float
   const int bf16 = d.in_dtype == PDSSM_BF16;
   unsigned char* ws = (unsigned char*)workspace;
   pdscan::nm_plan(a, bf16, norm_near(dims, x), 1, norm_most(dims));
-  a.partw = (float*)(ws + n.w);
-  a.parts = (float*)(ws + n.s);
+  a.part = (float*)(ws + n.part);
   a.header = (uint32_t*)ws;
+  // heads with weights of their own: parts are chunks, [w of all heads][s of all]; else chunks and heads, [w][s]
+  const int64_t both = res_scale ? 2 : 1, all = (int64_t)d.H * d.d;
+  a.part_chunk = both * all;
+  a.part_head = d.per_head ? d.d : both * d.d;
+  a.part_s = d.per_head ? all : d.d;
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e = pdscan::launch_norm_bwd(a, bf16, st);
   SsSumArgs s = {};
+  s.part = a.part;
   s.mid = (float*)(ws + n.mid);
   s.parts = d.per_head ? a.chunks : a.chunks * d.H;
-  s.width = s.first = d.per_head ? n.width : d.d;
-  s.part = a.partw;
+  s.first = d.per_head ? all : d.d;
+  s.width = both * s.first;
   s.out = g_w;
+  s.out2 = g_res_scale;
   if (e == hipSuccess) e = pdscan::launch_ssm_sum(s, st);
-  if (res_scale) {
-    s.part = a.parts;
-    s.out = g_res_scale;
-    if (e == hipSuccess) e = pdscan::launch_ssm_sum(s, st);
-  }
   return launched(e);
 }
 

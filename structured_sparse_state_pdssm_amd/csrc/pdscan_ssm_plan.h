@@ -105,15 +105,16 @@ struct SsSplit {
   bool states;                   // and more than one piece
 };
 
-// `width` workgroups take a run, `room` of them fill the card; `states`
+// `width` workgroups take a run, `room` of them are on the card at once; `states`
 // workgroups take a piece of the state pass (its waves are light: eight times the card).
 inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, long long states, bool always) {
   SsSplit s;
   constexpr int kUnit = 64, kLeast = 128;
   const long long seqs = packed ? 1 : B;
   const long long have = packed ? width * 2 : B * width;   // (of sequences of different lengths the longest counts)
-  long long n = have * 2 >= room ? 1 : (room + have - 1) / have;
-  if (n > L / (2 * kLeast)) n = L / (2 * kLeast);
+  // Runs cost the state passes, not their number: where sequences are cut, four times the room evens out the end.
+  long long n = have * 2 >= room ? 1 : (4 * room + seqs * width - 1) / (seqs * width);
+  if (n > L / kLeast) n = L / kLeast;
   s.cut = n > 1;
   long long m = (s.cut || always) ? (8 * 256 + seqs * states - 1) / (seqs * states) : 1;   // pieces
   if (m > L / kLeast) m = L / kLeast;
@@ -182,7 +183,8 @@ struct NmArgs {
   LaView x, z, r, y;             // [B][H][L][d]; z.p, r.p may be NULL
   LaView gy, gx, gz;
   const float *w, *s;            // [H][d] or [d]; s may be NULL
-  float *partw, *parts;          // (gradient) [chunks][H][d]
+  float* part;                   // (gradient) sums of a workgroup's rows, for w and behind them for s
+  int64_t part_chunk, part_head, part_s;   // floats between those of chunks, heads, and the two
   uint32_t* header;              // workspace header
   int B, H, L, d, gate, per_head;
   int cols, slots, tiles;        // lanes of a workgroup side by side in (head, row), rows at once, tiles of the former
