@@ -171,12 +171,12 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
     // stage: steps behind the end have d = 0, which leaves the state as it is
     const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
     const SsRaw<T, V> xc = xn, zc = zn;
+    float d[V], none[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float raw = dn.get(v) + pars[0][sc + v];
-      const float d = !live ? 0.0f : a.softplus ? ss_softplus_of(raw, ss_decay(raw)) : raw;
-      du[st][sc + v] = make_float2(d, d * xc.get(v));
-    }
+    for (int v = 0; v < V; ++v) d[v] = dn.get(v) + pars[0][sc + v];
+    ss_steps<V, false>(d, none, a.softplus, live);
+#pragma unroll
+    for (int v = 0; v < V; ++v) du[st][sc + v] = make_float2(d[v], d[v] * xc.get(v));
     {
       SsVec<float, VB> b, k;
 #pragma unroll
@@ -269,9 +269,10 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
     if (live) {
       float o[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        o[v] = __builtin_fmaf(pars[1][sc + v], xc.get(v), ys[st][sc + v]);
-        if (gated) {
+      for (int v = 0; v < V; ++v) o[v] = __builtin_fmaf(pars[1][sc + v], xc.get(v), ys[st][sc + v]);
+      if (gated) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
           const float z = zc.get(v);
           o[v] *= z * ss_sigmoid<T>(z);
         }
@@ -344,18 +345,21 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
   for (int i = 0; i < tiles; ++i) {
     const int t0 = at(i), p = i & 1;
     const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
+    float d[V], x[V], none[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float raw = dn.get(v) + bias[v];
-      const float d = !live ? 0.0f : a.softplus ? ss_softplus_of(raw, ss_decay(raw)) : raw;
-      float x = live ? xn.get(v) : 0.0f;
-      if (!REV) x *= d;
-      if (gated && live) {
+    for (int v = 0; v < V; ++v) d[v] = dn.get(v) + bias[v];
+    ss_steps<V, false>(d, none, a.softplus, live);
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = REV ? (live ? xn.get(v) : 0.0f) : d[v] * xn.get(v);
+    if (gated) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         const float z = zn.get(v);
-        x *= z * ss_sigmoid<T>(z);
+        x[v] *= z * ss_sigmoid<T>(z);
       }
-      du[p][st][sc + v] = make_float2(d, x);
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) du[p][st][sc + v] = make_float2(d[v], x[v]);
     if (tid < BT) {
       SsVec<float, VB> b;
 #pragma unroll
@@ -503,18 +507,23 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   for (int t0 = last; t0 >= 0; t0 -= TT, turn ^= 1) {
     const bool live = sok && t0 + st < s.len;
     const SsRaw<T, V> xc = xn;
+    float d[V], sg[V], g[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float raw = dn.get(v) + pars[0][sc + v], e = ss_decay(raw);
-      const float d = !live ? 0.0f : a.softplus ? ss_softplus_of(raw, e) : raw;
-      float g = live ? gn.get(v) : 0.0f;
-      if (gated) {
-        const float z = zn.get(v), k = ss_sigmoid<T>(z);
-        gzs[st][sc + v] = g * k * __builtin_fmaf(z, 1.0f - k, 1.0f);
-        g *= z * k;
-      }
-      pre[st][sc + v] = make_float4(d, d * xc.get(v), g, a.softplus ? ss_sigmoid_of(raw, e) : 1.0f);
+      d[v] = dn.get(v) + pars[0][sc + v];
+      g[v] = live ? gn.get(v) : 0.0f;
     }
+    ss_steps<V, true>(d, sg, a.softplus, live);
+    if (gated) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float z = zn.get(v), k = ss_sigmoid<T>(z);
+        gzs[st][sc + v] = g[v] * k * __builtin_fmaf(z, 1.0f - k, 1.0f);
+        g[v] *= z * k;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) pre[st][sc + v] = make_float4(d[v], d[v] * xc.get(v), g[v], sg[v]);
 #pragma unroll
     for (int i = 0; i < BR; ++i) {
       const int t = bt + i * BS;

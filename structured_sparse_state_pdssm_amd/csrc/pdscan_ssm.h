@@ -147,6 +147,31 @@ __device__ __forceinline__ float ss_softplus_of(float x, float e) {
   return fmaxf(x, 0.0f) + __builtin_fmaf(kLn2, __builtin_amdgcn_logf(w), e - (w - 1.0f));
 }
 
+// Steps of V cells, their slopes (sg[v]) where asked for, and zero behind the
+// end.  The cells side by side in one uniform branch: taken one by one, each
+// would wait for its own exponential and logarithm.
+template <int V, bool SLOPE>
+__device__ __forceinline__ void ss_steps(float (&d)[V], float (&sg)[V], int softplus, bool live) {
+  if (softplus) {
+    float e[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = ss_decay(d[v]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (SLOPE) sg[v] = ss_sigmoid_of(d[v], e[v]);
+      d[v] = ss_softplus_of(d[v], e[v]);
+    }
+  } else if (SLOPE) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) sg[v] = 1.0f;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    asm("" : "+v"(d[v]));   // (kept out of a branch on `live`)
+    d[v] = live ? d[v] : 0.0f;
+  }
+}
+
 template <int CTRL>
 __device__ __forceinline__ float ss_dpp(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
