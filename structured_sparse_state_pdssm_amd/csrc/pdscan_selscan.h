@@ -111,8 +111,8 @@ template <typename T, int S, int NS, int TS>
 __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(const SsArgs a) {
   constexpr int W = kSsTimeWaves, CW = 64 / NS, TT = W * TS, NP = S * NS;
   constexpr int V = TS * CW / 64, VB = TS * NP / 64;   // elements of a thread when a tile is staged
-  __shared__ __align__(16) float2 du[TT][CW];          // step, step times input
-  __shared__ __align__(16) float Bs[TT][NP], Cs[TT][NP];
+  __shared__ __align__(16) float2 du2[2][TT][CW];      // step, step times input; of two tiles in turn
+  __shared__ __align__(16) float Bs2[2][TT][NP], Cs2[2][TT][NP];
   __shared__ __align__(16) float ys[TT][CW], pars[2][CW];
   __shared__ __align__(16) float Es[W - 1][S * 64], Ps[W - 1][S * 64], Hs[2][S * 64];   // Hs: the state that enters a tile
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -166,17 +166,37 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
     Cp += ss_rows<T>(a.Cm, TT);
   };
   fetch(0);
+  // The outputs of a tile leave after the next one is staged: two barriers a tile.
+  SsRaw<T, V> xc = {}, zc = {};
+  auto finish = [&](bool live) {
+    if (live) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = __builtin_fmaf(pars[1][sc + v], xc.get(v), ys[st][sc + v]);
+      if (gated) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float z = zc.get(v);
+          o[v] *= z * ss_sigmoid<T>(z);
+        }
+      }
+      ss_store_at<T, V>(yp, yo, o);
+    }
+    yp += ss_rows<T>(a.y, TT);
+  };
   int turn = 0;
   for (int t0 = 0; t0 < s.len; t0 += TT, turn ^= 1) {
+    auto& du = du2[turn];
+    auto& Bs = Bs2[turn];
+    auto& Cs = Cs2[turn];
     // stage: steps behind the end have d = 0, which leaves the state as it is
     const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
-    const SsRaw<T, V> xc = xn, zc = zn;
     float d[V], none[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = dn.get(v) + pars[0][sc + v];
     ss_steps<V, false>(d, none, a.softplus, live);
 #pragma unroll
-    for (int v = 0; v < V; ++v) du[st][sc + v] = make_float2(d[v], d[v] * xc.get(v));
+    for (int v = 0; v < V; ++v) du[st][sc + v] = make_float2(d[v], d[v] * xn.get(v));
     {
       SsVec<float, VB> b, k;
 #pragma unroll
@@ -188,6 +208,9 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
       *(SsVec<float, VB>*)&Cs[bt][bn] = k;
     }
     __syncthreads();
+    if (t0) finish(sok);   // (a tile behind which there is another is whole)
+    xc = xn;
+    zc = zn;
     if (t0 + TT < s.len) fetch(t0 + TT);
 
     // this wave's steps from zero
@@ -265,22 +288,9 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
       if (NS == 4 || (lane & 15) < CW) ys[wave * TS + t4 + (lane >> 4)][lane & (CW - 1)] = r;
       __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
-    if (live) {
-      float o[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = __builtin_fmaf(pars[1][sc + v], xc.get(v), ys[st][sc + v]);
-      if (gated) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float z = zc.get(v);
-          o[v] *= z * ss_sigmoid<T>(z);
-        }
-      }
-      ss_store_at<T, V>(yp, yo, o);
-    }
-    yp += ss_rows<T>(a.y, TT);
   }
+  __syncthreads();
+  if (s.len > 0) finish(sok && (s.len - 1) / TT * TT + st < s.len);
   if (s.last && wave == W - 1) {
     float H[S];
     ss_lane_get(H, Hs[turn], lane);
