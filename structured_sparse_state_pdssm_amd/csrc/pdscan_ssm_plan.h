@@ -107,16 +107,29 @@ struct SsSplit {
 
 // `width` workgroups take a run, `room` of them are on the card at once; `states`
 // workgroups take a piece of the state pass (its waves are light: eight times the card).
-inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, long long states, bool always) {
+//
+// A sequence that is not cut takes its steps one after another, however
+// empty the card; cut, its steps cost `more` times what they do on a full
+// card (the state passes), and the launches what some `fixed` steps take.
+// 768 channels of 16 states, bf16, in us, uncut / cut:
+//   forwards (1.75, 500)  512 steps of 1: 27 / 29, of 4: 28 / 32;  1024 of 1: 51 / 30, of 4: 51 / 48, of 8: 60 / 66;
+//                         2048 of 6: 113 / 91, of 8: 114 / 110, of 12: 141 / 159
+//   backwards (.95, 240)  256 of 1: 71 / 71, of 8: 84 / 86;  512 of 4: 113 / 87, of 8: 133 / 126;
+//                         2048 of 8: 459 / 359, of 12: 559 / 539
+// Sequences of different lengths, where the longest counts, are taken as three of a third of the rows:
+//   16 in 2048 rows 32 / 49 and 130 / 117, 16 in 8192 102 / 88 and 358 / 254; 2048 channels, 40 in 8192 192 / 250 and 836 / 867
+inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, long long states, bool bwd) {
   SsSplit s;
   constexpr int kUnit = 64, kLeast = 128;
   const long long seqs = packed ? 1 : B;
-  const long long have = packed ? width * 2 : B * width;   // (of sequences of different lengths the longest counts)
+  const int like = packed ? (B < 3 ? B : 3) : B;
+  const double fill = (double)like * width / room, steps = (double)L / (packed ? like : 1);
+  const bool pays = fill < 0.9 && steps * (1.0 - (bwd ? 0.95 : 1.75) * fill) > (bwd ? 240.0 : 500.0);
   // Runs cost the state passes, not their number: where sequences are cut, four times the room evens out the end.
-  long long n = have * 2 >= room ? 1 : (4 * room + seqs * width - 1) / (seqs * width);
+  long long n = pays ? (4 * room + seqs * width - 1) / (seqs * width) : 1;
   if (n > L / kLeast) n = L / kLeast;
   s.cut = n > 1;
-  long long m = (s.cut || always) ? (8 * 256 + seqs * states - 1) / (seqs * states) : 1;   // pieces
+  long long m = (s.cut || bwd) ? (8 * 256 + seqs * states - 1) / (seqs * states) : 1;   // pieces
   if (m > L / kLeast) m = L / kLeast;
   if (m < n) m = n;
   if (m < 1) m = 1;
