@@ -87,8 +87,9 @@ def _sig(x):
 
 
 def sigmoid(x):
-    # an exponential (its argument put right: 4), an addition, a reciprocal
-    return x.map(_sig, lambda v: _sig(v) * (1 - _sig(v)), 8) if isinstance(x, Bound) else _sig(x)
+    # An exponential (two for it and its argument's product), an addition, a reciprocal and a product.  Where it is taken
+    # the short way the argument, x log2 e, is off by half a step of itself and by that of log2 e: 1.3 |x| U of e^-x.
+    return x.map(_sig, lambda v: _sig(v) * (1 - _sig(v)), 8 + 1.3 * np.abs(x.v)) if isinstance(x, Bound) else _sig(x)
 
 
 def softplus(x):

@@ -335,38 +335,28 @@ __global__ __launch_bounds__(256) void pdssm_conv_state_bwd_kernel(const CvArgs 
 template <typename T, int W>
 __global__ __launch_bounds__(256) void pdssm_conv_step_kernel(const CvStepArgs a) {
   constexpr int V = 4;
-  __shared__ int dup;
   const int tid = threadIdx.x, nb = (a.D / V + 255) / 256;
   const unsigned id = ss_block(a.row);
   const int b = id / nb, c = (id % nb * 256 + tid) * V;
   if (b >= a.B) return;
   const int slot = a.idx ? a.idx[b] : b;
-  bool bad = slot < 0 || slot >= a.slots;
-  if (!bad && a.idx) {
-    // a slot named twice: the first row has it
-    if (tid == 0) dup = 0;
-    __syncthreads();
-    int found = 0;
-    for (int r = tid; r < b; r += 256) found |= a.idx[r] == slot;
-    if (found) dup = 1;
-    __syncthreads();
-    bad = dup;
+  const bool ok = c < a.D, has = ok && slot >= 0 && slot < a.slots;
+  const int64_t yp = (int64_t)b * a.y.sb + c, sp = (int64_t)slot * (W - 1) * a.D + c;
+  SsRaw<T, V> win[W] = {};
+  float w[W][V] = {}, bias[V] = {}, o[V];
+  if (has) {   // under way before the search for an earlier row of the same slot
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) ss_load_raw(win[j], a.state, sp + (int64_t)j * a.D);
+    ss_load_raw(win[W - 1], a.x.p, (int64_t)b * a.x.sb + c);
+    cv_weights(w, bias, a.w, a.bias, c);
   }
-  if (c >= a.D) return;
-  const int64_t yp = (int64_t)b * a.y.sb + c;
-  if (bad) {   // an empty row gives zeros; a slot past the pool, or another row's, NaN
+  if (ss_taken(a.idx, b, slot, a.slots, tid & 63)) {
     const float f = slot < 0 ? 0.0f : __builtin_nanf("");
-    const float o[V] = {f, f, f, f};
-    ss_store<T, V>(a.y.p, yp, o);
+    const float e[V] = {f, f, f, f};
+    if (ok) ss_store<T, V>(a.y.p, yp, e);
     return;
   }
-  const int64_t sp = (int64_t)slot * (W - 1) * a.D + c;
-  SsRaw<T, V> win[W];
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) ss_load_raw(win[j], a.state, sp + (int64_t)j * a.D);
-  ss_load_raw(win[W - 1], a.x.p, (int64_t)b * a.x.sb + c);
-  float w[W][V], bias[V], o[V];
-  cv_weights(w, bias, a.w, a.bias, c);
+  if (!ok) return;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const float p = cv_pre<T, W, V>(win, w, bias[v], v);

@@ -91,18 +91,15 @@ __device__ __forceinline__ bool ss_unit(const SsArgs& a, int per, SsUnit& u) {
   return true;
 }
 
-// The first piece of the run that segment s is.
-__device__ __forceinline__ int ss_piece(const SsArgs& a, const SsSeg& s, int sid) {
-  if (!a.s.cu) return s.b * a.npiece + s.t0 / a.piece;
+// Piece `more` of the run that segment s is, counted over all.
+__device__ __forceinline__ int ss_piece(const SsArgs& a, const SsSeg& s, int sid, int more) {
+  if (!a.s.cu) return s.b * a.npiece + s.t0 / a.piece + more;
   if (!a.pieces) return s.b;
-  return __builtin_amdgcn_readfirstlane(a.pieces[s.b] + (a.runs ? (sid - a.runs[s.b]) * a.run : 0));
+  const int first = __builtin_amdgcn_readfirstlane(a.pieces[s.b]);
+  return ss_piece_at(first, (a.runs ? __builtin_amdgcn_readfirstlane(sid - a.runs[s.b]) * a.run : 0) + more, a.npieces);
 }
-
-// The gradient's tile at step t of piece `at` of sequence b, which starts at
-// row t0: tiles of different pieces do not meet.
 __device__ __forceinline__ int64_t ss_tile(const SsArgs& a, int b, int at, int t0, int t) {
-  const int per = (a.s.L + kSsBwdTile - 1) / kSsBwdTile;
-  return (a.s.cu ? (int64_t)at + t0 / kSsBwdTile : (int64_t)b * per + t0 / kSsBwdTile) + t / kSsBwdTile;
+  return ss_tile_of(a.s.cu ? 0 : (a.s.L + kSsBwdTile - 1) / kSsBwdTile, b, at, t0, t, kSsBwdTile);
 }
 
 // ---- prompts
@@ -127,7 +124,7 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
   if (wave == W - 1) {
     float H[S];
     if (a.seg)
-      ss_load_state(H, a.seg, (int64_t)ss_piece(a, s, u.sid) * a.D + ch, q * S, a.N, ok);
+      ss_load_state(H, a.seg, (int64_t)ss_piece(a, s, u.sid, 0) * a.D + ch, q * S, a.N, ok);
     else
       ss_load_state(H, a.h0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     ss_lane_put(Hs[0], H, lane);
@@ -457,7 +454,6 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     }
     return;
   }
-  const int piece0 = ss_piece(a, s, u.sid);
   float A2[S], gA[S];
   ss_load_A(A2, a.A, ch, q * S, a.N, ok);
   if (wave == 0) {
@@ -465,7 +461,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     if (s.last)
       ss_load_state(R, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     else
-      ss_load_state(R, a.adj, (int64_t)(piece0 + (s.len - 1) / a.piece) * a.D + ch, q * S, a.N, ok);
+      ss_load_state(R, a.adj, (int64_t)ss_piece(a, s, u.sid, (s.len - 1) / a.piece) * a.D + ch, q * S, a.N, ok);
     ss_lane_put(Rt[0][cg], R, lane);
   }
 #pragma unroll
@@ -547,11 +543,12 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     if (t0) fetch(t0 - TT);
     // the state at the tile's start: what it was from its piece's start, and what entered there
     if (t0 < pc * a.piece) --pc;
-    const int64_t tile = ss_tile(a, s.b, piece0 + pc, s.t0 + pc * a.piece, t0 - pc * a.piece);
+    const int at = ss_piece(a, s, u.sid, pc);
+    const int64_t tile = ss_tile(a, s.b, at, s.t0 + pc * a.piece, t0 - pc * a.piece);
     float hin[S] = {}, H0[S];
     if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), lane);
     const float cum = ok ? a.cum[tile * a.D + ch] : 0.0f;
-    ss_load_state(H0, a.seg ? a.seg : a.h0, (int64_t)(a.seg ? piece0 + pc : s.b) * a.D + ch, q * S, a.N, ok);
+    ss_load_state(H0, a.seg ? a.seg : a.h0, (int64_t)(a.seg ? at : s.b) * a.D + ch, q * S, a.N, ok);
 
     // from zero, forwards and backwards
     const int me = cg * W + wave, tw = wave * TS;
@@ -767,69 +764,51 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
 // ---- one token
 //
 // Four states a lane, a channel in neighbouring lanes: the state streams
-// through in whole lines, once each way, which is the time.
+// through in whole lines, once each way, which is the time.  Everything is
+// under way before the search for an earlier row of the same slot.
 template <typename T, int NS>
 __global__ __launch_bounds__(256) void pdssm_selscan_step_kernel(const SsStepArgs a) {
   constexpr int CW = 256 / NS;
-  __shared__ int dup;
   const int tid = threadIdx.x, nb = (a.D + CW - 1) / CW;
   const unsigned id = ss_block(a.row);
   const int b = id / nb, ch = id % nb * CW + tid / NS, q = tid % NS, n0 = q * 4;
   if (b >= a.B) return;
   const int slot = a.idx ? a.idx[b] : b;
-  const bool ok = ch < a.D;
-  bool bad = slot < 0 || slot >= a.slots;
-  if (!bad && a.idx) {
-    // a slot named twice: the first row has it
-    if (tid == 0) dup = 0;
-    __syncthreads();
-    int found = 0;
-    for (int r = tid; r < b; r += 256) found |= a.idx[r] == slot;
-    if (found) dup = 1;
-    __syncthreads();
-    bad = dup;
+  const bool ok = ch < a.D, has = ok && n0 < a.N && slot >= 0 && slot < a.slots;
+  float* hp = a.state + ((int64_t)slot * a.D + ch) * a.N + n0;
+  float4 h = make_float4(0, 0, 0, 0), A = h;
+  SsRaw<T, 4> vb = {}, vc = {};
+  float x = 0.0f, raw = 0.0f, z = 0.0f, skip = 0.0f;
+  if (has) {
+    h = *(const float4*)hp;
+    const int g = ch / (a.D / a.G);
+    A = *(const float4*)(a.A + (int64_t)ch * a.N + n0);
+    ss_load_raw(vb, a.Bm.p, (int64_t)b * a.Bm.sb + (int64_t)g * a.Bm.sh + n0);
+    ss_load_raw(vc, a.Cm.p, (int64_t)b * a.Cm.sb + (int64_t)g * a.Cm.sh + n0);
+    x = T::get(((const typename T::E*)a.x.p)[(int64_t)b * a.x.sb + ch]);
+    raw = T::get(((const typename T::E*)a.dt.p)[(int64_t)b * a.dt.sb + ch]) + (a.bias ? a.bias[ch] : 0.0f);
+    if (a.z.p) z = T::get(((const typename T::E*)a.z.p)[(int64_t)b * a.z.sb + ch]);
+    skip = a.skip ? a.skip[ch] : 0.0f;
   }
-  if (bad) {   // an empty row gives zeros; a slot past the pool, or another row's, NaN
+  if (ss_taken(a.idx, b, slot, a.slots, tid & 63)) {
     const float f = slot < 0 ? 0.0f : __builtin_nanf("");
     if (ok && q == 0) ss_store<T, 1>(a.y.p, (int64_t)b * a.y.sb + ch, &f);
     return;
   }
-  if (!ok) return;   // (whole channels: their lanes leave together)
-  const int g = ch / (a.D / a.G);
-  const bool has = n0 < a.N;
-  float4 h = make_float4(0, 0, 0, 0), A = h;
-  float B[4] = {}, C[4] = {};
-  float* hp = a.state + ((int64_t)slot * a.D + ch) * a.N + n0;
-  if (has) {
-    h = *(const float4*)hp;
-    A = *(const float4*)(a.A + (int64_t)ch * a.N + n0);
-    const auto vb = ss_load<T, 4>(a.Bm.p, (int64_t)b * a.Bm.sb + (int64_t)g * a.Bm.sh + n0);
-    const auto vc = ss_load<T, 4>(a.Cm.p, (int64_t)b * a.Cm.sb + (int64_t)g * a.Cm.sh + n0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      B[i] = T::get(vb.e[i]);
-      C[i] = T::get(vc.e[i]);
-    }
-  }
-  const float x = T::get(((const typename T::E*)a.x.p)[(int64_t)b * a.x.sb + ch]);
-  const float raw = T::get(((const typename T::E*)a.dt.p)[(int64_t)b * a.dt.sb + ch]) + (a.bias ? a.bias[ch] : 0.0f);
   const float d = a.softplus ? ss_softplus_of(raw, ss_decay(raw)) : raw, u = d * x, w = d * kLog2e;
-  h.x = __builtin_fmaf(ss_exp2(w * A.x), h.x, u * B[0]);
-  h.y = __builtin_fmaf(ss_exp2(w * A.y), h.y, u * B[1]);
-  h.z = __builtin_fmaf(ss_exp2(w * A.z), h.z, u * B[2]);
-  h.w = __builtin_fmaf(ss_exp2(w * A.w), h.w, u * B[3]);
-  float y = (C[0] * h.x + C[1] * h.y) + (C[2] * h.z + C[3] * h.w);
+  h.x = __builtin_fmaf(ss_exp2(w * A.x), h.x, u * vb.get(0));
+  h.y = __builtin_fmaf(ss_exp2(w * A.y), h.y, u * vb.get(1));
+  h.z = __builtin_fmaf(ss_exp2(w * A.z), h.z, u * vb.get(2));
+  h.w = __builtin_fmaf(ss_exp2(w * A.w), h.w, u * vb.get(3));
+  if (has) *(float4*)hp = h;
+  float y = has ? (vc.get(0) * h.x + vc.get(1) * h.y) + (vc.get(2) * h.z + vc.get(3) * h.w) : 0.0f;
   y += ss_dpp<kDppXor1>(y);
   if constexpr (NS >= 4) y += ss_dpp<kDppXor2>(y);
   if constexpr (NS >= 8) y += ss_dpp<kDppHalfMirror>(y);
   if constexpr (NS >= 16) y += ss_dpp<kDppRor8>(y);
-  if (has) *(float4*)hp = h;
-  if (q == 0) {
-    y = __builtin_fmaf(a.skip ? a.skip[ch] : 0.0f, x, y);
-    if (a.z.p) {
-      const float z = T::get(((const typename T::E*)a.z.p)[(int64_t)b * a.z.sb + ch]);
-      y *= z * ss_sigmoid<T>(z);
-    }
+  if (ok && q == 0) {
+    y = __builtin_fmaf(skip, x, y);
+    if (a.z.p) y *= z * ss_sigmoid<T>(z);
     ss_store<T, 1>(a.y.p, (int64_t)b * a.y.sb + ch, &y);
   }
 }

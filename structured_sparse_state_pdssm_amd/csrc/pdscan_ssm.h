@@ -252,6 +252,18 @@ __device__ __forceinline__ long long ss_near(unsigned id, long long n) {
   return (long long)(id % 8) * per + id / 8;   // at or past n: nothing to do
 }
 
+// Whether row b of a step has no state of its own: a slot that is empty, past
+// the pool, or an earlier row's.  Every wave searches for itself: 256 rows are
+// four loads at once, and no wave waits for another.
+__device__ __forceinline__ bool ss_taken(const int32_t* idx, int b, int slot, int slots, int lane) {
+  if (slot < 0 || slot >= slots) return true;
+  if (!idx) return false;
+  int found = 0;
+#pragma unroll 4
+  for (int r = lane; r < b; r += 64) found |= idx[r] == slot;
+  return __any(found);
+}
+
 struct SsSeg {
   int b, t0, len;                // sequence; first row of the step axis, rows
   int64_t vb;                    // row of the batch axis

@@ -252,7 +252,7 @@ hipError_t scan_states(SsArgs& a, const pdssm_selscan_dims* d, const ScanWs& w, 
   const SsSplit& p = w.split;
   const int bf16 = d->in_dtype == PDSSM_BF16;
   a.header = ws && bytes >= pdscan::kLaHeader ? (uint32_t*)ws : nullptr;
-  a.piece = p.piece; a.npiece = p.npiece; a.run = p.run;
+  a.piece = p.piece; a.npiece = p.npiece; a.run = p.run; a.npieces = p.pieces;
   pdscan::SsSegs pieces = {cu, nullptr, d->B, d->L, p.npiece, p.piece, p.pieces};
   pdscan::SsSegs runs = {cu, nullptr, d->B, d->L, p.nseg, p.seg, p.segs};
   hipError_t e = hipSuccess;

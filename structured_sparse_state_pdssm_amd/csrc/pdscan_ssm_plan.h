@@ -21,6 +21,18 @@ struct SsSegs {
   int B, L, nseg, seg, segs;     // nseg per sequence (not packed), steps per segment, segments in all (bound)
 };
 
+// Indexes of pieces and tiles, also on the host.  Offsets of packed sequences
+// that are out of order can ask for more pieces than there is room for; the
+// table drops those behind the bound, and a run that names one gets the last.
+constexpr int ss_piece_at(int first, int more, int pieces) {
+  return first > pieces - 1 - more ? pieces - 1 : first + more;
+}
+// The gradient's tile at step t of piece `at` of sequence b, which starts at
+// row t0: tiles of different pieces do not meet (per: tiles of a sequence, 0 where packed).
+constexpr int64_t ss_tile_of(int per, int b, int at, int t0, int t, int tile) {
+  return (per ? (int64_t)b * per : (int64_t)at) + t0 / tile + t / tile;
+}
+
 // One pass of the selective scan.  Element (b, t, d) of x, dt, z, y and their
 // gradients is at sb b + st t + d; B and C have a head axis of G groups.
 struct SsArgs {
@@ -31,7 +43,7 @@ struct SsArgs {
   float *hL, *gh0;               // gh0 may be NULL
   SsSegs s;                      // of this launch: pieces in the state pass, runs of `run` pieces in the others
   const int32_t *pieces, *runs;  // packed: first piece and first run of every sequence (runs NULL: whole sequences)
-  int piece, npiece, run;        // steps of a piece, pieces of a sequence (not packed)
+  int piece, npiece, run, npieces;   // steps of a piece, pieces of a sequence (not packed), of a run, in all
   float *seg, *adj;              // [pieces][D][N]: contributions of pieces, then entering (adjoint) states; NULL: one piece
   float *sum;                    // [pieces][D]: sums of the steps d_t of a piece
   float *ckpt, *cum;             // states at the tiles' starts, each piece from zero, and the sums up to there

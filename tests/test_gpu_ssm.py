@@ -259,6 +259,86 @@ def test_scan_packed(dt, lens, N, G):
         close(g[k], sums[k], k)
 
 
+def test_scan_of_whole_sequences_from_many_pieces():
+    """Enough channels that no sequence is cut, while the states behind the gradient still come in pieces: batched, and packed."""
+    P = lib()
+    x, gy, gh = scan_inputs(48, 260, 256, 8, BF, seed=7)
+    check_scan_bwd(x, P.pdssm_selscan_bwd(**x, g_y=gy, g_hL=gh), gy, gh)
+    lens = (130, 0, 129, 45)
+    x, gy, gh = scan_inputs(1, sum(lens), 4096, 8, BF, S=4, seed=8)
+    g = P.pdssm_selscan_bwd(**x, g_y=gy, g_hL=gh, cu_seqlens=bounds(lens))
+    for i, m in enumerate(lens):
+        at = slice(sum(lens[:i]), sum(lens[:i]) + m)
+        if not m:
+            assert torch.equal(g["g_h0"][i], gh[i])
+            continue
+        xi = dict(x, h0=x["h0"][i:i + 1], **{k: x[k][:, at] for k in ("x", "dt", "z")}, **{k: x[k][:, :, at] for k in ("Bm", "Cm")})
+        r = O.selscan_bwd(**scan_args(xi), g_y=bound(gy[:, at]), g_hL=bound(gh[i:i + 1]))
+        for k in ("g_x", "g_dt", "g_z"):
+            close(g[k][:, at], r[k], f"{k} of {i}")
+        for k in ("g_B", "g_C"):
+            close(g[k][:, :, at], r[k], f"{k} of {i}")
+        close(g["g_h0"][i:i + 1], r["g_h0"], f"g_h0 of {i}")
+
+
+def test_rows_past_32_bits():
+    """Tensors of more than 4 GiB: the last sequence of a packed call is what it is by itself."""
+    P = lib()
+    L, last, D, N = 270000, 70, 8192, 8
+    r = torch.Generator("cuda").manual_seed(3)
+    t = lambda *s: torch.randn(s, generator=r, device="cuda", dtype=BF)  # noqa: E731
+    cu = torch.tensor([0, L - last, L], dtype=torch.int32).cuda()
+    x, gy = t(1, L, D), t(1, L, D)
+    tail = slice(L - last, L)
+    w = torch.randn(D, 4, generator=r, device="cuda")
+    y, xL = P.pdssm_conv_fwd(x, w, cu_seqlens=cu)
+    y2, xL2 = P.pdssm_conv_fwd(x[:, tail].clone(), w)
+    assert torch.equal(y[:, tail], y2) and torch.equal(xL[1:], xL2)
+    g = P.pdssm_conv_bwd(x, w, gy, cu_seqlens=cu, out={"g_x": y})
+    assert torch.equal(g["g_x"][:, tail], P.pdssm_conv_bwd(x[:, tail].clone(), w, gy[:, tail].clone())["g_x"])
+    n = torch.randn(D, generator=r, device="cuda")
+    assert torch.equal(P.pdssm_norm_fwd(x, n, out=y)[:, tail], P.pdssm_norm_fwd(x[:, tail].clone(), n))
+    assert torch.equal(P.pdssm_norm_bwd(x, n, gy, out={"g_x": y})["g_x"][:, tail], P.pdssm_norm_bwd(x[:, tail].clone(), n, gy[:, tail].clone())["g_x"])
+    del y
+    A = -torch.exp(torch.randn(D, N, generator=r, device="cuda"))
+    Bm, Cm = (t(1, L, 1, N).transpose(1, 2) for _ in range(2))
+    part = dict(x=x[:, tail].clone(), dt=x[:, tail].clone(), A=A, Bm=Bm[:, :, tail], Cm=Cm[:, :, tail])
+    y, hL = P.pdssm_selscan_fwd(x, x, A, Bm, Cm, cu_seqlens=cu)
+    check_scan(part, y[:, tail], hL[1:])
+    g = P.pdssm_selscan_bwd(x, x, A, Bm, Cm, gy, cu_seqlens=cu, out={"g_x": y})
+    ref = O.selscan_bwd(**scan_args(part), g_y=bound(gy[:, tail]))
+    for k in ("g_x", "g_dt"):
+        close(g[k][:, tail], ref[k], k)
+    for k in ("g_B", "g_C"):
+        close(g[k][:, :, tail], ref[k], k)
+
+
+@DT
+def test_offsets_that_are_not_in_order(dt):
+    """Offsets out of range or of order are cut to the rows: every call ends, and touches nothing outside its tensors (the
+    guard rows around the outputs stay as they are); what comes before the first wrong offset is right."""
+    P = lib()
+    L, D, N = 700, 48, 16
+    for off in ((0, 300, 5000, 700), (0, 300, 100, 700), (-50, 300, 250, 900), (0, 700, 0, 700, 0, 700, 0, 700), (700, 0, 700, 3)):
+        S = len(off) - 1
+        x, gy, gh = scan_inputs(1, L, D, N, dt, 2, S=S, seed=11)
+        cu = torch.tensor(off, dtype=torch.int32).cuda()
+        guard = lambda t, rows=8: torch.full((t.shape[0], t.shape[1] + 2 * rows, *t.shape[2:]), 7.0, dtype=t.dtype, device="cuda")  # noqa: E731
+        full = {k: guard(gy) for k in ("y", "g_x", "g_dt", "g_z", "c", "cg")}
+        mid = {k: t[:, 8:-8] for k, t in full.items()}
+        y, hL = P.pdssm_selscan_fwd(**x, cu_seqlens=cu, out={"y": mid["y"]})
+        P.pdssm_selscan_bwd(**x, g_y=gy, g_hL=gh, cu_seqlens=cu, out={k: mid[k] for k in ("g_x", "g_dt", "g_z")})
+        c, cy, cx = conv_inputs(1, L, D, 4, dt, S=S)
+        P.pdssm_conv_fwd(**c, cu_seqlens=cu, out={"y": mid["c"]})
+        P.pdssm_conv_bwd(**c, g_y=cy, g_xL=cx, cu_seqlens=cu, out={"g_x": mid["cg"]})
+        torch.cuda.synchronize()
+        for t in full.values():
+            assert (t[:, :8] == 7).all() and (t[:, -8:] == 7).all()
+        if off[:2] == (0, 300) and off[2] != 100:
+            one = dict(x, h0=x["h0"][:1], **{k: x[k][:, :300] for k in ("x", "dt", "z")}, **{k: x[k][:, :, :300] for k in ("Bm", "Cm")})
+            check_scan(one, y[:, :300], hL[:1])
+
+
 @DT
 def test_scan_decays_of_all_sizes(dt):
     """Steps that forget everything, and steps that forget nothing."""
