@@ -91,12 +91,12 @@ __device__ __forceinline__ bool ss_unit(const SsArgs& a, int per, SsUnit& u) {
   return true;
 }
 
-// Piece `more` of the run that segment s is, counted over all.
-__device__ __forceinline__ int ss_piece(const SsArgs& a, const SsSeg& s, int sid, int more) {
-  if (!a.s.cu) return s.b * a.npiece + s.t0 / a.piece + more;
+// The first piece of the run that segment s is, counted over all.
+__device__ __forceinline__ int ss_piece(const SsArgs& a, const SsSeg& s, int sid) {
+  if (!a.s.cu) return __builtin_amdgcn_readfirstlane(s.b * a.npiece + s.t0 / a.piece);
   if (!a.pieces) return s.b;
   const int first = __builtin_amdgcn_readfirstlane(a.pieces[s.b]);
-  return ss_piece_at(first, (a.runs ? __builtin_amdgcn_readfirstlane(sid - a.runs[s.b]) * a.run : 0) + more, a.npieces);
+  return ss_piece_at(first, a.runs ? __builtin_amdgcn_readfirstlane(sid - a.runs[s.b]) * a.run : 0, a.npieces);
 }
 __device__ __forceinline__ int64_t ss_tile(const SsArgs& a, int b, int at, int t0, int t) {
   return ss_tile_of(a.s.cu ? 0 : (a.s.L + kSsBwdTile - 1) / kSsBwdTile, b, at, t0, t, kSsBwdTile);
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
   if (wave == W - 1) {
     float H[S];
     if (a.seg)
-      ss_load_state(H, a.seg, (int64_t)ss_piece(a, s, u.sid, 0) * a.D + ch, q * S, a.N, ok);
+      ss_load_state(H, a.seg, (int64_t)ss_piece(a, s, u.sid) * a.D + ch, q * S, a.N, ok);
     else
       ss_load_state(H, a.h0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     ss_lane_put(Hs[0], H, lane);
@@ -302,12 +302,18 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
 // state and the sum at the start of every tile of the gradient.  Backwards
 // (REV) it is the adjoint state that flows out of the piece's start,
 // l = a_t (l + g_t C_t), with g the gradient of y before its gate.
+template <int S, int NS>
+struct SsStateLds {
+  static constexpr int TT = 16, CC = kSsStateGroups * (64 / NS);
+  alignas(16) float2 du[2][TT][CC];
+  alignas(16) float Bs[2][TT][S * NS];
+};
 template <typename T, int S, int NS, bool REV>
-__global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a) {
+__device__ __forceinline__ void ss_state_body(const SsArgs& a, SsStateLds<S, NS>& lds) {
   constexpr int CG = kSsStateGroups, CW = 64 / NS, CC = CG * CW, NP = S * NS, TT = 16;
   constexpr int V = TT * CC / 256, VB = TT * NP / 64 < 8 ? TT * NP / 64 : 8, BT = TT * NP / VB;   // B by BT threads
-  __shared__ __align__(16) float2 du[2][TT][CC];
-  __shared__ __align__(16) float Bs[2][TT][NP];
+  auto& du = lds.du;
+  auto& Bs = lds.Bs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   SsUnit u;
   SsSeg s;
@@ -401,6 +407,16 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
   if (!REV && ok && q == 0) a.sum[(int64_t)u.sid * a.D + ch] = (float)total;
 }
 
+// Both directions in one launch (z), as neither waits for the other.
+template <typename T, int S, int NS>
+__global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a) {
+  __shared__ SsStateLds<S, NS> lds;
+  if (blockIdx.z)
+    ss_state_body<T, S, NS, true>(a, lds);
+  else
+    ss_state_body<T, S, NS, false>(a, lds);
+}
+
 // ---- gradient
 //
 //   l_t = g_t C_t + a_{t+1} l_{t+1}                    g = g_y silu(z)
@@ -441,11 +457,12 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   const int c = lane / NS, q = lane % NS, lc = cg * CW + c, ch = u.c0 + lc;
   const bool ok = ch < u.end;
   const bool found = ss_segment(a.s, u.sid, s);
+  float* partA = a.partA + (int64_t)u.sid * a.D * (a.N + 2);
   if (!found || s.len <= 0) {   // no rows: nothing but sums of none and what passes through
     const float zero[S] = {};
     if (wave == 0) {
-      ss_store_state(zero, a.partA, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
-      if (ok && q < 2) a.partD[((int64_t)u.sid * 2 + q) * a.D + ch] = 0.0f;
+      ss_store_state(zero, partA, ch, q * S, a.N, ok);
+      if (ok && q < 2) partA[(int64_t)a.D * (a.N + q) + ch] = 0.0f;
       if (found && s.first && a.gh0) {
         float r[S];
         ss_load_state(r, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
@@ -454,6 +471,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     }
     return;
   }
+  const int piece0 = ss_piece(a, s, u.sid);
   float A2[S], gA[S];
   ss_load_A(A2, a.A, ch, q * S, a.N, ok);
   if (wave == 0) {
@@ -461,7 +479,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     if (s.last)
       ss_load_state(R, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     else
-      ss_load_state(R, a.adj, (int64_t)ss_piece(a, s, u.sid, (s.len - 1) / a.piece) * a.D + ch, q * S, a.N, ok);
+      ss_load_state(R, a.adj, (int64_t)ss_piece_at(piece0, (s.len - 1) / a.piece, a.npieces) * a.D + ch, q * S, a.N, ok);
     ss_lane_put(Rt[0][cg], R, lane);
   }
 #pragma unroll
@@ -508,7 +526,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     zp -= ss_rows<T>(a.z, TT);
     Bp -= ss_rows<T>(vbc, TT);
   };
-  int pc = (s.len - 1) / a.piece, turn = 0;   // piece of the tile
+  int pc = __builtin_amdgcn_readfirstlane((s.len - 1) / a.piece), turn = 0;   // piece of the tile
   fetch(last);
   for (int t0 = last; t0 >= 0; t0 -= TT, turn ^= 1) {
     const bool live = sok && t0 + st < s.len;
@@ -543,7 +561,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     if (t0) fetch(t0 - TT);
     // the state at the tile's start: what it was from its piece's start, and what entered there
     if (t0 < pc * a.piece) --pc;
-    const int at = ss_piece(a, s, u.sid, pc);
+    const int at = ss_piece_at(piece0, pc, a.npieces);
     const int64_t tile = ss_tile(a, s.b, at, s.t0 + pc * a.piece, t0 - pc * a.piece);
     float hin[S] = {}, H0[S];
     if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), lane);
@@ -752,11 +770,11 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
 #pragma unroll
       for (int j = 0; j < S; ++j) sumA[j] += e[j];
     }
-    ss_store_state(sumA, a.partA, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
+    ss_store_state(sumA, partA, ch, q * S, a.N, ok);
     if (ok && q < 2) {
       float o = 0.0f;
       for (int t = 0; t < TT; ++t) o += outs[q * (TT * CC + 16) + t * CC + lc];
-      a.partD[((int64_t)u.sid * 2 + q) * a.D + ch] = o;
+      partA[(int64_t)a.D * (a.N + q) + ch] = o;
     }
   }
 }

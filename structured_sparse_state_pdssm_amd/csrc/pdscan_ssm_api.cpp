@@ -160,7 +160,7 @@ int scan_grid(const pdssm_selscan_dims* d, const SsSplit& s) {
 
 struct ScanWs {
   SsSplit split;
-  size_t table, pieces, run_table, runs, seg, adj, sum, ckpt, cum, part, partA, partD, mid, total;
+  size_t table, pieces, run_table, runs, seg, adj, sum, ckpt, cum, part, partA, mid, total;
   int blocks;                          // (gradient) channel blocks of a group
 };
 
@@ -214,9 +214,8 @@ ScanWs scan_bwd_ws(const pdssm_selscan_dims* d) {
   w.ckpt = l.put(tiles * scan_blocks(d, 1) * shape.S * 64 * 4);
   w.cum = l.put(tiles * d->D * 4);
   w.part = l.put(2 * (size_t)d->G * w.blocks * rows * d->N * 4);
-  w.partA = l.put((size_t)w.split.segs * d->D * d->N * 4);
-  w.partD = l.put((size_t)w.split.segs * d->D * 2 * 4);
-  w.mid = l.put(w.split.segs > pdscan::kSsSumMost ? (size_t)pdscan::kSsSumMid * d->D * d->N * 4 : 0);
+  w.partA = l.put((size_t)w.split.segs * d->D * (d->N + 2) * 4);
+  w.mid = l.put(w.split.segs > pdscan::kSsSumMost ? (size_t)pdscan::kSsSumMid * d->D * (d->N + 2) * 4 : 0);
   w.total = l.at;
   return w;
 }
@@ -274,24 +273,19 @@ hipError_t scan_states(SsArgs& a, const pdssm_selscan_dims* d, const ScanWs& w, 
   }
   if (p.states || bwd) {
     a.s = pieces;
-    if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, 0, st);
+    if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, st);
   }
   if (p.states) {
     pdscan::SsCarryArgs c = {};
     c.A = a.A;
-    c.user = a.h0;
-    c.seg = a.seg;
+    c.user[0] = a.h0;
+    c.user[1] = a.ghL;
+    c.seg[0] = a.seg;
+    c.seg[1] = a.adj;
     c.sum = a.sum;
     c.starts = a.pieces;
-    c.B = d->B; c.D = d->D; c.N = d->N; c.nseg = p.npiece;
+    c.B = d->B; c.D = d->D; c.N = d->N; c.npiece = p.npiece;
     if (e == hipSuccess) e = pdscan::launch_selscan_carry(c, st);
-    if (a.adj) {
-      if (e == hipSuccess) e = pdscan::launch_selscan_state(a, bf16, 1, st);
-      c.user = a.ghL;
-      c.seg = a.adj;
-      c.rev = 1;
-      if (e == hipSuccess) e = pdscan::launch_selscan_carry(c, st);
-    }
   }
   a.s = runs;
   return e;
@@ -440,11 +434,12 @@ int pdssm_conv_bwd(const pdssm_conv_dims* dims, const pdssm_view* x, const float
   SsSumArgs s = {};
   s.part = a.part;
   s.mid = (float*)(ws + n.mid);
-  s.out = g_w;
-  s.out2 = g_bias;
+  s.out[0] = g_w;
+  s.out[1] = g_bias;
+  s.share[0] = (int64_t)d.D * d.W;
+  s.share[1] = d.D;
   s.parts = n.parts;
   s.width = n.width;
-  s.first = (int64_t)d.D * d.W;
   if (e == hipSuccess) e = pdscan::launch_ssm_sum(s, st);
   return launched(e);
 }
@@ -554,7 +549,6 @@ int pdssm_selscan_bwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const
   a.cum = (float*)(ws + w.cum);
   a.part = (float*)(ws + w.part);
   a.partA = (float*)(ws + w.partA);
-  a.partD = (float*)(ws + w.partD);
   hipError_t e = scan_states(a, dims, w, cu_seqlens, ws, workspace_bytes, true, st);
   if (e == hipSuccess) e = pdscan::launch_selscan_bwd(a, bf16, st);
   pdscan::SsFoldArgs f = {};
@@ -564,20 +558,16 @@ int pdssm_selscan_bwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const
   f.cu = cu_seqlens;
   f.B = d.B; f.L = d.L; f.N = d.N; f.G = d.G; f.blocks = w.blocks;
   f.rows = a.rows;
+  f.sum.part = a.partA;
+  f.sum.mid = (float*)(ws + w.mid);
+  f.sum.parts = w.split.segs;
+  f.sum.width = (int64_t)d.D * (d.N + 2);
+  f.sum.out[0] = g_A;
+  f.sum.out[1] = g_skip;
+  f.sum.out[2] = g_bias;
+  f.sum.share[0] = (int64_t)d.D * d.N;
+  f.sum.share[1] = f.sum.share[2] = d.D;
   if (e == hipSuccess) e = pdscan::launch_selscan_fold(f, bf16, st);
-  SsSumArgs s = {};
-  s.part = a.partA;
-  s.mid = (float*)(ws + w.mid);
-  s.out = g_A;
-  s.parts = w.split.segs;
-  s.width = s.first = (int64_t)d.D * d.N;
-  if (e == hipSuccess) e = pdscan::launch_ssm_sum(s, st);
-  s.part = a.partD;
-  s.out = g_skip;
-  s.out2 = g_bias;
-  s.width = 2ll * d.D;
-  s.first = d.D;
-  if (e == hipSuccess) e = pdscan::launch_ssm_sum(s, st);
   return launched(e);
 }
 
@@ -664,10 +654,10 @@ int pdssm_norm_bwd(const pdssm_norm_dims* dims, const pdssm_view* x, const float
   s.part = a.part;
   s.mid = (float*)(ws + n.mid);
   s.parts = d.per_head ? a.chunks : a.chunks * d.H;
-  s.first = d.per_head ? all : d.d;
-  s.width = both * s.first;
-  s.out = g_w;
-  s.out2 = g_res_scale;
+  s.share[0] = s.share[1] = d.per_head ? all : d.d;
+  s.width = both * s.share[0];
+  s.out[0] = g_w;
+  s.out[1] = g_res_scale;
   if (e == hipSuccess) e = pdscan::launch_ssm_sum(s, st);
   return launched(e);
 }

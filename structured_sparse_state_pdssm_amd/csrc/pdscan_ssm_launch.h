@@ -8,7 +8,7 @@
 namespace pdscan {
 
 hipError_t launch_selscan_fwd(const SsArgs& a, int bf16, hipStream_t st);
-hipError_t launch_selscan_state(const SsArgs& a, int bf16, int rev, hipStream_t st);
+hipError_t launch_selscan_state(const SsArgs& a, int bf16, hipStream_t st);   // with a.adj backwards too
 hipError_t launch_selscan_carry(const SsCarryArgs& a, hipStream_t st);
 hipError_t launch_selscan_bwd(const SsArgs& a, int bf16, hipStream_t st);
 hipError_t launch_selscan_fold(const SsFoldArgs& a, int bf16, hipStream_t st);

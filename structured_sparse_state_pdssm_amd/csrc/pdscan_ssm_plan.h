@@ -48,7 +48,7 @@ struct SsArgs {
   float *sum;                    // [pieces][D]: sums of the steps d_t of a piece
   float *ckpt, *cum;             // states at the tiles' starts, each piece from zero, and the sums up to there
   float *part;                   // partial g_B and g_C [2][blocks of all groups][rows][N]
-  float *partA, *partD;          // [segments][D][N]; [segments][2][D]: g_skip, g_bias
+  float* partA;                  // [segments][D N + 2 D]: g_A, g_skip, g_bias
   uint32_t* header;              // workspace header
   int D, N, G, softplus;
   unsigned row;                  // workgroups along x of the launch
@@ -56,29 +56,32 @@ struct SsArgs {
 };
 
 struct SsCarryArgs {
-  const float *A, *user;         // user: state before the first segment in this direction [B][D][N], NULL: zero
-  float *seg;
-  const float *sum;
-  const int32_t* starts;         // packed: first segment of every sequence
-  int B, D, N, nseg, rev, blocks;
+  const float *A, *user[2];      // user: states before the first piece, adjoint states behind the last [B][D][N], NULL: zero
+  float* seg[2];                 // of both directions; the second NULL: forwards only
+  const float* sum;
+  const int32_t* starts;         // packed: first piece of every sequence
+  int B, D, N, npiece, blocks;
   unsigned row;
 };
 
-// Sums that finish a gradient: over channel blocks into g_B and g_C, over segments into the parameters'.
+// Sums of `parts` rows of `width` columns, of which each output takes its share in turn (NULL: no more).
+struct SsSumArgs {
+  const float* part;
+  float* out[3];
+  int64_t share[3];
+  float* mid;                    // [kSsSumMid][width] where there are more than kSsSumMost parts
+  int parts;
+  int64_t width;
+};
+// What finishes a scan's gradient: channel blocks' parts of g_B and g_C, and those sums.
 struct SsFoldArgs {
   const float* part;
   LaView out[2];
   const int32_t* cu;
   int B, L, N, G, blocks;        // blocks per group
   long long rows;
-};
-// Sums of `parts` rows of `width` columns: the first `first` go to out, the others to out2 (NULL: nowhere).
-struct SsSumArgs {
-  const float* part;
-  float *out, *out2;
-  float* mid;                    // [kSsSumMid][width] where there are more than kSsSumMost parts
-  int parts;
-  int64_t width, first;
+  unsigned folds;                // workgroups of each of g_B and g_C; the sums' come behind them
+  SsSumArgs sum;
 };
 constexpr int kSsSumMost = 256, kSsSumMid = 64;
 
@@ -118,7 +121,7 @@ struct SsSplit {
 };
 
 // `width` workgroups take a run, `room` of them are on the card at once; `states`
-// workgroups take a piece of the state pass (its waves are light: eight times the card).
+// workgroups take a piece of the state pass (a few of them a compute unit).
 //
 // A sequence that is not cut takes its steps one after another, however
 // empty the card; cut, its steps cost `more` times what they do on a full
@@ -132,16 +135,16 @@ struct SsSplit {
 //   16 in 2048 rows 32 / 49 and 130 / 117, 16 in 8192 102 / 88 and 358 / 254; 2048 channels, 40 in 8192 192 / 250 and 836 / 867
 inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, long long states, bool bwd) {
   SsSplit s;
-  constexpr int kUnit = 64, kLeast = 128;
+  constexpr int kUnit = 64, kLeast = 64, kRun = 128;   // steps of a piece and of a run, at least
   const long long seqs = packed ? 1 : B;
   const int like = packed ? (B < 3 ? B : 3) : B;
   const double fill = (double)like * width / room, steps = (double)L / (packed ? like : 1);
   const bool pays = fill < 0.9 && steps * (1.0 - (bwd ? 0.95 : 1.75) * fill) > (bwd ? 240.0 : 500.0);
   // Runs cost the state passes, not their number: where sequences are cut, four times the room evens out the end.
   long long n = pays ? (4 * room + seqs * width - 1) / (seqs * width) : 1;
-  if (n > L / kLeast) n = L / kLeast;
+  if (n > L / kRun) n = L / kRun;
   s.cut = n > 1;
-  long long m = (s.cut || bwd) ? (8 * 256 + seqs * states - 1) / (seqs * states) : 1;   // pieces
+  long long m = (s.cut || bwd) ? (4 * 256 + seqs * states - 1) / (seqs * states) : 1;   // pieces
   if (m > L / kLeast) m = L / kLeast;
   if (m < n) m = n;
   if (m < 1) m = 1;

@@ -69,11 +69,10 @@ hipError_t launch_selscan_fwd(const SsArgs& a, int, hipStream_t) {
   if (a.seg && !a.s.cu && a.s.nseg > 1 && a.s.seg % a.piece) fail("a run of part of a piece", a.s.seg, a.piece);
   return hipSuccess;
 }
-hipError_t launch_selscan_state(const SsArgs& a, int, int rev, hipStream_t) {
+hipError_t launch_selscan_state(const SsArgs& a, int, hipStream_t) {
   launch_of(units(a, ss_channels(a.N) * kSsStateGroups), 256);
   pieces_ok(a);
   segs_ok(a);
-  if (rev && !a.adj) fail("an adjoint pass without its states");
   return hipSuccess;
 }
 hipError_t launch_selscan_carry(const SsCarryArgs& a, hipStream_t) {
@@ -91,18 +90,18 @@ hipError_t launch_selscan_bwd(const SsArgs& a, int, hipStream_t) {
   holds(a.ckpt, (most + 1) * a.G * ss_blocks(a.D / a.G, per) * ss_shape(a.N).S * 256);
   holds(a.cum, (most + 1) * a.D * 4);
   holds(a.part, 2ll * a.G * ss_blocks(a.D / a.G, per * kSsBwdGroups) * a.rows * a.N * 4);
-  holds(a.partA, (long long)a.s.segs * a.D * a.N * 4);
-  holds(a.partD, (long long)a.s.segs * a.D * 8);
+  holds(a.partA, (long long)a.s.segs * a.D * (a.N + 2) * 4);
   return hipSuccess;
 }
-hipError_t launch_selscan_fold(const SsFoldArgs&, int, hipStream_t) { ++g_launches; return hipSuccess; }
-hipError_t launch_ssm_sum(const SsSumArgs& a, hipStream_t) {
+static void sum_ok(const SsSumArgs& a) {
   ++g_launches;
   holds(a.part, a.parts * a.width * 4);
   if (a.parts > kSsSumMost) holds(a.mid, kSsSumMid * a.width * 4);
-  if ((a.width + 63) / 64 > 0xffffff) fail("columns of a sum", a.width);
-  return hipSuccess;
+  if ((a.width + 63) / 64 > 0xffffff - 8192) fail("columns of a sum", a.width);
+  if (a.share[0] + a.share[1] + a.share[2] < a.width) fail("columns without an output", a.width);
 }
+hipError_t launch_selscan_fold(const SsFoldArgs& a, int, hipStream_t) { sum_ok(a.sum); return hipSuccess; }
+hipError_t launch_ssm_sum(const SsSumArgs& a, hipStream_t) { sum_ok(a); return hipSuccess; }
 hipError_t launch_selscan_step(const SsStepArgs& a, int, hipStream_t) {
   const int ns = a.N <= 8 ? 2 : a.N <= 16 ? 4 : a.N <= 32 ? 8 : 16, cw = 256 / ns;
   launch_of((long long)a.B * ((a.D + cw - 1) / cw), 256);
@@ -368,7 +367,7 @@ int main() {
     for (int sid = 0; sid < (int)rr.size(); ++sid)   // the gradient reads them
       for (int t = 0; t < rr[sid].len; t += 32) {
         const int pc = p.states ? t / p.piece : 0;
-        const int piece = p.states ? pdscan::ss_piece_at(pieces[rr[sid].b], (p.cut ? (sid - runs[rr[sid].b]) * p.run : 0) + pc, p.pieces) : rr[sid].b;
+        const int piece = p.states ? pdscan::ss_piece_at(pdscan::ss_piece_at(pieces[rr[sid].b], p.cut ? (sid - runs[rr[sid].b]) * p.run : 0, p.pieces), pc, p.pieces) : rr[sid].b;
         if (piece < 0 || piece >= p.pieces) fail("a piece past the workspace", piece, p.pieces);
         const long long at = pdscan::ss_tile_of(0, rr[sid].b, piece, rr[sid].t0 + (p.states ? pc * p.piece : 0), p.states ? t - pc * p.piece : t, 32);
         if (at < 0 || at >= tiles) fail("a tile past the workspace", at, tiles);
