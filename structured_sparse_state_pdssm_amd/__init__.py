@@ -536,6 +536,8 @@ __all__ += ["linattn_dims", "linattn_workspace_bytes", "linattn_bwd_workspace_by
             "pdssm_linattn_bwd", "pdssm_linattn_step"]
 
 from ._ssm import (  # noqa: E402,F401
+    conv_bwd_workspace_bytes,
+    norm_bwd_workspace_bytes,
     pdssm_conv_bwd,
     pdssm_conv_fwd,
     pdssm_conv_step,
@@ -544,7 +546,10 @@ from ._ssm import (  # noqa: E402,F401
     pdssm_selscan_bwd,
     pdssm_selscan_fwd,
     pdssm_selscan_step,
+    selscan_bwd_workspace_bytes,
+    selscan_workspace_bytes,
 )
 
 __all__ += ["pdssm_conv_fwd", "pdssm_conv_bwd", "pdssm_conv_step", "pdssm_selscan_fwd", "pdssm_selscan_bwd",
-            "pdssm_selscan_step", "pdssm_norm_fwd", "pdssm_norm_bwd"]
+            "pdssm_selscan_step", "pdssm_norm_fwd", "pdssm_norm_bwd", "conv_bwd_workspace_bytes",
+            "selscan_workspace_bytes", "selscan_bwd_workspace_bytes", "norm_bwd_workspace_bytes"]

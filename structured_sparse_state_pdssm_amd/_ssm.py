@@ -24,7 +24,6 @@ import struct
 
 import torch
 
-from ._lib import lib  # noqa: F401
 from ._linattn import (
     _ANY,
     _FLOATS,
@@ -120,6 +119,25 @@ def _new(t, shape, dtype, like):
     if like.dtype is dtype:
         return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
     return like.new_empty(shape, dtype=dtype)
+
+
+# ---- bytes of workspace, for calls that bring their own (packed: B sequences in L rows)
+
+def conv_bwd_workspace_bytes(B, L, D, W, bf16=False, packed=False):
+    return _bytes(_conv_bytes, _pack(_struct_conv, B, L, D, W, bool(bf16), bool(packed), 1))
+
+
+def selscan_workspace_bytes(B, L, D, N, G=1, bf16=False, packed=False):
+    """May be 0: no workspace is needed then."""
+    return _bytes(_scan_bytes, _pack(_struct_scan, B, L, D, N, G, bool(bf16), bool(packed), 1))
+
+
+def selscan_bwd_workspace_bytes(B, L, D, N, G=1, bf16=False, packed=False):
+    return _bytes(_scan_bwd_bytes, _pack(_struct_scan, B, L, D, N, G, bool(bf16), bool(packed), 1))
+
+
+def norm_bwd_workspace_bytes(B, H, L, d, bf16=False, per_head=False):
+    return _bytes(_norm_bytes, _pack(_struct_norm, B, H, L, d, bool(bf16), 0, bool(per_head), 1.0))
 
 
 # ---- convolution

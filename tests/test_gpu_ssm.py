@@ -681,6 +681,71 @@ def test_given_workspace(dt):
             f(ws[:64])
 
 
+@DT
+def test_workspaces_of_the_size_asked_for(dt):
+    """The bytes that the queries name are enough, and the bytes behind them stay as they are."""
+    P = lib()
+    bf = dt == BF
+
+    def room(n):
+        whole = torch.full((n + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+        return whole, whole[:n]
+
+    for B, L, pack in ((1, 700, None), (2, 130, None), (1, 700, (5, 0, 600, 95))):
+        S = len(pack) if pack else B
+        x, gy, gh = scan_inputs(B, L, 48, 16, dt, 2, S=S)
+        cu = bounds(pack) if pack else None
+        n = P.selscan_workspace_bytes(S, L, 48, 16, 2, bf, pack is not None)
+        if n:
+            whole, ws = room(n)
+            P.pdssm_selscan_fwd(**x, cu_seqlens=cu, workspace=ws)
+            assert (whole[n:] == 0x5a).all()
+        n = P.selscan_bwd_workspace_bytes(S, L, 48, 16, 2, bf, pack is not None)
+        whole, ws = room(n)
+        P.pdssm_selscan_bwd(**x, g_y=gy, g_hL=gh, cu_seqlens=cu, workspace=ws)
+        assert (whole[n:] == 0x5a).all()
+        c, cy, cx = conv_inputs(B, L, 48, 4, dt, S=S)
+        n = P.conv_bwd_workspace_bytes(S, L, 48, 4, bf, pack is not None)
+        whole, ws = room(n)
+        P.pdssm_conv_bwd(**c, g_y=cy, g_xL=cx, cu_seqlens=cu, workspace=ws)
+        assert (whole[n:] == 0x5a).all()
+    for per_head in (True, False):
+        m, _, ny = norm_inputs((2, 3, 400, 64), dt, "before", True, per_head)
+        n = P.norm_bwd_workspace_bytes(2, 3, 400, 64, bf, per_head)
+        whole, ws = room(n)
+        P.pdssm_norm_bwd(**m, g_y=ny, gate="before", workspace=ws)
+        assert (whole[n:] == 0x5a).all()
+
+
+@DT
+def test_rows_outside_the_sequences_do_not_matter(dt):
+    """Not-a-number and infinity before the first and behind the last sequence change nothing."""
+    P = lib()
+    lens, before, after = (70, 0, 33, 600), 5, 40
+    S, n = len(lens), sum((70, 0, 33, 600))
+    x, gy, gh = scan_inputs(1, before + n + after, 48, 16, dt, 2, S=S)
+    c, cy, cx = conv_inputs(1, before + n + after, 48, 4, dt, S=S)
+    cu = bounds(lens) + before
+    got = []
+    for fill in (0.0, float("nan"), float("inf")):
+        for t in (x["x"], x["dt"], x["z"], gy, c["x"], cy):
+            t[:, :before] = fill
+            t[:, before + n:] = fill
+        for k in ("Bm", "Cm"):
+            x[k][:, :, :before] = fill
+            x[k][:, :, before + n:] = fill
+        y, hL = P.pdssm_selscan_fwd(**x, cu_seqlens=cu)
+        g = P.pdssm_selscan_bwd(**x, g_y=gy, g_hL=gh, cu_seqlens=cu)
+        v, vL = P.pdssm_conv_fwd(**c, cu_seqlens=cu)
+        e = P.pdssm_conv_bwd(**c, g_y=cy, g_xL=cx, cu_seqlens=cu)
+        rows = lambda t: t[:, before:before + n]  # noqa: E731
+        heads = lambda t: t[:, :, before:before + n]  # noqa: E731
+        got.append([rows(y), hL, rows(v), vL, rows(e["g_x"]), e["g_w"], e["g_bias"], e["g_x0"], heads(g["g_B"]), heads(g["g_C"])]
+                   + [rows(g[k]) for k in ("g_x", "g_dt", "g_z")] + [g[k] for k in ("g_A", "g_D", "g_dt_bias", "g_h0")])
+    for other in got[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(got[0], other))
+
+
 def test_refused_on_the_device():
     """What only the C ABI sees: overlaps, alignment, limits."""
     P = lib()
