@@ -120,7 +120,7 @@ template <typename F>
 hipError_t by_states(int N, F f) {   // f(S, NS) as constants
   if (N <= 8) f(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
   else if (N <= 16) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
-  else if (N <= 32) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  else if (N <= 32) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
   else f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
   return hipGetLastError();
 }

@@ -32,7 +32,6 @@ using pdscan::launched;
 using pdscan::set_error;
 using pdscan::view_span;
 
-constexpr int kCus = 256;              // compute units of the card
 constexpr int64_t kMost = 0x7fffff00;  // rows, workgroups and threads are numbered in 31 bits
 
 // Arguments of a call as they are checked: first each by itself, then what may not overlap.
@@ -187,12 +186,12 @@ int64_t scan_blocks(const pdssm_selscan_dims* d, int groups) {
   return (int64_t)d->G * pdscan::ss_blocks(d->D / d->G, pdscan::ss_channels(d->N) * groups);
 }
 
-// Workgroups of four waves that the card holds: three a compute unit, two where a lane has eight states.
-int room(const pdssm_selscan_dims* d) { return (pdscan::ss_shape(d->N).S >= 8 ? 2 : 3) * kCus; }
+// Workgroups of four waves that a compute unit holds, by their registers.
+int per_cu(const pdssm_selscan_dims* d) { return pdscan::ss_shape(d->N).S >= 8 ? 2 : 3; }
 
 ScanWs scan_ws(const pdssm_selscan_dims* d) {
   ScanWs w = {};
-  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, 1), room(d), scan_blocks(d, pdscan::kSsStateGroups), false);
+  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, 1), per_cu(d), scan_blocks(d, pdscan::kSsStateGroups), false);
   Layout l;
   put_pieces(w, l, d, false);
   w.total = w.split.states ? l.at : 0;
@@ -204,7 +203,7 @@ ScanWs scan_bwd_ws(const pdssm_selscan_dims* d) {
   const int per = pdscan::ss_channels(d->N);
   const size_t rows = (size_t)(d->packed ? 1 : d->B) * d->L;
   w.blocks = pdscan::ss_blocks(d->D / d->G, per * pdscan::kSsBwdGroups);
-  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, pdscan::kSsBwdGroups), room(d),
+  w.split = pdscan::ss_split(d->B, d->L, d->packed, scan_blocks(d, pdscan::kSsBwdGroups), per_cu(d),
                              scan_blocks(d, pdscan::kSsStateGroups), true);
   Layout l;
   put_pieces(w, l, d, true);

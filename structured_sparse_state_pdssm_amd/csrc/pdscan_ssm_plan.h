@@ -100,7 +100,7 @@ struct SsShape {
   int S, NS;
 };
 inline constexpr SsShape ss_shape(int N) {
-  return N <= 8 ? SsShape{2, 4} : N <= 16 ? SsShape{4, 4} : N <= 32 ? SsShape{8, 4} : SsShape{8, 8};
+  return N <= 8 ? SsShape{2, 4} : N <= 16 ? SsShape{4, 4} : N <= 32 ? SsShape{4, 8} : SsShape{8, 8};
 }
 inline constexpr int ss_channels(int N) { return 64 / ss_shape(N).NS; }   // of a wave
 inline int ss_blocks(int K, int per) { return (K + per - 1) / per; }        // channel blocks of a group of K
@@ -120,26 +120,34 @@ struct SsSplit {
   bool states;                   // and more than one piece
 };
 
-// `width` workgroups take a run, `room` of them are on the card at once; `states`
-// workgroups take a piece of the state pass (a few of them a compute unit).
+// Time of `fill` times the workgroups that the card holds, `per` a compute unit,
+// in rounds of it full: with one of three it is not three times as fast, but takes .6 of the time.
+inline double ss_rounds(double fill, int per, bool bwd) {
+  const double whole = (double)(long long)fill;
+  const int left = (int)((fill - whole) * per + 0.999);
+  if (left <= 0) return whole;
+  if (left >= per) return whole + 1;
+  return whole + (per == 3 ? (left == 1 ? (bwd ? 0.6 : 0.67) : (bwd ? 0.78 : 0.8)) : bwd ? 0.75 : 0.8);
+}
+
+// `width` workgroups take a run, `per` of them are on a compute unit at once;
+// `states` workgroups take a piece of the state pass, a few of them a compute unit.
 //
-// A sequence that is not cut takes its steps one after another, however
-// empty the card; cut, its steps cost `more` times what they do on a full
-// card (the state passes), and the launches what some `fixed` steps take.
-// 768 channels of 16 states, bf16, in us, uncut / cut:
-//   forwards (1.75, 500)  512 steps of 1: 27 / 29, of 4: 28 / 32;  1024 of 1: 51 / 30, of 4: 51 / 48, of 8: 60 / 66;
-//                         2048 of 6: 113 / 91, of 8: 114 / 110, of 12: 141 / 159
-//   backwards (.95, 240)  256 of 1: 71 / 71, of 8: 84 / 86;  512 of 4: 113 / 87, of 8: 133 / 126;
-//                         2048 of 8: 459 / 359, of 12: 559 / 539
+// A sequence that is not cut takes its steps one after another: its time goes
+// by rounds of the card.  Cut, time goes by the work, 1.45 times it
+// forwards and 1.08 backwards (the state passes), and the launches add what 280 and 100
+// steps take.  768 channels of 16 states (16 sequences fill the card once), bf16, in us, uncut / cut:
+//   forwards   512 steps of 1: 27 / 28, of 4: 28 / 32;  1024 of 1: 51 / 26, of 4: 51 / 45;  2048 of 6: 113 / 95, of 8: 114 / 110, of 12: 141 / 159
+//   backwards  256 of 1: 71 / 44;  384 of 4: 95 / 64;  2048 of 8: 459 / 340, of 12: 559 / 520, of 16: 604 / 651, of 20: 896 / 812, of 24: 1001 / 973
 // Sequences of different lengths, where the longest counts, are taken as three of a third of the rows:
-//   16 in 2048 rows 32 / 49 and 130 / 117, 16 in 8192 102 / 88 and 358 / 254; 2048 channels, 40 in 8192 192 / 250 and 836 / 867
-inline SsSplit ss_split(int B, int L, int packed, long long width, long long room, long long states, bool bwd) {
+//   16 in 2048 rows 32 / 49 and 130 / 99, 16 in 8192 102 / 88 and 358 / 235; 2048 channels, 40 in 8192 192 / 250 and 868 / 852
+inline SsSplit ss_split(int B, int L, int packed, long long width, int per, long long states, bool bwd) {
   SsSplit s;
-  constexpr int kUnit = 64, kLeast = 64, kRun = 128;   // steps of a piece and of a run, at least
-  const long long seqs = packed ? 1 : B;
+  constexpr int kCus = 256, kUnit = 32, kLeast = 64, kRun = 128;   // steps of a piece and of a run, at least
+  const long long seqs = packed ? 1 : B, room = (long long)per * kCus;
   const int like = packed ? (B < 3 ? B : 3) : B;
   const double fill = (double)like * width / room, steps = (double)L / (packed ? like : 1);
-  const bool pays = fill < 0.9 && steps * (1.0 - (bwd ? 0.95 : 1.75) * fill) > (bwd ? 240.0 : 500.0);
+  const bool pays = (bwd ? 1.08 : 1.45) * fill + (bwd ? 100.0 : 280.0) / steps < ss_rounds(fill, per, bwd);
   // Runs cost the state passes, not their number: where sequences are cut, four times the room evens out the end.
   long long n = pays ? (4 * room + seqs * width - 1) / (seqs * width) : 1;
   if (n > L / kRun) n = L / kRun;

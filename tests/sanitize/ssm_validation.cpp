@@ -335,7 +335,7 @@ int main() {
   auto rnd = [&](int n) { seed = seed * 1664525u + 1013904223u; return (int)((seed >> 8) % (unsigned)n); };
   for (int turn = 0; turn < 3000; ++turn) {
     const int B = 1 + rnd(6), L = 1 + rnd(3000), D = 8 * (1 + rnd(40));
-    const pdscan::SsSplit p = pdscan::ss_split(B, L, 1, (D + 15) / 16, 768, (D + 63) / 64, true);
+    const pdscan::SsSplit p = pdscan::ss_split(B, L, 1, (D + 15) / 16, 3, (D + 63) / 64, true);
     int off[8];
     for (int i = 0; i <= B; ++i) off[i] = turn % 3 ? rnd(L + 1) : rnd(3 * L) - L;
     if (turn % 4 == 0)
