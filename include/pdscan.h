@@ -459,7 +459,7 @@ int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, cons
  *   - packed = 1, cu_seqlens, rows outside the sequences, offsets out of order:
  *     as there.  L, and B L, at most 2^31 - 257;
  *   - everything is finite (not checked).  What is not spoils its own channel, from its
- *     token on, and in a scan and its gradients what its tile of up to 64 tokens and
+ *     token on, and in a scan and its gradients what its tile of 32 tokens and
  *     its segment share. */
 typedef struct {
   int32_t B;               /* sequences */
@@ -520,7 +520,7 @@ int pdssm_selscan_fwd(const pdssm_selscan_dims* dims, const pdssm_view* x, const
 
 /* Its gradient, given g_y [B,L,D] and g_hL [B,D,N] (NULL: zero).  Nothing of
  * the forward pass is kept: the states are formed again, from states at every 32nd step
- * that the workspace holds (D N / 8 bytes a row, and N / 4 a row and channel block for sums).
+ * that the workspace holds (D N / 8 bytes a row, and 8 N a row and workgroup of channels for sums over them).
  *   g_x, g_dt, g_z [B,L,D] (g_z NULL with z), g_B, g_C [B,G,L,N] (views)
  *   g_A [D,N], g_skip [D], g_bias [D] (out, required); g_h0 [B,D,N] (out, optional) */
 int pdssm_selscan_bwd_workspace_bytes(const pdssm_selscan_dims* dims, size_t* bytes);

@@ -6,17 +6,25 @@
 //
 // What bounds it.  The decay differs by channel and by state, so no matrix
 // product forms it: every cell (t, d, n) costs an exponential (8 cycles of a
-// SIMD for 64 lanes) and four multiplications or additions (4 each), 24 cycles
-// run step by step.  Run so, a layer has too few chains to fill the card, so time is
-// split too, without doing the exponentials twice: a wave takes some steps of
-// a tile, keeps their decays a_t and drives d_t x_t B_t in registers while it
-// forms its end state from zero, learns through LDS the state that enters its
-// steps, and runs the recurrence again on the registers (one multiply-add more:
-// 28 cycles).  Sequences that are too few even so are cut into segments, whose
-// contributions a pass of their own forms first.
+// SIMD for 64 lanes; the exponential and the other units do not overlap) and four
+// multiplications or additions (4 each), 24 cycles run step by step.  Run so, a
+// layer has too few chains to fill the card, so time is split too, without
+// doing the exponentials twice: a wave takes eight steps of a tile of 32,
+// keeps their decays a_t and drives d_t x_t B_t in registers while it forms its
+// end state from zero, learns through LDS the state that enters its steps, and
+// runs the recurrence again on the registers (one multiply-add more: 28 cycles).
+// Sequences that are too few even so are cut into runs, which start from
+// states that a pass of its own forms first (ss_split).
+//
+// 16 x 2048 steps, 768 channels, 16 states, bf16: 141 us (160 under the
+// profiler).  The vector units are what it waits for: 136 us at 2.1 GHz by their counter, of
+// which the cells' 28 cycles are 84; the rest is what a (t, d) needs once (softplus, the gate,
+// roundings) and the exchanges.  Memory, 205 MB, would take 40.  Three barriers a tile took 151, two 141.
 //
 // Layout.  A lane holds S states of one channel; NS lanes hold a channel, a wave
-// 64 / NS channels.
+// 64 / NS channels: four states a lane up to 32 (eight, and half the lanes,
+// need twice the registers: 4 x 2048 x 768 of 32 states 144 us forwards and 423
+// backwards, 116 and 350 so; 16 x 2048 280 and 1511, 239 and 1270).
 #pragma once
 
 #include "pdscan_ssm.h"
@@ -298,7 +306,8 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
 // ---- contributions of pieces
 //
 // The state that a piece adds, from zero, and the sum of its steps; a wave
-// takes its channels through the piece alone.  With ckpt it also writes the
+// takes its channels through the piece alone (16 x 2048 x 768 x 16
+// 96 us under the profiler, 81 of them the vector units).  With ckpt it also writes the
 // state and the sum at the start of every tile of the gradient.  Backwards
 // (REV) it is the adjoint state that flows out of the piece's start,
 // l = a_t (l + g_t C_t), with g the gradient of y before its gate.
@@ -433,8 +442,13 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 // step and state, over the 16 lanes that hold channels.  Exchanges halve what is
 // left of four steps' products twice, so that only a quarter of them is added
 // up inside the rows of 16 lanes.  (On the matrix cores, as products with a row
-// of ones, they took 32 cycles each, 660 us for the whole kernel at 16 x 2048 x
-// 768 in bf16.)
+// of ones, they took 32 cycles each: 660 us for the kernel below.)
+//
+// 16 x 2048 x 768 x 16 in bf16: 505 us (529 under the profiler), of which the
+// vector units work 382: some 60000 instructions a wave for its 64 tiles of 32 cells a
+// lane.  The rest are waits at the three barriers of a tile.  The tile's
+// outputs leave before the next is staged: with two tiles' rows in LDS and two barriers the
+// whole gradient took 690 us instead of 590.
 template <typename T, int S, int NS>
 __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_selscan_bwd_kernel(const SsArgs a) {
   constexpr int W = kSsTimeWaves, CG = kSsBwdGroups, TS = kSsBwdSteps, TT = W * TS, CW = 64 / NS, CC = CG * CW, NP = S * NS;
@@ -782,8 +796,9 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
 // ---- one token
 //
 // Four states a lane, a channel in neighbouring lanes: the state streams
-// through in whole lines, once each way, which is the time.  Everything is
-// under way before the search for an earlier row of the same slot.
+// through in whole lines, once each way, which is the time (250 rows of 2048 x
+// 16: 69 MB in 17 us).  Everything is under way before the search for an
+// earlier row of the same slot.
 template <typename T, int NS>
 __global__ __launch_bounds__(256) void pdssm_selscan_step_kernel(const SsStepArgs a) {
   constexpr int CW = 256 / NS;
