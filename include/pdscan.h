@@ -457,7 +457,7 @@ int pdssm_linattn_step(const pdssm_linattn_dims* dims, const pdssm_view* q, cons
  *     the gradients of both fp32 and contiguous; a convolution's states hold
  *     inputs as they are, in in_dtype;
  *   - packed = 1, cu_seqlens, rows outside the sequences, offsets out of order:
- *     as there.  L, and B L, at most 2^31 - 257;
+ *     as there.  L, and B L, at most 2^31 - 256;
  *   - everything is finite (not checked).  What is not spoils its own channel, from its
  *     token on, and in a scan and its gradients what its tile of 32 tokens and
  *     its segment share. */
@@ -554,7 +554,8 @@ typedef struct {
  *   y = residual + res_scale (w u / sqrt(mean(u^2) + eps)) [silu(z) with PDSSM_GATE_AFTER]
  *   u = x, or x silu(z) with PDSSM_GATE_BEFORE
  *   x, z, residual, y [B,H,L,d] (views; z NULL without a gate; residual NULL: zero)
- *   w, res_scale [H,d] or [d] (res_scale NULL: one) */
+ *   w, res_scale [H,d] or [d] (res_scale NULL: one)
+ * B L at most 2^30 - 128, H at most 2^23 - 1, H d with per_head below 2^29. */
 int pdssm_norm_fwd(const pdssm_norm_dims* dims, const pdssm_view* x, const float* w, const pdssm_view* z,
                    const pdssm_view* residual, const float* res_scale, const pdssm_view* y, void* stream);
 

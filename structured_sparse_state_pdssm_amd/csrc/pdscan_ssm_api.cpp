@@ -306,6 +306,9 @@ int check_norm(const pdssm_norm_dims* d) {
     return set_error(PDSSM_EUNSUPPORTED, "d=%d must be a multiple of 8, at most %d", d->d, pdscan::kNmMaxD);
   if ((int64_t)d->B * d->L > kMost / 2 || (int64_t)d->H * 256 > kMost || d->L > kMost / 2)
     return set_error(PDSSM_EUNSUPPORTED, "B=%d sequences of L=%d rows and H=%d heads are too many", d->B, d->L, d->H);
+  // a gradient's last sum takes four threads a column, w's and res_scale's, and a launch fewer than 2^32
+  if (d->per_head && (int64_t)d->H * d->d >= 1 << 29)
+    return set_error(PDSSM_EUNSUPPORTED, "weights of H=%d heads of d=%d elements are too many", d->H, d->d);
   return PDSSM_OK;
 }
 

@@ -294,6 +294,7 @@ int main() {
   M([](auto& d) { d.d = 12; }, PDSSM_EUNSUPPORTED, "rows of twelve");
   M([](auto& d) { d.d = 8200; }, PDSSM_EUNSUPPORTED, "long rows");
   M([](auto& d) { d.B = 1 << 30; d.L = 8; }, PDSSM_EUNSUPPORTED, "rows past 31 bits");
+  M([](auto& d) { d.B = d.L = 1; d.H = 1 << 16; d.d = 8192; }, PDSSM_EUNSUPPORTED, "weights whose sums pass a launch");
   if (g_launches != before) fail("a refused call launched", g_launches - before);
 
   // every size that passes covers its rows and stays inside its workspace
