@@ -45,16 +45,20 @@ __device__ __forceinline__ void ss_load_A(float (&A2)[S], const float* A, int64_
   for (int s = 0; s < S; ++s) A2[s] = ok && n0 + s < N ? A[ch * N + n0 + s] * kLog2e : 0.0f;
 }
 
+// A lane's S states from the n0-th of channel row `at` (N is a multiple of 8: all of them or none).
 template <int S>
 __device__ __forceinline__ void ss_load_state(float (&h)[S], const float* p, int64_t at, int n0, int N, bool ok) {
+  SsVec<float, S> v = {};
+  if (p && ok && n0 < N) v = *(const SsVec<float, S>*)(p + at * N + n0);
 #pragma unroll
-  for (int s = 0; s < S; ++s) h[s] = p && ok && n0 + s < N ? p[at * N + n0 + s] : 0.0f;
+  for (int s = 0; s < S; ++s) h[s] = v.e[s];
 }
 template <int S>
 __device__ __forceinline__ void ss_store_state(const float (&h)[S], float* p, int64_t at, int n0, int N, bool ok) {
+  SsVec<float, S> v;
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (ok && n0 + s < N) p[at * N + n0 + s] = h[s];
+  for (int s = 0; s < S; ++s) v.e[s] = h[s];
+  if (ok && n0 < N) *(SsVec<float, S>*)(p + at * N + n0) = v;
 }
 
 // S floats of this lane in an LDS or global array of [..][S / 4][64] vectors (S = 2: pairs).
@@ -455,11 +459,16 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 // up inside the rows of 16 lanes.  (On the matrix cores, as products with a row
 // of ones, they took 32 cycles each: 660 us for the kernel below.)
 //
-// 16 x 2048 x 768 x 16 in bf16: 505 us (529 under the profiler), of which the
-// vector units work 382: some 60000 instructions a wave for its 64 tiles of 32 cells a
-// lane.  The rest are waits at the three barriers of a tile.  The tile's
-// outputs leave before the next is staged: with two tiles' rows in LDS and two barriers the
-// whole gradient took 690 us instead of 590.
+// 16 x 2048 x 768 x 16 in bf16: the whole gradient 526 us, of which this kernel is
+// some 440: 60000 vector instructions a wave for its 64 tiles of 32 cells a
+// lane, three waves a SIMD.  The tile's outputs leave before the next is
+// staged: with two tiles' rows in LDS and two barriers the gradient took 690 us instead of 590.
+//
+// No register of it may be spilled.  A reload in the loop waits for every load
+// under way (592 us, and 191 instead of 164 for 9 packed in 4097 x 512 x 32), and a
+// value stored to scratch where only some lanes are on can come back as something else in
+// the others: addresses, here.  So offsets and, where there is no room, indexes
+// are formed where they are used.
 template <typename T, int S, int NS>
 __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_selscan_bwd_kernel(const SsArgs a) {
   constexpr int W = kSsTimeWaves, CG = kSsBwdGroups, TS = kSsBwdSteps, TT = W * TS, CW = 64 / NS, CC = CG * CW, NP = S * NS;
@@ -473,6 +482,8 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   __shared__ __align__(16) float gs[2][CG][TT][NP];   // g_B, g_C
   __shared__ __align__(16) float Es[CG * W][S * 64], Ps[CG * W][S * 64], Rs[CG * W][S * 64];
   __shared__ __align__(16) float Rt[2][CG][S * 64];   // the adjoint state that enters a tile, from its end
+  constexpr bool kPark = S >= 8;   // 256 registers do not hold everything: the entering states of a wave's steps lie here meanwhile
+  __shared__ __align__(16) float Hin[kPark ? CG * W : 1][kPark ? S * 64 : 4];
   __shared__ __align__(16) float pars[2][CC];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6) % W, cg = __builtin_amdgcn_readfirstlane(tid >> 6) / W;
   if (ss_block(a.row) == 0 && tid < 2) a.header[tid] = 0;
@@ -510,15 +521,21 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
 #pragma unroll
   for (int j = 0; j < S; ++j) gA[j] = 0.0f;
 
-  const int st = tid * V / CC, sc = tid * V % CC;
-  const bool second = tid >= BT, sok = u.c0 + sc < u.end, gated = a.z.p != nullptr;
-  const int bt = tid % BT * VB / NP, bn = tid % BT * VB % NP;   // and rows BT VB / NP further on
-  const bool bok = bn < a.N;
-  const LaView& vbc = second ? a.Cm : a.Bm;
-  const uint32_t xo = ss_off<T>(a.x, st, sc), dto = ss_off<T>(a.dt, st, sc), zo = ss_off<T>(a.z, st, sc), go = ss_off<T>(a.gy, st, sc);
-  const uint32_t gxo = ss_off<T>(a.gx, st, sc), gdo = ss_off<T>(a.gdt, st, sc), gzo = ss_off<T>(a.gz, st, sc);
+  // Where a thread stages and stores: a step's V channels; VB states of B or C, and rows BT VB / NP further on.
+  // With eight states a lane there is no room to hold it through the loop.
+  struct At { int st, sc, bt, bn; };
+  auto where = [](int i) { return At{i * V / CC, i * V % CC, i % BT * VB / NP, i % BT * VB % NP}; };
+  const At held = where(tid);
+  auto here = [&] { return S < 8 ? held : where(ss_thread_here()); };
+  const bool second = __builtin_amdgcn_readfirstlane(tid >> 6) >= BT / 64, sok = u.c0 + here().sc < u.end, gated = a.z.p != nullptr;
+  const bool bok = here().bn < a.N;
+  // (whole waves take B or C; by value: a reference would be followed through memory in every tile)
+  LaView vbc;
+  vbc.p = second ? a.Cm.p : a.Bm.p;
+  vbc.sb = second ? a.Cm.sb : a.Bm.sb;
+  vbc.sh = second ? a.Cm.sh : a.Bm.sh;
+  vbc.st = second ? a.Cm.st : a.Bm.st;
   constexpr int BS = BT * VB / NP;
-  const uint32_t Bo = ss_off<T>(vbc, bt, bn);
   if (tid < CC) {
     const int k = u.c0 + tid;
     pars[0][tid] = a.bias && k < u.end ? a.bias[k] : 0.0f;
@@ -536,15 +553,16 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   const char *gp = ss_tile_at<T>(a.gy, s.vb, t1, u.c0), *Bp = ss_tile_at<T>(vbc, s.vb, t1, u.g * vbc.sh);
   char *gxp = ss_tile_at<T>(a.gx, s.vb, t1, u.c0), *gdp = ss_tile_at<T>(a.gdt, s.vb, t1, u.c0), *gzp = ss_tile_at<T>(a.gz, s.vb, t1, u.c0);
   auto fetch = [&](int t) {   // and the pointers back to the tile before it
+    const auto [st, sc, bt, bn] = here();
     if (sok && t + st < s.len) {
-      ss_load_at(xn, xp, xo);
-      ss_load_at(dn, dp, dto);
-      ss_load_at(gn, gp, go);
-      if (gated) ss_load_at(zn, zp, zo);
+      ss_load_at(xn, xp, ss_off_here<T>(a.x, st, sc));
+      ss_load_at(dn, dp, ss_off_here<T>(a.dt, st, sc));
+      ss_load_at(gn, gp, ss_off_here<T>(a.gy, st, sc));
+      if (gated) ss_load_at(zn, zp, ss_off_here<T>(a.z, st, sc));
     }
 #pragma unroll
     for (int i = 0; i < BR; ++i)
-      if (bok && t + bt + i * BS < s.len) ss_load_at(Bn[i], Bp + ss_rows<T>(vbc, i * BS), Bo);
+      if (bok && t + bt + i * BS < s.len) ss_load_at(Bn[i], Bp + ss_rows<T>(vbc, i * BS), ss_off_here<T>(vbc, bt, bn));
     xp -= ss_rows<T>(a.x, TT);
     dp -= ss_rows<T>(a.dt, TT);
     gp -= ss_rows<T>(a.gy, TT);
@@ -552,15 +570,25 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     Bp -= ss_rows<T>(vbc, TT);
   };
   int pc = __builtin_amdgcn_readfirstlane((s.len - 1) / a.piece), turn = 0;   // piece of the tile
+  auto arrived = [&] {
+    ss_arrived(xn);
+    ss_arrived(dn);
+    ss_arrived(zn);
+    ss_arrived(gn);
+#pragma unroll
+    for (int i = 0; i < BR; ++i) ss_arrived(Bn[i]);
+  };
   fetch(last);
+  arrived();
   for (int t0 = last; t0 >= 0; t0 -= TT, turn ^= 1) {
+    const auto [st, sc, bt, bn] = here();
     const bool live = sok && t0 + st < s.len;
     const SsRaw<T, V> xc = xn;
     float d[V], sg[V], g[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       d[v] = dn.get(v) + pars[0][sc + v];
-      g[v] = live ? gn.get(v) : 0.0f;
+      g[v] = gn.get(v);   // (behind the end, which the first tile has, nothing was loaded: zero)
     }
     ss_steps<V, true>(d, sg, a.softplus, live);
     if (gated) {
@@ -576,10 +604,9 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
 #pragma unroll
     for (int i = 0; i < BR; ++i) {
       const int t = bt + i * BS;
-      const bool blive = bok && t0 + t < s.len;
       SsVec<float, VB> b;
 #pragma unroll
-      for (int v = 0; v < VB; ++v) b.e[v] = blive ? Bn[i].get(v) : 0.0f;
+      for (int v = 0; v < VB; ++v) b.e[v] = Bn[i].get(v);
       *(SsVec<float, VB>*)(second ? &Cs[t][bn] : &Bs[t][bn]) = b;
     }
     __syncthreads();
@@ -588,10 +615,15 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     if (t0 < pc * a.piece) --pc;
     const int at = ss_piece_at(piece0, pc, a.npieces);
     const int64_t tile = ss_tile(a, s.b, at, s.t0 + pc * a.piece, t0 - pc * a.piece);
-    float hin[S] = {}, H0[S];
-    if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), lane);
-    const float cum = ok ? a.cum[tile * a.D + ch] : 0.0f;
-    ss_load_state(H0, a.seg ? a.seg : a.h0, (int64_t)(a.seg ? at : s.b) * a.D + ch, q * S, a.N, ok);
+    float hin[S] = {}, H0[S], cum = 0.0f;
+    {
+      const int ln = S < 8 && sizeof(typename T::E) == 2 ? lane : ss_thread_here() & 63, k = cg * CW + ln / NS;
+      const bool has = u.c0 + k < u.end;
+      if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), ln);
+      if (has) cum = (a.cum + tile * a.D + u.c0)[k];
+      const float* entered = a.seg ? a.seg + ((int64_t)at * a.D + u.c0) * a.N : a.h0 ? a.h0 + ((int64_t)s.b * a.D + u.c0) * a.N : nullptr;
+      ss_load_state(H0, entered, k, ln % NS * S, a.N, has);
+    }
 
     // from zero, forwards and backwards
     const int me = cg * W + wave, tw = wave * TS;
@@ -679,11 +711,14 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     for (int t = 0; t < TS; ++t)
 #pragma unroll
       for (int j = 0; j < S; ++j) hs[t][j] = h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
+    if constexpr (kPark) ss_lane_put(Hin[me], hin, lane);
     float far[2][2 * S];   // products of the two steps before: g_B's S, then g_C's
 #pragma unroll
     for (int t = TS - 1; t >= 0; --t) {
       const float4 w = pre[tw + t][lc];
       float b[S], k[S], y = 0.0f, lb = 0.0f, pa = 0.0f, v[2 * S];
+      if constexpr (kPark)
+        if (t == 0) ss_lane_get(hin, Hin[me], lane);
       ss_row_get(b, &Bs[tw + t][q * S]);
       ss_row_get(k, &Cs[tw + t][q * S]);
 #pragma unroll
@@ -735,71 +770,82 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
       if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
-    if (live) {
-      float ox[V], od[V], oz[V];
+    // The next tile's rows are here by now.  Waited for before anything is
+    // stored: behind the stores, the wait would be for them too.
+    arrived();
+    {
+      const auto [st, sc, bt, bn] = here();
+      if (live) {
+        float ox[V], od[V], oz[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float4 w = pre[st][sc + v];
-        const float* o = outs + st * CC + sc + v;
-        const float y = o[0], lb = o[TT * CC + 16], pa = kLn2 * o[2 * (TT * CC + 16)];
-        const float x = xc.get(v), skip = pars[1][sc + v];
-        ox[v] = __builtin_fmaf(w.x, lb, w.z * skip);
-        od[v] = __builtin_fmaf(x, lb, pa) * w.w;
-        oz[v] = gated ? gzs[st][sc + v] * __builtin_fmaf(skip, x, y) : 0.0f;
-        gD[v] = __builtin_fmaf(w.z, x, gD[v]);
-        gb[v] += od[v];
+        for (int v = 0; v < V; ++v) {
+          const float4 w = pre[st][sc + v];
+          const float* o = outs + st * CC + sc + v;
+          const float y = o[0], lb = o[TT * CC + 16], pa = kLn2 * o[2 * (TT * CC + 16)];
+          const float x = xc.get(v), skip = pars[1][sc + v];
+          ox[v] = __builtin_fmaf(w.x, lb, w.z * skip);
+          od[v] = __builtin_fmaf(x, lb, pa) * w.w;
+          oz[v] = gated ? gzs[st][sc + v] * __builtin_fmaf(skip, x, y) : 0.0f;
+          gD[v] = __builtin_fmaf(w.z, x, gD[v]);
+          gb[v] += od[v];
+        }
+        ss_store_at<T, V>(gxp, ss_off_here<T>(a.gx, st, sc), ox);
+        ss_store_at<T, V>(gdp, ss_off_here<T>(a.gdt, st, sc), od);
+        if (gated) ss_store_at<T, V>(gzp, ss_off_here<T>(a.gz, st, sc), oz);
       }
-      ss_store_at<T, V>(gxp, gxo, ox);
-      ss_store_at<T, V>(gdp, gdo, od);
-      if (gated) ss_store_at<T, V>(gzp, gzo, oz);
-    }
-    gxp -= ss_rows<T>(a.gx, TT);
-    gdp -= ss_rows<T>(a.gdt, TT);
-    gzp -= ss_rows<T>(a.gz, TT);
-    // this workgroup's part of g_B (first half of the threads) and g_C
+      gxp -= ss_rows<T>(a.gx, TT);
+      gdp -= ss_rows<T>(a.gdt, TT);
+      gzp -= ss_rows<T>(a.gz, TT);
+      // this workgroup's part of g_B (first half of the threads) and g_C
 #pragma unroll
-    for (int i = 0; i < BR; ++i) {
-      const int t = bt + i * BS;
-      if (!bok || t0 + t >= s.len) continue;
-      const int nb = a.G * ((a.D / a.G + CC - 1) / CC);
-      const int64_t r = s.vb * a.s.L + s.t0 + t0 + t;
-      float* o = a.part + ((((int64_t)(second ? nb : 0) + u.block) * a.rows) + r) * a.N + bn;
-      SsVec<float, VB> v;
+      for (int i = 0; i < BR; ++i) {
+        const int t = bt + i * BS;
+        if (!bok || t0 + t >= s.len) continue;
+        const int nb = a.G * ((a.D / a.G + CC - 1) / CC);
+        const int64_t r = s.vb * a.s.L + s.t0 + t0 + t;
+        float* o = a.part + ((((int64_t)(second ? nb : 0) + u.block) * a.rows) + r) * a.N + bn;
+        SsVec<float, VB> v;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) {
-        v.e[j] = gs[second][0][t][bn + j];
-        if constexpr (CG == 2) v.e[j] += gs[second][CG - 1][t][bn + j];
+        for (int j = 0; j < VB; ++j) {
+          v.e[j] = gs[second][0][t][bn + j];
+          if constexpr (CG == 2) v.e[j] += gs[second][CG - 1][t][bn + j];
+        }
+        *(SsVec<float, VB>*)o = v;
       }
-      *(SsVec<float, VB>*)o = v;
     }
   }
-  if (s.first && wave == 0 && a.gh0) {
-    float R[S];
-    ss_lane_get(R, Rt[turn][cg], lane);
-    ss_store_state(R, a.gh0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
-  }
-  // sums over this workgroup's steps: the four waves', then the staging threads' of every channel
-  __syncthreads();
-  ss_lane_put(Es[cg * W + wave], gA, lane);
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    outs[st * CC + sc + v] = gD[v];
-    outs[TT * CC + 16 + st * CC + sc + v] = gb[v];
-  }
-  __syncthreads();
-  if (wave == 0) {
-    float sumA[S], e[S];
-    ss_lane_get(sumA, Es[cg * W], lane);
-    for (int v = 1; v < W; ++v) {
-      ss_lane_get(e, Es[cg * W + v], lane);
-#pragma unroll
-      for (int j = 0; j < S; ++j) sumA[j] += e[j];
+  {   // (nothing of this is held through the loop)
+    const int i = ss_thread_here(), lane = i & 63, c = lane / NS, q = lane % NS, lc = cg * CW + c, ch = u.c0 + lc;
+    const bool ok = ch < u.end;
+    const auto [st, sc, bt, bn] = where(i);
+    if (s.first && wave == 0 && a.gh0) {
+      float R[S];
+      ss_lane_get(R, Rt[turn][cg], lane);
+      ss_store_state(R, a.gh0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     }
-    ss_store_state(sumA, partA, ch, q * S, a.N, ok);
-    if (ok && q < 2) {
-      float o = 0.0f;
-      for (int t = 0; t < TT; ++t) o += outs[q * (TT * CC + 16) + t * CC + lc];
-      partA[(int64_t)a.D * (a.N + q) + ch] = o;
+    // sums over this workgroup's steps: the four waves', then the staging threads' of every channel
+    __syncthreads();
+    ss_lane_put(Es[cg * W + wave], gA, lane);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      outs[st * CC + sc + v] = gD[v];
+      outs[TT * CC + 16 + st * CC + sc + v] = gb[v];
+    }
+    __syncthreads();
+    if (wave == 0) {
+      float sumA[S], e[S];
+      ss_lane_get(sumA, Es[cg * W], lane);
+      for (int v = 1; v < W; ++v) {
+        ss_lane_get(e, Es[cg * W + v], lane);
+#pragma unroll
+        for (int j = 0; j < S; ++j) sumA[j] += e[j];
+      }
+      ss_store_state(sumA, partA, ch, q * S, a.N, ok);
+      if (ok && q < 2) {
+        float o = 0.0f;
+        for (int t = 0; t < TT; ++t) o += outs[q * (TT * CC + 16) + t * CC + lc];
+        partA[(int64_t)a.D * (a.N + q) + ch] = o;
+      }
     }
   }
 }

@@ -82,6 +82,19 @@ __device__ __forceinline__ void ss_load_at(SsRaw<T, V>& r, const char* tile, uin
     for (int i = 0; i < SsRaw<T, V>::kWords; ++i) r.w[i] = q.e[i];
   }
 }
+// The thread's number as a value of its own: what follows from it is formed
+// where it stands, not ahead of a loop.
+__device__ __forceinline__ int ss_thread_here() {
+  int i = threadIdx.x;
+  asm volatile("" : "+v"(i));
+  return i;
+}
+// Waits here for what is on its way.
+template <typename T, int V>
+__device__ __forceinline__ void ss_arrived(SsRaw<T, V>& r) {
+#pragma unroll
+  for (int i = 0; i < SsRaw<T, V>::kWords; ++i) asm volatile("" : "+v"(r.w[i]));
+}
 template <typename T, int V>
 __device__ __forceinline__ void ss_load_raw(SsRaw<T, V>& r, const void* p, int64_t at) {
   using Q = SsVec<uint32_t, SsRaw<T, V>::kWords>;
@@ -111,6 +124,13 @@ __device__ __forceinline__ char* ss_tile_at(const LaView& v, int64_t vb, int64_t
 template <typename T>
 __device__ __forceinline__ uint32_t ss_off(const LaView& v, int row, int c) {
   return ((uint32_t)row * (uint32_t)v.st + (uint32_t)c) * (uint32_t)sizeof(typename T::E);
+}
+// The same, formed where it stands: a register less to hold through a loop.
+// (Rows of a tile and step strides, at most 2^23, are within 24 bits.)
+template <typename T>
+__device__ __forceinline__ uint32_t ss_off_here(const LaView& v, int row, int c) {
+  asm volatile("" : "+v"(row));
+  return (__umul24((uint32_t)row, (uint32_t)v.st) + (uint32_t)c) * (uint32_t)sizeof(typename T::E);
 }
 // Bytes of `rows` rows.
 template <typename T>
