@@ -459,12 +459,10 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 // up inside the rows of 16 lanes.  (On the matrix cores, as products with a row
 // of ones, they took 32 cycles each: 660 us for the kernel below.)
 //
-// As forwards, the waves change parts with the tiles: the first part's state
-// and the last part's adjoint are known, and are not formed from zero.
-//
-// 16 x 2048 x 768 x 16 in bf16: the whole gradient 509 us, 527 with all four waves
-// doing the same.  The tile's outputs leave before the next is staged (with two tiles'
-// rows in LDS and two barriers the gradient took 690 us where it took 590 so).
+// 16 x 2048 x 768 x 16 in bf16: the whole gradient 526 us, of which this kernel is
+// some 440: 60000 vector instructions a wave for its 64 tiles of 32 cells a
+// lane, three waves a SIMD.  The tile's outputs leave before the next is
+// staged: with two tiles' rows in LDS and two barriers the gradient took 690 us instead of 590.
 //
 // No register of it may be spilled.  A reload in the loop waits for every load
 // under way (592 us, and 191 instead of 164 for 9 packed in 4097 x 512 x 32), and a
@@ -483,6 +481,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   __shared__ float outs[3 * (TT * CC + 16)];       // C . h, l . B, sum A q h: 16 banks apart
   __shared__ __align__(16) float gs[2][CG][TT][NP];   // g_B, g_C
   __shared__ __align__(16) float Es[CG * W][S * 64], Ps[CG * W][S * 64], Rs[CG * W][S * 64];
+  __shared__ __align__(16) float Rt[2][CG][S * 64];   // the adjoint state that enters a tile, from its end
   constexpr bool kPark = S >= 8;   // 256 registers do not hold everything: the entering states of a wave's steps lie here meanwhile
   __shared__ __align__(16) float Hin[kPark ? CG * W : 1][kPark ? S * 64 : 4];
   __shared__ __align__(16) float pars[2][CC];
@@ -511,14 +510,13 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   const int piece0 = ss_piece(a, s, u.sid);
   float A2[S], gA[S];
   ss_load_A(A2, a.A, ch, q * S, a.N, ok);
-  // the adjoint state behind the last tile; the wave with a tile's first steps goes on with the last ones of the tile before
-  float l[S] = {};
-  int part = wave;
-  if (part == W - 1) {
+  if (wave == 0) {
+    float R[S];
     if (s.last)
-      ss_load_state(l, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+      ss_load_state(R, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     else
-      ss_load_state(l, a.adj, (int64_t)ss_piece_at(piece0, (s.len - 1) / a.piece, a.npieces) * a.D + ch, q * S, a.N, ok);
+      ss_load_state(R, a.adj, (int64_t)ss_piece_at(piece0, (s.len - 1) / a.piece, a.npieces) * a.D + ch, q * S, a.N, ok);
+    ss_lane_put(Rt[0][cg], R, lane);
   }
 #pragma unroll
   for (int j = 0; j < S; ++j) gA[j] = 0.0f;
@@ -571,7 +569,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     zp -= ss_rows<T>(a.z, TT);
     Bp -= ss_rows<T>(vbc, TT);
   };
-  int pc = __builtin_amdgcn_readfirstlane((s.len - 1) / a.piece);   // piece of the tile
+  int pc = __builtin_amdgcn_readfirstlane((s.len - 1) / a.piece), turn = 0;   // piece of the tile
   auto arrived = [&] {
     ss_arrived(xn);
     ss_arrived(dn);
@@ -580,21 +578,9 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
 #pragma unroll
     for (int i = 0; i < BR; ++i) ss_arrived(Bn[i]);
   };
-  // the state at a tile's start: what it was from its piece's start, and what entered there
-  float hin[S] = {}, H0[S] = {}, cum = 0.0f;
-  auto entering = [&](int t0) {
-    const int at = ss_piece_at(piece0, pc, a.npieces), ln = ss_thread_here() & 63, k = cg * CW + ln / NS;
-    const int64_t tile = ss_tile(a, s.b, at, s.t0 + pc * a.piece, t0 - pc * a.piece);
-    const bool has = u.c0 + k < u.end;
-    if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), ln);
-    cum = has ? (a.cum + tile * a.D + u.c0)[k] : 0.0f;
-    const float* entered = a.seg ? a.seg + ((int64_t)at * a.D + u.c0) * a.N : a.h0 ? a.h0 + ((int64_t)s.b * a.D + u.c0) * a.N : nullptr;
-    ss_load_state(H0, entered, k, ln % NS * S, a.N, has);
-  };
   fetch(last);
-  if (part == 0) entering(last);
   arrived();
-  for (int t0 = last; t0 >= 0; t0 -= TT, part = (part + W - 1) % W) {
+  for (int t0 = last; t0 >= 0; t0 -= TT, turn ^= 1) {
     const auto [st, sc, bt, bn] = here();
     const bool live = sok && t0 + st < s.len;
     const SsRaw<T, V> xc = xn;
@@ -625,19 +611,31 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     }
     __syncthreads();
     if (t0) fetch(t0 - TT);
+    // the state at the tile's start: what it was from its piece's start, and what entered there
+    if (t0 < pc * a.piece) --pc;
+    const int at = ss_piece_at(piece0, pc, a.npieces);
+    const int64_t tile = ss_tile(a, s.b, at, s.t0 + pc * a.piece, t0 - pc * a.piece);
+    float hin[S] = {}, H0[S], cum = 0.0f;
+    {
+      const int ln = S < 8 && sizeof(typename T::E) == 2 ? lane : ss_thread_here() & 63, k = cg * CW + ln / NS;
+      const bool has = u.c0 + k < u.end;
+      if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), ln);
+      if (has) cum = (a.cum + tile * a.D + u.c0)[k];
+      const float* entered = a.seg ? a.seg + ((int64_t)at * a.D + u.c0) * a.N : a.h0 ? a.h0 + ((int64_t)s.b * a.D + u.c0) * a.N : nullptr;
+      ss_load_state(H0, entered, k, ln % NS * S, a.N, has);
+    }
 
-    // Forwards and backwards: the parts in the middle from zero.  The first
-    // one's state and the last one's adjoint are known, their own
-    // contribution to the other direction is of no use.
-    const int lane = (S < 8 ? tid : ss_thread_here()) & 63, q = lane % NS, lc = cg * CW + lane / NS;   // (as above, not held)
-    const int me = cg * W + part, tw = part * TS;
-    float dec[TS][S], hs[TS][S], h[S], sum = 0.0f;
+    // from zero, forwards and backwards
+    const int me = cg * W + wave, tw = wave * TS;
+    float dec[TS][S], hs[TS][S], h[S], l[S], sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < S; ++j) h[j] = l[j] = 0.0f;
 #pragma unroll
     for (int t4 = 0; t4 < TS; t4 += 4) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = t4 + i;
-        const float2 w = *(const float2*)&pre[tw + t][lc];
+        const float4 w = pre[tw + t][lc];
         float b[S];
         ss_row_get(b, &Bs[tw + t][q * S]);
         sum += w.x;
@@ -645,61 +643,54 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
         for (int j = 0; j < S; ++j) {
           dec[t][j] = ss_exp2(w.x * A2[j]);
           hs[t][j] = w.y * b[j];
+          h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    auto keep = [&] {   // the states of these steps from h
+    ss_lane_put(Es[me], h, lane);
 #pragma unroll
-      for (int t = 0; t < TS; ++t)
+    for (int j = 0; j < S; ++j) h[j] = ss_exp2(sum * A2[j]);
+    ss_lane_put(Ps[me], h, lane);
 #pragma unroll
-        for (int j = 0; j < S; ++j) hs[t][j] = h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
-    };
-    if (part == 0) {
+    for (int t4 = TS - 4; t4 >= 0; t4 -= 4) {
 #pragma unroll
-      for (int j = 0; j < S; ++j) h[j] = hin[j] = __builtin_fmaf(ss_exp2(cum * A2[j]), H0[j], hin[j]);
-      keep();
-      ss_lane_put(Es[me], h, lane);
-    } else {
-      if (part < W - 1) {
+      for (int i = 3; i >= 0; --i) {
+        const int t = t4 + i;
+        const float g1 = pre[tw + t][lc].z;
+        float k[S];
+        ss_row_get(k, &Cs[tw + t][q * S]);
 #pragma unroll
-        for (int j = 0; j < S; ++j) h[j] = l[j] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < TS; ++t)
-#pragma unroll
-          for (int j = 0; j < S; ++j) h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
-        ss_lane_put(Es[me], h, lane);
-#pragma unroll
-        for (int j = 0; j < S; ++j) h[j] = ss_exp2(sum * A2[j]);
-        ss_lane_put(Ps[me], h, lane);
+        for (int j = 0; j < S; ++j) l[j] = dec[t][j] * __builtin_fmaf(g1, k[j], l[j]);
       }
-#pragma unroll
-      for (int j = 0; j < S; ++j) hin[j] = l[j];   // (the last part's, for later)
-#pragma unroll
-      for (int t4 = TS - 4; t4 >= 0; t4 -= 4) {
-#pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          const int t = t4 + i;
-          const float g1 = pre[tw + t][lc].z;
-          float k[S];
-          ss_row_get(k, &Cs[tw + t][q * S]);
-#pragma unroll
-          for (int j = 0; j < S; ++j) l[j] = dec[t][j] * __builtin_fmaf(g1, k[j], l[j]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      ss_lane_put(Rs[me], l, lane);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    ss_lane_put(Rs[me], l, lane);
     __syncthreads();
-    // what enters at both ends of this part's steps
-    if (part == W - 1) {
+    // what enters at both ends of this wave's steps; the first wave's adjoint leaves the tile then
 #pragma unroll
-      for (int j = 0; j < S; ++j) l[j] = hin[j];
-    } else {
-      ss_lane_get(l, Rs[cg * W + W - 1], lane);
+    for (int j = 0; j < S; ++j) hin[j] = __builtin_fmaf(ss_exp2(cum * A2[j]), H0[j], hin[j]);
 #pragma unroll
-      for (int v = W - 2; v > 0; --v) {
-        if (v > part) {
+    for (int v = 0; v < W - 1; ++v) {
+      if (v < wave) {
+        float e[S], p[S];
+        ss_lane_get(e, Es[cg * W + v], lane);
+        ss_lane_get(p, Ps[cg * W + v], lane);
+#pragma unroll
+        for (int j = 0; j < S; ++j) hin[j] = __builtin_fmaf(p[j], hin[j], e[j]);
+      }
+    }
+    {
+      float r[S], p[S];   // own contribution and decay, for the first wave
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        r[j] = l[j];
+        p[j] = h[j];
+      }
+      ss_lane_get(l, Rt[turn][cg], lane);
+#pragma unroll
+      for (int v = W - 1; v > 0; --v) {
+        if (v > wave) {
           float e[S], f[S];
           ss_lane_get(e, Rs[cg * W + v], lane);
           ss_lane_get(f, Ps[cg * W + v], lane);
@@ -707,24 +698,19 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
           for (int j = 0; j < S; ++j) l[j] = __builtin_fmaf(f[j], l[j], e[j]);
         }
       }
-    }
-    if (part) {
-      ss_lane_get(hin, Es[cg * W], lane);
+      if (wave == 0) {
 #pragma unroll
-      for (int v = 1; v < W - 1; ++v) {
-        if (v < part) {
-          float e[S], p[S];
-          ss_lane_get(e, Es[cg * W + v], lane);
-          ss_lane_get(p, Ps[cg * W + v], lane);
-#pragma unroll
-          for (int j = 0; j < S; ++j) hin[j] = __builtin_fmaf(p[j], hin[j], e[j]);
-        }
+        for (int j = 0; j < S; ++j) r[j] = __builtin_fmaf(p[j], l[j], r[j]);
+        ss_lane_put(Rt[turn ^ 1][cg], r, lane);
       }
-#pragma unroll
-      for (int j = 0; j < S; ++j) h[j] = hin[j];
-      keep();
     }
     __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < S; ++j) h[j] = hin[j];
+#pragma unroll
+    for (int t = 0; t < TS; ++t)
+#pragma unroll
+      for (int j = 0; j < S; ++j) hs[t][j] = h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
     if constexpr (kPark) ss_lane_put(Hin[me], hin, lane);
     float far[2][2 * S];   // products of the two steps before: g_B's S, then g_C's
 #pragma unroll
@@ -787,10 +773,6 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     // The next tile's rows are here by now.  Waited for before anything is
     // stored: behind the stores, the wait would be for them too.
     arrived();
-    if (t0) {
-      if (t0 - TT < pc * a.piece) --pc;
-      if (part == 1) entering(t0 - TT);   // (this wave has the first part there)
-    }
     {
       const auto [st, sc, bt, bn] = here();
       if (live) {
@@ -836,7 +818,11 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     const int i = ss_thread_here(), lane = i & 63, c = lane / NS, q = lane % NS, lc = cg * CW + c, ch = u.c0 + lc;
     const bool ok = ch < u.end;
     const auto [st, sc, bt, bn] = where(i);
-    if (s.first && part == W - 1 && a.gh0) ss_store_state(l, a.gh0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+    if (s.first && wave == 0 && a.gh0) {
+      float R[S];
+      ss_lane_get(R, Rt[turn][cg], lane);
+      ss_store_state(R, a.gh0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+    }
     // sums over this workgroup's steps: the four waves', then the staging threads' of every channel
     __syncthreads();
     ss_lane_put(Es[cg * W + wave], gA, lane);
