@@ -13,20 +13,13 @@
 // keeps their decays a_t and drives d_t x_t B_t in registers while it forms its
 // end state from zero, learns through LDS the state that enters its steps, and
 // runs the recurrence again on the registers (one multiply-add more: 28 cycles).
-// The first wave of a tile knows its state and runs once, the last one's state
-// from zero is of no use: they do one recurrence, not two.  The waves change parts with the
-// tiles, so that every SIMD has its share of these, and a tile's last is the next one's
-// first, with the state in its registers.
 // Sequences that are too few even so are cut into runs, which start from
 // states that a pass of its own forms first (ss_split).
 //
-// 16 x 2048 steps, 768 channels, 16 states, bf16: 134 us.  The vector units are
-// what it waits for: cells 24 to 28 cycles, 72 to 84 us, and as much again for what a (t, d)
-// needs once (softplus, the gate, roundings) and the exchanges.  Memory, 205 MB, would
-// take 40.  Two recurrences in every part took 141, three barriers a tile 151.
-// Sums of outputs formed behind the second barrier, in the first part too, keep 120
-// registers and four waves a SIMD (65536 x 1024: 503 us, 138 registers 533; fp32
-// held to 128 registers spills two: 24 x 2048 x 768 339 us, 284 so).
+// 16 x 2048 steps, 768 channels, 16 states, bf16: 141 us (160 under the
+// profiler).  The vector units are what it waits for: 136 us at 2.1 GHz by their counter, of
+// which the cells' 28 cycles are 84; the rest is what a (t, d) needs once (softplus, the gate,
+// roundings) and the exchanges.  Memory, 205 MB, would take 40.  Three barriers a tile took 151, two 141.
 //
 // Layout.  A lane holds S states of one channel; NS lanes hold a channel, a wave
 // 64 / NS channels: four states a lane up to 32 (eight, and half the lanes,
@@ -130,7 +123,7 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
   __shared__ __align__(16) float2 du2[2][TT][CW];      // step, step times input; of two tiles in turn
   __shared__ __align__(16) float Bs2[2][TT][NP], Cs2[2][TT][NP];
   __shared__ __align__(16) float ys[TT][CW], pars[2][CW];
-  __shared__ __align__(16) float Es[W - 1][S * 64], Ps[W - 1][S * 64];
+  __shared__ __align__(16) float Es[W - 1][S * 64], Ps[W - 1][S * 64], Hs[2][S * 64];   // Hs: the state that enters a tile
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (ss_block(a.row) == 0 && tid < 2 && a.header) a.header[tid] = 0;
   SsUnit u;
@@ -140,11 +133,14 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
   const bool ok = ch < u.end;
   float A2[S];
   ss_load_A(A2, a.A, ch, q * S, a.N, ok);
-  float h[S];
-  if (a.seg)
-    ss_load_state(h, a.seg, (int64_t)ss_piece(a, s, u.sid) * a.D + ch, q * S, a.N, ok);
-  else
-    ss_load_state(h, a.h0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+  if (wave == W - 1) {
+    float H[S];
+    if (a.seg)
+      ss_load_state(H, a.seg, (int64_t)ss_piece(a, s, u.sid) * a.D + ch, q * S, a.N, ok);
+    else
+      ss_load_state(H, a.h0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+    ss_lane_put(Hs[0], H, lane);
+  }
 
   // this thread's part of a tile: V channels of one step, VB states of one step
   const int st = tid * V / CW, sc = tid * V % CW, bt = tid * VB / NP, bn = tid * VB % NP;
@@ -197,27 +193,25 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
     }
     yp += ss_rows<T>(a.y, TT);
   };
-  // The waves take turns: the one with a tile's last steps, whose state then is
-  // the tile's, goes on with the first of the next.
-  int turn = 0, part = wave;
-  for (int t0 = 0; t0 < s.len; t0 += TT, turn ^= 1, part = (part + 1) % W) {
+  int turn = 0;
+  for (int t0 = 0; t0 < s.len; t0 += TT, turn ^= 1) {
     auto& du = du2[turn];
     auto& Bs = Bs2[turn];
     auto& Cs = Cs2[turn];
     // stage: steps behind the end have d = 0, which leaves the state as it is
-    const bool live = sok && t0 + st < s.len;
+    const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
     float d[V], none[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = dn.get(v) + pars[0][sc + v];
     ss_steps<V, false>(d, none, a.softplus, live);
 #pragma unroll
     for (int v = 0; v < V; ++v) du[st][sc + v] = make_float2(d[v], d[v] * xn.get(v));
-    {   // (behind the end: of an earlier tile, with a step of zero)
+    {
       SsVec<float, VB> b, k;
 #pragma unroll
       for (int v = 0; v < VB; ++v) {
-        b.e[v] = Bn.get(v);
-        k.e[v] = Cn.get(v);
+        b.e[v] = blive ? Bn.get(v) : 0.0f;
+        k.e[v] = blive ? Cn.get(v) : 0.0f;
       }
       *(SsVec<float, VB>*)&Bs[bt][bn] = b;
       *(SsVec<float, VB>*)&Cs[bt][bn] = k;
@@ -228,104 +222,99 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
     zc = zn;
     if (t0 + TT < s.len) fetch(t0 + TT);
 
-    // The first part's entering state is known: its steps are run once.  The
-    // last part's end state from zero is of no use; the others' joins the parts.
-    const int at = part * TS;
-    float dec[TS][S], drv[TS][S], y[TS];
-    auto decays = [&](int t, const float2& w, const float (&b)[S]) {
+    // this wave's steps from zero
+    float dec[TS][S], drv[TS][S], h[S], P[S], sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        dec[t][j] = ss_exp2(w.x * A2[j]);
-        drv[t][j] = w.y * b[j];
-      }
-    };
-    float sum = 0.0f;
-    if (part) {
-#pragma unroll
-      for (int j = 0; j < S; ++j) h[j] = 0.0f;
-    }
+    for (int j = 0; j < S; ++j) h[j] = 0.0f;
 #pragma unroll
     for (int t4 = 0; t4 < TS; t4 += 4) {
       float2 w[4];
       float b[4][S];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[i] = du[at + t4 + i][c];
-        ss_row_get(b[i], &Bs[at + t4 + i][q * S]);
+        w[i] = du[wave * TS + t4 + i][c];
+        ss_row_get(b[i], &Bs[wave * TS + t4 + i][q * S]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const int t = t4 + i;
         sum += w[i].x;
-        decays(t4 + i, w[i], b[i]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    auto run = [&](int t) {
 #pragma unroll
-      for (int j = 0; j < S; ++j) h[j] = __builtin_fmaf(dec[t][j], h[j], drv[t][j]);
-    };
-    if (part == 0) {
-#pragma unroll
-      for (int t = 0; t < TS; ++t) {
-        run(t);
-#pragma unroll
-        for (int j = 0; j < S; ++j) drv[t][j] = h[j];
-      }
-      ss_lane_put(Es[0], h, lane);
-    } else if (part < W - 1) {
-#pragma unroll
-      for (int t = 0; t < TS; ++t) run(t);
-      ss_lane_put(Es[part], h, lane);
-#pragma unroll
-      for (int j = 0; j < S; ++j) h[j] = ss_exp2(sum * A2[j]);
-      ss_lane_put(Ps[part], h, lane);
-    }
-    __syncthreads();
-    if (part) {   // the state that enters this part's steps, and the steps again
-      ss_lane_get(h, Es[0], lane);
-#pragma unroll
-      for (int v = 1; v < W - 1; ++v) {
-        if (v < part) {
-          float e[S], p[S];
-          ss_lane_get(e, Es[v], lane);
-          ss_lane_get(p, Ps[v], lane);
-#pragma unroll
-          for (int j = 0; j < S; ++j) h[j] = __builtin_fmaf(p[j], h[j], e[j]);
+        for (int j = 0; j < S; ++j) {
+          dec[t][j] = ss_exp2(w[i].x * A2[j]);
+          drv[t][j] = w[i].y * b[i][j];
+          h[j] = __builtin_fmaf(dec[t][j], h[j], drv[t][j]);
         }
       }
-#pragma unroll
-      for (int t = 0; t < TS; ++t) {
-        run(t);
-#pragma unroll
-        for (int j = 0; j < S; ++j) drv[t][j] = h[j];
-      }
-    }
-#pragma unroll
-    for (int t4 = 0; t4 < TS; t4 += 4) {
-      float k[4][S];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ss_row_get(k[i], &Cs[at + t4 + i][q * S]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[t4 + i] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < S; ++j) y[t4 + i] = __builtin_fmaf(k[i][j], drv[t4 + i][j], y[t4 + i]);
-      }
       __builtin_amdgcn_sched_barrier(0);
     }
-    // four steps' sums over the states, one step a row of 16 lanes
+#pragma unroll
+    for (int j = 0; j < S; ++j) P[j] = ss_exp2(sum * A2[j]);
+    if (wave < W - 1) {
+      ss_lane_put(Es[wave], h, lane);
+      ss_lane_put(Ps[wave], P, lane);
+    }
+    __syncthreads();
+    // the state that enters them; the last wave's is behind the tile then
+    float own[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) own[j] = h[j];
+    ss_lane_get(h, Hs[turn], lane);
+#pragma unroll
+    for (int v = 0; v < W - 1; ++v) {
+      if (v < wave) {
+        float e[S], p[S];
+        ss_lane_get(e, Es[v], lane);
+        ss_lane_get(p, Ps[v], lane);
+#pragma unroll
+        for (int j = 0; j < S; ++j) h[j] = __builtin_fmaf(p[j], h[j], e[j]);
+      }
+    }
+    if (wave == W - 1) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) own[j] = __builtin_fmaf(P[j], h[j], own[j]);
+      ss_lane_put(Hs[turn ^ 1], own, lane);
+    }
+    // and the steps again
 #pragma unroll
     for (int t4 = 0; t4 < TS; t4 += 4) {
-      float r = ss_fold_rows(y[t4], y[t4 + 1], y[t4 + 2], y[t4 + 3]);
+      float y[4], k[4][S];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss_row_get(k[i], &Cs[wave * TS + t4 + i][q * S]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = t4 + i;
+        y[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          h[j] = __builtin_fmaf(dec[t][j], h[j], drv[t][j]);
+          y[i] = __builtin_fmaf(k[i][j], h[j], y[i]);
+        }
+      }
+      // four steps' sums over the states, one step a row of 16 lanes
+      float r = ss_fold_rows(y[0], y[1], y[2], y[3]);
       if constexpr (NS == 8) r += ss_dpp<kDppRor8>(r);
-      if (NS == 4 || (lane & 15) < CW) ys[at + t4 + (lane >> 4)][lane & (CW - 1)] = r;
+      if (NS == 4 || (lane & 15) < CW) ys[wave * TS + t4 + (lane >> 4)][lane & (CW - 1)] = r;
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   __syncthreads();
   if (s.len > 0) finish(sok && (s.len - 1) / TT * TT + st < s.len);
-  if (s.last && part == 0) ss_store_state(h, a.hL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+  if (s.last && wave == W - 1) {
+    float H[S];
+    ss_lane_get(H, Hs[turn], lane);
+    ss_store_state(H, a.hL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
+  }
 }
 
+// ---- contributions of pieces
+//
+// The state that a piece adds, from zero, and the sum of its steps; a wave
+// takes its channels through the piece alone (16 x 2048 x 768 x 16
+// 96 us under the profiler, 81 of them the vector units).  With ckpt it also writes the
+// state and the sum at the start of every tile of the gradient.  Backwards
+// (REV) it is the adjoint state that flows out of the piece's start,
+// l = a_t (l + g_t C_t), with g the gradient of y before its gate.
 template <int S, int NS>
 struct SsStateLds {
   static constexpr int TT = 16, CC = kSsStateGroups * (64 / NS);
