@@ -20,6 +20,10 @@
 // profiler).  The vector units are what it waits for: 136 us at 2.1 GHz by their counter, of
 // which the cells' 28 cycles are 84; the rest is what a (t, d) needs once (softplus, the gate,
 // roundings) and the exchanges.  Memory, 205 MB, would take 40.  Three barriers a tile took 151, two 141.
+// A tile's first wave could run its steps once, from the state that it knows, and its last
+// one without an end state from zero: 134 us, the gradient 509 instead of 529.  But the state from
+// tile to tile then takes an exponential's error at every step, not at every
+// eighth (h_L after 77 steps off by 2.8e-7 instead of 1.3e-7); not done.
 //
 // Layout.  A lane holds S states of one channel; NS lanes hold a channel, a wave
 // 64 / NS channels: four states a lane up to 32 (eight, and half the lanes,
@@ -199,19 +203,19 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
     auto& Bs = Bs2[turn];
     auto& Cs = Cs2[turn];
     // stage: steps behind the end have d = 0, which leaves the state as it is
-    const bool live = sok && t0 + st < s.len, blive = bok && t0 + bt < s.len;
+    const bool live = sok && t0 + st < s.len;
     float d[V], none[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = dn.get(v) + pars[0][sc + v];
     ss_steps<V, false>(d, none, a.softplus, live);
 #pragma unroll
     for (int v = 0; v < V; ++v) du[st][sc + v] = make_float2(d[v], d[v] * xn.get(v));
-    {
+    {   // (behind the end: of an earlier tile, with a step of zero)
       SsVec<float, VB> b, k;
 #pragma unroll
       for (int v = 0; v < VB; ++v) {
-        b.e[v] = blive ? Bn.get(v) : 0.0f;
-        k.e[v] = blive ? Cn.get(v) : 0.0f;
+        b.e[v] = Bn.get(v);
+        k.e[v] = Cn.get(v);
       }
       *(SsVec<float, VB>*)&Bs[bt][bn] = b;
       *(SsVec<float, VB>*)&Cs[bt][bn] = k;
@@ -448,7 +452,7 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 // up inside the rows of 16 lanes.  (On the matrix cores, as products with a row
 // of ones, they took 32 cycles each: 660 us for the kernel below.)
 //
-// 16 x 2048 x 768 x 16 in bf16: the whole gradient 526 us, of which this kernel is
+// 16 x 2048 x 768 x 16 in bf16: the whole gradient 529 us, of which this kernel is
 // some 440: 60000 vector instructions a wave for its 64 tiles of 32 cells a
 // lane, three waves a SIMD.  The tile's outputs leave before the next is
 // staged: with two tiles' rows in LDS and two barriers the gradient took 690 us instead of 590.
