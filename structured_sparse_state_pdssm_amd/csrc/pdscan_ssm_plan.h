@@ -137,10 +137,10 @@ inline double ss_rounds(double fill, int per, bool bwd) {
 // by rounds of the card.  Cut, time goes by the work, 1.45 times it
 // forwards and 1.08 backwards (the state passes), and the launches add what 280 and 100
 // steps take.  768 channels of 16 states (16 sequences fill the card once), bf16, in us, uncut / cut:
-//   forwards   512 steps of 1: 27 / 28, of 4: 28 / 32;  1024 of 1: 51 / 26, of 4: 51 / 45;  2048 of 6: 113 / 95, of 8: 114 / 110, of 12: 141 / 159
-//   backwards  256 of 1: 71 / 44;  384 of 4: 95 / 64;  2048 of 8: 459 / 340, of 12: 559 / 520, of 16: 604 / 651, of 20: 896 / 812, of 24: 1001 / 973
+//   forwards   512 steps of 1: 28 / 27, of 4: 30 / 33;  1024 of 1: 50 / 28, of 4: 53 / 46;  2048 of 6: 117 / 101, of 8: 114 / 116, of 12: 142 / 163
+//   backwards  256 of 1: 61 / 50;  384 of 4: 81 / 64;  2048 of 8: 389 / 311, of 12: 499 / 449, of 16: 529 / 567, of 20: 727 / 700, of 24: 848 / 842
 // Sequences of different lengths, where the longest counts, are taken as three of a third of the rows:
-//   16 in 2048 rows 32 / 49 and 130 / 99, 16 in 8192 102 / 88 and 358 / 235; 2048 channels, 40 in 8192 192 / 250 and 868 / 852
+//   16 in 2048 rows 33 / 45 and 111 / 94, 16 in 8192 102 / 89 and 333 / 215; 2048 channels, 40 in 8192 191 / 242 and 713 / 716
 inline SsSplit ss_split(int B, int L, int packed, long long width, int per, long long states, bool bwd) {
   SsSplit s;
   constexpr int kCus = 256, kUnit = 32, kLeast = 64, kRun = 128;   // steps of a piece and of a run, at least
