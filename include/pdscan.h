@@ -508,6 +508,8 @@ typedef struct {
  *   A [D,N]; skip, dt_bias [D] or NULL (zero); h0 [B,D,N] or NULL (zero)
  *   h_L [B,D,N] (out, required)
  * Steps d_t >= 0 and A <= 0 (not checked; exp(d A) past fp32 overflows).
+ * With softplus any dt is a step: the type's lowest value, and minus infinity, are
+ * steps of zero, which leave the state as it is.
  * Precision: fp32 throughout, sums of steps over more than a tile in 64 bits;
  * an exponential is good to two steps of fp32.  Decays below 2^-126 are zero.
  * Where the query answers 0 (enough sequences and channels to run each

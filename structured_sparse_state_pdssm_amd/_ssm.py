@@ -238,7 +238,8 @@ def _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, h0, cu_seqlens):
 def pdssm_selscan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, h0=None, cu_seqlens=None,
                       workspace=None, out=None):
     """Prompts.  Returns (y [B,L,D], h_L [B,D,N]).  ``out`` may hold "y" and
-    "h_L" to write to."""
+    "h_L" to write to.  A token whose dt is the type's lowest value (or minus
+    infinity) is a step of zero (softplus): the state passes it as it is."""
     d, sshape, specs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, h0, cu_seqlens)
     given = _given(out, ("y", "h_L"))
     y, hL = given.get("y"), given.get("h_L")
