@@ -142,6 +142,14 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 __device__ __forceinline__ float ss_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// What goes into a decay's exponent, a sum of steps or a product by log2 e, ends at fp32's
+// largest number: were it infinite, its product with a decay or a step of zero would
+// not be a number.
+__device__ __forceinline__ float ss_held(float x) {
+  constexpr float most = 3.40282347e38f;
+  return __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, most), -most);
+}
+
 // e^-|x|, with what the product by log2 e lost put back (a step of fp32 or
 // two, instead of |x| of them).  It is zero from |x| = 104 on, and |x| ends at 128:
 // past 2.4e38 that product would be infinite, what it lost too, and zero times

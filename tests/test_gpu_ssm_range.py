@@ -194,3 +194,54 @@ def test_what_is_no_number_stays_one(dt):
     y = P.pdssm_selscan_step(**dict(row, dt=none), state=pool)
     assert torch.isnan(y[0, 3]) and torch.isnan(pool[0, 3]).all()
     assert int(torch.isnan(y).sum()) == 1 and int(torch.isnan(pool).sum()) == 16
+
+
+@DT
+@pytest.mark.parametrize("shape,lens", [((2, 70, 48, 24, 2), None), ((1, 700, 40, 40, 1), None), ((1, 700, 48, 16, 2), (5, 0, 600, 33, 62)),
+                                        ((1, 40, 16, 64, 1), None)])
+def test_steps_of_the_highest_value(shape, lens, dt):
+    """Steps without an input that forget everything, many in a row: their sum passes fp32.  A step of 1e4 forgets
+    everything too where A is below -0.02, and nothing where A is zero."""
+    P = lib()
+    B, L, D, N, G = shape
+    x, gy, gh = scan_inputs(B, L, D, N, dt, G, S=len(lens) if lens else B)
+    x["A"] = x["A"].clamp(max=-0.02)
+    cu = bounds(lens) if lens else None
+    m = mask_of(x["dt"])
+    x["x"] = put(x["x"], m, 0.0)
+    high = float(torch.finfo(dt).max)
+    a, b = (scan_all(dict(x, dt=put(x["dt"], m, v)), gy, gh, cu) for v in (high, 1e4))
+    for g in (a, b):
+        g["g_x"][m] = 0   # (a step's size times what follows from it)
+    same(a, b)
+    x["A"][:, ::3] = 0.0
+    a, b = (P.pdssm_selscan_fwd(**dict(x, dt=put(x["dt"], m, v)), cu_seqlens=cu) for v in (high, 1e4))
+    same(dict(zip("yh", a)), dict(zip("yh", b)))
+    row = {k: (t[:, 0] if k in ("x", "dt", "z") else t[:, :, 0] if k in ("Bm", "Cm") else t) for k, t in x.items() if k != "h0"}
+    row["x"] = torch.zeros_like(row["x"])
+    got = []
+    for v in (high, 1e4):
+        pool = x["h0"].clone()
+        y = P.pdssm_selscan_step(**dict(row, dt=torch.full_like(row["dt"], v)), state=pool)
+        got.append(dict(y=y, pool=pool))
+    same(*got)
+    assert torch.equal(pool[..., ::3], x["h0"][..., ::3]) and (pool[:B, :, 1::3] == 0).all()
+
+
+@DT
+def test_decays_of_the_lowest_value(dt):
+    """A state that every step forgets is kept by a step of zero."""
+    P = lib()
+    x, gy, gh = scan_inputs(1, 300, 48, 24, dt, 2)
+    m = mask_of(x["dt"])
+    x["dt"] = put(x["dt"], m, lowest(dt))
+    got = []
+    for v in (lowest(F32), -1e8):   # (other steps are above 1e-5: both forget everything)
+        x["A"][:, ::3] = v
+        y, hL = P.pdssm_selscan_fwd(**x)
+        pool = x["h0"].clone()
+        row = {k: (t[:, 0] if k in ("x", "dt", "z") else t[:, :, 0] if k in ("Bm", "Cm") else t) for k, t in x.items() if k != "h0"}
+        step = P.pdssm_selscan_step(**row, state=pool)
+        got.append(dict(y=y, h_L=hL, step=step, pool=pool))
+    same(*got)
+    assert torch.equal(pool, x["h0"])   # (the first token is switched off)
