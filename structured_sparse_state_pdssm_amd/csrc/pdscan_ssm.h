@@ -276,13 +276,6 @@ __device__ __forceinline__ float ss_sum(float x) {
 // The workgroup's number, in a launch of la_grid_rows.
 __device__ __forceinline__ unsigned ss_block(unsigned row) { return blockIdx.y * row + blockIdx.x; }
 
-// Workgroups go to the eight dies in turn; this numbers them so that a die
-// has neighbours: they share rows' cache lines and, in a scan, B and C.
-__device__ __forceinline__ long long ss_near(unsigned id, long long n) {
-  const long long per = (n + 7) / 8;
-  return (long long)(id % 8) * per + id / 8;   // at or past n: nothing to do
-}
-
 // Whether row b of a step has no state of its own: a slot that is empty, past
 // the pool, or an earlier row's.  Every wave searches for itself: 256 rows are
 // four loads at once, and no wave waits for another.

@@ -33,6 +33,15 @@ constexpr int64_t ss_tile_of(int per, int b, int at, int t0, int t, int tile) {
   return (per ? (int64_t)b * per : (int64_t)at) + t0 / tile + t / tile;
 }
 
+// Workgroups go to the eight dies in turn; this numbers them so that a die
+// has neighbours: they share rows' cache lines and, in a scan, B and C.  At or
+// past n: nothing to do; so is what the last of several rows of a grid has behind
+// the eight dies' units, which would be the next die's first ones.
+constexpr long long ss_near(unsigned id, long long n) {
+  const long long per = (n + 7) / 8, at = id / 8;
+  return at < per ? (long long)(id % 8) * per + at : n;
+}
+
 // One pass of the selective scan.  Element (b, t, d) of x, dt, z, y and their
 // gradients is at sb b + st t + d; B and C have a head axis of G groups.
 struct SsArgs {
