@@ -173,12 +173,13 @@ def pdssm_conv_bwd(x, w, g_y, bias=None, x0=None, g_xL=None, silu=True, cu_seqle
                    out=None):
     """Gradient of pdssm_conv_fwd, given the gradients of y and (optional)
     x_L.  Returns dict(g_x, g_w, g_bias[, g_x0]), typed as their inputs; g_bias
-    and g_x0 also where bias and x0 are left out (zero)."""
+    and g_x0 also where bias and x0 are left out (zero).  ``out`` may hold any
+    of those returned to write to, and nothing else."""
     d, sshape, specs = _conv_args(x, w, bias, x0, silu, cu_seqlens)
     _tensors((g_y, "g_y", 3, "[B,L,D]"))
-    names = ("g_x", "g_w", "g_bias", "g_x0")
+    names = ["g_x", "g_w", "g_bias"] + ["g_x0"] * bool(want_x0)
     given = _given(out, names)
-    res = {n: given.get(n) for n in names if n != "g_x0" or want_x0}
+    res = {n: given.get(n) for n in names}
     index, dt, dev = x.get_device(), x.dtype, x.device
     D = x.shape[2]
     outs = [(res["g_x"], "g_x", x.shape, dt, _ROWS), (res["g_w"], "g_w", w.shape, _f32, _WHOLE),
@@ -263,13 +264,14 @@ def pdssm_selscan_bwd(x, dt, A, Bm, Cm, g_y, D=None, z=None, dt_bias=None, softp
     """Gradient of pdssm_selscan_fwd, given the gradients of y and (optional)
     h_L.  Returns dict(g_x, g_dt, g_A, g_B, g_C, g_D, g_dt_bias[, g_z][, g_h0]),
     shaped and typed as their inputs; g_D, g_dt_bias and g_h0 also where
-    those are left out (zero).  ``out`` may hold any of them to write to."""
+    those are left out (zero).  ``out`` may hold any of those returned to
+    write to, and nothing else."""
     d, sshape, specs = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, h0, cu_seqlens)
     _tensors((g_y, "g_y", 3, "[B,L,D]"))
     index, ty, dev = x.get_device(), x.dtype, x.device
     K = x.shape[2]
     names = ["g_x", "g_dt", "g_A", "g_B", "g_C", "g_D", "g_dt_bias"] + ["g_z"] * (z is not None) + ["g_h0"] * bool(want_h0)
-    given = _given(out, ("g_x", "g_dt", "g_A", "g_B", "g_C", "g_D", "g_dt_bias", "g_z", "g_h0"))
+    given = _given(out, names)
     res = {n: given.get(n) for n in names}
     outs = [(res["g_x"], "g_x", x.shape, ty, _ROWS), (res["g_dt"], "g_dt", x.shape, ty, _ROWS),
             (res["g_A"], "g_A", A.shape, _f32, _WHOLE), (res["g_B"], "g_B", Bm.shape, ty, _ROWS),
@@ -365,13 +367,13 @@ def pdssm_norm_fwd(x, w, z=None, gate=None, residual=None, res_scale=None, eps=1
 def pdssm_norm_bwd(x, w, g_y, z=None, gate=None, res_scale=None, eps=1e-5, workspace=None, out=None):
     """Gradient of pdssm_norm_fwd; the residual's is g_y itself.  Returns
     dict(g_x, g_w[, g_z][, g_res_scale]), shaped and typed as their inputs.
-    ``out`` may hold any of them to write to."""
+    ``out`` may hold any of those returned to write to, and nothing else."""
     d, wshape, specs = _norm_args(x, w, z, gate, res_scale, eps)
     if not isinstance(g_y, torch.Tensor):
         raise TypeError("g_y must be a torch.Tensor")
     index, dt, dev = x.get_device(), x.dtype, x.device
-    given = _given(out, ("g_x", "g_w", "g_z", "g_res_scale"))
     names = ["g_x", "g_w"] + ["g_z"] * (z is not None) + ["g_res_scale"] * (res_scale is not None)
+    given = _given(out, names)
     res = {n: given.get(n) for n in names}
     _verify(specs + [(g_y, "g_y", x.shape, dt, _ROWS), (res["g_x"], "g_x", x.shape, dt, _ROWS),
                      (res["g_w"], "g_w", wshape, _f32, _WHOLE), (res.get("g_z"), "g_z", x.shape, dt, _ROWS),
