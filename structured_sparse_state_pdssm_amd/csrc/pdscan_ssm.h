@@ -139,6 +139,7 @@ __device__ __forceinline__ int64_t ss_rows(const LaView& v, int rows) {
 }
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLog2eRest = (float)(1.44269504088896340736 - (double)kLog2e);   // what fp32 drops of log2 e
 
 __device__ __forceinline__ float ss_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -150,14 +151,14 @@ __device__ __forceinline__ float ss_held(float x) {
   return __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, most), -most);
 }
 
-// e^-|x|, with what the product by log2 e lost put back (a step of fp32 or
-// two, instead of |x| of them).  It is zero from |x| = 104 on, and |x| ends at 128:
+// e^-|x|, with what the product by log2 e lost put back, and what log2 e itself
+// lost (a step of fp32 or two, instead of |x| of them; without the second .22 |x| half steps).  It is zero from |x| = 104 on, and |x| ends at 128:
 // past 2.4e38 that product would be infinite, what it lost too, and zero times
 // that not a number (a type's lowest value switches a token off).  One
 // instruction, which passes on what is not a number as fmaxf would not.
 __device__ __forceinline__ float ss_decay(float x) {
   const float n = __builtin_elementwise_maximum(-fabsf(x), -128.0f), t = kLog2e * n, e = ss_exp2(t);
-  return __builtin_fmaf(e, kLn2 * __builtin_fmaf(n, kLog2e, -t), e);
+  return __builtin_fmaf(e, kLn2 * __builtin_fmaf(n, kLog2eRest, __builtin_fmaf(n, kLog2e, -t)), e);
 }
 // 1 / (1 + e^-x) from e = e^-|x|.
 __device__ __forceinline__ float ss_sigmoid_of(float x, float e) {
