@@ -17,7 +17,7 @@ __global__ __launch_bounds__(256) void pdssm_selscan_carry_kernel(const SsCarryA
   const int ch = (int)(e / a.N);
   const int s0 = a.starts ? a.starts[b] : b * a.npiece, s1 = a.starts ? a.starts[b + 1] : s0 + a.npiece, n = s1 - s0;
   float4 A = *(const float4*)(a.A + e), S = make_float4(0, 0, 0, 0);
-  A = make_float4(ss_held(A.x * kLog2e), ss_held(A.y * kLog2e), ss_held(A.z * kLog2e), ss_held(A.w * kLog2e));
+  A = make_float4(ss_held_decay(A.x * kLog2e), ss_held_decay(A.y * kLog2e), ss_held_decay(A.z * kLog2e), ss_held_decay(A.w * kLog2e));
   float* seg = a.seg[rev];
   if (a.user[rev]) S = *(const float4*)(a.user[rev] + b * state + e);
   constexpr int U = 8;

@@ -39,7 +39,7 @@ namespace pdscan {
 template <int S>
 __device__ __forceinline__ void ss_load_A(float (&A2)[S], const float* A, int64_t ch, int n0, int N, bool ok) {
 #pragma unroll
-  for (int s = 0; s < S; ++s) A2[s] = ok && n0 + s < N ? ss_held(A[ch * N + n0 + s] * kLog2e) : 0.0f;
+  for (int s = 0; s < S; ++s) A2[s] = ok && n0 + s < N ? ss_held_decay(A[ch * N + n0 + s] * kLog2e) : 0.0f;
 }
 
 // A lane's S states from the n0-th of channel row `at` (N is a multiple of 8: all of them or none).
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    sum = ss_held(sum);
+    sum = ss_held_sum(sum);
 #pragma unroll
     for (int j = 0; j < S; ++j) P[j] = ss_exp2(sum * A2[j]);
     if (wave < W - 1) {
@@ -402,7 +402,7 @@ __device__ __forceinline__ void ss_state_body(const SsArgs& a, SsStateLds<S, NS>
     if (!REV && a.ckpt && t0 % kSsBwdTile == 0) {
       const int64_t tile = ss_tile(a, s.b, u.sid, s.t0, t0);
       if (wblk < nblk) ss_lane_put(a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), h, lane);
-      if (ok && q == 0) a.cum[tile * a.D + ch] = ss_held((float)total);
+      if (ok && q == 0) a.cum[tile * a.D + ch] = ss_held_sum((float)total);
     }
     float sum = 0.0f;
 #pragma unroll
@@ -422,7 +422,7 @@ __device__ __forceinline__ void ss_state_body(const SsArgs& a, SsStateLds<S, NS>
   }
   if (!a.seg) return;
   ss_store_state(h, REV ? a.adj : a.seg, (int64_t)u.sid * a.D + ch, q * S, a.N, ok);
-  if (!REV && ok && q == 0) a.sum[(int64_t)u.sid * a.D + ch] = ss_held((float)total);
+  if (!REV && ok && q == 0) a.sum[(int64_t)u.sid * a.D + ch] = ss_held_sum((float)total);
 }
 
 // Both directions in one launch (z), as neither waits for the other.
@@ -643,7 +643,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
       __builtin_amdgcn_sched_barrier(0);
     }
     ss_lane_put(Es[me], h, lane);
-    sum = ss_held(sum);
+    sum = ss_held_sum(sum);
 #pragma unroll
     for (int j = 0; j < S; ++j) h[j] = ss_exp2(sum * A2[j]);
     ss_lane_put(Ps[me], h, lane);
@@ -880,7 +880,7 @@ __global__ __launch_bounds__(256) void pdssm_selscan_step_kernel(const SsStepArg
     if (ok && q == 0) ss_store<T, 1>(a.y.p, (int64_t)b * a.y.sb + ch, &f);
     return;
   }
-  const float d = a.softplus ? ss_softplus_of(raw, ss_decay(raw)) : raw, u = d * x, w = ss_held(d * kLog2e);
+  const float d = a.softplus ? ss_softplus_of(raw, ss_decay(raw)) : raw, u = d * x, w = ss_held_sum(d * kLog2e);
   h.x = __builtin_fmaf(ss_exp2(w * A.x), h.x, u * vb.get(0));
   h.y = __builtin_fmaf(ss_exp2(w * A.y), h.y, u * vb.get(1));
   h.z = __builtin_fmaf(ss_exp2(w * A.z), h.z, u * vb.get(2));

@@ -139,26 +139,26 @@ __device__ __forceinline__ int64_t ss_rows(const LaView& v, int rows) {
 }
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr float kLog2eRest = (float)(1.44269504088896340736 - (double)kLog2e);   // what fp32 drops of log2 e
+constexpr float kLn2Rest = (float)(0.69314718055994530942 - (double)kLn2);   // what fp32 drops of ln 2
 
 __device__ __forceinline__ float ss_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// What goes into a decay's exponent, a sum of steps or a product by log2 e, ends at fp32's
+// What goes into a decay's exponent, a sum of steps or A log2 e, ends at fp32's
 // largest number: were it infinite, its product with a decay or a step of zero would
-// not be a number.
-__device__ __forceinline__ float ss_held(float x) {
-  constexpr float most = 3.40282347e38f;
-  return __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, most), -most);
-}
+// not be a number.  One instruction each (steps are not negative, A is not positive).
+constexpr float kMost = 3.40282347e38f;
+__device__ __forceinline__ float ss_held_sum(float x) { return __builtin_elementwise_minimum(x, kMost); }
+__device__ __forceinline__ float ss_held_decay(float x) { return __builtin_elementwise_maximum(x, -kMost); }
 
-// e^-|x|, with what the product by log2 e lost put back, and what log2 e itself
-// lost (a step of fp32 or two, instead of |x| of them; without the second .22 |x| half steps).  It is zero from |x| = 104 on, and |x| ends at 128:
-// past 2.4e38 that product would be infinite, what it lost too, and zero times
+// e^-|x|, to a step of fp32 or two: 2^t with t = n log2 e rounded, times e^r, 1 + r, of
+// what is left, r = n - t ln 2 with ln 2 in two parts (Cody and Waite's reduction; with
+// one part r would be .05 |x| half steps off, left out altogether |x| of them).  It is zero from |x|
+// = 104 on, and |x| ends at 128: past 2.4e38 t would be infinite, r too, and zero times
 // that not a number (a type's lowest value switches a token off).  One
 // instruction, which passes on what is not a number as fmaxf would not.
 __device__ __forceinline__ float ss_decay(float x) {
   const float n = __builtin_elementwise_maximum(-fabsf(x), -128.0f), t = kLog2e * n, e = ss_exp2(t);
-  return __builtin_fmaf(e, kLn2 * __builtin_fmaf(n, kLog2eRest, __builtin_fmaf(n, kLog2e, -t)), e);
+  return __builtin_fmaf(e, __builtin_fmaf(-t, kLn2Rest, __builtin_fmaf(-t, kLn2, n)), e);
 }
 // 1 / (1 + e^-x) from e = e^-|x|.
 __device__ __forceinline__ float ss_sigmoid_of(float x, float e) {
