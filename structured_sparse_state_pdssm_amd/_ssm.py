@@ -25,7 +25,6 @@ import struct
 import torch
 
 from ._linattn import (
-    _ANY,
     _FLOATS,
     _ROWS,
     _WHOLE,

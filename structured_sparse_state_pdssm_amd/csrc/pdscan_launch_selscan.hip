@@ -161,13 +161,13 @@ hipError_t launch_selscan_state(const SsArgs& args, int bf16, hipStream_t st) {
 
 hipError_t launch_selscan_bwd(const SsArgs& args, int bf16, hipStream_t st) {
   SsArgs a = args;
-  const LaGrid g = units(a, ss_channels(a.N) * kSsBwdGroups, 256 * kSsBwdGroups);
+  const LaGrid g = units(a, ss_channels(a.N), 256);
   return by_states(a.N, [&](auto s, auto ns) {
     constexpr int S = decltype(s)::value, NS = decltype(ns)::value;
     if (bf16)
-      hipLaunchKernelGGL((pdssm_selscan_bwd_kernel<SsBf16, S, NS>), dim3(g.x, g.y), dim3(256 * kSsBwdGroups), 0, st, a);
+      hipLaunchKernelGGL((pdssm_selscan_bwd_kernel<SsBf16, S, NS>), dim3(g.x, g.y), dim3(256), 0, st, a);
     else
-      hipLaunchKernelGGL((pdssm_selscan_bwd_kernel<SsF32, S, NS>), dim3(g.x, g.y), dim3(256 * kSsBwdGroups), 0, st, a);
+      hipLaunchKernelGGL((pdssm_selscan_bwd_kernel<SsF32, S, NS>), dim3(g.x, g.y), dim3(256), 0, st, a);
   });
 }
 

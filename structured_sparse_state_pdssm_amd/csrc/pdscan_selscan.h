@@ -464,27 +464,27 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 // the others: addresses, here.  So offsets and, where there is no room, indexes
 // are formed where they are used.
 template <typename T, int S, int NS>
-__global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_selscan_bwd_kernel(const SsArgs a) {
-  constexpr int W = kSsTimeWaves, CG = kSsBwdGroups, TS = kSsBwdSteps, TT = W * TS, CW = 64 / NS, CC = CG * CW, NP = S * NS;
-  constexpr int NT = 256 * CG, V = TT * CC / NT;
-  constexpr int BT = NT / 2, VB = TT * NP / BT < 8 ? TT * NP / BT : 8, BR = TT * NP / BT / VB;   // B by one half of the threads, C by the other
-  static_assert(TS % 4 == 0, "sums over the channels take four steps at once");
+__global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_bwd_kernel(const SsArgs a) {
+  constexpr int W = kSsTimeWaves, TS = kSsBwdSteps, TT = W * TS, CC = 64 / NS, NP = S * NS;
+  constexpr int V = TT * CC / 256;
+  constexpr int BT = 128, VB = TT * NP / BT < 8 ? TT * NP / BT : 8, BR = TT * NP / BT / VB;   // B by one half of the threads, C by the other
+  static_assert(kSsBwdGroups == 1 && TS % 4 == 0, "a workgroup's waves share their channels; sums over them take four steps at once");
   __shared__ __align__(16) float4 pre[TT][CC];     // d, d x, g, slope of d
   __shared__ __align__(16) float gzs[TT][CC];      // slope of the gate times g_y
   __shared__ __align__(16) float Bs[TT][NP], Cs[TT][NP];
   __shared__ float outs[3 * (TT * CC + 16)];       // C . h, l . B, sum A q h: 16 banks apart
-  __shared__ __align__(16) float gs[2][CG][TT][NP];   // g_B, g_C
-  __shared__ __align__(16) float Es[CG * W][S * 64], Ps[CG * W][S * 64], Rs[CG * W][S * 64];
-  __shared__ __align__(16) float Rt[2][CG][S * 64];   // the adjoint state that enters a tile, from its end
+  __shared__ __align__(16) float gs[2][TT][NP];   // g_B, g_C
+  __shared__ __align__(16) float Es[W][S * 64], Ps[W][S * 64], Rs[W][S * 64];
+  __shared__ __align__(16) float Rt[2][S * 64];   // the adjoint state that enters a tile, from its end
   constexpr bool kPark = S >= 8;   // 256 registers do not hold everything: the entering states of a wave's steps lie here meanwhile
-  __shared__ __align__(16) float Hin[kPark ? CG * W : 1][kPark ? S * 64 : 4];
+  __shared__ __align__(16) float Hin[kPark ? W : 1][kPark ? S * 64 : 4];
   __shared__ __align__(16) float pars[2][CC];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6) % W, cg = __builtin_amdgcn_readfirstlane(tid >> 6) / W;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6) % W;   // (so that the compiler knows its range: 531 -> 529 us)
   if (ss_block(a.row) == 0 && tid < 2) a.header[tid] = 0;
   SsUnit u;
   if (!ss_unit(a, CC, u)) return;
   SsSeg s;
-  const int c = lane / NS, q = lane % NS, lc = cg * CW + c, ch = u.c0 + lc;
+  const int lc = lane / NS, q = lane % NS, ch = u.c0 + lc;
   const bool ok = ch < u.end;
   const bool found = ss_segment(a.s, u.sid, s);
   float* partA = a.partA + (int64_t)u.sid * a.D * (a.N + 2);
@@ -510,7 +510,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
       ss_load_state(R, a.ghL, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     else
       ss_load_state(R, a.adj, (int64_t)ss_piece_at(piece0, (s.len - 1) / a.piece, a.npieces) * a.D + ch, q * S, a.N, ok);
-    ss_lane_put(Rt[0][cg], R, lane);
+    ss_lane_put(Rt[0], R, lane);
   }
 #pragma unroll
   for (int j = 0; j < S; ++j) gA[j] = 0.0f;
@@ -539,7 +539,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
   float gD[V], gb[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) gD[v] = gb[v] = 0.0f;
-  const int wblk = u.c0 % (a.D / a.G) / CW + cg, nblk = (a.D / a.G + CW - 1) / CW;
+  const int wblk = u.c0 % (a.D / a.G) / CC, nblk = (a.D / a.G + CC - 1) / CC;
   SsRaw<T, V> xn = {}, dn = {}, zn = {}, gn = {};
   SsRaw<T, VB> Bn[BR] = {};
   const int last = (s.len - 1) / TT * TT, t1 = s.t0 + last;
@@ -611,7 +611,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     const int64_t tile = ss_tile(a, s.b, at, s.t0 + pc * a.piece, t0 - pc * a.piece);
     float hin[S] = {}, H0[S], cum = 0.0f;
     {
-      const int ln = S < 8 && sizeof(typename T::E) == 2 ? lane : ss_thread_here() & 63, k = cg * CW + ln / NS;
+      const int ln = S < 8 && sizeof(typename T::E) == 2 ? lane : ss_thread_here() & 63, k = ln / NS;
       const bool has = u.c0 + k < u.end;
       if (wblk < nblk) ss_lane_get(hin, a.ckpt + ((tile * a.G + u.g) * nblk + wblk) * (S * 64), ln);
       if (has) cum = (a.cum + tile * a.D + u.c0)[k];
@@ -620,7 +620,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     }
 
     // from zero, forwards and backwards
-    const int me = cg * W + wave, tw = wave * TS;
+    const int tw = wave * TS;
     float dec[TS][S], hs[TS][S], h[S], l[S], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < S; ++j) h[j] = l[j] = 0.0f;
@@ -642,11 +642,11 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    ss_lane_put(Es[me], h, lane);
+    ss_lane_put(Es[wave], h, lane);
     sum = ss_held_sum(sum);
 #pragma unroll
     for (int j = 0; j < S; ++j) h[j] = ss_exp2(sum * A2[j]);
-    ss_lane_put(Ps[me], h, lane);
+    ss_lane_put(Ps[wave], h, lane);
 #pragma unroll
     for (int t4 = TS - 4; t4 >= 0; t4 -= 4) {
 #pragma unroll
@@ -660,7 +660,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    ss_lane_put(Rs[me], l, lane);
+    ss_lane_put(Rs[wave], l, lane);
     __syncthreads();
     // what enters at both ends of this wave's steps; the first wave's adjoint leaves the tile then
 #pragma unroll
@@ -669,8 +669,8 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     for (int v = 0; v < W - 1; ++v) {
       if (v < wave) {
         float e[S], p[S];
-        ss_lane_get(e, Es[cg * W + v], lane);
-        ss_lane_get(p, Ps[cg * W + v], lane);
+        ss_lane_get(e, Es[v], lane);
+        ss_lane_get(p, Ps[v], lane);
 #pragma unroll
         for (int j = 0; j < S; ++j) hin[j] = __builtin_fmaf(p[j], hin[j], e[j]);
       }
@@ -682,13 +682,13 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
         r[j] = l[j];
         p[j] = h[j];
       }
-      ss_lane_get(l, Rt[turn][cg], lane);
+      ss_lane_get(l, Rt[turn], lane);
 #pragma unroll
       for (int v = W - 1; v > 0; --v) {
         if (v > wave) {
           float e[S], f[S];
-          ss_lane_get(e, Rs[cg * W + v], lane);
-          ss_lane_get(f, Ps[cg * W + v], lane);
+          ss_lane_get(e, Rs[v], lane);
+          ss_lane_get(f, Ps[v], lane);
 #pragma unroll
           for (int j = 0; j < S; ++j) l[j] = __builtin_fmaf(f[j], l[j], e[j]);
         }
@@ -696,7 +696,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
       if (wave == 0) {
 #pragma unroll
         for (int j = 0; j < S; ++j) r[j] = __builtin_fmaf(p[j], l[j], r[j]);
-        ss_lane_put(Rt[turn ^ 1][cg], r, lane);
+        ss_lane_put(Rt[turn ^ 1], r, lane);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -706,14 +706,14 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     for (int t = 0; t < TS; ++t)
 #pragma unroll
       for (int j = 0; j < S; ++j) hs[t][j] = h[j] = __builtin_fmaf(dec[t][j], h[j], hs[t][j]);
-    if constexpr (kPark) ss_lane_put(Hin[me], hin, lane);
+    if constexpr (kPark) ss_lane_put(Hin[wave], hin, lane);
     float far[2][2 * S];   // products of the two steps before: g_B's S, then g_C's
 #pragma unroll
     for (int t = TS - 1; t >= 0; --t) {
       const float4 w = pre[tw + t][lc];
       float b[S], k[S], y = 0.0f, lb = 0.0f, pa = 0.0f, v[2 * S];
       if constexpr (kPark)
-        if (t == 0) ss_lane_get(hin, Hin[me], lane);
+        if (t == 0) ss_lane_get(hin, Hin[wave], lane);
       ss_row_get(b, &Bs[tw + t][q * S]);
       ss_row_get(k, &Cs[tw + t][q * S]);
 #pragma unroll
@@ -758,7 +758,7 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
             SsVec<float, U> o;
 #pragma unroll
             for (int i = 0; i < U; ++i) o.e[i] = g[j + i];
-            *(SsVec<float, U>*)&gs[j / S][cg][at][q * S + j % S] = o;
+            *(SsVec<float, U>*)&gs[j / S][at][q * S + j % S] = o;
           }
         }
       }
@@ -801,26 +801,23 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
         float* o = a.part + ((((int64_t)(second ? nb : 0) + u.block) * a.rows) + r) * a.N + bn;
         SsVec<float, VB> v;
 #pragma unroll
-        for (int j = 0; j < VB; ++j) {
-          v.e[j] = gs[second][0][t][bn + j];
-          if constexpr (CG == 2) v.e[j] += gs[second][CG - 1][t][bn + j];
-        }
+        for (int j = 0; j < VB; ++j) v.e[j] = gs[second][t][bn + j];
         *(SsVec<float, VB>*)o = v;
       }
     }
   }
   {   // (nothing of this is held through the loop)
-    const int i = ss_thread_here(), lane = i & 63, c = lane / NS, q = lane % NS, lc = cg * CW + c, ch = u.c0 + lc;
+    const int i = ss_thread_here(), lane = i & 63, lc = lane / NS, q = lane % NS, ch = u.c0 + lc;
     const bool ok = ch < u.end;
     const auto [st, sc, bt, bn] = where(i);
     if (s.first && wave == 0 && a.gh0) {
       float R[S];
-      ss_lane_get(R, Rt[turn][cg], lane);
+      ss_lane_get(R, Rt[turn], lane);
       ss_store_state(R, a.gh0, (int64_t)s.b * a.D + ch, q * S, a.N, ok);
     }
     // sums over this workgroup's steps: the four waves', then the staging threads' of every channel
     __syncthreads();
-    ss_lane_put(Es[cg * W + wave], gA, lane);
+    ss_lane_put(Es[wave], gA, lane);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       outs[st * CC + sc + v] = gD[v];
@@ -829,9 +826,9 @@ __global__ __launch_bounds__(256 * kSsBwdGroups, S >= 8 ? 2 : 3) void pdssm_sels
     __syncthreads();
     if (wave == 0) {
       float sumA[S], e[S];
-      ss_lane_get(sumA, Es[cg * W], lane);
+      ss_lane_get(sumA, Es[0], lane);
       for (int v = 1; v < W; ++v) {
-        ss_lane_get(e, Es[cg * W + v], lane);
+        ss_lane_get(e, Es[v], lane);
 #pragma unroll
         for (int j = 0; j < S; ++j) sumA[j] += e[j];
       }

@@ -209,7 +209,7 @@ __device__ __forceinline__ float ss_dpp(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppRor4 = 0x124, kDppRor8 = 0x128,
-              kDppShl1 = 0x101, kDppShl4 = 0x104;
+              kDppShl4 = 0x104;
 
 // Exchanges across a wave, by hand, as the compiler's builtins give the first
 // result twice; each waits for the two states that it has to be behind what wrote

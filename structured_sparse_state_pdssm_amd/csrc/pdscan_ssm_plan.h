@@ -117,7 +117,7 @@ inline int ss_blocks(int K, int per) { return (K + per - 1) / per; }        // c
 // A tile is four waves of eight steps each.
 constexpr int kSsFwdSteps = 8;
 constexpr int kSsBwdSteps = 8, kSsTimeWaves = 4, kSsBwdTile = kSsBwdSteps * kSsTimeWaves;
-constexpr int kSsBwdGroups = 1;   // channel groups (waves side by side) of a gradient's workgroup
+constexpr int kSsBwdGroups = 1;   // channel groups of a gradient's workgroup: two would halve the partial g_B and g_C and were slower
 constexpr int kSsStateGroups = 4;
 
 // How a call cuts the step axis.  A piece is what a wave of the state pass
