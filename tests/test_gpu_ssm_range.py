@@ -245,3 +245,25 @@ def test_decays_of_the_lowest_value(dt):
         got.append(dict(y=y, h_L=hL, step=step, pool=pool))
     same(*got)
     assert torch.equal(pool, x["h0"])   # (the first token is switched off)
+
+
+@DT
+def test_sequences_without_rows(dt):
+    """Packed sequences none of which has a row: states pass through, rows stay as they are, weights have no gradient."""
+    P = lib()
+    for L in (1, 700):
+        x, gy, gh = scan_inputs(1, L, 48, 16, dt, 2, S=3)
+        for at in (0, L):
+            cu = torch.full((4,), at, dtype=torch.int32, device="cuda")
+            mark = lambda t: torch.full_like(t, 7.0)  # noqa: E731
+            y, hL = P.pdssm_selscan_fwd(**x, cu_seqlens=cu, out={"y": mark(gy)})
+            g = P.pdssm_selscan_bwd(**x, g_y=gy, g_hL=gh, cu_seqlens=cu, out={
+                "g_x": mark(gy), "g_dt": mark(gy), "g_z": mark(gy), "g_B": mark(x["Bm"]), "g_C": mark(x["Cm"])})
+            assert torch.equal(hL, x["h0"]) and torch.equal(g["g_h0"], gh)
+            assert all((t == 7).all() for t in (y, g["g_x"], g["g_dt"], g["g_z"], g["g_B"], g["g_C"]))
+            assert all((g[k] == 0).all() for k in ("g_A", "g_D", "g_dt_bias"))
+            c, cy, cx = conv_inputs(1, L, 48, 4, dt, S=3)
+            y, xL = P.pdssm_conv_fwd(**c, cu_seqlens=cu, out={"y": mark(cy)})
+            g = P.pdssm_conv_bwd(**c, g_y=cy, g_xL=cx, cu_seqlens=cu, out={"g_x": mark(cy)})
+            assert torch.equal(xL, c["x0"]) and torch.equal(g["g_x0"], cx)
+            assert (y == 7).all() and (g["g_x"] == 7).all() and (g["g_w"] == 0).all() and (g["g_bias"] == 0).all()
