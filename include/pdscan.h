@@ -510,8 +510,11 @@ typedef struct {
  * Steps d_t >= 0 and A <= 0 (not checked; exp(d A) past fp32 overflows).
  * With softplus any dt is a step: the type's lowest value, and minus infinity, are
  * steps of zero, which leave the state as it is.
- * Precision: fp32 throughout, sums of steps over more than a tile in 64 bits;
- * an exponential is good to two steps of fp32.  Decays below 2^-126 are zero.
+ * Precision: fp32 throughout, sums of steps over more than a tile formed in 64
+ * bits.  A decay is 2^(d (A log2 e)), both products rounded: 2.3 |d A| half steps of
+ * fp32 and the exponential's two, so that its error counts where it is not small itself.
+ * Decays below 2^-126 are zero.  The e^-|x| of softplus and of fp32 gates is good to two
+ * steps whatever x; gates of bf16 calls take a shorter way (1.3 |z| half steps).
  * Where the query answers 0 (enough sequences and channels to run each
  * sequence in one) workspace may be NULL. */
 int pdssm_selscan_workspace_bytes(const pdssm_selscan_dims* dims, size_t* bytes);
@@ -557,6 +560,8 @@ typedef struct {
  *   u = x, or x silu(z) with PDSSM_GATE_BEFORE
  *   x, z, residual, y [B,H,L,d] (views; z NULL without a gate; residual NULL: zero)
  *   w, res_scale [H,d] or [d] (res_scale NULL: one)
+ * A row's sum of squares has to be within fp32 (elements up to 2e17): a row
+ * past it has a norm of zero.
  * B L at most 2^30 - 128, H at most 2^23 - 1, H d with per_head below 2^29. */
 int pdssm_norm_fwd(const pdssm_norm_dims* dims, const pdssm_view* x, const float* w, const pdssm_view* z,
                    const pdssm_view* residual, const float* res_scale, const pdssm_view* y, void* stream);

@@ -17,7 +17,7 @@
 // states that a pass of its own forms first (ss_split).
 //
 // 16 x 2048 steps, 768 channels, 16 states, bf16: 141 us (159 under the
-// profiler).  The vector units are what it waits for: 135 us at 2.1 GHz by their counter, of
+// profiler).  The vector units are what it waits for: 136 us at 2.1 GHz by their counter, of
 // which the cells' 28 cycles are 84; the rest is what a (t, d) needs once (softplus, the gate,
 // roundings) and the exchanges.  Memory, 205 MB, would take 40.  Three barriers a tile took 151, two 141.
 // A tile's first wave could run its steps once, from the state that it knows, and its last
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(256, S >= 8 ? 2 : 3) void pdssm_selscan_kernel(cons
 //
 // The state that a piece adds, from zero, and the sum of its steps; a wave
 // takes its channels through the piece alone (16 x 2048 x 768 x 16
-// 94 us under the profiler, 81 of them the vector units).  With ckpt it also writes the
+// 94 to 99 us under the profiler, 82 of them the vector units).  With ckpt it also writes the
 // state and the sum at the start of every tile of the gradient.  Backwards
 // (REV) it is the adjoint state that flows out of the piece's start,
 // l = a_t (l + g_t C_t), with g the gradient of y before its gate.
@@ -453,8 +453,8 @@ __global__ __launch_bounds__(256) void pdssm_selscan_state_kernel(const SsArgs a
 // up inside the rows of 16 lanes.  (On the matrix cores, as products with a row
 // of ones, they took 32 cycles each: 660 us for the kernel below.)
 //
-// 16 x 2048 x 768 x 16 in bf16: the whole gradient 529 us; this kernel 471 under the
-// profiler, 385 of them the vector units: 60000 instructions a wave for its 64 tiles of 32 cells a
+// 16 x 2048 x 768 x 16 in bf16: the whole gradient 529 us; this kernel 460 to 505 under
+// the profiler, 387 of them the vector units: 61000 instructions a wave for its 64 tiles of 32 cells a
 // lane, three waves a SIMD.  The tile's outputs leave before the next is
 // staged: with two tiles' rows in LDS and two barriers the gradient took 690 us instead of 590.
 //

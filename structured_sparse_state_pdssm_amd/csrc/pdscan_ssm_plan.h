@@ -150,6 +150,9 @@ inline double ss_rounds(double fill, int per, bool bwd) {
 //   backwards  256 of 1: 61 / 50;  384 of 4: 81 / 64;  2048 of 8: 389 / 311, of 12: 499 / 449, of 16: 529 / 567, of 20: 727 / 700, of 24: 848 / 842
 // Sequences of different lengths, where the longest counts, are taken as three of a third of the rows:
 //   16 in 2048 rows 33 / 45 and 111 / 94, 16 in 8192 102 / 89 and 333 / 215; 2048 channels, 40 in 8192 191 / 242 and 713 / 716
+// That suits lengths with a long tail, as drawn for these.  Where all are alike it cuts what would fill the card
+// whole (the same sequences in a batch / packed): forwards 40 of 512 94 / 170, 16 of 2048 141 / 231, 32 of 2048 253 / 487;
+// backwards 348 / 472, 536 / 679, 1037 / 1514.  Whoever has such lengths is better off with a batch.
 inline SsSplit ss_split(int B, int L, int packed, long long width, int per, long long states, bool bwd) {
   SsSplit s;
   constexpr int kCus = 256, kUnit = 32, kLeast = 64, kRun = 128;   // steps of a piece and of a run, at least

@@ -267,3 +267,19 @@ def test_sequences_without_rows(dt):
             g = P.pdssm_conv_bwd(**c, g_y=cy, g_xL=cx, cu_seqlens=cu, out={"g_x": mark(cy)})
             assert torch.equal(xL, c["x0"]) and torch.equal(g["g_x0"], cx)
             assert (y == 7).all() and (g["g_x"] == 7).all() and (g["g_w"] == 0).all() and (g["g_bias"] == 0).all()
+
+
+@DT
+@pytest.mark.parametrize("d", [64, 1032])
+def test_rows_whose_squares_pass_fp32(d, dt):
+    """They have a norm of zero and no gradient; their neighbours are what they are by themselves."""
+    P = lib()
+    x, res, gy = norm_inputs((1, 2, 6, d), dt, None, False, True)
+    x["x"][:, :, 2] = x["x"][:, :, 2].sign() * 1e20
+    y, g = P.pdssm_norm_fwd(**x, residual=res), P.pdssm_norm_bwd(**x, g_y=gy)
+    assert torch.equal(y[:, :, 2], res[:, :, 2]) and (g["g_x"][:, :, 2] == 0).all()
+    keep = [0, 1, 3, 4, 5]
+    part = dict(x, x=x["x"][:, :, keep].contiguous())
+    y2, g2 = P.pdssm_norm_fwd(**part, residual=res[:, :, keep].contiguous()), P.pdssm_norm_bwd(**part, g_y=gy[:, :, keep].contiguous())
+    assert torch.equal(y[:, :, keep], y2) and torch.equal(g["g_x"][:, :, keep], g2["g_x"])
+    assert torch.isfinite(g["g_w"]).all()
